@@ -70,7 +70,18 @@ enum {
     QSA_DEV_BAD_CELL = 4,          /* a cell < 0 or on a page >= n_lpages (masked) */
     QSA_DEV_BAD_PAGE = 8,          /* a page-table entry >= n_ppages (masked) */
     QSA_DEV_BAD_UNION_COUNT = 16,  /* a union count outside [0, union_stride] (clamped) */
-    QSA_DEV_WAIT_TIMEOUT = 32      /* a pipelined kernel gave up waiting; its output is invalid */
+    QSA_DEV_WAIT_TIMEOUT = 32,     /* a pipelined kernel gave up waiting; its output is invalid */
+    QSA_DEV_BAD_SEQ_LEN = 64,      /* a length that is negative or longer than its page table (clamped) */
+    QSA_DEV_NO_PAGE = 128,         /* the free list ran out, or a token's page is not resident (slot -1) */
+    QSA_DEV_TOKEN_OVERFLOW = 256,  /* more new tokens than the token arrays hold (the rest is not mapped) */
+    QSA_DEV_BAD_AXIS = 512         /* a pair's axis outside [0, n_axes) (axis 0 is used) */
+};
+
+/* Element types of the 16- and 32-bit tensors that more than one type is allowed for. */
+enum {
+    QSA_BF16 = 0,
+    QSA_F16 = 1,
+    QSA_F32 = 2
 };
 
 /* Attention kernel variants (all sm_103a).  QSA_ATTN_DEFAULT picks the fastest. */
@@ -215,6 +226,143 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
                     const int32_t* page_tables, int32_t pt_stride, int32_t n_lpages, int32_t n_ppages,
                     int32_t n_kv, const int32_t* sel, const int32_t* sel_count, int32_t sel_stride,
                     int32_t n_q, float sm_scale, float* out, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Serving a cache: the operators around the paged INT8 cache that the attention
+ * calls above read.  None of them is part of the selected-cell method; they use
+ * its cache (pools, scales, page tables, 64-cell pages, d = 128, non-resident
+ * pages masked) and its conventions.  A step of a serving loop is
+ *     qsa_extend_tables -> qsa_rope_append -> qsa_paged_attn or qsa_decode_attn
+ * on one stream, with nothing read back by the host in between.  Here the query
+ * heads of a KV head are n_heads / n_kv, any whole number (not only 12).
+ * Scale arrays, like pools, must be 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+
+/* Attention of one new token per sequence over its whole paged cache: for
+ * sequence s and query head i, with n = seq_lens[s] and KV head i / (n_heads / n_kv),
+ *     out[s][i][:] = sum over cells c of softmax(q . k_c * sm_scale) * v_c,
+ * c running over the cells max(0, n - window) .. n-1 (window = 0: over 0 .. n-1)
+ * whose page is resident.  Zeros when no such cell exists.  Where lse is not
+ * NULL, lse[s][i] = log(sum over the same cells of exp(q . k_c * sm_scale)),
+ * natural logarithm, -infinity when no such cell exists.
+ *   - q: [n_seq][n_heads][128] of q_type (QSA_BF16 or QSA_F16); out: the same
+ *     shape of out_type (QSA_BF16, QSA_F16 or QSA_F32); lse: FP32 [n_seq][n_heads].
+ *     n_heads is a multiple of n_kv.
+ *   - page_tables: sequence s's table is page_tables[s * pt_stride ...], n_lpages
+ *     entries; pt_stride == 0 gives every sequence one shared table, otherwise
+ *     pt_stride >= n_lpages.  Entries past the sequence's last cell, and cells
+ *     outside the window, are never read; nor are the contents of cells past n in
+ *     the last page used (they may hold anything).
+ *   - A length outside [0, n_lpages * 64] is clamped and reported
+ *     (QSA_DEV_BAD_SEQ_LEN); an entry >= n_ppages is masked and reported
+ *     (QSA_DEV_BAD_PAGE).
+ *   - The cache's length is split over the GPU and the parts joined in a fixed
+ *     order: the same call gives the same bits.
+ *   - Scores: Q rounded to FP16 after an exact power-of-two scaling of each row
+ *     (exact for elements within 2^26 of the row's largest), K as the exact
+ *     INT8 integers, FP32 sums.  Weights times V scales are rounded to FP16 once
+ *     (relative 2^-11; FP16's range is kept by powers of two), V exact, FP32 sums.
+ *   - workspace: device memory of at least qsa_paged_attn_workspace_bytes(n_kv,
+ *     n_heads) bytes, 256-byte aligned; its contents need not be set and are
+ *     not kept.  Two calls that can overlap on the device need one each.
+ *   - QSA_ERR_UNSUPPORTED when n_seq * n_lpages * n_kv * ceil(n_heads / n_kv / 16)
+ *     exceeds 2^30 or n_ppages * n_kv * 64 exceeds 2^31 - 64; QSA_ERR_CAPACITY for
+ *     too small a workspace.  n_seq == 0 returns QSA_OK with no launch. */
+int qsa_paged_attn(const void* q, int32_t q_type, const int8_t* k_pool, const int8_t* v_pool,
+                   const uint16_t* k_scale, const uint16_t* v_scale, const int32_t* page_tables,
+                   int32_t pt_stride, int32_t n_lpages, int32_t n_ppages, int32_t n_kv, int32_t n_heads,
+                   const int32_t* seq_lens, int32_t n_seq, int32_t window, float sm_scale,
+                   void* out, int32_t out_type, float* lse, void* workspace, size_t workspace_bytes,
+                   int32_t* dev_status, void* stream);
+
+/* Workspace of qsa_paged_attn (independent of lengths and of n_seq); 0 for
+ * n_kv <= 0 or n_heads not a positive multiple of n_kv. */
+size_t qsa_paged_attn_workspace_bytes(int32_t n_kv, int32_t n_heads);
+
+/* Rotary positions, and the cache's write.  For each of n_tok tokens: pair j of
+ * every query and key head is turned by the angle positions[pair_axis[j]][t] *
+ * inv_freq[j] (radians), (a, b) -> (a cos - b sin, b cos + a sin); then each key
+ * and value row is quantised and written to the cell slots[t].
+ *   - q: [n_tok][n_heads][128], k, v: [n_tok][n_kv][128] of `type` (QSA_BF16 or
+ *     QSA_F16), tokens q_stride, k_stride, v_stride elements apart (multiples of
+ *     8; slices of one projection's output), 16-byte aligned.  q may be NULL
+ *     (then q_out is not written).
+ *   - positions: int32 [n_axes][pos_stride], pos_stride >= n_tok, n_axes 1 to 4
+ *     (time, height, width, ...); any int32 value.  inv_freq: FP64 [n_pairs],
+ *     finite.  pair_axis: int32 [n_pairs] or NULL (every pair on axis 0).
+ *     n_pairs is a multiple of 8 up to 64, or 0 for no rotation at all (then the
+ *     three pointers may be NULL).  Pair j is dims (j, j + n_pairs), or (2j, 2j + 1)
+ *     when interleaved; dims from 2 n_pairs on pass through.  The angle is formed
+ *     as a 64-bit fixed-point fraction of a turn, so positions far out lose nothing.
+ *   - q_out: as q, q_out_stride elements between tokens; the rotated queries,
+ *     rounded once.  q_out == q with equal strides is allowed.
+ *   - Rotated keys are quantised from FP32, not rounded to 16 bits before.  A
+ *     row's scale is max |x| / 127 rounded up to FP16 (at most 65504), its
+ *     integers round(x / scale), ties to even, within [-127, 127].  A row that
+ *     holds an infinity or NaN gets a NaN scale.
+ *   - slots: int32 [n_tok], physical cell (page * 64 + cell of the page) or < 0:
+ *     the token is not written.  A slot past the pool is not written and
+ *     reported (QSA_DEV_BAD_CELL).  Slots >= 0 must be distinct: two tokens of one
+ *     call with the same slot leave that cell a mixture of the two.
+ *   - Nothing but the named cells and q_out is written.  n_tok == 0 returns QSA_OK. */
+int qsa_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, int32_t type, const int32_t* positions, int32_t n_axes, int32_t pos_stride,
+                    const double* inv_freq, const int32_t* pair_axis, int32_t n_pairs, int32_t interleaved,
+                    void* q_out, int64_t q_out_stride, int8_t* k_pool, int8_t* v_pool, uint16_t* k_scale,
+                    uint16_t* v_scale, const int32_t* slots, int32_t n_ppages, int32_t n_heads, int32_t n_kv,
+                    int32_t n_tok, int32_t* dev_status, void* stream);
+
+/* The rotation of qsa_rope_append alone: x [n_tok][n_heads][128] -> out, tokens
+ * x_stride and out_stride elements apart (queries or keys of a layer that keeps no
+ * cache, such as an image encoder's).  Arguments as there; out == x is allowed with
+ * equal strides. */
+int qsa_rope(const void* x, int64_t x_stride, int32_t type, const int32_t* positions, int32_t n_axes,
+             int32_t pos_stride, const double* inv_freq, const int32_t* pair_axis, int32_t n_pairs,
+             int32_t interleaved, void* out, int64_t out_stride, int32_t n_heads, int32_t n_tok,
+             int32_t* dev_status, void* stream);
+
+/* Cells read back as the values they stand for: k_out[i][h][:] = int8 * scale of
+ * cell slots[i] for KV head h, and v_out likewise, computed in FP32 and rounded
+ * once to out_type (QSA_BF16, QSA_F16 or QSA_F32); [n_cell][n_kv][128], 16-byte
+ * aligned.  For a consumer of plain keys and values: a prefix handed to another
+ * attention, a cache moved or checked.  A slot < 0 gives zeros, a slot past the
+ * pool zeros and QSA_DEV_BAD_CELL; a slot may be named more than once.
+ * n_cell == 0 returns QSA_OK. */
+int qsa_cache_gather(const int8_t* k_pool, const int8_t* v_pool, const uint16_t* k_scale,
+                     const uint16_t* v_scale, const int32_t* slots, int32_t n_cell, int32_t n_ppages,
+                     int32_t n_kv, void* k_out, void* v_out, int32_t out_type, int32_t* dev_status, void* stream);
+
+/* Page tables extended and slots mapped for a step's new tokens.  Sequence s
+ * holds seq_lens[s] cells and gets new_lens[s] more; its pages beyond
+ * ceil(seq_lens[s] / 64) are taken from the free list, sequences in order, and
+ * written to its page table.  The new tokens of all sequences, in order, are
+ * numbered t = 0, 1, ...:
+ *     positions[t] = the token's cell in its sequence, token_seq[t] = s,
+ *     slots[t] = its physical cell (page * 64 + cell of the page), or -1,
+ * and for t from the total on, up to n_tok: slot -1, position 0, sequence -1.
+ *   - page_tables: int32 [n_seq][pt_stride], n_lpages <= pt_stride entries in
+ *     use; only the entries of new pages are written.
+ *   - free_pages: int32 [n_free] physical pages; *free_head (NULL: 0) of them are
+ *     already taken.  *free_head_out = that plus the pages taken now (at most
+ *     n_free).  It must not be the same word as *free_head: keep two and swap.
+ *     n_free, n_seq and n_tok are at most 2^30.
+ *   - seq_lens_out [n_seq] = lengths after the step; cu_tokens [n_seq + 1] = first
+ *     token of each sequence, then the total.  seq_lens_out must be neither seq_lens
+ *     nor new_lens.
+ *   - Reported, never faulting: lengths that are negative or do not fit n_lpages
+ *     pages (clamped, QSA_DEV_BAD_SEQ_LEN); more new tokens than n_tok (the tokens
+ *     from n_tok on are not added to their sequences, QSA_DEV_TOKEN_OVERFLOW); a
+ *     head outside [0, n_free] (clamped), a free list that ran out (entry and slots
+ *     -1) or a token on a page that is not resident (slot -1), QSA_DEV_NO_PAGE; a
+ *     page outside [0, n_ppages) taken from the list (as if run out) or >= n_ppages
+ *     in the table (slot -1), QSA_DEV_BAD_PAGE.
+ *   - slots, positions and token_seq must be 16-byte aligned.  One launch, no
+ *     atomics on results, no workspace; n_seq == 0 fills the padding. */
+int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t n_seq, int32_t* page_tables,
+                      int32_t pt_stride, int32_t n_lpages, int32_t n_ppages, const int32_t* free_pages,
+                      int32_t n_free, const int32_t* free_head, int32_t n_tok, int32_t* slots,
+                      int32_t* positions, int32_t* token_seq, int32_t* seq_lens_out, int32_t* cu_tokens,
+                      int32_t* free_head_out, int32_t* dev_status, void* stream);
 
 /* Self-test of the bounded waits (not part of the method: the pages have no
  * counterpart).  Every pipelined kernel here waits on mbarriers with a wall-time

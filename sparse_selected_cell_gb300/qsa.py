@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -20,10 +20,12 @@ LIB_PATH = os.path.join(PKG, "libqsa.so")
 QSA_OK, QSA_ERR_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_CAPACITY, QSA_ERR_CUDA, QSA_ERR_DEVICE_CHECK = range(6)
 ATTN_DEFAULT, ATTN_TCGEN05, ATTN_TCGEN05_SM = 0, 1, 2
 DEV_BITS = {1: "bad selection count", 2: "union overflow", 4: "bad cell", 8: "bad page-table entry",
-            16: "bad union count", 32: "device wait timeout"}
+            16: "bad union count", 32: "device wait timeout", 64: "bad sequence length", 128: "no page",
+            256: "token overflow", 512: "bad axis"}
+BF16, F16, F32 = 0, 1, 2          # element types (QSA_BF16, QSA_F16, QSA_F32)
 
 _lib = None
-_P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _S, _L = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 
 
 class QsaError(RuntimeError):
@@ -62,6 +64,20 @@ def lib():
         L.qsa_select_attn.restype = ctypes.c_int
         L.qsa_decode_attn.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _F, _P, _P, _P]
         L.qsa_decode_attn.restype = ctypes.c_int
+        L.qsa_paged_attn.argtypes = [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _F, _P, _I, _P, _P,
+                                     _S, _P, _P]
+        L.qsa_paged_attn.restype = ctypes.c_int
+        L.qsa_paged_attn_workspace_bytes.argtypes = [_I, _I]
+        L.qsa_paged_attn_workspace_bytes.restype = _S
+        L.qsa_rope_append.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _I, _I, _P, _P, _I, _I, _P, _L, _P, _P, _P, _P,
+                                      _P, _I, _I, _I, _I, _P, _P]
+        L.qsa_rope_append.restype = ctypes.c_int
+        L.qsa_rope.argtypes = [_P, _L, _I, _P, _I, _I, _P, _P, _I, _I, _P, _L, _I, _I, _P, _P]
+        L.qsa_rope.restype = ctypes.c_int
+        L.qsa_cache_gather.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _P]
+        L.qsa_cache_gather.restype = ctypes.c_int
+        L.qsa_extend_tables.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.qsa_extend_tables.restype = ctypes.c_int
         L.qsa_wait_selftest.argtypes = [_I, _P, _P]
         L.qsa_wait_selftest.restype = ctypes.c_int
         _lib = L
@@ -254,6 +270,245 @@ def decode_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, sel, sel_count
                                _ptr(dev_status), _stream(stream))
     _check("qsa_decode_attn", rc)
     return out
+
+
+# ---------------------------------------------------------------- serving a cache
+# The operators around the paged cache (include/qsa.h, "Serving a cache").  Single
+# tokens make these calls short, so the checks below are written out for speed:
+# one device comparison per tensor, raw addresses into ctypes, no wrappers.
+
+_TYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+_I32 = torch.int32
+
+
+def _want(t, name: str, dtype, dev, shape=None, contiguous: bool = True) -> int:
+    """The address of t, a tensor of the given dtype (or one of several) on device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a tensor on {dev}")
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _here(t, name: str) -> torch.device:
+    """The device of t, which has to be the current one: the library launches there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev = t.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _raw_stream(stream, dev) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _status_ptr(dev_status, dev) -> Optional[int]:
+    return None if dev_status is None else _want(dev_status, "dev_status", _I32, dev)
+
+
+_SCALE = (torch.float16, torch.int16, torch.uint16)
+
+
+def _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev):
+    """Addresses of the four arrays of a cache, then (n_ppages, n_kv)."""
+    kp = _want(k_pool, "k_pool", torch.int8, dev)
+    shape = k_pool.shape
+    if len(shape) != 4 or shape[2] != gen.PAGE_CELLS or shape[3] != gen.HEAD_DIM:
+        raise ValueError(f"k_pool must be [n_ppages, n_kv, 64, 128], got {tuple(shape)}")
+    return (kp, _want(v_pool, "v_pool", torch.int8, dev, shape), _want(k_scale, "k_scale", _SCALE, dev, shape[:3]),
+            _want(v_scale, "v_scale", _SCALE, dev, shape[:3]), shape[0], shape[1])
+
+
+def paged_attn_workspace_bytes(n_kv: int, n_heads: int) -> int:
+    """Bytes of workspace paged_attn needs for these head counts (whatever the lengths)."""
+    return int(lib().qsa_paged_attn_workspace_bytes(int(n_kv), int(n_heads)))
+
+
+def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_scale: Optional[float] = None,
+               window: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """One new token per sequence over its whole paged cache, or its last `window` cells (qsa_paged_attn):
+    q BF16 or FP16 [n_seq, n_heads, 128], page_tables int32 [n_seq, n_lpages], seq_lens int32 [n_seq] -> out
+    [n_seq, n_heads, 128] (float32 unless an `out` of another type is given); lse float32 [n_seq, n_heads] is
+    written when given.  A workspace that is not given is allocated here."""
+    dev = _here(q, "q")
+    qp = _want(q, "q", (torch.bfloat16, torch.float16), dev)
+    kp, vp, ksp, vsp, n_ppages, n_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != gen.HEAD_DIM or n_kv == 0 or shape[1] == 0 or shape[1] % n_kv:
+        raise ValueError(f"q must be [n_seq, n_heads, 128] with n_heads a multiple of {n_kv}, got {tuple(shape)}")
+    n_seq, n_heads = shape[0], shape[1]
+    tp = _want(page_tables, "page_tables", _I32, dev)
+    if page_tables.dim() != 2 or page_tables.shape[0] != n_seq:
+        raise ValueError(f"page_tables must be [{n_seq}, n_lpages], got {tuple(page_tables.shape)}")
+    width = page_tables.shape[1]
+    lp = _want(seq_lens, "seq_lens", _I32, dev, (n_seq,))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    op = _want(out, "out", (torch.float32, torch.bfloat16, torch.float16), dev, shape)
+    sp = None if lse is None else _want(lse, "lse", torch.float32, dev, (n_seq, n_heads))
+    if workspace is None:
+        workspace = torch.empty(paged_attn_workspace_bytes(n_kv, n_heads), dtype=torch.uint8, device=dev)
+    wp = _want(workspace, "workspace", workspace.dtype, dev)
+    rc = lib().qsa_paged_attn(qp, _TYPE[q.dtype], kp, vp, ksp, vsp, tp, width, width, n_ppages, n_kv, n_heads, lp, n_seq,
+                              min(int(window), 0x7FFFFFFF), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, op,
+                              _TYPE[out.dtype], sp, wp, workspace.nbytes, _status_ptr(dev_status, dev),
+                              _raw_stream(stream, dev))
+    if rc != QSA_OK:
+        raise QsaError("qsa_paged_attn", rc)
+    return out
+
+
+def _rows(t, name: str, dtype, dev, n_tok=None, n_heads=None):
+    """Address and token stride of a [n_tok, n_heads, 128] tensor whose tokens may lie apart."""
+    p = _want(t, name, dtype, dev, contiguous=False)
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != gen.HEAD_DIM or (n_tok is not None and shape[0] != n_tok) or \
+            (n_heads is not None and shape[1] != n_heads):
+        raise ValueError(f"{name} must be [{n_tok or 'n_tok'}, {n_heads or 'n_heads'}, 128], got {tuple(shape)}")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != gen.HEAD_DIM and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    return p, s[0] if shape[0] > 1 else shape[1] * gen.HEAD_DIM
+
+
+def _rotation(positions, inv_freq, pair_axis, n_tok, dev):
+    """(positions, n_axes, pos_stride, inv_freq, pair_axis, n_pairs) of a rotation; inv_freq None: none."""
+    if inv_freq is None:
+        return None, 0, 0, None, None, 0
+    pp = _want(positions, "positions", _I32, dev)
+    if positions.dim() not in (1, 2) or positions.shape[-1] != n_tok:
+        raise ValueError(f"positions must be [n_axes, {n_tok}] or [{n_tok}], got {tuple(positions.shape)}")
+    n_pairs = inv_freq.numel()
+    fp = _want(inv_freq, "inv_freq", torch.float64, dev, (n_pairs,))
+    ap = None if pair_axis is None else _want(pair_axis, "pair_axis", _I32, dev, (n_pairs,))
+    return pp, positions.shape[0] if positions.dim() == 2 else 1, n_tok, fp, ap, n_pairs
+
+
+def rope(x, positions, inv_freq, pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False,
+         out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotary positions with one or several axes (qsa_rope): x BF16 or FP16 [n_tok, n_heads, 128], positions int32
+    [n_axes, n_tok] (or [n_tok]), inv_freq float64 [n_pairs], pair_axis int32 [n_pairs] (None: axis 0) -> out (may be x)."""
+    dev = _here(x, "x")
+    xp, xs = _rows(x, "x", (torch.bfloat16, torch.float16), dev)
+    n_tok, n_heads = x.shape[0], x.shape[1]
+    rot = _rotation(positions, inv_freq, pair_axis, n_tok, dev)
+    if out is None:
+        out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=x.dtype, device=dev)
+    op, os_ = _rows(out, "out", x.dtype, dev, n_tok, n_heads)
+    rc = lib().qsa_rope(xp, xs, _TYPE[x.dtype], *rot, bool(interleaved), op, os_, n_heads, n_tok,
+                        _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+    if rc != QSA_OK:
+        raise QsaError("qsa_rope", rc)
+    return out
+
+
+def rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale, v_scale, slots,
+                interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                dev_status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotates a step's queries and keys and writes keys and values to their slots of the cache as INT8 rows with FP16
+    scales (qsa_rope_append): q [n_tok, n_heads, 128] (None: keys and values only), k and v [n_tok, n_kv, 128], all BF16
+    or all FP16, tokens any multiple of 8 elements apart; positions, inv_freq, pair_axis as in rope (inv_freq None: no
+    rotation); slots int32 [n_tok], < 0 = not written -> the rotated q (q_out, which may be q)."""
+    dev = _here(k, "k")
+    kp_, ks_ = _rows(k, "k", (torch.bfloat16, torch.float16), dev)
+    n_tok, n_kv, dtype = k.shape[0], k.shape[1], k.dtype
+    vp_, vs_ = _rows(v, "v", dtype, dev, n_tok, n_kv)
+    kp, vp, ksp, vsp, n_ppages, pool_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
+    if pool_kv != n_kv:
+        raise ValueError(f"k has {n_kv} heads, the cache {pool_kv}")
+    rot = _rotation(positions, inv_freq, pair_axis, n_tok, dev)
+    sp = _want(slots, "slots", _I32, dev, (n_tok,))
+    qp = op = None
+    qs = os_ = n_heads = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", dtype, dev, n_tok)
+        n_heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=dtype, device=dev)
+        op, os_ = _rows(q_out, "q_out", dtype, dev, n_tok, n_heads)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = lib().qsa_rope_append(qp, qs, kp_, ks_, vp_, vs_, _TYPE[dtype], *rot, bool(interleaved), op, os_, kp, vp, ksp,
+                               vsp, sp, n_ppages, n_heads, n_kv, n_tok, _status_ptr(dev_status, dev),
+                               _raw_stream(stream, dev))
+    if rc != QSA_OK:
+        raise QsaError("qsa_rope_append", rc)
+    return q_out
+
+
+def cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype: torch.dtype = torch.bfloat16,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Cells read back as the values they stand for (qsa_cache_gather): slots int32 [n_cell] -> (k, v)
+    [n_cell, n_kv, 128] of `dtype`, or of the given outputs' type."""
+    dev = _here(k_pool, "k_pool")
+    kp, vp, ksp, vsp, n_ppages, n_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
+    sp = _want(slots, "slots", _I32, dev)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [n_cell], got {tuple(slots.shape)}")
+    shape = (slots.shape[0], n_kv, gen.HEAD_DIM)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
+    ko = _want(k_out, "k_out", (torch.bfloat16, torch.float16, torch.float32), dev, shape)
+    vo = _want(v_out, "v_out", k_out.dtype, dev, shape)
+    rc = lib().qsa_cache_gather(kp, vp, ksp, vsp, sp, shape[0], n_ppages, n_kv, ko, vo, _TYPE[k_out.dtype],
+                                _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+    if rc != QSA_OK:
+        raise QsaError("qsa_cache_gather", rc)
+    return k_out, v_out
+
+
+class StepTables(NamedTuple):
+    """What extend_tables writes beside the page tables (all int32)."""
+    slots: torch.Tensor           # [n_tok] physical cell of each new token, -1 = none
+    positions: torch.Tensor       # [n_tok] its cell in its sequence
+    token_seq: torch.Tensor       # [n_tok] its sequence, -1 behind the last token
+    seq_lens: torch.Tensor        # [n_seq] lengths after the step
+    cu_tokens: torch.Tensor       # [n_seq + 1] first token of each sequence, then the total
+    free_head: torch.Tensor       # [1] pages of the free list that are taken now
+
+
+def extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok: int, n_ppages: int,
+                  free_head: Optional[torch.Tensor] = None, out=None, dev_status: Optional[torch.Tensor] = None,
+                  stream=None) -> StepTables:
+    """Page tables extended in place and slots mapped for a step's new tokens (qsa_extend_tables): seq_lens and new_lens
+    int32 [n_seq], page_tables int32 [n_seq, n_lpages], free_pages int32 [n_free] of which *free_head are taken, n_tok =
+    length of the token arrays (at least the new tokens of all sequences).  `out`: six tensors as in StepTables to reuse."""
+    dev = _here(seq_lens, "seq_lens")
+    n_seq = seq_lens.shape[0]
+    sl, nl = _want(seq_lens, "seq_lens", _I32, dev, (n_seq,)), _want(new_lens, "new_lens", _I32, dev, (n_seq,))
+    tp = _want(page_tables, "page_tables", _I32, dev)
+    if page_tables.dim() != 2 or page_tables.shape[0] != n_seq:
+        raise ValueError(f"page_tables must be [{n_seq}, n_lpages], got {tuple(page_tables.shape)}")
+    width = page_tables.shape[1]
+    if not (0 <= n_tok < 1 << 31 and 0 <= n_ppages < 1 << 31):
+        raise ValueError("n_tok and n_ppages must be non-negative 32-bit numbers")
+    fp = _want(free_pages, "free_pages", _I32, dev)
+    if out is None:
+        out = [torch.empty(n, dtype=_I32, device=dev) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1)]
+    slots, positions, token_seq, lens_out, cu, head_out = out
+    rc = lib().qsa_extend_tables(
+        sl, nl, n_seq, tp, width, width, n_ppages, fp, free_pages.numel(),
+        None if free_head is None else _want(free_head, "free_head", _I32, dev, (1,)), n_tok,
+        _want(slots, "slots", _I32, dev, (n_tok,)), _want(positions, "positions", _I32, dev, (n_tok,)),
+        _want(token_seq, "token_seq", _I32, dev, (n_tok,)), _want(lens_out, "seq_lens_out", _I32, dev, (n_seq,)),
+        _want(cu, "cu_tokens", _I32, dev, (n_seq + 1,)), _want(head_out, "free_head_out", _I32, dev, (1,)),
+        _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+    if rc != QSA_OK:
+        raise QsaError("qsa_extend_tables", rc)
+    return StepTables(slots, positions, token_seq, lens_out, cu, head_out)
 
 
 def wait_selftest(limit_us: int, dev_status: torch.Tensor, stream=None) -> None:
