@@ -14,14 +14,18 @@
 // of bytes.  Each CTA sums the page counts itself (the lengths are device data; no
 // host value is needed, so a captured graph follows the lengths).  A run touches at
 // most two items that it does not hold whole, its first and its last: their partial
-// (max, sum, O) go to the workspace and paged_join_kernel, launched beside this
-// kernel and waiting for it on the device, joins them in the order of the CTAs.
+// (max, sum, O) go to the workspace and paged_join_kernel joins them in the order of
+// the CTAs.
 //
-// A CTA: a producer warp copies whole pages of one KV head (8 KB of K, 8 KB of V by
-// TMA in the 128-byte swizzle, 128-byte scale rows by bulk copy) into a ring; four
-// consumer warps take pages in turn, each page by one warp with its own running
-// softmax, and merge at the end of each item.  The tensor work is mma.sync
-// m16n8k16: 16 rows per tile (12 query heads) would fill an eighth of a
+// A CTA: four warps take the run's pages in turn, each page by one warp with its own
+// running softmax, and merge at the end of each item.  Every warp has a ring of five
+// 16-cell units (2 KB of K, 2 KB of V, two 32-byte rows of scales) of its own, filled
+// by 16-byte asynchronous copies, 512 consecutive bytes an instruction, 16-byte pieces
+// XOR-swizzled by (row & 7) as they land (a bulk copy would leave every row on the
+// same banks, eightfold conflicts for V).  It computes on two units while three are in
+// flight and refills what it has used, so no warp waits for another inside an item,
+// and 100 to 166 KB per SM are on the way at any time.  A page's table entry is looked
+// up a page ahead.  The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an eighth of a
 // tcgen05.mma's 128 rows, whose operands would also have to be written back to
 // shared memory in 16 bits, twice the traffic of the INT8 rows; here they are
 // converted in registers, exactly.
@@ -39,28 +43,25 @@
 //     weigh 2^-12).  The running maximum moves only when a score passes it by 7 in
 //     log2; O follows it and f.  V goes from the INT8 page to the B operands by
 //     ldmatrix.trans on byte pairs.
-#include <cuda.h>
-
-#include <atomic>
-
 #include "serve.cuh"
-#include "tc_ptx.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kWarps = 4;                          // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);        // and one producer
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;                      // rows of a tile (query heads of one KV head)
-constexpr int kPageBytes = kPage * kHeadDim;       // one KV head's page of K or V
-constexpr int kScaleBytes = kPage * 2;
-constexpr int kStageBytes = 2 * kPageBytes + 2 * kScaleBytes;
-constexpr int kMaxStages = 8;
+constexpr int kUnit = 16;                          // cells of a unit; a step of the softmax is two
+constexpr int kDepth = 5;                          // units of a warp's ring
+constexpr int kUnitBytes = kUnit * kHeadDim;       // of K, and of V
+constexpr int kUnitScales = kUnit * 2;             // bytes of K scales, and of V scales
+constexpr int kWarpBytes = kDepth * 2 * (kUnitBytes + kUnitScales);
+constexpr int kMergeRows = 8;                      // rows merged at a time
+constexpr int kSmem = kWarps * kWarpBytes + kWarps * kMergeRows * kHeadDim * 4;
 constexpr int kMaxCtas = 320;                      // two per SM of 152, with room
-constexpr int kMinPages = 4;                       // pages of a run at least: one per consumer warp
+constexpr int kMinPages = 4;                       // pages of a run at least: one per warp
 constexpr float kLazy = 7.f;
 constexpr int kPBits = 7;                          // a row's largest |p v_scale| becomes 2^7 to 2^8 (2^15 at most) in P
-constexpr uint64_t kWaitNs = 1000000000ull;
 
 // Workspace: a record per CTA for the join, then two partial results per CTA (0: the
 // item its run begins inside, 1: the item its run ends inside).
@@ -115,21 +116,12 @@ __device__ __forceinline__ void int8x4_to_f16_even_odd(uint32_t w, uint32_t& out
     out02 = f16x2_sub(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u);
     out13 = f16x2_sub(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
 }
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// One KV head's page (64 rows of 128 bytes) into a 1,024-byte aligned buffer, 16-byte
-// pieces XOR-swizzled by (row & 7).  x = 0; row is a multiple of 64 inside the pool.
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Four consecutive elements of the output.
 __device__ __forceinline__ void store4(void* out, int type, size_t at, float a, float b, float c, float d) {
@@ -180,89 +172,85 @@ struct Walk {
             q = seq_of(a, s, false);
         } while (q.np == 0);
     }
+    // `pages` further; the place must exist.
+    __device__ __forceinline__ void advance(const PagedArgs& a, int n_hk, int pages) {
+        off += pages;
+        while (off >= q.np) {
+            const int rest = off - q.np;
+            next_item(a, n_hk);
+            if (s >= a.n_seq) return;
+            off = rest;
+        }
+    }
 };
 
 struct Ctx {
-    uint32_t ring, scales, full, empty;   // shared-memory addresses
-    uint32_t* resident;                   // per stage: the page is there
-    float* merge;                         // [kWarps][rows][128], 16-float pieces swapped in odd rows
-    float* merge_m;                       // [kWarps][16] running maxima, then sums
-    volatile int* abort_flag;
-    int stages, rows;                     // rows: rows of the widest tile
+    uint32_t ring;                        // shared-memory address of this warp's units, 2 * kUnitBytes each
+    uint32_t scales;                      // and of their scales, 2 * kUnitScales each
+    float* merge;                         // [kWarps][kMergeRows][128], 16-float pieces swapped in odd rows
+    float* merge_m;                       // [kWarps][kMergeRows] running maxima, then sums
     int begin, end, chunk;                // this CTA's pages
     int n_hk, tiles, group;
 };
 
-// ---------------------------------------------------------------- producer warp
-__device__ __noinline__ void produce(const PagedArgs& a, const Ctx& c, Walk w, const CUtensorMap* kmap,
-                                     const CUtensorMap* vmap) {
-    const int lane = threadIdx.x & 31;
-    int st = 0, uses = 0;                 // stage, times round the ring
-    bool ok = true;
-    for (int pos = c.begin; pos < c.end && ok;) {
-        const int n = min(w.q.np - w.off, c.end - pos), h = w.hk / c.tiles;
-        const int32_t* table = a.page_tables + (size_t)w.s * a.pt_stride + w.q.p0 + w.off;
-        for (int i0 = 0; i0 < n && ok; i0 += 32) {
-            int entry = -1;
-            if (i0 + lane < n) {
-                entry = __ldg(table + i0 + lane);
-                if (entry >= a.n_ppages) {
-                    report(a.dev_status, QSA_DEV_BAD_PAGE);
-                    entry = -1;
-                }
-            }
-            for (int i = i0; i < min(n, i0 + 32); ++i) {
-                const int page = __shfl_sync(0xffffffffu, entry, i - i0);
-                const uint32_t full = c.full + 8 * st;
-                if (uses > 0) {
-                    ok = tc::mbar_wait(c.empty + 8 * st, (uint32_t)(uses - 1) & 1u, c.abort_flag, kWaitNs);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                }
-                if (lane == 0) {
-                    c.resident[st] = page >= 0;
-                    if (page >= 0) {
-                        const long long block = (long long)page * a.n_kv + h;
-                        const uint32_t dst = c.ring + st * 2 * kPageBytes, sdst = c.scales + st * 2 * kScaleBytes;
-                        mbar_expect_tx(full, kStageBytes);
-                        tma_page(dst, kmap, (int)(block * kPage), full);
-                        bulk_copy(sdst, a.k_scale + block * kPage, kScaleBytes, full);
-                        tma_page(dst + kPageBytes, vmap, (int)(block * kPage), full);
-                        bulk_copy(sdst + kScaleBytes, a.v_scale + block * kPage, kScaleBytes, full);
-                    } else {
-                        tc::mbar_arrive(full);
-                    }
-                }
-                __syncwarp();
-                if (++st == c.stages) {
-                    st = 0;
-                    ++uses;
-                }
-            }
-        }
-        pos += n;
-        w.next_item(a, c.n_hk);
-    }
-    if (!ok) {                            // gave up: wait for the copies in flight before the CTA may leave
-        if (lane == 0) report(a.dev_status, QSA_DEV_WAIT_TIMEOUT);
-        for (int k = 0; k < c.stages; ++k) {
-            // stage k was filled uses + (k < st) times; its last fill has parity (fills - 1) & 1
-            const int fills = uses + (k < st);
-            if (fills > 0) tc::mbar_wait_drain(c.full + 8 * k, (uint32_t)(fills - 1) & 1u, kWaitNs);
-        }
-    }
-    // rows of the sequences that have no page at all
-    for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
-        if (seq_of(a, s, false).np > 0) continue;
-        const size_t row = (size_t)s * a.n_heads;
-        for (int e = lane; e < a.n_heads * (kHeadDim / 4); e += 32)
-            store4(a.out, a.out_type, row * kHeadDim + 4 * e, 0.f, 0.f, 0.f, 0.f);
-        if (a.lse)
-            for (int e = lane; e < a.n_heads; e += 32) a.lse[row + e] = -INFINITY;
-    }
-}
+// ---------------------------------------------------------------- copies
+// A warp's copies, unit by unit over its pages of the run (every kWarps-th).  The
+// table entry of the page after the current one is already on its way.
+struct Fetch {
+    Walk w;                               // on the page looked up last
+    int idx, at;                          // that page's place in the run; where w stands
+    int entry;
+    int v;                                // units so far
+    uint32_t resident;                    // per slot: its unit's page is there
+    long long block;                      // the current page: pool block, whether it is there, its cells' limits
+    bool ok;
+    int lo, hi;
 
-// ---------------------------------------------------------------- consumer warps
+    __device__ __forceinline__ void look(const PagedArgs& a, const Ctx& c, int page) {
+        idx = page;
+        if (c.begin + idx >= c.end) return;
+        w.advance(a, c.n_hk, idx - at);
+        at = idx;
+        entry = __ldg(a.page_tables + (size_t)w.s * a.pt_stride + w.q.p0 + w.off);
+    }
+    // The next unit into slot `slot` of the ring; one group, empty behind the run's end.
+    __device__ __forceinline__ void put(const PagedArgs& a, const Ctx& c, int slot) {
+        const int lane = threadIdx.x & 31, u = v & 3;
+        if (u == 0) {                     // a new page
+            ok = c.begin + idx < c.end && entry >= 0;
+            if (ok && entry >= a.n_ppages) {
+                if (lane == 0) report(a.dev_status, QSA_DEV_BAD_PAGE);
+                ok = false;
+            }
+            block = (long long)entry * a.n_kv + w.hk / c.tiles;
+            const int cell0 = (w.q.p0 + w.off) * kPage;
+            lo = w.q.first - cell0;
+            hi = w.q.n - cell0;
+            if (c.begin + idx < c.end) look(a, c, idx + kWarps);
+        }
+        resident = ok ? resident | (1u << slot) : resident & ~(1u << slot);
+        if (ok && kUnit * u < hi && kUnit * (u + 1) > lo) {   // units outside the sequence or window are not read
+            // lane l copies piece l & 7 of rows l / 8 + 4 j; for odd j, (row & 7) flips bit 2 of the piece
+            const uint32_t dst = c.ring + slot * 2 * kUnitBytes + (uint32_t)(lane >> 3) * kHeadDim +
+                                 (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
+            const long long row = block * kPage + kUnit * u;
+            const int8_t* ksrc = a.k_pool + row * kHeadDim + 16 * lane;
+            const int8_t* vsrc = a.v_pool + row * kHeadDim + 16 * lane;
+#pragma unroll
+            for (int j = 0; j < kUnitBytes / 512; ++j) copy16((dst ^ ((j & 1) << 6)) + 512 * j, ksrc + 512 * j);
+            if (lane < 4)                 // 32 bytes of K scales, 32 of V scales
+                copy16(c.scales + slot * 2 * kUnitScales + 16 * lane,
+                       (lane < 2 ? a.k_scale : a.v_scale) + row + 8 * (lane & 1));
+#pragma unroll
+            for (int j = 0; j < kUnitBytes / 512; ++j)
+                copy16((dst ^ ((j & 1) << 6)) + kUnitBytes + 512 * j, vsrc + 512 * j);
+        }
+        copies_commit();
+        ++v;
+    }
+};
+
+// ---------------------------------------------------------------- two units
 // Running state of one warp over the pages of one item: rows g and g + 8 of lane
 // (g, t) = (lane / 4, lane % 4).
 struct State {
@@ -272,15 +260,18 @@ struct State {
     int f0, f1;                           // P and O carry 2^f
 };
 
-__device__ __forceinline__ void page_step(State& s, const uint32_t (&qa)[8][4], float rs0, float rs1, float kmul,
-                                          uint32_t k_base, uint32_t sc_base, int lo, int hi, int lane) {
+// The 32 cells of units in slots x and y; cells lo .. hi - 1 of them count (hi > lo).
+__device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], float rs0, float rs1, float kmul, const Ctx& c,
+                                       int x, int y, int lo, int hi, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int pg = (g >> 1) | ((g & 1) << 2);            // cell (of eight) of this lane's K column
+    const uint32_t unit[2] = {c.ring + x * 2 * kUnitBytes, c.ring + y * 2 * kUnitBytes};
+    const uint32_t scale[2] = {c.scales + x * 2 * kUnitScales, c.scales + y * 2 * kUnitScales};
     // ---- S = Q K^T
-    float sc[8][4];
+    float sc[4][4];
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        const uint32_t row = k_base + (uint32_t)(8 * nt + pg) * kHeadDim;
+    for (int nt = 0; nt < 4; ++nt) {
+        const uint32_t row = unit[nt >> 1] + (uint32_t)(8 * (nt & 1) + pg) * kHeadDim;
         const uint4 w0 = lds128(row + (uint32_t)((t ^ pg) << 4)), w1 = lds128(row + (uint32_t)(((4 + t) ^ pg) << 4));
         const uint32_t kw[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
         sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
@@ -292,20 +283,20 @@ __device__ __forceinline__ void page_step(State& s, const uint32_t (&qa)[8][4], 
         }
     }
     // ---- scales of the lane's columns: cells 8 nt + t and 8 nt + t + 4 of columns 2t, 2t + 1
-    const bool whole = lo == 0 && hi == kPage;           // warp-uniform
+    const bool whole = lo <= 0 && hi >= 2 * kUnit;       // warp-uniform
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
+    for (int nt = 0; nt < 4; ++nt) {
         float ks[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ks[e] = lds_half(sc_base + 2 * (8 * nt + t + 4 * e)) * kmul;
+        for (int e = 0; e < 2; ++e) ks[e] = lds_half(scale[nt >> 1] + 2 * (8 * (nt & 1) + t + 4 * e)) * kmul;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] *= ks[e & 1];
         if (!whole) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int c = 8 * nt + t + 4 * e;
-                if (c < lo || c >= hi) sc[nt][e] = sc[nt][e + 2] = -INFINITY;
+                const int cell = 8 * nt + t + 4 * e;
+                if (cell < lo || cell >= hi) sc[nt][e] = sc[nt][e + 2] = -INFINITY;
             }
         }
         mx0 = fmax3(mx0, sc[nt][0], sc[nt][1]);
@@ -332,13 +323,13 @@ __device__ __forceinline__ void page_step(State& s, const uint32_t (&qa)[8][4], 
     const float mu0 = s.m0 == -INFINITY ? 0.f : s.m0, mu1 = s.m1 == -INFINITY ? 0.f : s.m1;
     float ps0 = 0.f, ps1 = 0.f, pm0 = 0.f, pm1 = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
+    for (int nt = 0; nt < 4; ++nt) {
         float vs[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int c = 8 * nt + t + 4 * e;
-            vs[e] = lds_half(sc_base + kScaleBytes + 2 * c);
-            if (!whole && (c < lo || c >= hi)) vs[e] = 0.f;   // its scale may be anything
+            const int cell = 8 * nt + t + 4 * e;
+            vs[e] = lds_half(scale[nt >> 1] + kUnitScales + 2 * (8 * (nt & 1) + t + 4 * e));
+            if (!whole && (cell < lo || cell >= hi)) vs[e] = 0.f;   // its scale may be anything
         }
         const float e0 = fast_exp2(fmaf(sc[nt][0], rs0, -mu0)), e1 = fast_exp2(fmaf(sc[nt][1], rs0, -mu0));
         const float e2 = fast_exp2(fmaf(sc[nt][2], rs1, -mu1)), e3 = fast_exp2(fmaf(sc[nt][3], rs1, -mu1));
@@ -372,18 +363,18 @@ __device__ __forceinline__ void page_step(State& s, const uint32_t (&qa)[8][4], 
         }
     }
     const float f0 = exp2i(s.f0), f1 = exp2i(s.f1);
-    // ---- O += P V, 16 cells at a time
+    // ---- O += P V, a unit at a time
     const int vr = lane & 7;
     const int vcell = ((vr >> 1) | ((vr & 1) << 2)) + 8 * ((lane >> 3) & 1);
-    const uint32_t v_base = k_base + kPageBytes + (uint32_t)vcell * kHeadDim;
 #pragma unroll
-    for (int ks16 = 0; ks16 < 4; ++ks16) {
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t v_base = unit[j] + kUnitBytes + (uint32_t)vcell * kHeadDim;
         uint32_t af[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float* p = sc[2 * ks16 + j];
-            af[2 * j] = pack_f16x2(p[0] * f0, p[1] * f0);
-            af[2 * j + 1] = pack_f16x2(p[2] * f1, p[3] * f1);
+        for (int e = 0; e < 2; ++e) {
+            const float* p = sc[2 * j + e];
+            af[2 * e] = pack_f16x2(p[0] * f0, p[1] * f0);
+            af[2 * e + 1] = pack_f16x2(p[2] * f1, p[3] * f1);
         }
         // byte pairs by ldmatrix.trans: of the 32 dims 32q .. 32q + 31, lane (g, t) gets, of cells
         // perm(2t), perm(2t + 1) (and those + 8), dims 32q + 2g, + 1 and 32q + 16 + 2g, + 1.  O tile
@@ -391,8 +382,7 @@ __device__ __forceinline__ void page_step(State& s, const uint32_t (&qa)[8][4], 
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t r[4];
-            ldsm_x4_t(v_base + ks16 * 16 * kHeadDim + (uint32_t)(((2 * q + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2],
-                      r[3]);
+            ldsm_x4_t(v_base + (uint32_t)(((2 * q + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 uint32_t e0, d0, e1, d1;
@@ -448,14 +438,23 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
     }
 }
 
-__device__ __forceinline__ void consume(const PagedArgs& a, const Ctx& c, Walk w) {
+// The run's pages, from place w on.
+__device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk w) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const Ws ws = workspace_of(a.workspace);
     const float kmul = a.sm_scale * kLog2e;
+    Fetch f;
+    f.w = w;
+    f.at = f.v = 0;
+    f.entry = -1;
+    f.resident = 0;
+    f.ok = false;
+    f.look(a, c, warp);
+#pragma unroll 1
+    for (int k = 0; k < kDepth; ++k) f.put(a, c, k);
     int next = c.begin + warp;            // this warp's next page
-    int st = warp, uses = 0;              // its stage (warp < stages) and the times round the ring
-    bool dead = false;                    // a wait ran out: go through the motions, so that no barrier is left waiting
+    int slot = 0;                         // where its next unit is
     for (int pos = c.begin; pos < c.end; w.next_item(a, c.n_hk)) {
         const int n = min(w.q.np - w.off, c.end - pos);
         const int h = w.hk / c.tiles, tile = w.hk - h * c.tiles;
@@ -477,24 +476,18 @@ __device__ __forceinline__ void consume(const PagedArgs& a, const Ctx& c, Walk w
             load_q(a, row0, rows, lane, qa, rs0, rs1);
 #pragma unroll 1
             for (; next < seg_end; next += kWarps) {
-                if (!dead) {
-                    const bool ok = tc::mbar_wait(c.full + 8 * st, (uint32_t)uses & 1u, c.abort_flag, kWaitNs);
-                    dead = __any_sync(0xffffffffu, !ok);
-                    if (dead && lane == 0) report(a.dev_status, QSA_DEV_WAIT_TIMEOUT);
-                }
-                if (!dead) {
-                    if (c.resident[st]) {
-                        const int cell0 = (w.q.p0 + w.off + (next - pos)) * kPage;
-                        page_step(s, qa, rs0, rs1, kmul, c.ring + st * 2 * kPageBytes, c.scales + st * 2 * kScaleBytes,
-                                  max(w.q.first - cell0, 0), min(w.q.n - cell0, kPage), lane);
-                    }
+                const int cell0 = (w.q.p0 + w.off + (next - pos)) * kPage;
+#pragma unroll 1
+                for (int half = 0; half < kPage; half += 2 * kUnit) {
+                    const int x = slot, y = slot + 1 == kDepth ? 0 : slot + 1;
+                    copies_wait<kDepth - 2>();   // one group a unit: all but the youngest three have landed
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(c.empty + 8 * st);
-                }
-                st += kWarps;
-                if (st >= c.stages) {     // kWarps <= stages
-                    st -= c.stages;
-                    ++uses;
+                    const int lo = w.q.first - cell0 - half, hi = w.q.n - cell0 - half;
+                    if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, qa, rs0, rs1, kmul, c, x, y, lo, hi, lane);
+                    __syncwarp();         // every lane has read the units
+                    f.put(a, c, x);
+                    f.put(a, c, y);
+                    slot = y + 1 == kDepth ? 0 : y + 1;
                 }
             }
             s.l0 += __shfl_xor_sync(0xffffffffu, s.l0, 1);
@@ -539,60 +532,59 @@ __device__ __forceinline__ void consume(const PagedArgs& a, const Ctx& c, Walk w
                 }
             }
         } else {
-            // merge the warps that had pages: (pos - begin) % kWarps is the first of them
-            consumers_sync();             // the last merge has been read
-            if (mine) {
+            // merge the warps that had pages, eight rows at a time; (pos - begin) % kWarps is the first of them
+            const int lead = (pos - c.begin) % kWarps;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = g + 8 * half;
-                    if (r < rows) {
-                        float* dst = c.merge + ((size_t)warp * c.rows + r) * kHeadDim;
+            for (int half = 0; half < 2; ++half) {
+                if (half * kMergeRows >= rows) break;
+                __syncthreads();          // the last merge has been read
+                if (mine && g + 8 * half < rows) {
+                    float* dst = c.merge + (warp * kMergeRows + g) * kHeadDim;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int d = (16 * q + 4 * t) ^ ((r & 1) << 4), e = 2 * q, v = 2 * half;
-                            *reinterpret_cast<float4*>(dst + d) =
-                                make_float4(s.o[e][v], s.o[e + 1][v], s.o[e][v + 1], s.o[e + 1][v + 1]);
-                        }
-                        if (t == 0) {
-                            c.merge_m[warp * kRowsTile + r] = half ? s.m1 : s.m0;
-                            c.merge_m[(kWarps + warp) * kRowsTile + r] = half ? s.l1 : s.l0;
-                        }
+                    for (int q = 0; q < 8; ++q) {
+                        const int d = (16 * q + 4 * t) ^ ((g & 1) << 4), e = 2 * q, v = 2 * half;
+                        *reinterpret_cast<float4*>(dst + d) =
+                            make_float4(s.o[e][v], s.o[e + 1][v], s.o[e][v + 1], s.o[e + 1][v + 1]);
+                    }
+                    if (t == 0) {
+                        c.merge_m[warp * kMergeRows + g] = half ? s.m1 : s.m0;
+                        c.merge_m[(kWarps + warp) * kMergeRows + g] = half ? s.l1 : s.l0;
                     }
                 }
-            }
-            consumers_sync();
-            const int lead = (pos - c.begin) % kWarps;
-            for (int r = warp; r < rows; r += kWarps) {
-                float m[kWarps], l[kWarps], M = -INFINITY;
+                __syncthreads();
+                for (int i = warp; i < kMergeRows && i + 8 * half < rows; i += kWarps) {
+                    const int r = i + 8 * half;
+                    float m[kWarps], l[kWarps], M = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const bool had = ((k - lead + kWarps) % kWarps) < n;
-                    m[k] = had ? c.merge_m[k * kRowsTile + r] : -INFINITY;
-                    l[k] = had ? c.merge_m[(kWarps + k) * kRowsTile + r] : 0.f;
-                    M = fmaxf(M, m[k]);
-                }
-                float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+                    for (int k = 0; k < kWarps; ++k) {
+                        const bool had = ((k - lead + kWarps) % kWarps) < n;
+                        m[k] = had ? c.merge_m[k * kMergeRows + i] : -INFINITY;
+                        l[k] = had ? c.merge_m[(kWarps + k) * kMergeRows + i] : 0.f;
+                        M = fmaxf(M, m[k]);
+                    }
+                    float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    if (((k - lead + kWarps) % kWarps) >= n) continue;
-                    const float wt = merge_weight(m[k], l[k], M);
-                    const float4 o = *reinterpret_cast<const float4*>(c.merge + ((size_t)k * c.rows + r) * kHeadDim +
-                                                                      ((4 * lane) ^ ((r & 1) << 4)));
-                    L += wt * l[k];
-                    x0 += wt * o.x;
-                    x1 += wt * o.y;
-                    x2 += wt * o.z;
-                    x3 += wt * o.w;
-                }
-                if (complete) {
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
-                    store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
-                    if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
-                } else {
-                    *reinterpret_cast<float4*>(&part->o[r][4 * lane]) = make_float4(x0, x1, x2, x3);
-                    if (lane == 0) {
-                        part->m[r] = M;
-                        part->l[r] = L;
+                    for (int k = 0; k < kWarps; ++k) {
+                        if (((k - lead + kWarps) % kWarps) >= n) continue;
+                        const float wt = merge_weight(m[k], l[k], M);
+                        const float4 o = *reinterpret_cast<const float4*>(c.merge + (k * kMergeRows + i) * kHeadDim +
+                                                                          ((4 * lane) ^ ((i & 1) << 4)));
+                        L += wt * l[k];
+                        x0 += wt * o.x;
+                        x1 += wt * o.y;
+                        x2 += wt * o.z;
+                        x3 += wt * o.w;
+                    }
+                    if (complete) {
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
+                        if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
+                    } else {
+                        *reinterpret_cast<float4*>(&part->o[r][4 * lane]) = make_float4(x0, x1, x2, x3);
+                        if (lane == 0) {
+                            part->m[r] = M;
+                            part->l[r] = L;
+                        }
                     }
                 }
             }
@@ -608,6 +600,7 @@ __device__ __forceinline__ void consume(const PagedArgs& a, const Ctx& c, Walk w
         }
         pos = seg_end;
     }
+    copies_wait<0>();                     // nothing in flight when a warp leaves
 }
 
 // Sum over the block of each thread's count and the sum before this thread.
@@ -624,47 +617,27 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& before) {
     int total = 0;
     before = inc - v;
 #pragma unroll
-    for (int k = 0; k <= kWarps; ++k) {
+    for (int k = 0; k < kWarps; ++k) {
         if (k < warp) before += s_warp[k];
         total += s_warp[k];
     }
     return total;
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
-paged_attn_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  int stages, int rows) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_bars[2 * kMaxStages];
-    __shared__ uint32_t s_resident[kMaxStages];
-    __shared__ float s_ml[2 * kWarps * kRowsTile];
-    __shared__ int s_warp[kWarps + 1], s_abort, s_start[3];
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedArgs a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ float s_ml[2 * kWarps * kMergeRows];
+    __shared__ int s_warp[kWarps], s_start[2];
     const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up now; it waits for this grid's end
 
     Ctx c;
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    c.ring = base;
-    c.scales = base + stages * 2 * kPageBytes;
-    c.merge = reinterpret_cast<float*>(smem_raw + (base - raw) + stages * kStageBytes);
+    c.ring = smem_u32(smem_raw) + (tid >> 5) * kDepth * 2 * kUnitBytes;
+    c.scales = smem_u32(smem_raw) + kWarps * kDepth * 2 * kUnitBytes + (tid >> 5) * kDepth * 2 * kUnitScales;
+    c.merge = reinterpret_cast<float*>(smem_raw + kWarps * kWarpBytes);
     c.merge_m = s_ml;
-    c.full = smem_u32(s_bars);
-    c.empty = c.full + 8 * kMaxStages;
-    c.resident = s_resident;
-    c.abort_flag = &s_abort;
-    c.stages = stages;
-    c.rows = rows;
     c.group = a.n_heads / a.n_kv;
     c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
     c.n_hk = a.n_kv * c.tiles;
-    if (tid == 0) {
-        for (int k = 0; k < stages; ++k) {
-            tc::mbar_init(c.full + 8 * k, 1);
-            tc::mbar_init(c.empty + 8 * k, 1);
-        }
-        s_abort = 0;
-        tc::fence_mbar_init();
-    }
 
     // ---- this CTA's run of the pages of all items
     const int per = (a.n_seq + kThreads - 1) / kThreads;   // consecutive sequences per thread
@@ -696,19 +669,26 @@ paged_attn_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ C
         w.hk = s_start[1] / w.q.np;
         w.off = s_start[1] - w.hk * w.q.np;
     }
-    if (tid >= 32 * kWarps) produce(a, c, w, &kmap, &vmap);
-    else consume(a, c, w);
+    if (c.begin < c.end) walk_run(a, c, w);
+    // rows of the sequences that have no page at all
+    for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
+        if (seq_of(a, s, false).np > 0) continue;
+        const size_t row = (size_t)s * a.n_heads;
+        for (int e = tid; e < a.n_heads * (kHeadDim / 4); e += kThreads)
+            store4(a.out, a.out_type, row * kHeadDim + 4 * e, 0.f, 0.f, 0.f, 0.f);
+        if (a.lse)
+            for (int e = tid; e < a.n_heads; e += kThreads) a.lse[row + e] = -INFINITY;
+    }
 }
 
 // Joins the parts of the item that run blockIdx.x begins and others end: row
 // blockIdx.y of it.  Warps take parts in turn, a lane four dims.
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
     __shared__ float s_o[4][kHeadDim], s_l[4];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Ws ws = workspace_of(a.workspace);
     const int c0 = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Rec rec = ws.rec[c0];
-    if (rec.item < 0) return;
+    if (rec.item < 0 || rec.last >= (int)gridDim.x) return;
     const int group = a.n_heads / a.n_kv, tiles = (group + kRowsTile - 1) / kRowsTile;
     const int h = rec.hk / tiles, tile = rec.hk - h * tiles;
     if (r >= min(kRowsTile, group - kRowsTile * tile)) return;
@@ -746,35 +726,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
     if (lane == 0 && a.lse) a.lse[row] = lse_of(M, L);
 }
 
-// ---------------------------------------------------------------- host side
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (a host function without state), looked up once.
-EncodeTiled encoder() {
-    static std::atomic<void*> found{nullptr};
-    void* p = found.load(std::memory_order_acquire);
-    if (!p) {
-        cudaDriverEntryPointQueryResult st;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-            st != cudaDriverEntryPointSuccess)
-            return nullptr;
-        found.store(p, std::memory_order_release);
-    }
-    return reinterpret_cast<EncodeTiled>(p);
-}
-
-bool page_map(CUtensorMap* map, const int8_t* pool, long long rows) {
-    const EncodeTiled encode = encoder();
-    if (!encode) return false;
-    const cuuint64_t dims[2] = {kHeadDim, (cuuint64_t)rows}, strides[1] = {kHeadDim};
-    const cuuint32_t box[2] = {kHeadDim, kPage}, steps[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(pool), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 size_t paged_attn_workspace(int, int) { return kMaxCtas * (sizeof(Rec) + 2 * sizeof(Part)); }
@@ -784,33 +735,15 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    CUtensorMap kmap{}, vmap{};
-    if (a.n_ppages > 0) {                 // an empty pool: every page is masked and no copy is made
-        const long long rows = (long long)a.n_ppages * a.n_kv * kPage;
-        if (!page_map(&kmap, a.k_pool, rows) || !page_map(&vmap, a.v_pool, rows)) return cudaErrorInvalidValue;
-    }
-    // two CTAs share an SM's shared memory: 113 KB each, the merge's rows first, the ring from the rest
     const int rows = a.n_heads / a.n_kv < kRowsTile ? a.n_heads / a.n_kv : kRowsTile;
-    const int merge = kWarps * rows * kHeadDim * 4;
-    int stages = (112 * 1024 - 3072 - merge) / kStageBytes;
-    stages = stages > kMaxStages ? kMaxStages : stages;
-    const int smem = 1024 + stages * kStageBytes + merge;
-    e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    paged_attn_kernel<<<grid, kThreads, smem, stream>>>(a, kmap, vmap, stages, rows);
+    paged_attn_kernel<<<grid, kThreads, kSmem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)rows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel, a);
+    paged_join_kernel<<<dim3((unsigned)grid, (unsigned)rows), 128, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace qsa
