@@ -30,11 +30,13 @@
 // shared memory in 16 bits, twice the traffic of the INT8 rows; here they are
 // converted in registers, exactly.
 //   * S = Q K^T on FP16 operands.  Q is scaled per row by a power of two (its
-//     largest element in [2^12, 2^13)) and held in registers; within each 64-dim
-//     half the dims are permuted (Q and K alike) so that a lane's K operands of four
-//     k steps are one 16-byte piece of the INT8 row.  Column g of a score tile is
-//     cell perm(g) = g / 2 + 4 (g & 1) of its eight: the 16-byte reads of eight lanes
-//     then fall in eight different bank groups of the swizzled page.
+//     largest element in [2^12, 2^13)) and held in registers.  K enters as K + 128, an
+//     unsigned byte in the low bits of an FP16 word, which is the subnormal (K + 128) *
+//     2^-24: three instructions for four values; the accumulators start at -128 sum(Q).
+//     Within each 64-dim half the dims are permuted (Q and K alike) so that a lane's K
+//     operands of four k steps are one 16-byte piece of the INT8 row.  Column g of a
+//     score tile is cell perm(g) = g / 2 + 4 (g & 1) of its eight: the 16-byte reads of
+//     eight lanes then fall in eight different bank groups of the swizzled rows.
 //   * The K scale, sm_scale and log2 e multiply the score column in FP32, the row's
 //     power of two enters with the exponent's multiply-add.
 //   * P = p * v_scale * 2^f in FP16, f per row such that the row's largest |p *
@@ -87,15 +89,8 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t&
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float lds_half(uint32_t addr) {
-    uint16_t b;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(addr) : "memory");
-    return __half2float(__ushort_as_half(b));
+__device__ __forceinline__ float half_at(const uint8_t* p) {
+    return __half2float(*reinterpret_cast<const __half*>(p));
 }
 // Largest over the four lanes that share rows g and g + 8.
 __device__ __forceinline__ float quad_max(float v) {
@@ -104,11 +99,18 @@ __device__ __forceinline__ float quad_max(float v) {
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// INT8 bytes of a word plus 128, as FP16 pairs (bytes 0, 2) and (1, 3), times 2^-24:
+// an integer in FP16's low bits is a subnormal of just that value, exact to the tensor
+// core, and takes no conversion.
+__device__ __forceinline__ void biased_pairs(uint32_t w, uint32_t& out02, uint32_t& out13) {
+    const uint32_t u = w ^ 0x80808080u;
+    out02 = u & 0x00FF00FFu;
+    out13 = __byte_perm(u, 0u, 0x4341);
 }
 // INT8 bytes (0, 2) and (1, 3) of a word as FP16 pairs, exactly (as int8x4_to_f16).
 __device__ __forceinline__ void int8x4_to_f16_even_odd(uint32_t w, uint32_t& out02, uint32_t& out13) {
@@ -185,8 +187,8 @@ struct Walk {
 };
 
 struct Ctx {
-    uint32_t ring;                        // shared-memory address of this warp's units, 2 * kUnitBytes each
-    uint32_t scales;                      // and of their scales, 2 * kUnitScales each
+    uint8_t* ring;                        // this warp's units in shared memory, 2 * kUnitBytes each
+    uint8_t* scales;                      // and their scales, 2 * kUnitScales each
     float* merge;                         // [kWarps][kMergeRows][128], 16-float pieces swapped in odd rows
     float* merge_m;                       // [kWarps][kMergeRows] running maxima, then sums
     int begin, end, chunk;                // this CTA's pages
@@ -231,7 +233,7 @@ struct Fetch {
         resident = ok ? resident | (1u << slot) : resident & ~(1u << slot);
         if (ok && kUnit * u < hi && kUnit * (u + 1) > lo) {   // units outside the sequence or window are not read
             // lane l copies piece l & 7 of rows l / 8 + 4 j; for odd j, (row & 7) flips bit 2 of the piece
-            const uint32_t dst = c.ring + slot * 2 * kUnitBytes + (uint32_t)(lane >> 3) * kHeadDim +
+            const uint32_t dst = smem_u32(c.ring) + slot * 2 * kUnitBytes + (uint32_t)(lane >> 3) * kHeadDim +
                                  (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
             const long long row = block * kPage + kUnit * u;
             const int8_t* ksrc = a.k_pool + row * kHeadDim + 16 * lane;
@@ -239,7 +241,7 @@ struct Fetch {
 #pragma unroll
             for (int j = 0; j < kUnitBytes / 512; ++j) copy16((dst ^ ((j & 1) << 6)) + 512 * j, ksrc + 512 * j);
             if (lane < 4)                 // 32 bytes of K scales, 32 of V scales
-                copy16(c.scales + slot * 2 * kUnitScales + 16 * lane,
+                copy16(smem_u32(c.scales) + slot * 2 * kUnitScales + 16 * lane,
                        (lane < 2 ? a.k_scale : a.v_scale) + row + 8 * (lane & 1));
 #pragma unroll
             for (int j = 0; j < kUnitBytes / 512; ++j)
@@ -260,27 +262,45 @@ struct State {
     int f0, f1;                           // P and O carry 2^f
 };
 
+// A tile's query rows g and g + 8 as FP16 A operands: each row times a power of two 2^-e
+// that puts its largest element in [2^12, 2^13).  Within each 64-dim half the dims are
+// permuted: k step 4 h + k holds dims 64 h + 16 t + 4 k + (0, 2 | 1, 3) of lane column t,
+// in the order in which biased_pairs takes a word's bytes.
+struct Query {
+    uint32_t a[8][4];
+    float rs0, rs1;                       // 2^e
+    float bias0, bias1;                   // -128 * (sum of the row) * 2^-24
+};
+
 // The 32 cells of units in slots x and y; cells lo .. hi - 1 of them count (hi > lo).
-__device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], float rs0, float rs1, float kmul, const Ctx& c,
-                                       int x, int y, int lo, int hi, int lane) {
+__device__ __forceinline__ void step32(State& s, const Query& q, float kmul, const Ctx& c, int x, int y, int lo, int hi,
+                                       int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int pg = (g >> 1) | ((g & 1) << 2);            // cell (of eight) of this lane's K column
-    const uint32_t unit[2] = {c.ring + x * 2 * kUnitBytes, c.ring + y * 2 * kUnitBytes};
-    const uint32_t scale[2] = {c.scales + x * 2 * kUnitScales, c.scales + y * 2 * kUnitScales};
-    // ---- S = Q K^T
+    const uint8_t* unit[2] = {c.ring + x * 2 * kUnitBytes, c.ring + y * 2 * kUnitBytes};
+    const uint8_t* scale[2] = {c.scales + x * 2 * kUnitScales, c.scales + y * 2 * kUnitScales};
+    // ---- S = Q K^T: Q (K + 128) from the accumulators' start at -128 sum(Q), in units of 2^-24
     float sc[4][4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-        const uint32_t row = unit[nt >> 1] + (uint32_t)(8 * (nt & 1) + pg) * kHeadDim;
-        const uint4 w0 = lds128(row + (uint32_t)((t ^ pg) << 4)), w1 = lds128(row + (uint32_t)(((4 + t) ^ pg) << 4));
-        const uint32_t kw[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        sc[nt][0] = sc[nt][1] = q.bias0;
+        sc[nt][2] = sc[nt][3] = q.bias1;
+    }
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            uint32_t b0, b1;
-            int8x4_to_f16(kw[kk], b0, b1);
-            mma_f16(sc[nt], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-        }
+    for (int hk = 0; hk < 2; ++hk) {
+        uint4 w[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            w[nt] = *reinterpret_cast<const uint4*>(unit[nt >> 1] + (8 * (nt & 1) + pg) * kHeadDim + (((4 * hk + t) ^ pg) << 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {             // four independent chains
+                uint32_t b0, b1;
+                biased_pairs(k == 0 ? w[nt].x : k == 1 ? w[nt].y : k == 2 ? w[nt].z : w[nt].w, b0, b1);
+                const uint32_t(&a)[4] = q.a[4 * hk + k];
+                mma_f16(sc[nt], a[0], a[1], a[2], a[3], b0, b1);
+            }
     }
     // ---- scales of the lane's columns: cells 8 nt + t and 8 nt + t + 4 of columns 2t, 2t + 1
     const bool whole = lo <= 0 && hi >= 2 * kUnit;       // warp-uniform
@@ -289,7 +309,7 @@ __device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], flo
     for (int nt = 0; nt < 4; ++nt) {
         float ks[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ks[e] = lds_half(scale[nt >> 1] + 2 * (8 * (nt & 1) + t + 4 * e)) * kmul;
+        for (int e = 0; e < 2; ++e) ks[e] = half_at(scale[nt >> 1] + 2 * (8 * (nt & 1) + t + 4 * e)) * kmul;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[nt][e] *= ks[e & 1];
         if (!whole) {
@@ -303,8 +323,8 @@ __device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], flo
         mx1 = fmax3(mx1, sc[nt][2], sc[nt][3]);
     }
     // ---- running maxima (lazily moved)
-    mx0 *= rs0;
-    mx1 *= rs1;
+    mx0 *= q.rs0;
+    mx1 *= q.rs1;
     float al0 = 1.f, al1 = 1.f;
     const bool moved = __any_sync(0xffffffffu, mx0 > s.m0 + kLazy || mx1 > s.m1 + kLazy);
     if (moved) {
@@ -328,11 +348,11 @@ __device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], flo
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int cell = 8 * nt + t + 4 * e;
-            vs[e] = lds_half(scale[nt >> 1] + kUnitScales + 2 * (8 * (nt & 1) + t + 4 * e));
+            vs[e] = half_at(scale[nt >> 1] + kUnitScales + 2 * (8 * (nt & 1) + t + 4 * e));
             if (!whole && (cell < lo || cell >= hi)) vs[e] = 0.f;   // its scale may be anything
         }
-        const float e0 = fast_exp2(fmaf(sc[nt][0], rs0, -mu0)), e1 = fast_exp2(fmaf(sc[nt][1], rs0, -mu0));
-        const float e2 = fast_exp2(fmaf(sc[nt][2], rs1, -mu1)), e3 = fast_exp2(fmaf(sc[nt][3], rs1, -mu1));
+        const float e0 = fast_exp2(fmaf(sc[nt][0], q.rs0, -mu0)), e1 = fast_exp2(fmaf(sc[nt][1], q.rs0, -mu0));
+        const float e2 = fast_exp2(fmaf(sc[nt][2], q.rs1, -mu1)), e3 = fast_exp2(fmaf(sc[nt][3], q.rs1, -mu1));
         ps0 += e0 + e1;
         ps1 += e2 + e3;
         sc[nt][0] = e0 * vs[0];
@@ -368,7 +388,7 @@ __device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], flo
     const int vcell = ((vr >> 1) | ((vr & 1) << 2)) + 8 * ((lane >> 3) & 1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint32_t v_base = unit[j] + kUnitBytes + (uint32_t)vcell * kHeadDim;
+        const uint32_t v_base = smem_u32(unit[j]) + kUnitBytes + (uint32_t)vcell * kHeadDim;
         uint32_t af[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -376,29 +396,26 @@ __device__ __forceinline__ void step32(State& s, const uint32_t (&qa)[8][4], flo
             af[2 * e] = pack_f16x2(p[0] * f0, p[1] * f0);
             af[2 * e + 1] = pack_f16x2(p[2] * f1, p[3] * f1);
         }
-        // byte pairs by ldmatrix.trans: of the 32 dims 32q .. 32q + 31, lane (g, t) gets, of cells
-        // perm(2t), perm(2t + 1) (and those + 8), dims 32q + 2g, + 1 and 32q + 16 + 2g, + 1.  O tile
-        // 4q + 2h + e holds dims 32q + 16h + 2n + e at column n.
+        // byte pairs by ldmatrix.trans: of the 32 dims 32 d4 .. + 31, lane (g, t) gets, of cells
+        // perm(2t), perm(2t + 1) (and those + 8), dims 32 d4 + 2g, + 1 and 32 d4 + 16 + 2g, + 1.
+        // O tile 4 d4 + 2h + e holds dims 32 d4 + 16h + 2n + e at column n.
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int d4 = 0; d4 < 4; ++d4) {
             uint32_t r[4];
-            ldsm_x4_t(v_base + (uint32_t)(((2 * q + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2], r[3]);
+            ldsm_x4_t(v_base + (uint32_t)(((2 * d4 + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2], r[3]);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 uint32_t e0, d0, e1, d1;
                 int8x4_to_f16_even_odd(r[2 * hh], e0, d0);
                 int8x4_to_f16_even_odd(r[2 * hh + 1], e1, d1);
-                mma_f16(s.o[4 * q + 2 * hh], af[0], af[1], af[2], af[3], e0, e1);
-                mma_f16(s.o[4 * q + 2 * hh + 1], af[0], af[1], af[2], af[3], d0, d1);
+                mma_f16(s.o[4 * d4 + 2 * hh], af[0], af[1], af[2], af[3], e0, e1);
+                mma_f16(s.o[4 * d4 + 2 * hh + 1], af[0], af[1], af[2], af[3], d0, d1);
             }
         }
     }
 }
 
-// The tile's query rows g and g + 8 as FP16 A operands, each row times a power of two
-// 2^-e that puts its largest element in [2^12, 2^13); rs = 2^e.
-__device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows, int lane, uint32_t (&qa)[8][4], float& rs0,
-                                       float& rs1) {
+__device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows, int lane, Query& q) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -419,11 +436,11 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        amax = quad_max(amax);
         const int e = amax > 0.f ? min(max(f32_exponent(amax) - 12, -114), 114) : 0;
         const float down = exp2i(-e);
-        (half ? rs1 : rs0) = exp2i(e);
+        (half ? q.rs1 : q.rs0) = exp2i(e);
+        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[8];
@@ -431,10 +448,18 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
 #pragma unroll
             for (int k = 0; k < 2; ++k) {   // k step 4 (j / 2) + 2 (j & 1) + k: four dims
                 const int kk = 4 * (j >> 1) + 2 * (j & 1) + k;
-                qa[kk][half] = pack_f16x2(x[4 * k] * down, x[4 * k + 1] * down);
-                qa[kk][2 + half] = pack_f16x2(x[4 * k + 2] * down, x[4 * k + 3] * down);
+                const uint32_t even = pack_f16x2(x[4 * k] * down, x[4 * k + 2] * down);
+                const uint32_t odd = pack_f16x2(x[4 * k + 1] * down, x[4 * k + 3] * down);
+                q.a[kk][half] = even;
+                q.a[kk][2 + half] = odd;
+                const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&even));
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&odd));
+                sum += (u.x + u.y) + (v.x + v.y);
             }
         }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        (half ? q.bias1 : q.bias0) = sum * -0x1p-17f;
     }
 }
 
@@ -443,7 +468,7 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const Ws ws = workspace_of(a.workspace);
-    const float kmul = a.sm_scale * kLog2e;
+    const float kmul = a.sm_scale * kLog2e * 0x1p24f;   // scores come in units of 2^-24
     Fetch f;
     f.w = w;
     f.at = f.v = 0;
@@ -464,7 +489,6 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         const int seg_end = pos + n;
         const bool mine = next < seg_end;
         State s;
-        float rs0 = 1.f, rs1 = 1.f;
 #pragma unroll
         for (int d = 0; d < 16; ++d) s.o[d][0] = s.o[d][1] = s.o[d][2] = s.o[d][3] = 0.f;
         s.m0 = s.m1 = -INFINITY;
@@ -472,8 +496,8 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         s.top0 = s.top1 = 0.f;
         s.f0 = s.f1 = 0;
         if (mine) {
-            uint32_t qa[8][4];
-            load_q(a, row0, rows, lane, qa, rs0, rs1);
+            Query query;
+            load_q(a, row0, rows, lane, query);
 #pragma unroll 1
             for (; next < seg_end; next += kWarps) {
                 const int cell0 = (w.q.p0 + w.off + (next - pos)) * kPage;
@@ -483,7 +507,7 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
                     copies_wait<kDepth - 2>();   // one group a unit: all but the youngest three have landed
                     __syncwarp();
                     const int lo = w.q.first - cell0 - half, hi = w.q.n - cell0 - half;
-                    if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, qa, rs0, rs1, kmul, c, x, y, lo, hi, lane);
+                    if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, query, kmul, c, x, y, lo, hi, lane);
                     __syncwarp();         // every lane has read the units
                     f.put(a, c, x);
                     f.put(a, c, y);
@@ -631,8 +655,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const int tid = threadIdx.x;
 
     Ctx c;
-    c.ring = smem_u32(smem_raw) + (tid >> 5) * kDepth * 2 * kUnitBytes;
-    c.scales = smem_u32(smem_raw) + kWarps * kDepth * 2 * kUnitBytes + (tid >> 5) * kDepth * 2 * kUnitScales;
+    c.ring = smem_raw + (tid >> 5) * kDepth * 2 * kUnitBytes;
+    c.scales = smem_raw + kWarps * kDepth * 2 * kUnitBytes + (tid >> 5) * kDepth * 2 * kUnitScales;
     c.merge = reinterpret_cast<float*>(smem_raw + kWarps * kWarpBytes);
     c.merge_m = s_ml;
     c.group = a.n_heads / a.n_kv;
