@@ -9,25 +9,28 @@
 // enough copies in flight, and that the arithmetic per byte fits beside them.
 //
 // Split.  The pages of all (sequence, KV head, 16-row tile) items, laid end to end,
-// are cut into equal runs of pages, one per CTA of a grid of two per SM: ragged
-// batches, one long sequence and many short ones all give every SM the same number
-// of bytes.  Each CTA sums the page counts itself (the lengths are device data; no
-// host value is needed, so a captured graph follows the lengths).  A run touches at
-// most two items that it does not hold whole, its first and its last: their partial
-// (max, sum, O) go to the workspace and paged_join_kernel joins them in the order of
-// the CTAs.
+// are cut into equal runs of pages, one per warp of a grid of two CTAs per SM: ragged
+// batches, one long sequence and many short ones all give every SM the same number of
+// bytes, and a warp keeps an item's running softmax to itself, so that short items
+// (most of a chat batch) need no merge at all.  The CTA sums the page counts itself
+// (the lengths are device data; no host value is needed, so a captured graph follows
+// the lengths).  An item cut between warps leaves parts (max, sum, O): those of one CTA
+// are merged once, when its run is done, in the shared memory its copies have left;
+// what is cut between CTAs goes to the workspace, at most two parts a CTA, and
+// paged_join_kernel, launched beside this kernel and waiting for it on the device,
+// joins them in the order of the CTAs.
 //
-// A CTA: four warps take the run's pages in turn, each page by one warp with its own
-// running softmax, and merge at the end of each item.  Every warp has a ring of five
-// 16-cell units (2 KB of K, 2 KB of V, two 32-byte rows of scales) of its own, filled
-// by 16-byte asynchronous copies, 512 consecutive bytes an instruction, 16-byte pieces
-// XOR-swizzled by (row & 7) as they land (a bulk copy would leave every row on the
-// same banks, eightfold conflicts for V).  It computes on two units while three are in
-// flight and refills what it has used, so no warp waits for another inside an item,
-// and 100 to 166 KB per SM are on the way at any time.  A page's table entry is looked
-// up a page ahead.  The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an eighth of a
-// tcgen05.mma's 128 rows, whose operands would also have to be written back to
-// shared memory in 16 bits, twice the traffic of the INT8 rows; here they are
+// A warp has a ring of five 16-cell units (2 KB of K, 2 KB of V, two 32-byte rows of
+// scales), filled by 16-byte asynchronous copies, 512 consecutive bytes an instruction,
+// 16-byte pieces XOR-swizzled by (row & 7) as they land (a bulk copy would leave every
+// row on the same banks, eightfold conflicts for V).  It computes on two units while
+// three are in flight and refills what it has used: 100 to 166 KB per SM are on the way
+// at any time.  A page's table entry is looked up a page ahead, an item's queries an
+// item ahead.
+//
+// The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an
+// eighth of a tcgen05.mma's 128 rows, whose operands would also have to be written back
+// to shared memory in 16 bits, twice the traffic of the INT8 rows; here they are
 // converted in registers, exactly.
 //   * S = Q K^T on FP16 operands.  Q is scaled per row by a power of two (its
 //     largest element in [2^12, 2^13)) and held in registers.  K enters as K + 128, an
@@ -58,30 +61,36 @@ constexpr int kDepth = 5;                          // units of a warp's ring
 constexpr int kUnitBytes = kUnit * kHeadDim;       // of K, and of V
 constexpr int kUnitScales = kUnit * 2;             // bytes of K scales, and of V scales
 constexpr int kWarpBytes = kDepth * 2 * (kUnitBytes + kUnitScales);
-constexpr int kMergeRows = 8;                      // rows merged at a time
-constexpr int kSmem = kWarps * kWarpBytes + kWarps * kMergeRows * kHeadDim * 4;
+constexpr int kSmem = kWarps * kWarpBytes;
 constexpr int kMaxCtas = 320;                      // two per SM of 152, with room
-constexpr int kMinPages = 4;                       // pages of a run at least: one per warp
 constexpr float kLazy = 7.f;
 constexpr int kPBits = 7;                          // a row's largest |p v_scale| becomes 2^7 to 2^8 (2^15 at most) in P
 
-// Workspace: a record per CTA for the join, then two partial results per CTA (0: the
-// item its run begins inside, 1: the item its run ends inside).
-struct Rec {
-    int item, last;      // the item cut at this run's end and the last CTA that holds a part of it; item < 0: none
-    int seq, hk;
-};
+// A part of an item's result: rows relative to their running maximum m (log2).  The
+// 16-float pieces of odd rows are swapped in pairs (see col()).
 struct Part {
     float o[kRowsTile][kHeadDim];
     float m[kRowsTile], l[kRowsTile];
 };
+__device__ __forceinline__ int col(int r, int d) { return d ^ ((r & 1) << 4); }
+static_assert(sizeof(Part) <= kDepth * 2 * kUnitBytes, "a part fits a warp's ring");
 
+// Workspace, per CTA: a record for the join; the parts of items that end inside a
+// warp's run; and the CTA's own two parts (0: of the item its run begins inside, 1: of
+// the item its run ends inside).
+struct Rec {
+    int last;            // last CTA with a part of the item that this CTA begins and does not end; < 0: there is none
+    int seq, hk, pad;
+};
+struct CtaSpace {
+    Part warp[kWarps], cta[2];
+};
 struct Ws {
     Rec* rec;
-    Part* part;
+    CtaSpace* cta;
 };
 __host__ __device__ __forceinline__ Ws workspace_of(uint8_t* p) {
-    return Ws{reinterpret_cast<Rec*>(p), reinterpret_cast<Part*>(p + kMaxCtas * sizeof(Rec))};
+    return Ws{reinterpret_cast<Rec*>(p), reinterpret_cast<CtaSpace*>(p + kMaxCtas * sizeof(Rec))};
 }
 
 // ---------------------------------------------------------------- small device helpers
@@ -189,15 +198,13 @@ struct Walk {
 struct Ctx {
     uint8_t* ring;                        // this warp's units in shared memory, 2 * kUnitBytes each
     uint8_t* scales;                      // and their scales, 2 * kUnitScales each
-    float* merge;                         // [kWarps][kMergeRows][128], 16-float pieces swapped in odd rows
-    float* merge_m;                       // [kWarps][kMergeRows] running maxima, then sums
-    int begin, end, chunk;                // this CTA's pages
+    int begin, end;                       // this warp's pages
     int n_hk, tiles, group;
 };
 
 // ---------------------------------------------------------------- copies
-// A warp's copies, unit by unit over its pages of the run (every kWarps-th).  The
-// table entry of the page after the current one is already on its way.
+// A warp's copies, unit by unit over its pages.  The table entry of the page after the
+// current one is already on its way.
 struct Fetch {
     Walk w;                               // on the page looked up last
     int idx, at;                          // that page's place in the run; where w stands
@@ -228,7 +235,7 @@ struct Fetch {
             const int cell0 = (w.q.p0 + w.off) * kPage;
             lo = w.q.first - cell0;
             hi = w.q.n - cell0;
-            if (c.begin + idx < c.end) look(a, c, idx + kWarps);
+            if (c.begin + idx < c.end) look(a, c, idx + 1);
         }
         resident = ok ? resident | (1u << slot) : resident & ~(1u << slot);
         if (ok && kUnit * u < hi && kUnit * (u + 1) > lo) {   // units outside the sequence or window are not read
@@ -415,24 +422,30 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
     }
 }
 
-__device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows, int lane, Query& q) {
+struct RawQuery {
+    uint4 w[2][4];                        // rows g and g + 8: dims 64 (j / 2) + 16 t + 8 (j & 1) .. + 7
+};
+__device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows, int lane, RawQuery& raw) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
-        uint4 w[4];
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {     // dims 64 (j / 2) + 16 t + 8 (j & 1) .. + 7
-            w[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows)
-                w[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (row0 + r) * kHeadDim +
-                                                            64 * (j >> 1) + 16 * t + 8 * (j & 1)));
+        for (int j = 0; j < 4; ++j) {
+            raw.w[half][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (g + 8 * half < rows)
+                raw.w[half][j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                      (row0 + g + 8 * half) * kHeadDim + 64 * (j >> 1) +
+                                                                      16 * t + 8 * (j & 1)));
         }
+}
+__device__ __forceinline__ void convert_q(const RawQuery& raw, int type, Query& q) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[8];
-            unpack8(w[j], a.q_type, x);
+            unpack8(raw.w[half][j], type, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
         }
@@ -444,7 +457,7 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[8];
-            unpack8(w[j], a.q_type, x);
+            unpack8(raw.w[half][j], type, x);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {   // k step 4 (j / 2) + 2 (j & 1) + k: four dims
                 const int kk = 4 * (j >> 1) + 2 * (j & 1) + k;
@@ -463,31 +476,55 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
     }
 }
 
-// The run's pages, from place w on.
-__device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk w) {
+// Rows of an item: the first one's number in q and out, and how many.
+__device__ __forceinline__ size_t first_row(const PagedArgs& a, const Ctx& c, int seq, int hk, int& rows) {
+    const int h = hk / c.tiles, tile = hk - h * c.tiles;
+    rows = min(kRowsTile, c.group - kRowsTile * tile);
+    return (size_t)seq * a.n_heads + h * c.group + kRowsTile * tile;
+}
+
+// What a warp leaves for the CTA's merge.
+struct Left {
+    int first;           // its run begins inside an item (seq, hk): 1 = and that ends in the run (part in the
+    int seq, hk;         // workspace), 2 = and goes on behind it (part in the ring); 0: it begins with an item
+    int open;            // its run ends inside an item begun in it (part in the ring): that item and its pages' end
+    int oseq, ohk, oend;
+};
+
+// One warp's pages, from place w on.
+__device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk w, Left& left) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const Ws ws = workspace_of(a.workspace);
     const float kmul = a.sm_scale * kLog2e * 0x1p24f;   // scores come in units of 2^-24
+    left = Left{0, w.s, w.hk, 0, 0, 0, 0};
     Fetch f;
     f.w = w;
     f.at = f.v = 0;
     f.entry = -1;
     f.resident = 0;
     f.ok = false;
-    f.look(a, c, warp);
+    f.look(a, c, 0);
+    int rows;
+    size_t row0 = first_row(a, c, w.s, w.hk, rows);
+    RawQuery raw;
+    load_q(a, row0, rows, lane, raw);
 #pragma unroll 1
     for (int k = 0; k < kDepth; ++k) f.put(a, c, k);
-    int next = c.begin + warp;            // this warp's next page
-    int slot = 0;                         // where its next unit is
-    for (int pos = c.begin; pos < c.end; w.next_item(a, c.n_hk)) {
+    int slot = 0;                         // where the next unit is
+#pragma unroll 1
+    for (int pos = c.begin; pos < c.end;) {
         const int n = min(w.q.np - w.off, c.end - pos);
-        const int h = w.hk / c.tiles, tile = w.hk - h * c.tiles;
-        const int rows = min(kRowsTile, c.group - kRowsTile * tile);
-        const size_t row0 = (size_t)w.s * a.n_heads + h * c.group + kRowsTile * tile;
-        const bool complete = w.off == 0 && n == w.q.np;
-        const int seg_end = pos + n;
-        const bool mine = next < seg_end;
+        Query query;
+        convert_q(raw, a.q_type, query);
+        // the item after this one: its queries are on their way while this one is worked on
+        const Walk here = w;
+        const size_t here0 = row0;
+        const int here_rows = rows;
+        if (pos + n < c.end) {
+            w.next_item(a, c.n_hk);
+            row0 = first_row(a, c, w.s, w.hk, rows);
+            load_q(a, row0, rows, lane, raw);
+        }
         State s;
 #pragma unroll
         for (int d = 0; d < 16; ++d) s.o[d][0] = s.o[d][1] = s.o[d][2] = s.o[d][3] = 0.f;
@@ -495,136 +532,155 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         s.l0 = s.l1 = 0.f;
         s.top0 = s.top1 = 0.f;
         s.f0 = s.f1 = 0;
-        if (mine) {
-            Query query;
-            load_q(a, row0, rows, lane, query);
+        const int cell0 = (here.q.p0 + here.off) * kPage;
+        int lo = here.q.first - cell0, hi = here.q.n - cell0;   // the item's cells, from the step's first one
 #pragma unroll 1
-            for (; next < seg_end; next += kWarps) {
-                const int cell0 = (w.q.p0 + w.off + (next - pos)) * kPage;
-#pragma unroll 1
-                for (int half = 0; half < kPage; half += 2 * kUnit) {
-                    const int x = slot, y = slot + 1 == kDepth ? 0 : slot + 1;
-                    copies_wait<kDepth - 2>();   // one group a unit: all but the youngest three have landed
-                    __syncwarp();
-                    const int lo = w.q.first - cell0 - half, hi = w.q.n - cell0 - half;
-                    if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, query, kmul, c, x, y, lo, hi, lane);
-                    __syncwarp();         // every lane has read the units
-                    f.put(a, c, x);
-                    f.put(a, c, y);
-                    slot = y + 1 == kDepth ? 0 : y + 1;
+        for (int step = 0; step < n * (kPage / (2 * kUnit)); ++step) {
+            const int x = slot, y = slot + 1 == kDepth ? 0 : slot + 1;
+            copies_wait<kDepth - 2>();    // one group a unit: all but the youngest three have landed
+            __syncwarp();
+            if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, query, kmul, c, x, y, lo, hi, lane);
+            __syncwarp();                 // every lane has read the units
+            f.put(a, c, x);
+            f.put(a, c, y);
+            slot = y + 1 == kDepth ? 0 : y + 1;
+            lo -= 2 * kUnit;
+            hi -= 2 * kUnit;
+        }
+        pos += n;
+        // ---- the item's end, or the run's
+        s.l0 += __shfl_xor_sync(0xffffffffu, s.l0, 1);
+        s.l0 += __shfl_xor_sync(0xffffffffu, s.l0, 2);
+        s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 1);
+        s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 2);
+        const bool ends = here.off + n == here.q.np;
+        const bool complete = here.off == 0 && ends;
+        Part* part = nullptr;
+        if (!complete) {
+            if (ends) {
+                left.first = 1;
+                part = &workspace_of(a.workspace).cta[blockIdx.x].warp[warp];
+            } else {                      // the run is over: its ring is free
+                if (here.off > 0) left.first = 2;
+                else {
+                    left.open = 1;
+                    left.oseq = here.s;
+                    left.ohk = here.hk;
+                    left.oend = pos - n + here.q.np;
                 }
-            }
-            s.l0 += __shfl_xor_sync(0xffffffffu, s.l0, 1);
-            s.l0 += __shfl_xor_sync(0xffffffffu, s.l0, 2);
-            s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 1);
-            s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 2);
-            const float back0 = exp2i(-s.f0), back1 = exp2i(-s.f1);
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-                s.o[d][0] *= back0;
-                s.o[d][1] *= back0;
-                s.o[d][2] *= back1;
-                s.o[d][3] *= back1;
+                copies_wait<0>();
+                __syncwarp();
+                part = reinterpret_cast<Part*>(c.ring);
             }
         }
-        Part* part = ws.part + 2 * blockIdx.x + (w.off == 0 ? 1 : 0);
-        if (n == 1) {
-            // one page, one warp: straight from the registers
-            if (mine) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = g + 8 * half;
-                    if (r >= rows) continue;
-                    const float l = half ? s.l1 : s.l0, m = half ? s.m1 : s.m0;
-                    const float inv = complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        for (int half = 0; half < 2; ++half) {
+            const int r = g + 8 * half;
+            if (r >= here_rows) continue;
+            const float l = half ? s.l1 : s.l0, m = half ? s.m1 : s.m0;
+            const float back = exp2i(half ? -s.f1 : -s.f0) * (complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int d = 16 * q + 4 * t, e = 2 * q, v = 2 * half;
-                        const float x0 = s.o[e][v] * inv, x1 = s.o[e + 1][v] * inv, x2 = s.o[e][v + 1] * inv,
-                                    x3 = s.o[e + 1][v + 1] * inv;
-                        if (complete) store4(a.out, a.out_type, (row0 + r) * kHeadDim + d, x0, x1, x2, x3);
-                        else *reinterpret_cast<float4*>(&part->o[r][d]) = make_float4(x0, x1, x2, x3);
-                    }
-                    if (t == 0) {
-                        if (!complete) {
-                            part->m[r] = m;
-                            part->l[r] = l;
-                        } else if (a.lse) {
-                            a.lse[row0 + r] = lse_of(m, l);
-                        }
-                    }
-                }
+            for (int k = 0; k < 8; ++k) {
+                const int d = 16 * k + 4 * t, e = 2 * k, v = 2 * half;
+                const float x0 = s.o[e][v] * back, x1 = s.o[e + 1][v] * back, x2 = s.o[e][v + 1] * back,
+                            x3 = s.o[e + 1][v + 1] * back;
+                if (complete) store4(a.out, a.out_type, (here0 + r) * kHeadDim + d, x0, x1, x2, x3);
+                else *reinterpret_cast<float4*>(&part->o[r][col(r, d)]) = make_float4(x0, x1, x2, x3);
             }
-        } else {
-            // merge the warps that had pages, eight rows at a time; (pos - begin) % kWarps is the first of them
-            const int lead = (pos - c.begin) % kWarps;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half * kMergeRows >= rows) break;
-                __syncthreads();          // the last merge has been read
-                if (mine && g + 8 * half < rows) {
-                    float* dst = c.merge + (warp * kMergeRows + g) * kHeadDim;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int d = (16 * q + 4 * t) ^ ((g & 1) << 4), e = 2 * q, v = 2 * half;
-                        *reinterpret_cast<float4*>(dst + d) =
-                            make_float4(s.o[e][v], s.o[e + 1][v], s.o[e][v + 1], s.o[e + 1][v + 1]);
-                    }
-                    if (t == 0) {
-                        c.merge_m[warp * kMergeRows + g] = half ? s.m1 : s.m0;
-                        c.merge_m[(kWarps + warp) * kMergeRows + g] = half ? s.l1 : s.l0;
-                    }
-                }
-                __syncthreads();
-                for (int i = warp; i < kMergeRows && i + 8 * half < rows; i += kWarps) {
-                    const int r = i + 8 * half;
-                    float m[kWarps], l[kWarps], M = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < kWarps; ++k) {
-                        const bool had = ((k - lead + kWarps) % kWarps) < n;
-                        m[k] = had ? c.merge_m[k * kMergeRows + i] : -INFINITY;
-                        l[k] = had ? c.merge_m[(kWarps + k) * kMergeRows + i] : 0.f;
-                        M = fmaxf(M, m[k]);
-                    }
-                    float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kWarps; ++k) {
-                        if (((k - lead + kWarps) % kWarps) >= n) continue;
-                        const float wt = merge_weight(m[k], l[k], M);
-                        const float4 o = *reinterpret_cast<const float4*>(c.merge + (k * kMergeRows + i) * kHeadDim +
-                                                                          ((4 * lane) ^ ((i & 1) << 4)));
-                        L += wt * l[k];
-                        x0 += wt * o.x;
-                        x1 += wt * o.y;
-                        x2 += wt * o.z;
-                        x3 += wt * o.w;
-                    }
-                    if (complete) {
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
-                        store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
-                        if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
-                    } else {
-                        *reinterpret_cast<float4*>(&part->o[r][4 * lane]) = make_float4(x0, x1, x2, x3);
-                        if (lane == 0) {
-                            part->m[r] = M;
-                            part->l[r] = L;
-                        }
-                    }
+            if (t == 0) {
+                if (!complete) {
+                    part->m[r] = m;
+                    part->l[r] = l;
+                } else if (a.lse) {
+                    a.lse[here0 + r] = lse_of(m, l);
                 }
             }
         }
-        if (threadIdx.x == 0 && seg_end == c.end) {
-            // the run's last item: cut here, and begun here, if pages of it are left
-            Rec rec{-1, 0, w.s, w.hk};
-            if (w.off == 0 && n < w.q.np) {
-                rec.item = 0;
-                rec.last = (pos + w.q.np - 1) / c.chunk;
-            }
-            ws.rec[blockIdx.x] = rec;
-        }
-        pos = seg_end;
     }
     copies_wait<0>();                     // nothing in flight when a warp leaves
+}
+
+// Merges the parts that the CTA's warps have left, item by item, a row to a warp.  The
+// warps' runs follow one another, so an item's parts are those of consecutive warps.
+__device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, const Left* s_left, uint8_t* rings, int chunk) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Ws ws = workspace_of(a.workspace);
+    Rec rec{-1, 0, 0, 0};
+    for (int w0 = 0, skip_first = 0; w0 < kWarps;) {
+        // a chain of parts: from warp w0's first part, or from its open one
+        const Left& x = s_left[w0];
+        const bool from_before = !skip_first && x.first != 0;   // only in warp 0: elsewhere the chain before took it
+        const bool open = x.open != 0;
+        if (!from_before && !open) {
+            ++w0;
+            skip_first = 0;
+            continue;
+        }
+        const int seq = from_before ? x.seq : x.oseq, hk = from_before ? x.hk : x.ohk, end = x.oend;
+        const Part* part[kWarps];
+        int n = 0, w1 = w0;
+        bool closed = false;
+        part[n++] = from_before && x.first == 1 ? &ws.cta[blockIdx.x].warp[w0]
+                                                : reinterpret_cast<const Part*>(rings + w0 * kDepth * 2 * kUnitBytes);
+        if (from_before && x.first == 1) closed = true;
+        while (!closed && w1 + 1 < kWarps && s_left[w1 + 1].first != 0) {
+            ++w1;
+            closed = s_left[w1].first == 1;
+#pragma unroll
+            for (int k = 1; k < kWarps; ++k)
+                if (k == n)
+                    part[k] = closed ? &ws.cta[blockIdx.x].warp[w1]
+                                     : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kUnitBytes);
+            ++n;
+        }
+        const bool complete = closed && !from_before;
+        int rows;
+        const size_t row0 = first_row(a, c, seq, hk, rows);
+        Part* to = &ws.cta[blockIdx.x].cta[from_before ? 0 : 1];
+        if (!complete && !from_before) rec = Rec{(end - 1) / chunk, seq, hk, 0};
+        for (int r = warp; r < rows; r += kWarps) {
+            float m[kWarps], l[kWarps], M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                m[k] = k < n ? part[k]->m[r] : -INFINITY;
+                l[k] = k < n ? part[k]->l[r] : 0.f;
+                M = fmaxf(M, m[k]);
+            }
+            float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                if (k >= n) continue;
+                const float wt = merge_weight(m[k], l[k], M);
+                const float4 o = *reinterpret_cast<const float4*>(&part[k]->o[r][col(r, 4 * lane)]);
+                L += wt * l[k];
+                x0 += wt * o.x;
+                x1 += wt * o.y;
+                x2 += wt * o.z;
+                x3 += wt * o.w;
+            }
+            if (complete) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
+                if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
+            } else {
+                *reinterpret_cast<float4*>(&to->o[r][col(r, 4 * lane)]) = make_float4(x0, x1, x2, x3);
+                if (lane == 0) {
+                    to->m[r] = M;
+                    to->l[r] = L;
+                }
+            }
+        }
+        // go on behind the chain: with the open part of the warp that it ended in, if that is another item's
+        skip_first = 1;
+        if (w1 == w0 && !from_before) {
+            ++w0;
+            skip_first = 0;
+        } else {
+            w0 = w1;
+            if (!closed) break;           // the chain reaches the run's end
+        }
+    }
+    if (threadIdx.x == 0) ws.rec[blockIdx.x] = rec;
 }
 
 // Sum over the block of each thread's count and the sum before this thread.
@@ -650,50 +706,55 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& before) {
 
 __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ float s_ml[2 * kWarps * kMergeRows];
-    __shared__ int s_warp[kWarps], s_start[2];
-    const int tid = threadIdx.x;
+    __shared__ int s_warp[kWarps], s_start[kWarps][2];
+    __shared__ Left s_left[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up now; it waits for this grid's end
 
     Ctx c;
-    c.ring = smem_raw + (tid >> 5) * kDepth * 2 * kUnitBytes;
-    c.scales = smem_raw + kWarps * kDepth * 2 * kUnitBytes + (tid >> 5) * kDepth * 2 * kUnitScales;
-    c.merge = reinterpret_cast<float*>(smem_raw + kWarps * kWarpBytes);
-    c.merge_m = s_ml;
+    c.ring = smem_raw + warp * kDepth * 2 * kUnitBytes;
+    c.scales = smem_raw + kWarps * kDepth * 2 * kUnitBytes + warp * kDepth * 2 * kUnitScales;
     c.group = a.n_heads / a.n_kv;
     c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
     c.n_hk = a.n_kv * c.tiles;
 
-    // ---- this CTA's run of the pages of all items
+    // ---- the warps' runs of the pages of all items
     const int per = (a.n_seq + kThreads - 1) / kThreads;   // consecutive sequences per thread
     const int s_lo = min(tid * per, a.n_seq), s_hi = min(s_lo + per, a.n_seq);
     int sum = 0, before;
     for (int s = s_lo; s < s_hi; ++s) sum += seq_of(a, s, blockIdx.x == 0).np;
     const int total = block_scan(sum, s_warp, before) * c.n_hk;   // at most 2^30, checked on the host
-    c.chunk = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kMinPages);
-    c.begin = (int)min((long long)blockIdx.x * c.chunk, (long long)total);
-    c.end = (int)min((long long)c.begin + c.chunk, (long long)total);
-    if (c.begin < c.end && c.begin >= before * c.n_hk && c.begin < (before + sum) * c.n_hk) {
-        int at = before, s = s_lo;                         // the one thread whose sequences hold the first page
+    const int runs = (int)gridDim.x * kWarps;
+    const int pages = max((total + runs - 1) / runs, 1), chunk = kWarps * pages;   // of a warp, of a CTA
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        // the one thread whose sequences hold warp k's first page
+        const long long first = (long long)blockIdx.x * chunk + k * pages;
+        if (first < (long long)before * c.n_hk || first >= (long long)(before + sum) * c.n_hk) continue;
+        int at = before, s = s_lo;
         for (;; ++s) {
             const int np = seq_of(a, s, false).np;
-            if (c.begin < (at + np) * c.n_hk) break;
+            if (first < (long long)(at + np) * c.n_hk) break;
             at += np;
         }
-        s_start[0] = s;
-        s_start[1] = c.begin - at * c.n_hk;
+        s_start[k][0] = s;
+        s_start[k][1] = (int)first - at * c.n_hk;
     }
-    if (tid == 0 && c.begin >= c.end) workspace_of(a.workspace).rec[blockIdx.x] = Rec{-1, 0, 0, 0};
+    c.begin = (int)min((long long)blockIdx.x * chunk + warp * pages, (long long)total);
+    c.end = min(c.begin + pages, total);
     __syncthreads();
-    Walk w;
-    w.s = w.hk = w.off = 0;
-    w.q = Seq{0, 0, 0, 1};
+    Left left{0, 0, 0, 0, 0, 0, 0};
     if (c.begin < c.end) {
-        w.s = s_start[0];
+        Walk w;
+        w.s = s_start[warp][0];
         w.q = seq_of(a, w.s, false);
-        w.hk = s_start[1] / w.q.np;
-        w.off = s_start[1] - w.hk * w.q.np;
+        w.hk = s_start[warp][1] / w.q.np;
+        w.off = s_start[warp][1] - w.hk * w.q.np;
+        walk_run(a, c, w, left);
     }
-    if (c.begin < c.end) walk_run(a, c, w);
+    if ((tid & 31) == 0) s_left[warp] = left;
+    __syncthreads();
+    merge_cta(a, c, s_left, smem_raw, chunk);
     // rows of the sequences that have no page at all
     for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
         if (seq_of(a, s, false).np > 0) continue;
@@ -705,54 +766,89 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
 }
 
-// Joins the parts of the item that run blockIdx.x begins and others end: row
-// blockIdx.y of it.  Warps take parts in turn, a lane four dims.
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a) {
+// Joins the parts of items that are cut between CTAs.  SPLIT (few items, many parts
+// each): block (k, r) takes row r of the k-th item that is cut, its warps sharing the
+// parts.  Otherwise (many items, a few parts each): block (k, r) takes the item that CTA
+// k begins and does not end, rows 4 r .. 4 r + 3, one to a warp.
+constexpr int kJoinThreads = 128;
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
     __shared__ float s_o[4][kHeadDim], s_l[4];
+    __shared__ int s_cta, s_count[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Ws ws = workspace_of(a.workspace);
-    const int c0 = blockIdx.x, r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int c0 = blockIdx.x;
+    if (SPLIT) {
+        // the CTA of the k-th record
+        if (threadIdx.x == 0) s_cta = -1;
+        constexpr int kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+        unsigned vote[kPer];
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {  // warp w looks at CTAs 32 (kPer w + j) + lane
+            const int i = 32 * (kPer * warp + j) + lane;
+            vote[j] = __ballot_sync(0xffffffffu, i < ctas && ws.rec[min(i, ctas - 1)].last >= 0);
+            mine += __popc(vote[j]);
+        }
+        if (lane == 0) s_count[warp] = mine;
+        __syncthreads();
+        int rank = 0;
+        for (int w = 0; w < warp; ++w) rank += s_count[w];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (((vote[j] >> lane) & 1u) && rank + __popc(vote[j] & ((1u << lane) - 1u)) == (int)blockIdx.x)
+                s_cta = 32 * (kPer * warp + j) + lane;
+            rank += __popc(vote[j]);
+        }
+        __syncthreads();
+        c0 = s_cta;
+        if (c0 < 0) return;
+    }
     const Rec rec = ws.rec[c0];
-    if (rec.item < 0 || rec.last >= (int)gridDim.x) return;
+    if (rec.last < 0 || rec.last >= ctas) return;
     const int group = a.n_heads / a.n_kv, tiles = (group + kRowsTile - 1) / kRowsTile;
     const int h = rec.hk / tiles, tile = rec.hk - h * tiles;
+    const int r = SPLIT ? blockIdx.y : 4 * blockIdx.y + warp;
     if (r >= min(kRowsTile, group - kRowsTile * tile)) return;
-    const int n = rec.last - c0 + 1;      // part 0 is run c0's last item, part i the first of run c0 + i
-    const Part* part = ws.part + 2 * c0;
-    auto at = [&](int i) { return part + (i == 0 ? 1 : 2 * i); };
+    const int n = rec.last - c0 + 1;      // part 0 is CTA c0's second, part i the first of CTA c0 + i
+    auto at = [&](int i) { return &ws.cta[c0 + i].cta[i == 0 ? 1 : 0]; };
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, at(i)->m[r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += 4) {
+    float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int i = SPLIT ? warp : 0; i < n; i += SPLIT ? 4 : 1) {
         const Part* p = at(i);
         const float l = p->l[r], wt = merge_weight(p->m[r], l, M);
-        const float4 o = *reinterpret_cast<const float4*>(&p->o[r][4 * lane]);
+        const float4 o = *reinterpret_cast<const float4*>(&p->o[r][col(r, 4 * lane)]);
         L += wt * l;
-        x0 += wt * o.x;
-        x1 += wt * o.y;
-        x2 += wt * o.z;
-        x3 += wt * o.w;
+        x[0] += wt * o.x;
+        x[1] += wt * o.y;
+        x[2] += wt * o.z;
+        x[3] += wt * o.w;
     }
-    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = make_float4(x0, x1, x2, x3);
-    if (lane == 0) s_l[warp] = L;
-    __syncthreads();
-    if (warp != 0) return;
-    L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    float x[4];
+    if (SPLIT) {
+        *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
+        if (lane == 0) s_l[warp] = L;
+        __syncthreads();
+        if (warp != 0) return;
+        L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        x[e] = (s_o[0][4 * lane + e] + s_o[1][4 * lane + e] + s_o[2][4 * lane + e] + s_o[3][4 * lane + e]) * inv;
+        for (int e = 0; e < 4; ++e)
+            x[e] = s_o[0][4 * lane + e] + s_o[1][4 * lane + e] + s_o[2][4 * lane + e] + s_o[3][4 * lane + e];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const size_t row = (size_t)rec.seq * a.n_heads + h * group + kRowsTile * tile + r;
-    store4(a.out, a.out_type, row * kHeadDim + 4 * lane, x[0], x[1], x[2], x[3]);
+    store4(a.out, a.out_type, row * kHeadDim + 4 * lane, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
     if (lane == 0 && a.lse) a.lse[row] = lse_of(M, L);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int, int) { return kMaxCtas * (sizeof(Rec) + 2 * sizeof(Part)); }
+size_t paged_attn_workspace(int, int) { return kMaxCtas * (sizeof(Rec) + sizeof(CtaSpace)); }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
@@ -766,8 +862,20 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     paged_attn_kernel<<<grid, kThreads, kSmem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    paged_join_kernel<<<dim3((unsigned)grid, (unsigned)rows), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    // at most one cut item per CTA and per item; up to 64 items a block finds its own among the records
+    const long long items = (long long)a.n_seq * a.n_kv * ((a.n_heads / a.n_kv + kRowsTile - 1) / kRowsTile);
+    const bool split = items <= 64;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = split ? dim3((unsigned)items, (unsigned)rows) : dim3((unsigned)grid, (unsigned)(rows + 3) / 4);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return split ? cudaLaunchKernelEx(&cfg, paged_join_kernel<true>, a, grid)
+                 : cudaLaunchKernelEx(&cfg, paged_join_kernel<false>, a, grid);
 }
 
 }  // namespace qsa
