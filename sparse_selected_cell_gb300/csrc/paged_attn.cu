@@ -20,13 +20,13 @@
 // paged_join_kernel, launched beside this kernel and waiting for it on the device,
 // joins them in the order of the CTAs.
 //
-// A warp has a ring of five 16-cell units (2 KB of K, 2 KB of V, two 32-byte rows of
+// A warp has a ring of three 32-cell steps (4 KB of K, 4 KB of V, two 64-byte rows of
 // scales), filled by 16-byte asynchronous copies, 512 consecutive bytes an instruction,
 // 16-byte pieces XOR-swizzled by (row & 7) as they land (a bulk copy would leave every
-// row on the same banks, eightfold conflicts for V).  It computes on two units while
-// three are in flight and refills what it has used: 100 to 166 KB per SM are on the way
-// at any time.  A page's table entry is looked up a page ahead, an item's queries an
-// item ahead.
+// row on the same banks, eightfold conflicts for V).  It computes on one step while two
+// are in flight and refills it when it is used: 133 to 200 KB per SM are on the way at
+// any time.  A page's table entry is looked up a page ahead, an item's queries an item
+// ahead.
 //
 // The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an
 // eighth of a tcgen05.mma's 128 rows, whose operands would also have to be written back
@@ -41,12 +41,14 @@
 //     score tile is cell perm(g) = g / 2 + 4 (g & 1) of its eight: the 16-byte reads of
 //     eight lanes then fall in eight different bank groups of the swizzled rows.
 //   * The K scale, sm_scale and log2 e multiply the score column in FP32, the row's
-//     power of two enters with the exponent's multiply-add.
-//   * P = p * v_scale * 2^f in FP16, f per row such that the row's largest |p *
-//     v_scale| so far is 2^7 to 2^15: P keeps FP16's 11 bits however scores and V
-//     scales lie, and what is below 2^-32 of the largest vanishes (2^20 such cells
-//     weigh 2^-12).  The running maximum moves only when a score passes it by 7 in
-//     log2; O follows it and f.  V goes from the INT8 page to the B operands by
+//     power of two enters with the exponent's multiply-add: p = 2^(score - R).
+//   * The row's reference R is not the running maximum of the scores but that of
+//     score + log2 |v_scale|, less 7 to 15: the product p * v_scale, which enters O += P V
+//     in FP16, then is at most 2^15 and its largest so far at least 2^7, so P keeps
+//     FP16's 11 bits however scores and V scales lie, and what is below 2^-32 of the
+//     largest vanishes (2^20 such cells weigh 2^-12).  R moves, and O and the row sum
+//     with it, only when a product would pass 2^15 (or the sum 2^60, with V scales of
+//     zero): one vote a step.  V goes from the INT8 rows to the B operands by
 //     ldmatrix.trans on byte pairs.
 #include "serve.cuh"
 
@@ -56,24 +58,24 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;                      // rows of a tile (query heads of one KV head)
-constexpr int kUnit = 16;                          // cells of a unit; a step of the softmax is two
-constexpr int kDepth = 5;                          // units of a warp's ring
-constexpr int kUnitBytes = kUnit * kHeadDim;       // of K, and of V
-constexpr int kUnitScales = kUnit * 2;             // bytes of K scales, and of V scales
-constexpr int kWarpBytes = kDepth * 2 * (kUnitBytes + kUnitScales);
+constexpr int kStep = 32;                          // cells of a step
+constexpr int kDepth = 3;                          // steps of a warp's ring
+constexpr int kStepBytes = kStep * kHeadDim;       // of K, and of V
+constexpr int kStepScales = kStep * 2;             // bytes of K scales, and of V scales
+constexpr int kWarpBytes = kDepth * 2 * (kStepBytes + kStepScales);
 constexpr int kSmem = kWarps * kWarpBytes;
 constexpr int kMaxCtas = 320;                      // two per SM of 152, with room
-constexpr float kLazy = 7.f;
-constexpr int kPBits = 7;                          // a row's largest |p v_scale| becomes 2^7 to 2^8 (2^15 at most) in P
+constexpr int kPBits = 7;                          // a row's largest |p v_scale| is set to 2^7 .. 2^8 when R moves
+constexpr float kPTop = 32768.f, kSumTop = 0x1p60f;
 
-// A part of an item's result: rows relative to their running maximum m (log2).  The
+// A part of an item's result: rows relative to their reference m (log2).  The
 // 16-float pieces of odd rows are swapped in pairs (see col()).
 struct Part {
     float o[kRowsTile][kHeadDim];
     float m[kRowsTile], l[kRowsTile];
 };
 __device__ __forceinline__ int col(int r, int d) { return d ^ ((r & 1) << 4); }
-static_assert(sizeof(Part) <= kDepth * 2 * kUnitBytes, "a part fits a warp's ring");
+static_assert(sizeof(Part) <= kDepth * 2 * kStepBytes, "a part fits a warp's ring");
 
 // Workspace, per CTA: a record for the join; the parts of items that end inside a
 // warp's run; and the CTA's own two parts (0: of the item its run begins inside, 1: of
@@ -97,9 +99,6 @@ __host__ __device__ __forceinline__ Ws workspace_of(uint8_t* p) {
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ float half_at(const uint8_t* p) {
-    return __half2float(*reinterpret_cast<const __half*>(p));
 }
 // Largest over the four lanes that share rows g and g + 8.
 __device__ __forceinline__ float quad_max(float v) {
@@ -142,8 +141,7 @@ __device__ __forceinline__ void store4(void* out, int type, size_t at, float a, 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
-// Weight of a partial state with running maximum m (log2) and sum l in a merge around
-// M.  m = -inf: nothing was summed (l = 0), or only NaN (l = NaN, which must show).
+// Weight of a partial state with reference m (log2) and sum l in a merge around M.  m = -inf: nothing was summed (l = 0), or only NaN (l = NaN, which must show).
 __device__ __forceinline__ float merge_weight(float m, float l, float M) {
     return m == -INFINITY ? l : fast_exp2(m - M);
 }
@@ -196,24 +194,27 @@ struct Walk {
 };
 
 struct Ctx {
-    uint8_t* ring;                        // this warp's units in shared memory, 2 * kUnitBytes each
-    uint8_t* scales;                      // and their scales, 2 * kUnitScales each
+    uint8_t* ring;                        // this warp's steps in shared memory, 2 * kStepBytes each
+    uint8_t* scales;                      // and their scales, 2 * kStepScales each
+    float* cols;                          // this warp's [2][32]: the step's K and V scales as the lanes need them
     int begin, end;                       // this warp's pages
     int n_hk, tiles, group;
 };
 
 // ---------------------------------------------------------------- copies
-// A warp's copies, unit by unit over its pages.  The table entry of the page after the
+// A warp's copies, step by step over its pages.  The table entry of the page after the
 // current one is already on its way.
 struct Fetch {
     Walk w;                               // on the page looked up last
     int idx, at;                          // that page's place in the run; where w stands
     int entry;
-    int v;                                // units so far
-    uint32_t resident;                    // per slot: its unit's page is there
-    long long block;                      // the current page: pool block, whether it is there, its cells' limits
-    bool ok;
-    int lo, hi;
+    bool second;                          // the next step is its page's second one
+    uint32_t resident;                    // per slot: its step's page is there
+    bool ok;                              // the current page is there
+    int lo, hi;                           // its cells' limits, from the next step's first one
+    const int8_t* ksrc;                   // the next step, for this lane
+    const int8_t* vsrc;
+    const uint16_t* ssrc;
 
     __device__ __forceinline__ void look(const PagedArgs& a, const Ctx& c, int page) {
         idx = page;
@@ -222,51 +223,63 @@ struct Fetch {
         at = idx;
         entry = __ldg(a.page_tables + (size_t)w.s * a.pt_stride + w.q.p0 + w.off);
     }
-    // The next unit into slot `slot` of the ring; one group, empty behind the run's end.
+    // The next step into slot `slot` of the ring; one group, empty behind the run's end.
     __device__ __forceinline__ void put(const PagedArgs& a, const Ctx& c, int slot) {
-        const int lane = threadIdx.x & 31, u = v & 3;
-        if (u == 0) {                     // a new page
+        const int lane = threadIdx.x & 31;
+        if (!second) {                    // a new page
             ok = c.begin + idx < c.end && entry >= 0;
             if (ok && entry >= a.n_ppages) {
                 if (lane == 0) report(a.dev_status, QSA_DEV_BAD_PAGE);
                 ok = false;
             }
-            block = (long long)entry * a.n_kv + w.hk / c.tiles;
+            if (ok) {
+                const long long row = ((long long)entry * a.n_kv + w.hk / c.tiles) * kPage;
+                ksrc = a.k_pool + row * kHeadDim + 16 * lane;
+                vsrc = a.v_pool + row * kHeadDim + 16 * lane;
+                ssrc = (lane < 4 ? a.k_scale : a.v_scale) + row + 8 * (lane & 3);
+            }
             const int cell0 = (w.q.p0 + w.off) * kPage;
             lo = w.q.first - cell0;
             hi = w.q.n - cell0;
             if (c.begin + idx < c.end) look(a, c, idx + 1);
         }
+        second = !second;
         resident = ok ? resident | (1u << slot) : resident & ~(1u << slot);
-        if (ok && kUnit * u < hi && kUnit * (u + 1) > lo) {   // units outside the sequence or window are not read
+        if (ok && hi > 0 && lo < kStep) {
             // lane l copies piece l & 7 of rows l / 8 + 4 j; for odd j, (row & 7) flips bit 2 of the piece
-            const uint32_t dst = smem_u32(c.ring) + slot * 2 * kUnitBytes + (uint32_t)(lane >> 3) * kHeadDim +
+            const uint32_t dst = smem_u32(c.ring) + slot * 2 * kStepBytes + (uint32_t)(lane >> 3) * kHeadDim +
                                  (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
-            const long long row = block * kPage + kUnit * u;
-            const int8_t* ksrc = a.k_pool + row * kHeadDim + 16 * lane;
-            const int8_t* vsrc = a.v_pool + row * kHeadDim + 16 * lane;
+            const uint32_t sdst = smem_u32(c.scales) + slot * 2 * kStepScales + 16 * lane;
+            if (hi >= kStep) {
 #pragma unroll
-            for (int j = 0; j < kUnitBytes / 512; ++j) copy16((dst ^ ((j & 1) << 6)) + 512 * j, ksrc + 512 * j);
-            if (lane < 4)                 // 32 bytes of K scales, 32 of V scales
-                copy16(smem_u32(c.scales) + slot * 2 * kUnitScales + 16 * lane,
-                       (lane < 2 ? a.k_scale : a.v_scale) + row + 8 * (lane & 1));
+                for (int j = 0; j < kStep / 4; ++j) copy16((dst ^ ((j & 1) << 6)) + 512 * j, ksrc + 512 * j);
+                if (lane < 8) copy16(sdst, ssrc);   // 64 bytes of K scales, 64 of V scales
 #pragma unroll
-            for (int j = 0; j < kUnitBytes / 512; ++j)
-                copy16((dst ^ ((j & 1) << 6)) + kUnitBytes + 512 * j, vsrc + 512 * j);
+                for (int j = 0; j < kStep / 4; ++j) copy16((dst ^ ((j & 1) << 6)) + kStepBytes + 512 * j, vsrc + 512 * j);
+            } else {                      // the sequence's end: its rows only, four at a time
+                if (lane < 8) copy16(sdst, ssrc);
+                for (int j = 0; 4 * j < hi; ++j) {
+                    copy16((dst ^ ((j & 1) << 6)) + 512 * j, ksrc + 512 * j);
+                    copy16((dst ^ ((j & 1) << 6)) + kStepBytes + 512 * j, vsrc + 512 * j);
+                }
+            }
         }
         copies_commit();
-        ++v;
+        ksrc += kStepBytes;
+        vsrc += kStepBytes;
+        ssrc += kStep;
+        lo -= kStep;
+        hi -= kStep;
     }
 };
 
-// ---------------------------------------------------------------- two units
+// ---------------------------------------------------------------- a step
 // Running state of one warp over the pages of one item: rows g and g + 8 of lane
 // (g, t) = (lane / 4, lane % 4).
 struct State {
     float o[16][4];
-    float m0, m1, l0, l1;                 // maxima in log2; l per lane, over the lane's own columns
-    float top0, top1;                     // largest |p v_scale| when f was last set
-    int f0, f1;                           // P and O carry 2^f
+    float r0, r1;                         // references R (log2); -inf: nothing yet
+    float l0, l1;                         // row sums, per lane, over the lane's own columns
 };
 
 // A tile's query rows g and g + 8 as FP16 A operands: each row times a power of two 2^-e
@@ -279,13 +292,48 @@ struct Query {
     float bias0, bias1;                   // -128 * (sum of the row) * 2^-24
 };
 
-// The 32 cells of units in slots x and y; cells lo .. hi - 1 of them count (hi > lo).
-__device__ __forceinline__ void step32(State& s, const Query& q, float kmul, const Ctx& c, int x, int y, int lo, int hi,
-                                       int lane) {
+// p = 2^(score - R) of the lane's columns, with their sums, and p * v_scale in place.
+__device__ __forceinline__ void weigh(const float (&sc)[4][4], float (&pv)[4][4], const float (&vs)[8], float rs0, float rs1,
+                                      float r0, float r1, float& sum0, float& sum1, float& top0, float& top1) {
+    sum0 = sum1 = top0 = top1 = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        const float e0 = fast_exp2(fmaf(sc[nt][0], rs0, -r0)), e1 = fast_exp2(fmaf(sc[nt][1], rs0, -r0));
+        const float e2 = fast_exp2(fmaf(sc[nt][2], rs1, -r1)), e3 = fast_exp2(fmaf(sc[nt][3], rs1, -r1));
+        sum0 += e0 + e1;
+        sum1 += e2 + e3;
+        pv[nt][0] = e0 * vs[2 * nt];
+        pv[nt][1] = e1 * vs[2 * nt + 1];
+        pv[nt][2] = e2 * vs[2 * nt];
+        pv[nt][3] = e3 * vs[2 * nt + 1];
+        top0 = fmax3(top0, fabsf(pv[nt][0]), fabsf(pv[nt][1]));
+        top1 = fmax3(top1, fabsf(pv[nt][2]), fabsf(pv[nt][3]));
+    }
+}
+
+// A new reference for a row: the largest score mx of the step (log2), and the largest
+// |2^(score - mx) * v_scale|, both over the row.
+__device__ __forceinline__ float new_reference(float r, float mx, float top) {
+    const int e = top > 0.f ? max(f32_exponent(top), -33) : 0;
+    return fmaxf(r, mx + (float)(e - kPBits));
+}
+
+// The 32 cells of slot x; cells lo .. hi - 1 of them count (hi > 0, lo < 32).
+__device__ __forceinline__ void step32(State& s, const Query& q, float kmul, const Ctx& c, int x, int lo, int hi, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int pg = (g >> 1) | ((g & 1) << 2);            // cell (of eight) of this lane's K column
-    const uint8_t* unit[2] = {c.ring + x * 2 * kUnitBytes, c.ring + y * 2 * kUnitBytes};
-    const uint8_t* scale[2] = {c.scales + x * 2 * kUnitScales, c.scales + y * 2 * kUnitScales};
+    const uint8_t* kst = c.ring + x * 2 * kStepBytes;
+    const bool whole = lo <= 0 && hi >= kStep;           // warp-uniform
+    // ---- the columns' scales, each converted once: lane (g, t) will need cells 8 nt + t + 4 e, in that order
+    {
+        const __half* sp = reinterpret_cast<const __half*>(c.scales + x * 2 * kStepScales) + lane;
+        const int at = 8 * (lane & 3) + 2 * (lane >> 3) + ((lane >> 2) & 1);
+        float ks = __half2float(sp[0]) * kmul, vs = __half2float(sp[kStep]);
+        if (!whole && (lane < lo || lane >= hi)) ks = vs = 0.f;   // they may be anything
+        c.cols[at] = ks;
+        c.cols[kStep + at] = vs;
+        __syncwarp();
+    }
     // ---- S = Q K^T: Q (K + 128) from the accumulators' start at -128 sum(Q), in units of 2^-24
     float sc[4][4];
 #pragma unroll
@@ -298,7 +346,7 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
         uint4 w[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
-            w[nt] = *reinterpret_cast<const uint4*>(unit[nt >> 1] + (8 * (nt & 1) + pg) * kHeadDim + (((4 * hk + t) ^ pg) << 4));
+            w[nt] = *reinterpret_cast<const uint4*>(kst + (8 * nt + pg) * kHeadDim + (((4 * hk + t) ^ pg) << 4));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -309,78 +357,46 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
                 mma_f16(sc[nt], a[0], a[1], a[2], a[3], b0, b1);
             }
     }
-    // ---- scales of the lane's columns: cells 8 nt + t and 8 nt + t + 4 of columns 2t, 2t + 1
-    const bool whole = lo <= 0 && hi >= 2 * kUnit;       // warp-uniform
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+    float vs[8];
+    {
+        const float4* cp = reinterpret_cast<const float4*>(c.cols + 8 * t);
+        const float4 k0 = cp[0], k1 = cp[1], v0 = cp[kStep / 4], v1 = cp[kStep / 4 + 1];
+        const float ks[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        vs[0] = v0.x, vs[1] = v0.y, vs[2] = v0.z, vs[3] = v0.w, vs[4] = v1.x, vs[5] = v1.y, vs[6] = v1.z, vs[7] = v1.w;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        float ks[2];
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ks[e] = half_at(scale[nt >> 1] + 2 * (8 * (nt & 1) + t + 4 * e)) * kmul;
+            for (int e = 0; e < 4; ++e) sc[nt][e] *= ks[2 * nt + (e & 1)];
+    }
+    if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] *= ks[e & 1];
-        if (!whole) {
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int cell = 8 * nt + t + 4 * e;
                 if (cell < lo || cell >= hi) sc[nt][e] = sc[nt][e + 2] = -INFINITY;
             }
-        }
-        mx0 = fmax3(mx0, sc[nt][0], sc[nt][1]);
-        mx1 = fmax3(mx1, sc[nt][2], sc[nt][3]);
     }
-    // ---- running maxima (lazily moved)
-    mx0 *= q.rs0;
-    mx1 *= q.rs1;
-    float al0 = 1.f, al1 = 1.f;
-    const bool moved = __any_sync(0xffffffffu, mx0 > s.m0 + kLazy || mx1 > s.m1 + kLazy);
-    if (moved) {
-        mx0 = quad_max(mx0);
-        mx1 = quad_max(mx1);
-        if (mx0 > s.m0 + kLazy) {                        // from -inf: O and l are zero, the factor does not matter
-            al0 = s.m0 == -INFINITY ? 1.f : fast_exp2(s.m0 - mx0);
-            s.m0 = mx0;
-        }
-        if (mx1 > s.m1 + kLazy) {
-            al1 = s.m1 == -INFINITY ? 1.f : fast_exp2(s.m1 - mx1);
-            s.m1 = mx1;
-        }
-    }
-    // ---- p, the row sums, and p * v_scale in place of the scores
-    const float mu0 = s.m0 == -INFINITY ? 0.f : s.m0, mu1 = s.m1 == -INFINITY ? 0.f : s.m1;
-    float ps0 = 0.f, ps1 = 0.f, pm0 = 0.f, pm1 = 0.f;
+    // ---- weights; the reference moves when a product or a sum passes its limit
+    float pv[4][4], sum0, sum1, top0, top1;
+    weigh(sc, pv, vs, q.rs0, q.rs1, s.r0, s.r1, sum0, sum1, top0, top1);
+    if (__any_sync(0xffffffffu, top0 > kPTop || top1 > kPTop || sum0 > kSumTop || sum1 > kSumTop || s.r0 == -INFINITY ||
+                                    s.r1 == -INFINITY)) {
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-        float vs[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int cell = 8 * nt + t + 4 * e;
-            vs[e] = half_at(scale[nt >> 1] + kUnitScales + 2 * (8 * (nt & 1) + t + 4 * e));
-            if (!whole && (cell < lo || cell >= hi)) vs[e] = 0.f;   // its scale may be anything
+        for (int nt = 0; nt < 4; ++nt) {
+            mx0 = fmax3(mx0, sc[nt][0], sc[nt][1]);
+            mx1 = fmax3(mx1, sc[nt][2], sc[nt][3]);
         }
-        const float e0 = fast_exp2(fmaf(sc[nt][0], q.rs0, -mu0)), e1 = fast_exp2(fmaf(sc[nt][1], q.rs0, -mu0));
-        const float e2 = fast_exp2(fmaf(sc[nt][2], q.rs1, -mu1)), e3 = fast_exp2(fmaf(sc[nt][3], q.rs1, -mu1));
-        ps0 += e0 + e1;
-        ps1 += e2 + e3;
-        sc[nt][0] = e0 * vs[0];
-        sc[nt][1] = e1 * vs[1];
-        sc[nt][2] = e2 * vs[0];
-        sc[nt][3] = e3 * vs[1];
-        pm0 = fmax3(pm0, fabsf(sc[nt][0]), fabsf(sc[nt][1]));
-        pm1 = fmax3(pm1, fabsf(sc[nt][2]), fabsf(sc[nt][3]));
-    }
-    s.l0 = s.l0 * al0 + ps0;
-    s.l1 = s.l1 * al1 + ps1;
-    // ---- the rows' powers of two for P: moved when P would pass 2^15, or when the maximum moved
-    if (__any_sync(0xffffffffu, moved || pm0 * exp2i(s.f0) > 32768.f || pm1 * exp2i(s.f1) > 32768.f)) {
-        s.top0 = fmaxf(s.top0 * al0, quad_max(pm0));
-        s.top1 = fmaxf(s.top1 * al1, quad_max(pm1));
-        const int n0 = s.top0 > 0.f ? kPBits - min(max(f32_exponent(s.top0), -100), 24) : s.f0;
-        const int n1 = s.top1 > 0.f ? kPBits - min(max(f32_exponent(s.top1), -100), 24) : s.f1;
-        al0 *= exp2i(n0 - s.f0);
-        al1 *= exp2i(n1 - s.f1);
-        s.f0 = n0;
-        s.f1 = n1;
+        mx0 = quad_max(mx0 * q.rs0);
+        mx1 = quad_max(mx1 * q.rs1);
+        weigh(sc, pv, vs, q.rs0, q.rs1, mx0, mx1, sum0, sum1, top0, top1);
+        const float n0 = new_reference(s.r0, mx0, quad_max(top0)), n1 = new_reference(s.r1, mx1, quad_max(top1));
+        const float al0 = s.r0 == -INFINITY ? 1.f : fast_exp2(s.r0 - n0), al1 = s.r1 == -INFINITY ? 1.f : fast_exp2(s.r1 - n1);
+        s.r0 = n0;
+        s.r1 = n1;
+        s.l0 *= al0;
+        s.l1 *= al1;
 #pragma unroll
         for (int d = 0; d < 16; ++d) {
             s.o[d][0] *= al0;
@@ -388,20 +404,21 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
             s.o[d][2] *= al1;
             s.o[d][3] *= al1;
         }
+        weigh(sc, pv, vs, q.rs0, q.rs1, n0, n1, sum0, sum1, top0, top1);
     }
-    const float f0 = exp2i(s.f0), f1 = exp2i(s.f1);
-    // ---- O += P V, a unit at a time
+    s.l0 += sum0;
+    s.l1 += sum1;
+    // ---- O += P V, 16 cells at a time
     const int vr = lane & 7;
     const int vcell = ((vr >> 1) | ((vr & 1) << 2)) + 8 * ((lane >> 3) & 1);
+    const uint32_t v_base = smem_u32(kst) + kStepBytes + (uint32_t)vcell * kHeadDim;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const uint32_t v_base = smem_u32(unit[j]) + kUnitBytes + (uint32_t)vcell * kHeadDim;
         uint32_t af[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float* p = sc[2 * j + e];
-            af[2 * e] = pack_f16x2(p[0] * f0, p[1] * f0);
-            af[2 * e + 1] = pack_f16x2(p[2] * f1, p[3] * f1);
+            af[2 * e] = pack_f16x2(pv[2 * j + e][0], pv[2 * j + e][1]);
+            af[2 * e + 1] = pack_f16x2(pv[2 * j + e][2], pv[2 * j + e][3]);
         }
         // byte pairs by ldmatrix.trans: of the 32 dims 32 d4 .. + 31, lane (g, t) gets, of cells
         // perm(2t), perm(2t + 1) (and those + 8), dims 32 d4 + 2g, + 1 and 32 d4 + 16 + 2g, + 1.
@@ -409,7 +426,8 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
 #pragma unroll
         for (int d4 = 0; d4 < 4; ++d4) {
             uint32_t r[4];
-            ldsm_x4_t(v_base + (uint32_t)(((2 * d4 + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2], r[3]);
+            ldsm_x4_t(v_base + j * 16 * kHeadDim + (uint32_t)(((2 * d4 + (lane >> 4)) ^ (vcell & 7)) << 4), r[0], r[1], r[2],
+                      r[3]);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 uint32_t e0, d0, e1, d1;
@@ -499,10 +517,13 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
     left = Left{0, w.s, w.hk, 0, 0, 0, 0};
     Fetch f;
     f.w = w;
-    f.at = f.v = 0;
+    f.at = 0;
     f.entry = -1;
     f.resident = 0;
-    f.ok = false;
+    f.ok = f.second = false;
+    f.ksrc = a.k_pool;
+    f.vsrc = a.v_pool;
+    f.ssrc = a.k_scale;
     f.look(a, c, 0);
     int rows;
     size_t row0 = first_row(a, c, w.s, w.hk, rows);
@@ -510,7 +531,7 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
     load_q(a, row0, rows, lane, raw);
 #pragma unroll 1
     for (int k = 0; k < kDepth; ++k) f.put(a, c, k);
-    int slot = 0;                         // where the next unit is
+    int slot = 0;                         // where the next step is
 #pragma unroll 1
     for (int pos = c.begin; pos < c.end;) {
         const int n = min(w.q.np - w.off, c.end - pos);
@@ -528,24 +549,20 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         State s;
 #pragma unroll
         for (int d = 0; d < 16; ++d) s.o[d][0] = s.o[d][1] = s.o[d][2] = s.o[d][3] = 0.f;
-        s.m0 = s.m1 = -INFINITY;
+        s.r0 = s.r1 = -INFINITY;
         s.l0 = s.l1 = 0.f;
-        s.top0 = s.top1 = 0.f;
-        s.f0 = s.f1 = 0;
         const int cell0 = (here.q.p0 + here.off) * kPage;
         int lo = here.q.first - cell0, hi = here.q.n - cell0;   // the item's cells, from the step's first one
 #pragma unroll 1
-        for (int step = 0; step < n * (kPage / (2 * kUnit)); ++step) {
-            const int x = slot, y = slot + 1 == kDepth ? 0 : slot + 1;
-            copies_wait<kDepth - 2>();    // one group a unit: all but the youngest three have landed
+        for (int step = 0; step < n * (kPage / kStep); ++step) {
+            copies_wait<kDepth - 1>();    // one group a step: all but the youngest two have landed
             __syncwarp();
-            if (((f.resident >> x) & 1u) && hi > 0 && lo < 2 * kUnit) step32(s, query, kmul, c, x, y, lo, hi, lane);
-            __syncwarp();                 // every lane has read the units
-            f.put(a, c, x);
-            f.put(a, c, y);
-            slot = y + 1 == kDepth ? 0 : y + 1;
-            lo -= 2 * kUnit;
-            hi -= 2 * kUnit;
+            if (((f.resident >> slot) & 1u) && hi > 0 && lo < kStep) step32(s, query, kmul, c, slot, lo, hi, lane);
+            __syncwarp();                 // every lane has read the step
+            f.put(a, c, slot);
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+            lo -= kStep;
+            hi -= kStep;
         }
         pos += n;
         // ---- the item's end, or the run's
@@ -577,8 +594,8 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         for (int half = 0; half < 2; ++half) {
             const int r = g + 8 * half;
             if (r >= here_rows) continue;
-            const float l = half ? s.l1 : s.l0, m = half ? s.m1 : s.m0;
-            const float back = exp2i(half ? -s.f1 : -s.f0) * (complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+            const float l = half ? s.l1 : s.l0, m = half ? s.r1 : s.r0;
+            const float back = complete ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int d = 16 * k + 4 * t, e = 2 * k, v = 2 * half;
@@ -621,7 +638,7 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         int n = 0, w1 = w0;
         bool closed = false;
         part[n++] = from_before && x.first == 1 ? &ws.cta[blockIdx.x].warp[w0]
-                                                : reinterpret_cast<const Part*>(rings + w0 * kDepth * 2 * kUnitBytes);
+                                                : reinterpret_cast<const Part*>(rings + w0 * kDepth * 2 * kStepBytes);
         if (from_before && x.first == 1) closed = true;
         while (!closed && w1 + 1 < kWarps && s_left[w1 + 1].first != 0) {
             ++w1;
@@ -630,7 +647,7 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
             for (int k = 1; k < kWarps; ++k)
                 if (k == n)
                     part[k] = closed ? &ws.cta[blockIdx.x].warp[w1]
-                                     : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kUnitBytes);
+                                     : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kStepBytes);
             ++n;
         }
         const bool complete = closed && !from_before;
@@ -708,12 +725,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ int s_warp[kWarps], s_start[kWarps][2];
     __shared__ Left s_left[kWarps];
+    __shared__ __align__(16) float s_cols[kWarps][2 * kStep];
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up now; it waits for this grid's end
 
     Ctx c;
-    c.ring = smem_raw + warp * kDepth * 2 * kUnitBytes;
-    c.scales = smem_raw + kWarps * kDepth * 2 * kUnitBytes + warp * kDepth * 2 * kUnitScales;
+    c.ring = smem_raw + warp * kDepth * 2 * kStepBytes;
+    c.scales = smem_raw + kWarps * kDepth * 2 * kStepBytes + warp * kDepth * 2 * kStepScales;
+    c.cols = s_cols[warp];
     c.group = a.n_heads / a.n_kv;
     c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
     c.n_hk = a.n_kv * c.tiles;
