@@ -20,6 +20,10 @@
 // paged_join_kernel, launched beside this kernel and waiting for it on the device,
 // joins them in the order of the CTAs.
 //
+// Few and short items (a small batch of short conversations) take paged_small_kernel
+// instead: a cluster of eight CTAs per item, whose parts are merged through distributed
+// shared memory; one launch, no sum over the lengths, no workspace.
+//
 // A warp has a ring of three 32-cell steps (4 KB of K, 4 KB of V, two 64-byte rows of
 // scales), filled by 16-byte asynchronous copies, 512 consecutive bytes an instruction,
 // 16-byte pieces XOR-swizzled by (row & 7) as they land (a bulk copy would leave every
@@ -50,6 +54,8 @@
 //     with it, only when a product would pass 2^15 (or the sum 2^60, with V scales of
 //     zero): one vote a step.  V goes from the INT8 rows to the B operands by
 //     ldmatrix.trans on byte pairs.
+#include <cooperative_groups.h>
+
 #include "serve.cuh"
 
 namespace qsa {
@@ -165,6 +171,12 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
     q.p0 = q.first / kPage;
     q.np = (n + kPage - 1) / kPage - q.p0;
     return q;
+}
+
+// Pages of a warp's run, of `total` in all.
+__device__ __forceinline__ int run_pages(int total, int ctas) {
+    const int runs = ctas * kWarps;
+    return max((total + runs - 1) / runs, 1);
 }
 
 // A place in the laid-out pages: sequence, item within it, page within the item.
@@ -503,13 +515,15 @@ __device__ __forceinline__ size_t first_row(const PagedArgs& a, const Ctx& c, in
 
 // What a warp leaves for the CTA's merge.
 struct Left {
-    int first;           // its run begins inside an item (seq, hk): 1 = and that ends in the run (part in the
-    int seq, hk;         // workspace), 2 = and goes on behind it (part in the ring); 0: it begins with an item
+    int first;           // its run begins inside an item (seq, hk), and that: 1 = ends in the run (part in the
+    int seq, hk;         // workspace), 2 = goes on behind it, 3 = ends with it (part in the ring); 0: no such item
     int open;            // its run ends inside an item begun in it (part in the ring): that item and its pages' end
     int oseq, ohk, oend;
 };
 
-// One warp's pages, from place w on.
+// One warp's pages, from place w on.  SMALL: they are all one item's, and what comes of
+// them stays in the ring.
+template <bool SMALL>
 __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk w, Left& left) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -571,23 +585,23 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 1);
         s.l1 += __shfl_xor_sync(0xffffffffu, s.l1, 2);
         const bool ends = here.off + n == here.q.np;
-        const bool complete = here.off == 0 && ends;
+        const bool complete = !SMALL && here.off == 0 && ends;
         Part* part = nullptr;
         if (!complete) {
-            if (ends) {
-                left.first = 1;
-                part = &workspace_of(a.workspace).cta[blockIdx.x].warp[warp];
-            } else {                      // the run is over: its ring is free
-                if (here.off > 0) left.first = 2;
-                else {
-                    left.open = 1;
-                    left.oseq = here.s;
-                    left.ohk = here.hk;
-                    left.oend = pos - n + here.q.np;
-                }
+            if (SMALL || here.off == 0) {
+                left.open = 1;
+                left.oseq = here.s;
+                left.ohk = here.hk;
+                left.oend = pos - n + here.q.np;
+            } else {
+                left.first = !ends ? 2 : pos < c.end ? 1 : 3;
+            }
+            if (SMALL || pos == c.end) {  // the run is over: its ring is free
                 copies_wait<0>();
                 __syncwarp();
                 part = reinterpret_cast<Part*>(c.ring);
+            } else {
+                part = &workspace_of(a.workspace).cta[blockIdx.x].warp[warp];
             }
         }
 #pragma unroll
@@ -639,15 +653,15 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         bool closed = false;
         part[n++] = from_before && x.first == 1 ? &ws.cta[blockIdx.x].warp[w0]
                                                 : reinterpret_cast<const Part*>(rings + w0 * kDepth * 2 * kStepBytes);
-        if (from_before && x.first == 1) closed = true;
+        if (from_before && x.first != 2) closed = true;
         while (!closed && w1 + 1 < kWarps && s_left[w1 + 1].first != 0) {
             ++w1;
-            closed = s_left[w1].first == 1;
+            closed = s_left[w1].first != 2;
 #pragma unroll
             for (int k = 1; k < kWarps; ++k)
                 if (k == n)
-                    part[k] = closed ? &ws.cta[blockIdx.x].warp[w1]
-                                     : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kStepBytes);
+                    part[k] = s_left[w1].first == 1 ? &ws.cta[blockIdx.x].warp[w1]
+                                                    : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kStepBytes);
             ++n;
         }
         const bool complete = closed && !from_before;
@@ -700,6 +714,18 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
     if (threadIdx.x == 0) ws.rec[blockIdx.x] = rec;
 }
 
+__device__ __forceinline__ Ctx context(const PagedArgs& a, uint8_t* smem, float* cols, int warp) {
+    Ctx c;
+    c.ring = smem + warp * kDepth * 2 * kStepBytes;
+    c.scales = smem + kWarps * kDepth * 2 * kStepBytes + warp * kDepth * 2 * kStepScales;
+    c.cols = cols;
+    c.group = a.n_heads / a.n_kv;
+    c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
+    c.n_hk = a.n_kv * c.tiles;
+    c.begin = c.end = 0;
+    return c;
+}
+
 // Sum over the block of each thread's count and the sum before this thread.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int& before) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -729,13 +755,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up now; it waits for this grid's end
 
-    Ctx c;
-    c.ring = smem_raw + warp * kDepth * 2 * kStepBytes;
-    c.scales = smem_raw + kWarps * kDepth * 2 * kStepBytes + warp * kDepth * 2 * kStepScales;
-    c.cols = s_cols[warp];
-    c.group = a.n_heads / a.n_kv;
-    c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
-    c.n_hk = a.n_kv * c.tiles;
+    Ctx c = context(a, smem_raw, s_cols[warp], warp);
 
     // ---- the warps' runs of the pages of all items
     const int per = (a.n_seq + kThreads - 1) / kThreads;   // consecutive sequences per thread
@@ -743,8 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     int sum = 0, before;
     for (int s = s_lo; s < s_hi; ++s) sum += seq_of(a, s, blockIdx.x == 0).np;
     const int total = block_scan(sum, s_warp, before) * c.n_hk;   // at most 2^30, checked on the host
-    const int runs = (int)gridDim.x * kWarps;
-    const int pages = max((total + runs - 1) / runs, 1), chunk = kWarps * pages;   // of a warp, of a CTA
+    const int pages = run_pages(total, (int)gridDim.x), chunk = kWarps * pages;   // of a warp, of a CTA
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
         // the one thread whose sequences hold warp k's first page
@@ -769,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         w.q = seq_of(a, w.s, false);
         w.hk = s_start[warp][1] / w.q.np;
         w.off = s_start[warp][1] - w.hk * w.q.np;
-        walk_run(a, c, w, left);
+        walk_run<false>(a, c, w, left);
     }
     if ((tid & 31) == 0) s_left[warp] = left;
     __syncthreads();
@@ -785,82 +804,201 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
 }
 
+// One item per cluster: warp i of its 32 takes pages i np / 32 .. (i + 1) np / 32.  Each
+// CTA merges its warps' parts into one, then CTA r of the cluster joins all eight CTAs'
+// rows r and r + 8.
+constexpr int kCluster = 8;
+constexpr int kSmallItems = 38, kSmallPages = 128;   // taken up to here: see launch_paged_attn
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
+paged_small_kernel(const __grid_constant__ PagedArgs a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ Part s_part;               // of this CTA; m = -inf and l = 0 where it has none
+    __shared__ int s_has[kWarps];
+    __shared__ __align__(16) float s_cols[kWarps][2 * kStep];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster.block_rank(), item = blockIdx.x / kCluster;
+    Ctx c = context(a, smem_raw, s_cols[warp], warp);
+    Walk w;
+    w.s = item / c.n_hk;
+    w.hk = item - w.s * c.n_hk;
+    w.q = seq_of(a, w.s, rank == 0 && tid == 0 && w.hk == 0);
+    const int i = rank * kWarps + warp, all = kCluster * kWarps;
+    c.begin = (int)((long long)w.q.np * i / all);
+    c.end = (int)((long long)w.q.np * (i + 1) / all);
+    w.off = c.begin;
+    Left left{0, 0, 0, 0, 0, 0, 0};
+    if (c.begin < c.end) walk_run<true>(a, c, w, left);
+    if (lane == 0) s_has[warp] = left.open;
+    int rows;
+    const size_t row0 = first_row(a, c, w.s, w.hk, rows);
+    __syncthreads();
+    for (int r = warp; r < rows; r += kWarps) {
+        float m[kWarps], l[kWarps], M = -INFINITY;
+        const Part* part[kWarps];
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            part[k] = reinterpret_cast<const Part*>(smem_raw + k * kDepth * 2 * kStepBytes);
+            m[k] = s_has[k] ? part[k]->m[r] : -INFINITY;
+            l[k] = s_has[k] ? part[k]->l[r] : 0.f;
+            M = fmaxf(M, m[k]);
+        }
+        float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            if (!s_has[k]) continue;
+            const float wt = merge_weight(m[k], l[k], M);
+            const float4 o = *reinterpret_cast<const float4*>(&part[k]->o[r][col(r, 4 * lane)]);
+            L += wt * l[k];
+            x0 += wt * o.x;
+            x1 += wt * o.y;
+            x2 += wt * o.z;
+            x3 += wt * o.w;
+        }
+        *reinterpret_cast<float4*>(&s_part.o[r][col(r, 4 * lane)]) = make_float4(x0, x1, x2, x3);
+        if (lane == 0) {
+            s_part.m[r] = M;
+            s_part.l[r] = L;
+        }
+    }
+    cluster.sync();
+    const int r = rank + kCluster * warp; // warps 0 and 1
+    if (r < rows) {
+        float m[kCluster], l[kCluster], M = -INFINITY;
+        float4 o[kCluster];
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) {
+            const Part* p = cluster.map_shared_rank(&s_part, k);
+            m[k] = p->m[r];
+            l[k] = p->l[r];
+            o[k] = *reinterpret_cast<const float4*>(&p->o[r][col(r, 4 * lane)]);
+            M = fmaxf(M, m[k]);
+        }
+        float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) {
+            const float wt = merge_weight(m[k], l[k], M);
+            L += wt * l[k];
+            x0 += wt * o[k].x;
+            x1 += wt * o[k].y;
+            x2 += wt * o[k].z;
+            x3 += wt * o[k].w;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
+        if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
+    }
+    cluster.sync();                       // no CTA leaves while its part is being read
+}
+
 // Joins the parts of items that are cut between CTAs.  SPLIT (few items, many parts
-// each): block (k, r) takes row r of the k-th item that is cut, its warps sharing the
-// parts.  Otherwise (many items, a few parts each): block (k, r) takes the item that CTA
-// k begins and does not end, rows 4 r .. 4 r + 3, one to a warp.
+// each): block (k, r) takes row r of item k, whose place among the runs it works out
+// from the lengths while the kernel before still runs; its warps share the parts.
+// Otherwise (many items, a few parts each): block (k, r) takes the item that CTA k begins
+// and does not end, rows 4 r .. 4 r + 3, one to a warp.
 constexpr int kJoinThreads = 128;
+constexpr int kJoinItems = 64;            // most items for SPLIT
+constexpr int kJoinLoads = 8;             // parts on their way at a time
 
 template <bool SPLIT>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, int ctas) {
-    __shared__ float s_o[4][kHeadDim], s_l[4];
-    __shared__ int s_cta, s_count[4];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int ctas) {
+    __shared__ float s_o[4][kHeadDim], s_m[4], s_l[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Ws ws = workspace_of(a.workspace);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int c0 = blockIdx.x;
-    if (SPLIT) {
-        // the CTA of the k-th record
-        if (threadIdx.x == 0) s_cta = -1;
-        constexpr int kPer = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
-        unsigned vote[kPer];
-        int mine = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {  // warp w looks at CTAs 32 (kPer w + j) + lane
-            const int i = 32 * (kPer * warp + j) + lane;
-            vote[j] = __ballot_sync(0xffffffffu, i < ctas && ws.rec[min(i, ctas - 1)].last >= 0);
-            mine += __popc(vote[j]);
-        }
-        if (lane == 0) s_count[warp] = mine;
-        __syncthreads();
-        int rank = 0;
-        for (int w = 0; w < warp; ++w) rank += s_count[w];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (((vote[j] >> lane) & 1u) && rank + __popc(vote[j] & ((1u << lane) - 1u)) == (int)blockIdx.x)
-                s_cta = 32 * (kPer * warp + j) + lane;
-            rank += __popc(vote[j]);
-        }
-        __syncthreads();
-        c0 = s_cta;
-        if (c0 < 0) return;
-    }
-    const Rec rec = ws.rec[c0];
-    if (rec.last < 0 || rec.last >= ctas) return;
     const int group = a.n_heads / a.n_kv, tiles = (group + kRowsTile - 1) / kRowsTile;
-    const int h = rec.hk / tiles, tile = rec.hk - h * tiles;
+    int c0, last, seq, hk;
+    if (SPLIT) {
+        const int n_hk = a.n_kv * tiles;
+        seq = blockIdx.x / n_hk;
+        hk = blockIdx.x - seq * n_hk;
+        // two sequences per lane: at most 64 items
+        const int n0 = 2 * lane < a.n_seq ? seq_of(a, 2 * lane, false).np : 0;
+        const int n1 = 2 * lane + 1 < a.n_seq ? seq_of(a, 2 * lane + 1, false).np : 0;
+        int before = (2 * lane < seq ? n0 : 0) + (2 * lane + 1 < seq ? n1 : 0), total = n0 + n1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+        }
+        const int np = __shfl_sync(0xffffffffu, seq & 1 ? n1 : n0, seq >> 1);
+        const int chunk = kWarps * run_pages(total * n_hk, ctas), start = before * n_hk + hk * np;
+        c0 = start / chunk;
+        last = (start + np - 1) / chunk;
+        if (np == 0 || last == c0) return;   // no page, or all in one CTA: done there
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        c0 = blockIdx.x;
+        const Rec rec = ws.rec[c0];
+        last = rec.last;
+        seq = rec.seq;
+        hk = rec.hk;
+        if (last < 0) return;
+    }
+    const int h = hk / tiles, tile = hk - h * tiles;
     const int r = SPLIT ? blockIdx.y : 4 * blockIdx.y + warp;
     if (r >= min(kRowsTile, group - kRowsTile * tile)) return;
-    const int n = rec.last - c0 + 1;      // part 0 is CTA c0's second, part i the first of CTA c0 + i
-    auto at = [&](int i) { return &ws.cta[c0 + i].cta[i == 0 ? 1 : 0]; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, at(i)->m[r]);
+    // part 0 is CTA c0's second, part i the first of CTA c0 + i
+    const int n = last - c0 + 1, step = SPLIT ? 4 : 1;
+    float M = -INFINITY, L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = SPLIT ? warp : 0; i0 < n; i0 += step * kJoinLoads) {
+        float m[kJoinLoads], l[kJoinLoads], top = M;
+        float4 o[kJoinLoads];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int i = SPLIT ? warp : 0; i < n; i += SPLIT ? 4 : 1) {
-        const Part* p = at(i);
-        const float l = p->l[r], wt = merge_weight(p->m[r], l, M);
-        const float4 o = *reinterpret_cast<const float4*>(&p->o[r][col(r, 4 * lane)]);
-        L += wt * l;
-        x[0] += wt * o.x;
-        x[1] += wt * o.y;
-        x[2] += wt * o.z;
-        x[3] += wt * o.w;
+        for (int j = 0; j < kJoinLoads; ++j) {
+            const int i = i0 + step * j;
+            m[j] = -INFINITY;
+            l[j] = 0.f;
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                const Part* p = &ws.cta[c0 + i].cta[i == 0 ? 1 : 0];
+                m[j] = p->m[r];
+                l[j] = p->l[r];
+                o[j] = *reinterpret_cast<const float4*>(&p->o[r][col(r, 4 * lane)]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinLoads; ++j) top = fmaxf(top, m[j]);
+        const float keep = merge_weight(M, L, top);
+        M = top;
+        L *= keep;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= keep;
+#pragma unroll
+        for (int j = 0; j < kJoinLoads; ++j) {
+            const float wt = merge_weight(m[j], l[j], M);
+            L += wt * l[j];
+            x[0] += wt * o[j].x;
+            x[1] += wt * o[j].y;
+            x[2] += wt * o[j].z;
+            x[3] += wt * o[j].w;
+        }
     }
     if (SPLIT) {
         *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
-        if (lane == 0) s_l[warp] = L;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = L;
+        }
         __syncthreads();
         if (warp != 0) return;
-        L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+        M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        L = x[0] = x[1] = x[2] = x[3] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            x[e] = s_o[0][4 * lane + e] + s_o[1][4 * lane + e] + s_o[2][4 * lane + e] + s_o[3][4 * lane + e];
+        for (int k = 0; k < 4; ++k) {
+            const float wt = merge_weight(s_m[k], s_l[k], M);
+            const float4 o = *reinterpret_cast<const float4*>(&s_o[k][4 * lane]);
+            L += wt * s_l[k];
+            x[0] += wt * o.x;
+            x[1] += wt * o.y;
+            x[2] += wt * o.z;
+            x[3] += wt * o.w;
+        }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const size_t row = (size_t)rec.seq * a.n_heads + h * group + kRowsTile * tile + r;
+    const size_t row = (size_t)seq * a.n_heads + h * group + kRowsTile * tile + r;
     store4(a.out, a.out_type, row * kHeadDim + 4 * lane, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
     if (lane == 0 && a.lse) a.lse[row] = lse_of(M, L);
 }
@@ -870,20 +1008,25 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
 size_t paged_attn_workspace(int, int) { return kMaxCtas * (sizeof(Rec) + sizeof(CtaSpace)); }
 
 cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
+    const int group = a.n_heads / a.n_kv, rows = group < kRowsTile ? group : kRowsTile;
+    const long long items = (long long)a.n_seq * a.n_kv * ((group + kRowsTile - 1) / kRowsTile);
+    cudaError_t e;
+    if (items <= kSmallItems && a.n_lpages <= kSmallPages) {
+        e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        paged_small_kernel<<<(unsigned)items * kCluster, kThreads, kSmem, stream>>>(a);
+        return cudaGetLastError();
+    }
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int rows = a.n_heads / a.n_kv < kRowsTile ? a.n_heads / a.n_kv : kRowsTile;
-    e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     paged_attn_kernel<<<grid, kThreads, kSmem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // at most one cut item per CTA and per item; up to 64 items a block finds its own among the records
-    const long long items = (long long)a.n_seq * a.n_kv * ((a.n_heads / a.n_kv + kRowsTile - 1) / kRowsTile);
-    const bool split = items <= 64;
+    const bool split = items <= kJoinItems;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -306,7 +306,7 @@ def _here(t, name: str) -> torch.device:
 
 def _raw_stream(stream, dev) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without the object
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -70,9 +70,12 @@ CASES = [  # lengths, KV heads, group
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens,n_kv,group", CASES)
-def test_against_definition(qsa, lens, n_kv, group):
-    q, cache, tables, n = make(lens, n_kv, group, seed=len(lens) * 100 + group)
+def test_against_definition(qsa, lens, n_kv, group, wide):
+    """wide: tables far longer than the sequences, which takes the kernel for long ones."""
+    width = max(300, max(lens) // 64 + 2) if wide else None
+    q, cache, tables, n = make(lens, n_kv, group, seed=len(lens) * 100 + group, width=width)
     out, lse = run(qsa, q, cache, tables, n)
     ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE))
 
@@ -246,6 +249,21 @@ def test_two_streams_and_a_captured_graph(qsa):
         graph.replay()
         torch.cuda.synchronize()
         ref.check_attn(out, None, ref.paged_attn(q, *cache, tables, lens, SCALE), str(lens))
+
+
+def test_cold_caches_and_a_small_call_before(qsa):
+    """A long sequence right after a short one, with the caches full of something else, so that copies land late and out
+    of order: the same bits as warm, several times."""
+    small = [t.cuda() for t in (lambda q, c, t, n: (q, *c, t, n))(*make([1021], 4, 12, seed=18))]
+    q, cache, tables, n = make([100000], 4, 12, seed=19)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    first = qsa.paged_attn(*d)
+    ref.check_attn(first, None, ref.paged_attn(q, *cache, tables, n, SCALE))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for k in range(20):
+        flush.fill_(k)
+        qsa.paged_attn(*small)
+        assert torch.equal(qsa.paged_attn(*d), first)
 
 
 def test_refusals(qsa):
