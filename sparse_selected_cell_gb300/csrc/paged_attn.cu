@@ -173,11 +173,14 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
     return q;
 }
 
-// Pages of a warp's run, of `total` in all.
-__device__ __forceinline__ int run_pages(int total, int ctas) {
-    const int runs = ctas * kWarps;
-    return max((total + runs - 1) / runs, 1);
+// The runs: run i of `runs` begins at page total i / runs, so that any two differ by a
+// page at most, and none is empty (fewer pages than warps: a page to each of the first);
+// and the CTA whose runs hold a page.
+__device__ __forceinline__ int run_begin(int total, int i, int runs) { return (int)((long long)total * min(i, runs) / runs); }
+__device__ __forceinline__ int cta_of(int total, int page, int runs) {
+    return (int)((((long long)page + 1) * runs - 1) / total) / kWarps;
 }
+__device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas * kWarps, total)); }
 
 // A place in the laid-out pages: sequence, item within it, page within the item.
 struct Walk {
@@ -391,9 +394,12 @@ __device__ __forceinline__ void step32(State& s, const Query& q, float kmul, con
     }
     // ---- weights; the reference moves when a product or a sum passes its limit
     float pv[4][4], sum0, sum1, top0, top1;
-    weigh(sc, pv, vs, q.rs0, q.rs1, s.r0, s.r1, sum0, sum1, top0, top1);
-    if (__any_sync(0xffffffffu, top0 > kPTop || top1 > kPTop || sum0 > kSumTop || sum1 > kSumTop || s.r0 == -INFINITY ||
-                                    s.r1 == -INFINITY)) {
+    bool move = __any_sync(0xffffffffu, s.r0 == -INFINITY || s.r1 == -INFINITY);   // an item's first step
+    if (!move) {
+        weigh(sc, pv, vs, q.rs0, q.rs1, s.r0, s.r1, sum0, sum1, top0, top1);
+        move = __any_sync(0xffffffffu, top0 > kPTop || top1 > kPTop || sum0 > kSumTop || sum1 > kSumTop);
+    }
+    if (move) {
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -468,22 +474,31 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
                                                                       16 * t + 8 * (j & 1)));
         }
 }
+// Largest |x| of packed 16-bit pairs, still packed.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w, int type) {
+    if (type == QSA_F16) {
+        const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&m), __habs2(*reinterpret_cast<const __half2*>(&w)));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __nv_bfloat162 r =
+        __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ void convert_q(const RawQuery& raw, int type, Query& q) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        float amax = 0.f;
+        uint32_t top = 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float x[8];
-            unpack8(raw.w[half][j], type, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+            const uint4& w = raw.w[half][j];
+            top = max_abs2(max_abs2(max_abs2(max_abs2(top, w.x, type), w.y, type), w.z, type), w.w, type);
         }
-        amax = quad_max(amax);
+        const float lo = type == QSA_F16 ? __half2float(__ushort_as_half((uint16_t)top)) : bf16_lo(top);
+        const float hi = type == QSA_F16 ? __half2float(__ushort_as_half((uint16_t)(top >> 16))) : bf16_hi(top);
+        const float amax = quad_max(fmaxf(lo, hi));
         const int e = amax > 0.f ? min(max(f32_exponent(amax) - 12, -114), 114) : 0;
         const float down = exp2i(-e);
         (half ? q.rs1 : q.rs0) = exp2i(e);
-        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[8];
@@ -491,19 +506,17 @@ __device__ __forceinline__ void convert_q(const RawQuery& raw, int type, Query& 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {   // k step 4 (j / 2) + 2 (j & 1) + k: four dims
                 const int kk = 4 * (j >> 1) + 2 * (j & 1) + k;
-                const uint32_t even = pack_f16x2(x[4 * k] * down, x[4 * k + 2] * down);
-                const uint32_t odd = pack_f16x2(x[4 * k + 1] * down, x[4 * k + 3] * down);
-                q.a[kk][half] = even;
-                q.a[kk][2 + half] = odd;
-                const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&even));
-                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&odd));
-                sum += (u.x + u.y) + (v.x + v.y);
+                q.a[kk][half] = pack_f16x2(x[4 * k] * down, x[4 * k + 2] * down);
+                q.a[kk][2 + half] = pack_f16x2(x[4 * k + 1] * down, x[4 * k + 3] * down);
             }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        (half ? q.bias1 : q.bias0) = sum * -0x1p-17f;
     }
+    // the rows' sums times 128 * 2^-24, by the same products: every K + 128 = 128
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) mma_f16(sum, q.a[kk][0], q.a[kk][1], q.a[kk][2], q.a[kk][3], 0x00800080u, 0x00800080u);
+    q.bias0 = -sum[0];
+    q.bias1 = -sum[2];
 }
 
 // Rows of an item: the first one's number in q and out, and how many.
@@ -633,7 +646,8 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
 
 // Merges the parts that the CTA's warps have left, item by item, a row to a warp.  The
 // warps' runs follow one another, so an item's parts are those of consecutive warps.
-__device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, const Left* s_left, uint8_t* rings, int chunk) {
+__device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, const Left* s_left, uint8_t* rings, int total,
+                                          int runs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Ws ws = workspace_of(a.workspace);
     Rec rec{-1, 0, 0, 0};
@@ -668,7 +682,7 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         int rows;
         const size_t row0 = first_row(a, c, seq, hk, rows);
         Part* to = &ws.cta[blockIdx.x].cta[from_before ? 0 : 1];
-        if (!complete && !from_before) rec = Rec{(end - 1) / chunk, seq, hk, 0};
+        if (!complete && !from_before) rec = Rec{cta_of(total, end - 1, runs), seq, hk, 0};
         for (int r = warp; r < rows; r += kWarps) {
             float m[kWarps], l[kWarps], M = -INFINITY;
 #pragma unroll
@@ -763,23 +777,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     int sum = 0, before;
     for (int s = s_lo; s < s_hi; ++s) sum += seq_of(a, s, blockIdx.x == 0).np;
     const int total = block_scan(sum, s_warp, before) * c.n_hk;   // at most 2^30, checked on the host
-    const int pages = run_pages(total, (int)gridDim.x), chunk = kWarps * pages;   // of a warp, of a CTA
+    const int runs = run_count(total, (int)gridDim.x);
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
         // the one thread whose sequences hold warp k's first page
-        const long long first = (long long)blockIdx.x * chunk + k * pages;
-        if (first < (long long)before * c.n_hk || first >= (long long)(before + sum) * c.n_hk) continue;
+        const int first = run_begin(total, blockIdx.x * kWarps + k, runs);
+        if (first < before * c.n_hk || first >= (before + sum) * c.n_hk) continue;
         int at = before, s = s_lo;
         for (;; ++s) {
             const int np = seq_of(a, s, false).np;
-            if (first < (long long)(at + np) * c.n_hk) break;
+            if (first < (at + np) * c.n_hk) break;
             at += np;
         }
         s_start[k][0] = s;
-        s_start[k][1] = (int)first - at * c.n_hk;
+        s_start[k][1] = first - at * c.n_hk;
     }
-    c.begin = (int)min((long long)blockIdx.x * chunk + warp * pages, (long long)total);
-    c.end = min(c.begin + pages, total);
+    c.begin = run_begin(total, blockIdx.x * kWarps + warp, runs);
+    c.end = run_begin(total, blockIdx.x * kWarps + warp + 1, runs);
     __syncthreads();
     Left left{0, 0, 0, 0, 0, 0, 0};
     if (c.begin < c.end) {
@@ -792,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     if ((tid & 31) == 0) s_left[warp] = left;
     __syncthreads();
-    merge_cta(a, c, s_left, smem_raw, chunk);
+    merge_cta(a, c, s_left, smem_raw, total, runs);
     // rows of the sequences that have no page at all
     for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
         if (seq_of(a, s, false).np > 0) continue;
@@ -923,10 +937,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             total += __shfl_xor_sync(0xffffffffu, total, o);
         }
         const int np = __shfl_sync(0xffffffffu, seq & 1 ? n1 : n0, seq >> 1);
-        const int chunk = kWarps * run_pages(total * n_hk, ctas), start = before * n_hk + hk * np;
-        c0 = start / chunk;
-        last = (start + np - 1) / chunk;
-        if (np == 0 || last == c0) return;   // no page, or all in one CTA: done there
+        const int start = before * n_hk + hk * np;
+        if (np == 0) return;
+        total *= n_hk;
+        const int runs = run_count(total, ctas);
+        c0 = cta_of(total, start, runs);
+        last = cta_of(total, start + np - 1, runs);
+        if (last == c0) return;           // all in one CTA: done there
         asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
