@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablesArg
     __shared__ unsigned s_taken;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned n_tok = (unsigned)a.n_tok;
+    wait_for_stream();
     const unsigned lo = blockIdx.x * (unsigned)kTile, hi = min(lo + kTile, n_tok);
     int head = a.free_head ? __ldg(a.free_head) : 0;
     if (head < 0 || head > a.n_free) {
@@ -210,8 +211,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablesArg
 
 cudaError_t launch_extend_tables(const TablesArgs& a, cudaStream_t stream) {
     const unsigned grid = a.n_tok > 0 ? (unsigned)((a.n_tok + kTile - 1) / kTile) : 1u;
-    extend_tables_kernel<<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(extend_tables_kernel, dim3(grid), kThreads, 0, stream, a);
 }
 
 }  // namespace qsa

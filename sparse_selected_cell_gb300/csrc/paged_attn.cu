@@ -767,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     __shared__ Left s_left[kWarps];
     __shared__ __align__(16) float s_cols[kWarps][2 * kStep];
     const int tid = threadIdx.x, warp = tid >> 5;
+    wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up now; it waits for this grid's end
 
     Ctx c = context(a, smem_raw, s_cols[warp], warp);
@@ -833,6 +834,7 @@ paged_small_kernel(const __grid_constant__ PagedArgs a) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    wait_for_stream();
     const int rank = (int)cluster.block_rank(), item = blockIdx.x / kCluster;
     Ctx c = context(a, smem_raw, s_cols[warp], warp);
     Walk w;
@@ -944,9 +946,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         c0 = cta_of(total, start, runs);
         last = cta_of(total, start + np - 1, runs);
         if (last == c0) return;           // all in one CTA: done there
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_stream();
     } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_stream();
         c0 = blockIdx.x;
         const Rec rec = ws.rec[c0];
         last = rec.last;
@@ -1031,8 +1033,7 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     if (items <= kSmallItems && a.n_lpages <= kSmallPages) {
         e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
-        paged_small_kernel<<<(unsigned)items * kCluster, kThreads, kSmem, stream>>>(a);
-        return cudaGetLastError();
+        return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kSmem, stream, a);
     }
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);
@@ -1040,21 +1041,12 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    paged_attn_kernel<<<grid, kThreads, kSmem, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_overlapped(paged_attn_kernel, dim3((unsigned)grid), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    const bool split = items <= kJoinItems;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = split ? dim3((unsigned)items, (unsigned)rows) : dim3((unsigned)grid, (unsigned)(rows + 3) / 4);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return split ? cudaLaunchKernelEx(&cfg, paged_join_kernel<true>, a, grid)
-                 : cudaLaunchKernelEx(&cfg, paged_join_kernel<false>, a, grid);
+    if (items <= kJoinItems)
+        return launch_overlapped(paged_join_kernel<true>, dim3((unsigned)items, (unsigned)rows), kJoinThreads, 0, stream, a, grid);
+    return launch_overlapped(paged_join_kernel<false>, dim3((unsigned)grid, (unsigned)(rows + 3) / 4), kJoinThreads, 0, stream,
+                             a, grid);
 }
 
 }  // namespace qsa

@@ -28,6 +28,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
     return type == QSA_F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
+// ---------------------------------------------------------------- launch overlap
+// These kernels are launched so that their blocks may be set up while the kernel before
+// them in the stream still drains; each waits here, before its first read, until that
+// kernel has finished and its writes are visible.  Whatever was launched before, and
+// whatever follows, sees plain stream order.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---------------------------------------------------------------- launchers
 struct PagedArgs {
     const void* q;
