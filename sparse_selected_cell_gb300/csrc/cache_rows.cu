@@ -9,23 +9,26 @@
 // reduction loses bits.  Its top 32 bits go to sincospif.  f comes from the frequency's
 // 53 bits by one integer product (FP64 arithmetic is slow on this GPU).
 //
-// Layout: one CTA per token, eight threads per 128-element row, so the token's 64
-// sines and cosines are formed once, into shared memory, and a thread keeps the
-// eight pairs it always works on in registers for all its rows.  Thread l of a row's
-// eight holds the 16-byte pieces l and l + n_pairs / 8 of the row, which are the two
-// halves of pairs 8l .. 8l + 7 (of interleaved pairs pieces l and l + 8, pairs 4l .. and
-// 4l + 32 ..): every load and store is 16 bytes wide and eight threads' are 128
-// consecutive bytes, and no value crosses threads but for the row's largest |x|.  Both
-// kernels here are bound by HBM; the rows of two passes are on their way before the
-// sines are formed.
+// Layout: a block takes every gridDim-th token, a warp four rows of it at a time, eight
+// threads per 128-element row.  Thread l of a row's eight holds the 16-byte pieces l and
+// l + n_pairs / 8 of the row, which are the two halves of pairs 8l .. 8l + 7 (of
+// interleaved pairs pieces l and l + 8, pairs 4l .. and 4l + 32 ..): every load and store
+// is 16 bytes wide and eight threads' are 128 consecutive bytes, no value crosses threads
+// but for the row's largest |x|, and a thread reads the sines of its eight pairs once per
+// token.  The next rows, of this token and the next, are on their way by asynchronous
+// copies, and the next token's sines are formed beside this one's rows.  Bound by HBM; a
+// token's rows are read and written by one block at about the same time because that is
+// what DRAM pages like (a token to a warp, every warp in a page of its own, copied at 5.2
+// of the 6.5 TB/s of a plain copy).
 #include "serve.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRowThreads = 8;                              // threads per row
-constexpr int kRowsPerPass = kRopeThreads / kRowThreads;    // 16
+constexpr int kRopeWarps = 4;                                // of a block; kRopeWide where tokens are few
+constexpr int kRopeWide = 8;
+constexpr int kRopeDepth = 3;                                // turns (four rows) of a warp on their way
+constexpr int kRopeBlocks = 5;                               // of kRopeWarps warps, per SM
 
 // frac(x / 2 pi) * 2^64 of a finite double (0 for what is not finite): x = m 2^(e - 52)
 // with m < 2^53, and m / 2 pi * 2^66 is one 64 x 64-bit product.
@@ -41,144 +44,209 @@ __device__ __forceinline__ unsigned long long turn_fraction(double x) {
     return field == 0x7FF ? 0ull : (bits >> 63) ? 0ull - f : f;
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ __align__(16) float s_cos[kHeadDim / 2], s_sin[kHeadDim / 2];
-    const int t = blockIdx.x, tid = threadIdx.x;
-    const int l = tid & (kRowThreads - 1);
+// round(x / scale), ties to even, within [-127, 127], of 16 values, as bytes; amax: the
+// row's largest |x|.  x times the reciprocal is within 2^-16 of a quotient up to 127, so it
+// rounds alike unless it lies next to a half; rows with such a value, and those beyond
+// 127 (a scale that FP16 does not hold), are divided out.
+__device__ __forceinline__ void quantise16(const float (&x)[2][8], float scale, float amax, uint32_t (&b)[2][2]) {
+    constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it rounds to an integer, in the low bits
+    const float inv = __fdiv_rn(1.f, scale);
+    uint32_t t[2][8];
+    float off = amax * inv < 127.4f ? 0.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float y = x[e][j] * inv, m = __fadd_rn(y, kMagic);
+            off = fmaxf(off, fabsf(y - __fadd_rn(m, -kMagic)));
+            t[e][j] = __float_as_uint(m);
+        }
+    if (!(off < 0.4999f)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                t[e][j] = (uint32_t)min(127, max(-127, __float2int_rn(__fdiv_rn(x[e][j], scale))));
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            b[e][j] = __byte_perm(__byte_perm(t[e][4 * j], t[e][4 * j + 1], 0x0040),
+                                  __byte_perm(t[e][4 * j + 2], t[e][4 * j + 3], 0x0040), 0x5410);
+}
+
+template <int TYPE, bool INTERLEAVED, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, kRopeBlocks * kRopeWarps / WARPS)
+rope_append_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ uint4 s_ring[WARPS][kRopeDepth][2][32];       // each thread's own pieces of the rows to come
+    __shared__ __align__(16) float s_cos[2][kHeadDim / 2], s_sin[2][kHeadDim / 2];   // this token's and the next's
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned n_tok = (unsigned)a.n_tok, stride = gridDim.x;
+    const int l = lane & 7;
     // the thread's two 16-byte pieces of any row, and whether they are turned
-    const bool turned = a.interleaved || 8 * l < a.n_pairs;
-    const int p0 = turned ? l : 2 * l;
-    const int p1 = a.interleaved ? l + 8 : turned ? l + a.n_pairs / 8 : 2 * l + 1;
+    const bool turned = INTERLEAVED || 8 * l < a.n_pairs;
+    const int p0 = turned ? l : l + a.n_pairs / 8;
+    const int p1 = INTERLEAVED || !turned ? l + 8 : l + a.n_pairs / 8;
+    const int n_rows = a.n_heads + (a.k_pool ? 2 * a.n_kv : 0);   // query, key, value rows
+    constexpr int kTurn = 4 * WARPS;                 // a warp's turns: rows 4 warp .. 4 warp + 3, then kTurn further
     wait_for_stream();
 
-    // the token's cell, for its key and value rows
-    long long cell_row = -1;
-    if (a.k_pool) {
-        const int slot = __ldg(a.slots + t);
-        if (slot >= 0) {
-            const int page = slot >> 6;
-            if (page < a.n_ppages) cell_row = (long long)page * a.n_kv * kPage + (slot & (kPage - 1));
-            else if (tid == 0) report(a.dev_status, QSA_DEV_BAD_CELL);
+    // asynchronous copies of the next turn's pieces, a group a turn, running ahead of the work over all tokens
+    unsigned l_tok = blockIdx.x;
+    int l_row = 4 * warp, l_slot = 0;
+    auto load = [&]() {
+        if (l_tok < n_tok && l_row < n_rows) {
+            const long long t = l_tok;
+            const int r = l_row + (lane >> 3), kv = r - a.n_heads;
+            if (r < n_rows) {
+                const uint16_t* src = kv < 0 ? a.q + t * a.q_stride + (size_t)r * kHeadDim
+                                      : kv < a.n_kv ? a.k + t * a.k_stride + (size_t)kv * kHeadDim
+                                                    : a.v + t * a.v_stride + (size_t)(kv - a.n_kv) * kHeadDim;
+                const uint32_t dst = smem_u32(&s_ring[warp][l_slot][0][lane]);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + 8 * p0) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(src + 8 * p1) : "memory");
+            }
+            l_slot = (l_slot + 1) % kRopeDepth;
+            l_row += kTurn;
+            if (l_row >= n_rows) {
+                l_tok += stride;
+                l_row = 4 * warp;
+            }
         }
-    }
-    const int n_rows = a.n_heads + (cell_row >= 0 ? 2 * a.n_kv : 0);
-    const int r0 = tid >> 3;                         // rows r0, r0 + 16, ...: query, key, value rows
-    auto load = [&](int r, uint4 (&w)[2]) {
-        w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= n_rows) return;
-        const int kv = r - a.n_heads;
-        const uint16_t* src = kv < 0 ? a.q + t * a.q_stride + (size_t)r * kHeadDim
-                              : kv < a.n_kv ? a.k + t * a.k_stride + (size_t)kv * kHeadDim
-                                            : a.v + t * a.v_stride + (size_t)(kv - a.n_kv) * kHeadDim;
-        w[0] = reinterpret_cast<const uint4*>(src)[p0];   // plain loads: q_out may be q itself
-        w[1] = reinterpret_cast<const uint4*>(src)[p1];
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint4 next[2][2];
-    load(r0, next[0]);
-    load(r0 + kRowsPerPass, next[1]);
+#pragma unroll 1
+    for (int k = 0; k < kRopeDepth; ++k) load();
 
-    if (tid < a.n_pairs) {
-        int axis = a.pair_axis ? __ldg(a.pair_axis + tid) : 0;
+    // this thread's pair: its position and its turns per position
+    const int pair = threadIdx.x;
+    const bool has = pair < a.n_pairs;
+    const int32_t* pos_at = a.positions;
+    unsigned long long f = 0;
+    int pos = 0;
+    if (has) {
+        int axis = a.pair_axis ? __ldg(a.pair_axis + pair) : 0;
         if (axis < 0 || axis >= a.n_axes) {
             report(a.dev_status, QSA_DEV_BAD_AXIS);
             axis = 0;
         }
-        const long long pos = __ldg(a.positions + (size_t)axis * a.pos_stride + t);
-        const unsigned long long f = turn_fraction(__ldg(a.inv_freq + tid));
-        const int turn = (int)(((unsigned long long)pos * f) >> 32);     // [-1/2, 1/2) turns, 2^-32 each
-        float sn, cs;
-        sincospif((float)turn * 0x1p-31f, &sn, &cs);
-        s_sin[tid] = sn;
-        s_cos[tid] = cs;
+        pos_at += (size_t)axis * a.pos_stride;
+        f = turn_fraction(__ldg(a.inv_freq + pair));
+        pos = __ldg(pos_at + blockIdx.x);
     }
-    __syncthreads();
-    float cs[8], sn[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int pair = a.interleaved ? 4 * l + (j & 3) + 32 * (j >> 2) : 8 * l + j;
-        cs[j] = pair < a.n_pairs ? s_cos[pair] : 1.f;
-        sn[j] = pair < a.n_pairs ? s_sin[pair] : 0.f;
-    }
-
-    // one row; the row maximum shuffles, so a warp's four rows go together
-    auto work = [&](int r, const uint4 (&w)[2]) {
-        const int kv = r - a.n_heads;                // >= 0: key rows, then value rows
-        const bool live = r < n_rows, is_v = kv >= a.n_kv;
-        const int h = is_v ? kv - a.n_kv : kv;
-        float x[2][8];
-        unpack8(w[0], a.type, x[0]);
-        unpack8(w[1], a.type, x[1]);
-        if (kv < 0 || !is_v) {
-            if (a.interleaved) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {        // pair j: elements 2j, 2j + 1 of the 16; a piece is turned whole
-                    if (4 * l + 32 * (j >> 2) >= a.n_pairs) continue;
-                    float& u = x[j >> 2][2 * (j & 3)];
-                    float& z = x[j >> 2][2 * (j & 3) + 1];
-                    const float p = u * cs[j] - z * sn[j];
-                    z = z * cs[j] + u * sn[j];
-                    u = p;
-                }
-            } else if (turned) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float u = x[0][j], z = x[1][j];
-                    x[0][j] = u * cs[j] - z * sn[j];
-                    x[1][j] = z * cs[j] + u * sn[j];
-                }
-            }
-        }
-        if (live && kv < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + (size_t)r * kHeadDim);
-            dst[p0] = make_uint4(pack2(x[0][0], x[0][1], a.type), pack2(x[0][2], x[0][3], a.type),
-                                 pack2(x[0][4], x[0][5], a.type), pack2(x[0][6], x[0][7], a.type));
-            dst[p1] = make_uint4(pack2(x[1][0], x[1][1], a.type), pack2(x[1][2], x[1][3], a.type),
-                                 pack2(x[1][4], x[1][5], a.type), pack2(x[1][6], x[1][7], a.type));
-        }
-        if ((r & ~3) + 3 < a.n_heads) return;        // warp-uniform: four query rows
-        // ---- key and value rows: scale = max |x| / 127 rounded up to FP16, so |x / scale| <= 127
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {                // NaN counts as infinite (fmaxf would drop it)
-            const float u = fabsf(x[0][j]), z = fabsf(x[1][j]);
-            amax = fmaxf(amax, fmaxf(u <= 3.402823466e38f ? u : INFINITY, z <= 3.402823466e38f ? z : INFINITY));
-        }
-#pragma unroll
-        for (int o = 1; o < kRowThreads; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (live && kv >= 0) {
-            const bool finite = amax < INFINITY;
-            uint16_t sb = __half_as_ushort(__float2half_ru(__fdiv_rn(amax, 127.f)));
-            if (sb > 0x7BFFu) sb = finite ? 0x7BFFu : 0x7FFFu;   // past FP16: the largest finite scale; not finite: NaN
-            const float scale = __half2float(__ushort_as_half(sb));
-            const float div = finite && sb != 0 ? scale : 1.f;
-            const long long row = cell_row + (long long)h * kPage;
-            int8_t* dst = (is_v ? a.v_pool : a.k_pool) + row * kHeadDim;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t b[2] = {0u, 0u};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    int i = __float2int_rn(__fdiv_rn(x[e][j], div));
-                    i = finite ? min(127, max(-127, i)) : 0;
-                    b[j >> 2] |= (uint32_t)(i & 0xFF) << (8 * (j & 3));
-                }
-                *reinterpret_cast<uint2*>(dst + 8 * (e ? p1 : p0)) = make_uint2(b[0], b[1]);
-            }
-            if (l == 0) (is_v ? a.v_scale : a.k_scale)[row] = sb;
-        }
+    auto form = [&](int buf, unsigned next) {        // the sines of the token that pos is of; then the next one's position
+        if (!has) return;
+        const int turn = (int)(((unsigned long long)(long long)pos * f) >> 32);   // [-1/2, 1/2) turns, 2^-32 each
+        sincospif((float)turn * 0x1p-31f, &s_sin[buf][pair], &s_cos[buf][pair]);
+        if (next < n_tok) pos = __ldg(pos_at + next);
     };
-    // warp-uniform trips (a warp's rows r .. r + 3): two passes at a time, the next two on their way
-    for (int r = r0; (r & ~3) < n_rows; r += 2 * kRowsPerPass) {
-        uint4 w[2][2];
+    form(0, blockIdx.x + stride);
+    int cell = a.k_pool ? __ldg(a.slots + blockIdx.x) : -1;
+
+    int slot = 0, buf = 0;
+#pragma unroll 1
+    for (unsigned tok = blockIdx.x; tok < n_tok; tok += stride, buf ^= 1) {
+        const long long t = tok;
+        __syncthreads();                             // this token's sines are there, the one before's have been read
+        if (tok + stride < n_tok) form(buf ^ 1, tok + 2 * stride);
+        long long cell_row = -1;
+        if (cell >= 0) {
+            const int page = cell >> 6;
+            if (page < a.n_ppages) cell_row = (long long)page * a.n_kv * kPage + (cell & (kPage - 1));
+            else if (threadIdx.x == 0) report(a.dev_status, QSA_DEV_BAD_CELL);
+        }
+        if (a.k_pool && tok + stride < n_tok) cell = __ldg(a.slots + tok + stride);
+        float cs[8], sn[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            w[e][0] = next[e][0];
-            w[e][1] = next[e][1];
-            load(r + (2 + e) * kRowsPerPass, next[e]);
+            const int first = INTERLEAVED ? 4 * l + 32 * e : 8 * l + 4 * e;   // pair of elements 4 e .. 4 e + 3 here
+            const float4 c = *reinterpret_cast<const float4*>(&s_cos[buf][first]);
+            const float4 z = *reinterpret_cast<const float4*>(&s_sin[buf][first]);
+            cs[4 * e] = c.x, cs[4 * e + 1] = c.y, cs[4 * e + 2] = c.z, cs[4 * e + 3] = c.w;
+            sn[4 * e] = z.x, sn[4 * e + 1] = z.y, sn[4 * e + 2] = z.z, sn[4 * e + 3] = z.w;
         }
-        work(r, w[0]);
-        if ((r & ~3) + kRowsPerPass < n_rows) work(r + kRowsPerPass, w[1]);
+        // ---- its rows, four to a warp at a time
+#pragma unroll 1
+        for (int r4 = 4 * warp; r4 < n_rows; r4 += kTurn) {
+            float x[2][8];
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRopeDepth - 1) : "memory");
+            unpack8(s_ring[warp][slot][0][lane], TYPE, x[0]);   // the thread's own copies: no other has to wait
+            unpack8(s_ring[warp][slot][1][lane], TYPE, x[1]);
+            load();
+            slot = (slot + 1) % kRopeDepth;
+            const int r = r4 + (lane >> 3), kv = r - a.n_heads;   // kv >= 0: key rows, then value rows
+            const bool is_v = kv >= a.n_kv;
+            if (kv < 0 || !is_v) {
+                if (INTERLEAVED) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {    // pair j: elements 2j, 2j + 1 of the 16; a piece is turned whole
+                        if (4 * l + 32 * (j >> 2) >= a.n_pairs) continue;
+                        float& u = x[j >> 2][2 * (j & 3)];
+                        float& z = x[j >> 2][2 * (j & 3) + 1];
+                        const float p = u * cs[j] - z * sn[j];
+                        z = z * cs[j] + u * sn[j];
+                        u = p;
+                    }
+                } else if (turned) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float u = x[0][j], z = x[1][j];
+                        x[0][j] = u * cs[j] - z * sn[j];
+                        x[1][j] = z * cs[j] + u * sn[j];
+                    }
+                }
+            }
+            if (kv < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.q_out_stride + (size_t)r * kHeadDim);
+                dst[p0] = make_uint4(pack2(x[0][0], x[0][1], TYPE), pack2(x[0][2], x[0][3], TYPE),
+                                     pack2(x[0][4], x[0][5], TYPE), pack2(x[0][6], x[0][7], TYPE));
+                dst[p1] = make_uint4(pack2(x[1][0], x[1][1], TYPE), pack2(x[1][2], x[1][3], TYPE),
+                                     pack2(x[1][4], x[1][5], TYPE), pack2(x[1][6], x[1][7], TYPE));
+            }
+            if (r4 + 3 < a.n_heads || cell_row < 0) continue;   // warp-uniform: query rows only, or no cell
+            // ---- key and value rows: scale = max |x| / 127 rounded up to FP16, so |x / scale| <= 127
+            float amax = 0.f;
+            uint32_t odd = 0u;                       // an infinity or NaN somewhere
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                amax = fmax3(amax, fabsf(x[0][j]), fabsf(x[1][j]));
+                odd |= (fabsf(x[0][j]) <= 3.402823466e38f && fabsf(x[1][j]) <= 3.402823466e38f) ? 0u : 1u;
+            }
+            if (odd) amax = INFINITY;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (kv >= 0 && r < n_rows) {
+                const bool finite = amax < INFINITY;
+                uint16_t sb = __half_as_ushort(__float2half_ru(__fdiv_rn(amax, 127.f)));
+                if (sb > 0x7BFFu) sb = finite ? 0x7BFFu : 0x7FFFu;   // past FP16: the largest finite scale; not finite: NaN
+                uint32_t b[2][2] = {{0u, 0u}, {0u, 0u}};
+                if (finite && sb != 0) quantise16(x, __half2float(__ushort_as_half(sb)), amax, b);
+                const long long row = cell_row + (long long)(is_v ? kv - a.n_kv : kv) * kPage;
+                int8_t* dst = (is_v ? a.v_pool : a.k_pool) + row * kHeadDim;
+                *reinterpret_cast<uint2*>(dst + 8 * p0) = make_uint2(b[0][0], b[0][1]);
+                *reinterpret_cast<uint2*>(dst + 8 * p1) = make_uint2(b[1][0], b[1][1]);
+                if (l == 0) (is_v ? a.v_scale : a.k_scale)[row] = sb;
+            }
+        }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <int TYPE, bool INTERLEAVED>
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // few tokens: as many warps to a token as still fit the GPU together
+    const int rows = a.n_heads + (a.k_pool ? 2 * a.n_kv : 0), wide = sms * kRopeBlocks * kRopeWarps / kRopeWide;
+    if (a.n_tok <= wide && rows > 4 * kRopeWarps)
+        return launch_overlapped(rope_append_kernel<TYPE, INTERLEAVED, kRopeWide>, dim3((unsigned)a.n_tok), 32 * kRopeWide, 0,
+                                 stream, a);
+    const int grid = a.n_tok < sms * kRopeBlocks ? a.n_tok : sms * kRopeBlocks;
+    return launch_overlapped(rope_append_kernel<TYPE, INTERLEAVED, kRopeWarps>, dim3((unsigned)grid), 32 * kRopeWarps, 0, stream,
+                             a);
 }
 
 // Read back: a row's threads take as many elements each as fill a 16-byte store (8, or 4
@@ -253,7 +321,8 @@ cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream) {
-    return launch_overlapped(rope_append_kernel, dim3((unsigned)a.n_tok), kRopeThreads, 0, stream, a);
+    if (a.type == QSA_F16) return a.interleaved ? launch_rope<QSA_F16, true>(a, stream) : launch_rope<QSA_F16, false>(a, stream);
+    return a.interleaved ? launch_rope<QSA_BF16, true>(a, stream) : launch_rope<QSA_BF16, false>(a, stream);
 }
 
 cudaError_t launch_cache_gather(const GatherArgs& a, cudaStream_t stream) {
