@@ -24,12 +24,12 @@
 // instead: a cluster of eight CTAs per item, whose parts are merged through distributed
 // shared memory; one launch, no sum over the lengths, no workspace.
 //
-// A warp has a ring of three 32-cell steps (4 KB of K, 4 KB of V, two 64-byte rows of
+// A warp has a ring of two 32-cell steps (4 KB of K, 4 KB of V, two 64-byte rows of
 // scales), filled by 16-byte asynchronous copies, 512 consecutive bytes an instruction,
 // 16-byte pieces XOR-swizzled by (row & 7) as they land (a bulk copy would leave every
-// row on the same banks, eightfold conflicts for V).  It computes on one step while two
-// are in flight and refills it when it is used: 133 to 200 KB per SM are on the way at
-// any time.  A page's table entry is looked up a page ahead, an item's queries an item
+// row on the same banks, eightfold conflicts for V).  It computes on one step while the
+// other is in flight and refills it when it is used: 67 to 133 KB per SM are on the way
+// at any time (a third step measured 1 to 3 % slower).  A page's table entry is looked up a page ahead, an item's queries an item
 // ahead.
 //
 // The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an
@@ -65,7 +65,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRowsTile = 16;                      // rows of a tile (query heads of one KV head)
 constexpr int kStep = 32;                          // cells of a step
-constexpr int kDepth = 3;                          // steps of a warp's ring
+constexpr int kDepth = 2;                          // steps of a warp's ring
 constexpr int kStepBytes = kStep * kHeadDim;       // of K, and of V
 constexpr int kStepScales = kStep * 2;             // bytes of K scales, and of V scales
 constexpr int kWarpBytes = kDepth * 2 * (kStepBytes + kStepScales);
@@ -176,7 +176,11 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
 // The runs: run i of `runs` begins at page total i / runs, so that any two differ by a
 // page at most, and none is empty (fewer pages than warps: a page to each of the first);
 // and the CTA whose runs hold a page.
-__device__ __forceinline__ int run_begin(int total, int i, int runs) { return (int)((long long)total * min(i, runs) / runs); }
+__device__ __forceinline__ int run_begin(int total, int i, int runs) {
+    i = min(i, runs);                     // total i / runs, in 32 bits: runs^2 < 2^31
+    const int q = total / runs, r = total - q * runs;
+    return q * i + r * i / runs;
+}
 __device__ __forceinline__ int cta_of(int total, int page, int runs) {
     return (int)((((long long)page + 1) * runs - 1) / total) / kWarps;
 }
@@ -582,7 +586,7 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
         int lo = here.q.first - cell0, hi = here.q.n - cell0;   // the item's cells, from the step's first one
 #pragma unroll 1
         for (int step = 0; step < n * (kPage / kStep); ++step) {
-            copies_wait<kDepth - 1>();    // one group a step: all but the youngest two have landed
+            copies_wait<kDepth - 1>();    // one group a step: all but the youngest ones have landed
             __syncwarp();
             if (((f.resident >> slot) & 1u) && hi > 0 && lo < kStep) step32(s, query, kmul, c, slot, lo, hi, lane);
             __syncwarp();                 // every lane has read the step
