@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 // CTA merges its warps' parts into one, then CTA r of the cluster joins all eight CTAs'
 // rows r and r + 8.
 constexpr int kCluster = 8;
-constexpr int kSmallItems = 38, kSmallPages = 128;   // taken up to here: see launch_paged_attn
+constexpr int kSmallItems = 38;           // 304 CTAs: all at once
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
 paged_small_kernel(const __grid_constant__ PagedArgs a) {
@@ -1034,7 +1034,11 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     const int group = a.n_heads / a.n_kv, rows = group < kRowsTile ? group : kRowsTile;
     const long long items = (long long)a.n_seq * a.n_kv * ((group + kRowsTile - 1) / kRowsTile);
     cudaError_t e;
-    if (items <= kSmallItems && a.n_lpages <= kSmallPages) {
+    // A cluster per item while all of them run at once and an item is not too long for one: tables of up to 64 pages,
+    // and two more for each item that keeps the GPU busy beside it.  Measured, us, cluster against runs and join: 4 items
+    // of 1,024 cells 7.1 / 10.6, of 4,096 9.4 / 11.4, of 8,192 13.5 / 12.6; 32 items of 1,024 7.9 / 12.1, of 8,192 18.7 /
+    // 22.7; 64 items (two waves) of 256 14.6 / 9.3.
+    if (items <= kSmallItems && a.n_lpages <= 64 + 2 * items) {
         e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kSmem, stream, a);
