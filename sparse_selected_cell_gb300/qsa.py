@@ -274,62 +274,98 @@ def decode_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, sel, sel_count
 
 # ---------------------------------------------------------------- serving a cache
 # The operators around the paged cache (include/qsa.h, "Serving a cache").  Single
-# tokens make these calls short, so the checks below are written out for speed:
-# one device comparison per tensor, raw addresses into ctypes, no wrappers.
+# tokens make these calls short (the kernels take a few microseconds), so each call
+# checks its arguments in one expression and passes raw addresses; only when that
+# fails are they gone through one by one, for the message.
 
 _TYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
-_I32 = torch.int32
+_I8, _I32, _F64, _BF = torch.int8, torch.int32, torch.float64, torch.bfloat16
+_T16 = (torch.bfloat16, torch.float16)
+_OUT = (torch.bfloat16, torch.float16, torch.float32)
+_SCALE = (torch.float16, torch.int16, torch.uint16)
+_current = torch._C._cuda_getDevice                 # torch.cuda.current_device() without its checks
+_raw_stream = torch._C._cuda_getCurrentRawStream    # torch.cuda.current_stream(dev).cuda_stream without the object
 
 
-def _want(t, name: str, dtype, dev, shape=None, contiguous: bool = True) -> int:
-    """The address of t, a tensor of the given dtype (or one of several) on device `dev`."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a tensor on {dev}")
-    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+def _want(t, name: str, dtypes, dev, shape=None, contiguous: bool = True):
+    """Raises what is wrong with t, a tensor of one of the dtypes on device index `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
 
 
-def _here(t, name: str) -> torch.device:
-    """The device of t, which has to be the current one: the library launches there."""
+def _here(t, name: str) -> int:
+    """The device index of t, which has to be the current one: the library launches there."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    dev = t.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
 
-def _raw_stream(stream, dev) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without the object
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _ok(t, dtype, dev, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _status_ptr(dev_status, dev) -> Optional[int]:
-    return None if dev_status is None else _want(dev_status, "dev_status", _I32, dev)
+def _pool_ok(k, v, ks, vs, dev) -> bool:
+    shape, scales = k.shape, ks.shape
+    return (k.dtype is _I8 and v.dtype is _I8 and ks.dtype in _SCALE and vs.dtype in _SCALE and len(shape) == 4
+            and shape[2] == 64 and shape[3] == 128 and v.shape == shape and scales == shape[:3] and vs.shape == scales
+            and k.get_device() == dev and v.get_device() == dev and ks.get_device() == dev and vs.get_device() == dev
+            and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())
 
 
-_SCALE = (torch.float16, torch.int16, torch.uint16)
-
-
-def _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev):
-    """Addresses of the four arrays of a cache, then (n_ppages, n_kv)."""
-    kp = _want(k_pool, "k_pool", torch.int8, dev)
+def _want_pool(k_pool, v_pool, k_scale, v_scale, dev):
+    _want(k_pool, "k_pool", (_I8,), dev)
     shape = k_pool.shape
     if len(shape) != 4 or shape[2] != gen.PAGE_CELLS or shape[3] != gen.HEAD_DIM:
         raise ValueError(f"k_pool must be [n_ppages, n_kv, 64, 128], got {tuple(shape)}")
-    return (kp, _want(v_pool, "v_pool", torch.int8, dev, shape), _want(k_scale, "k_scale", _SCALE, dev, shape[:3]),
-            _want(v_scale, "v_scale", _SCALE, dev, shape[:3]), shape[0], shape[1])
+    _want(v_pool, "v_pool", (_I8,), dev, shape)
+    _want(k_scale, "k_scale", _SCALE, dev, shape[:3])
+    _want(v_scale, "v_scale", _SCALE, dev, shape[:3])
+
+
+def _stream_of(stream, dev) -> int:
+    if stream is None:
+        return _raw_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _status_of(dev_status, dev) -> Optional[int]:
+    if dev_status is None:
+        return None
+    _want(dev_status, "dev_status", (_I32,), dev)
+    return dev_status.data_ptr()
 
 
 def paged_attn_workspace_bytes(n_kv: int, n_heads: int) -> int:
     """Bytes of workspace paged_attn needs for these head counts (whatever the lengths)."""
     return int(lib().qsa_paged_attn_workspace_bytes(int(n_kv), int(n_heads)))
+
+
+def _refuse_paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, out, lse, workspace):
+    dev = _here(q, "q")
+    _want(q, "q", _T16, dev)
+    _want_pool(k_pool, v_pool, k_scale, v_scale, dev)
+    n_kv, shape = k_pool.shape[1], q.shape
+    if len(shape) != 3 or shape[2] != gen.HEAD_DIM or n_kv == 0 or shape[1] == 0 or shape[1] % n_kv:
+        raise ValueError(f"q must be [n_seq, n_heads, 128] with n_heads a multiple of {n_kv}, got {tuple(shape)}")
+    _want(page_tables, "page_tables", (_I32,), dev)
+    if page_tables.dim() != 2 or page_tables.shape[0] != shape[0]:
+        raise ValueError(f"page_tables must be [{shape[0]}, n_lpages], got {tuple(page_tables.shape)}")
+    _want(seq_lens, "seq_lens", (_I32,), dev, shape[:1])
+    if out is not None:
+        _want(out, "out", _OUT, dev, shape)
+    if lse is not None:
+        _want(lse, "lse", (torch.float32,), dev, shape[:2])
+    if workspace is not None:
+        _want(workspace, "workspace", (getattr(workspace, "dtype", None),), dev)
 
 
 def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_scale: Optional[float] = None,
@@ -340,58 +376,87 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
     q BF16 or FP16 [n_seq, n_heads, 128], page_tables int32 [n_seq, n_lpages], seq_lens int32 [n_seq] -> out
     [n_seq, n_heads, 128] (float32 unless an `out` of another type is given); lse float32 [n_seq, n_heads] is
     written when given.  A workspace that is not given is allocated here."""
-    dev = _here(q, "q")
-    qp = _want(q, "q", (torch.bfloat16, torch.float16), dev)
-    kp, vp, ksp, vsp, n_ppages, n_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != gen.HEAD_DIM or n_kv == 0 or shape[1] == 0 or shape[1] % n_kv:
-        raise ValueError(f"q must be [n_seq, n_heads, 128] with n_heads a multiple of {n_kv}, got {tuple(shape)}")
-    n_seq, n_heads = shape[0], shape[1]
-    tp = _want(page_tables, "page_tables", _I32, dev)
-    if page_tables.dim() != 2 or page_tables.shape[0] != n_seq:
-        raise ValueError(f"page_tables must be [{n_seq}, n_lpages], got {tuple(page_tables.shape)}")
-    width = page_tables.shape[1]
-    lp = _want(seq_lens, "seq_lens", _I32, dev, (n_seq,))
+    try:
+        dev, shape, tables, n_kv = q.get_device(), q.shape, page_tables.shape, k_pool.shape[1]
+        good = (dev >= 0 and dev == _current() and q.dtype in _T16 and q.is_contiguous()
+                and _pool_ok(k_pool, v_pool, k_scale, v_scale, dev)
+                and len(shape) == 3 and shape[2] == 128 and shape[1] > 0 and n_kv > 0 and shape[1] % n_kv == 0
+                and page_tables.dtype is _I32 and len(tables) == 2 and tables[0] == shape[0]
+                and page_tables.get_device() == dev and page_tables.is_contiguous()
+                and _ok(seq_lens, _I32, dev, shape[:1])
+                and (out is None or (out.dtype in _OUT and _ok(out, out.dtype, dev, shape)))
+                and (lse is None or _ok(lse, torch.float32, dev, shape[:2]))
+                and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, out, lse, workspace)
+        raise ValueError("paged_attn: arguments do not fit together")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
-    op = _want(out, "out", (torch.float32, torch.bfloat16, torch.float16), dev, shape)
-    sp = None if lse is None else _want(lse, "lse", torch.float32, dev, (n_seq, n_heads))
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(paged_attn_workspace_bytes(n_kv, n_heads), dtype=torch.uint8, device=dev)
-    wp = _want(workspace, "workspace", workspace.dtype, dev)
-    rc = lib().qsa_paged_attn(qp, _TYPE[q.dtype], kp, vp, ksp, vsp, tp, width, width, n_ppages, n_kv, n_heads, lp, n_seq,
-                              min(int(window), 0x7FFFFFFF), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, op,
-                              _TYPE[out.dtype], sp, wp, workspace.nbytes, _status_ptr(dev_status, dev),
-                              _raw_stream(stream, dev))
+        workspace = torch.empty(paged_attn_workspace_bytes(n_kv, shape[1]), dtype=torch.uint8, device=q.device)
+    rc = (_lib or lib()).qsa_paged_attn(
+        q.data_ptr(), _TYPE[q.dtype], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_tables.data_ptr(), tables[1], tables[1], k_pool.shape[0], n_kv, shape[1], seq_lens.data_ptr(), shape[0],
+        min(window, 0x7FFFFFFF), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _TYPE[out.dtype],
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev),
+        _stream_of(stream, dev))
     if rc != QSA_OK:
         raise QsaError("qsa_paged_attn", rc)
     return out
 
 
-def _rows(t, name: str, dtype, dev, n_tok=None, n_heads=None):
-    """Address and token stride of a [n_tok, n_heads, 128] tensor whose tokens may lie apart."""
-    p = _want(t, name, dtype, dev, contiguous=False)
+def _rows_ok(t, dtype, dev, n_tok, n_heads, stride) -> bool:
+    """A [n_tok, n_heads, 128] tensor whose tokens may lie apart (the heads of a token side by side)."""
+    return (t.dtype is dtype and t.shape == (n_tok, n_heads, 128) and t.get_device() == dev
+            and stride[2] == 1 and (stride[1] == 128 or n_heads == 1))
+
+
+def _want_rows(t, name: str, dtypes, dev, n_tok=None, n_heads=None):
+    _want(t, name, dtypes, dev, contiguous=False)
     shape = t.shape
     if len(shape) != 3 or shape[2] != gen.HEAD_DIM or (n_tok is not None and shape[0] != n_tok) or \
             (n_heads is not None and shape[1] != n_heads):
-        raise ValueError(f"{name} must be [{n_tok or 'n_tok'}, {n_heads or 'n_heads'}, 128], got {tuple(shape)}")
+        raise ValueError(f"{name} must be [{'n_tok' if n_tok is None else n_tok}, "
+                         f"{'n_heads' if n_heads is None else n_heads}, 128], got {tuple(shape)}")
     s = t.stride()
     if s[2] != 1 or (s[1] != gen.HEAD_DIM and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
-    return p, s[0] if shape[0] > 1 else shape[1] * gen.HEAD_DIM
 
 
-def _rotation(positions, inv_freq, pair_axis, n_tok, dev):
+def _apart(stride, n_tok, n_heads) -> int:
+    """Elements from one token to the next (a single token's stride says nothing)."""
+    return stride[0] if n_tok > 1 else n_heads * 128
+
+
+def _rotation_ok(positions, inv_freq, pair_axis, n_tok, dev) -> bool:
+    if inv_freq is None:
+        return True
+    at, pairs = positions.shape, inv_freq.shape
+    return (positions.dtype is _I32 and len(at) in (1, 2) and at[-1] == n_tok and positions.get_device() == dev
+            and positions.is_contiguous() and len(pairs) == 1 and _ok(inv_freq, _F64, dev, pairs)
+            and (pair_axis is None or _ok(pair_axis, _I32, dev, pairs)))
+
+
+def _want_rotation(positions, inv_freq, pair_axis, n_tok, dev):
+    if inv_freq is None:
+        return
+    _want(positions, "positions", (_I32,), dev)
+    if positions.dim() not in (1, 2) or positions.shape[-1] != n_tok:
+        raise ValueError(f"positions must be [n_axes, {n_tok}] or [{n_tok}], got {tuple(positions.shape)}")
+    _want(inv_freq, "inv_freq", (_F64,), dev, (inv_freq.numel(),))
+    if pair_axis is not None:
+        _want(pair_axis, "pair_axis", (_I32,), dev, inv_freq.shape)
+
+
+def _rotation(positions, inv_freq, pair_axis, n_tok):
     """(positions, n_axes, pos_stride, inv_freq, pair_axis, n_pairs) of a rotation; inv_freq None: none."""
     if inv_freq is None:
         return None, 0, 0, None, None, 0
-    pp = _want(positions, "positions", _I32, dev)
-    if positions.dim() not in (1, 2) or positions.shape[-1] != n_tok:
-        raise ValueError(f"positions must be [n_axes, {n_tok}] or [{n_tok}], got {tuple(positions.shape)}")
-    n_pairs = inv_freq.numel()
-    fp = _want(inv_freq, "inv_freq", torch.float64, dev, (n_pairs,))
-    ap = None if pair_axis is None else _want(pair_axis, "pair_axis", _I32, dev, (n_pairs,))
-    return pp, positions.shape[0] if positions.dim() == 2 else 1, n_tok, fp, ap, n_pairs
+    at = positions.shape
+    return (positions.data_ptr(), at[0] if len(at) == 2 else 1, n_tok, inv_freq.data_ptr(),
+            None if pair_axis is None else pair_axis.data_ptr(), inv_freq.shape[0])
 
 
 def rope(x, positions, inv_freq, pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -399,17 +464,38 @@ def rope(x, positions, inv_freq, pair_axis: Optional[torch.Tensor] = None, inter
     """Rotary positions with one or several axes (qsa_rope): x BF16 or FP16 [n_tok, n_heads, 128], positions int32
     [n_axes, n_tok] (or [n_tok]), inv_freq float64 [n_pairs], pair_axis int32 [n_pairs] (None: axis 0) -> out (may be x)."""
     dev = _here(x, "x")
-    xp, xs = _rows(x, "x", (torch.bfloat16, torch.float16), dev)
+    _want_rows(x, "x", _T16, dev)
     n_tok, n_heads = x.shape[0], x.shape[1]
-    rot = _rotation(positions, inv_freq, pair_axis, n_tok, dev)
+    _want_rotation(positions, inv_freq, pair_axis, n_tok, dev)
     if out is None:
-        out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=x.dtype, device=dev)
-    op, os_ = _rows(out, "out", x.dtype, dev, n_tok, n_heads)
-    rc = lib().qsa_rope(xp, xs, _TYPE[x.dtype], *rot, bool(interleaved), op, os_, n_heads, n_tok,
-                        _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+        out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=x.dtype, device=x.device)
+    _want_rows(out, "out", (x.dtype,), dev, n_tok, n_heads)
+    rc = lib().qsa_rope(x.data_ptr(), _apart(x.stride(), n_tok, n_heads), _TYPE[x.dtype],
+                        *_rotation(positions, inv_freq, pair_axis, n_tok), bool(interleaved), out.data_ptr(),
+                        _apart(out.stride(), n_tok, n_heads), n_heads, n_tok, _status_of(dev_status, dev),
+                        _stream_of(stream, dev))
     if rc != QSA_OK:
         raise QsaError("qsa_rope", rc)
     return out
+
+
+def _refuse_rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale, v_scale, slots, q_out):
+    dev = _here(k, "k")
+    _want_rows(k, "k", _T16, dev)
+    n_tok, n_kv = k.shape[0], k.shape[1]
+    _want_rows(v, "v", (k.dtype,), dev, n_tok, n_kv)
+    _want_pool(k_pool, v_pool, k_scale, v_scale, dev)
+    if k_pool.shape[1] != n_kv:
+        raise ValueError(f"k has {n_kv} heads, the cache {k_pool.shape[1]}")
+    _want_rotation(positions, inv_freq, pair_axis, n_tok, dev)
+    _want(slots, "slots", (_I32,), dev, (n_tok,))
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return
+    _want_rows(q, "q", (k.dtype,), dev, n_tok)
+    if q_out is not None:
+        _want_rows(q_out, "q_out", (k.dtype,), dev, n_tok, q.shape[1])
 
 
 def rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale, v_scale, slots,
@@ -419,31 +505,54 @@ def rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale
     scales (qsa_rope_append): q [n_tok, n_heads, 128] (None: keys and values only), k and v [n_tok, n_kv, 128], all BF16
     or all FP16, tokens any multiple of 8 elements apart; positions, inv_freq, pair_axis as in rope (inv_freq None: no
     rotation); slots int32 [n_tok], < 0 = not written -> the rotated q (q_out, which may be q)."""
-    dev = _here(k, "k")
-    kp_, ks_ = _rows(k, "k", (torch.bfloat16, torch.float16), dev)
-    n_tok, n_kv, dtype = k.shape[0], k.shape[1], k.dtype
-    vp_, vs_ = _rows(v, "v", dtype, dev, n_tok, n_kv)
-    kp, vp, ksp, vsp, n_ppages, pool_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
-    if pool_kv != n_kv:
-        raise ValueError(f"k has {n_kv} heads, the cache {pool_kv}")
-    rot = _rotation(positions, inv_freq, pair_axis, n_tok, dev)
-    sp = _want(slots, "slots", _I32, dev, (n_tok,))
+    try:
+        dev, dtype, ks, vs = k.get_device(), k.dtype, k.stride(), v.stride()
+        n_tok, n_kv = k.shape[0], k.shape[1]
+        n_heads = 0
+        good = (dev >= 0 and dev == _current() and dtype in _T16 and _rows_ok(k, dtype, dev, n_tok, n_kv, ks)
+                and _rows_ok(v, dtype, dev, n_tok, n_kv, vs) and _pool_ok(k_pool, v_pool, k_scale, v_scale, dev)
+                and k_pool.shape[1] == n_kv and _rotation_ok(positions, inv_freq, pair_axis, n_tok, dev)
+                and _ok(slots, _I32, dev, (n_tok,)))
+        if q is not None:
+            n_heads, qs = q.shape[1], q.stride()
+            good = (good and _rows_ok(q, dtype, dev, n_tok, n_heads, qs)
+                    and (q_out is None or _rows_ok(q_out, dtype, dev, n_tok, n_heads, q_out.stride())))
+        elif q_out is not None:
+            good = False
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale, v_scale, slots, q_out)
+        raise ValueError("rope_append: arguments do not fit together")
     qp = op = None
-    qs = os_ = n_heads = 0
+    qs_ = os_ = 0
     if q is not None:
-        qp, qs = _rows(q, "q", dtype, dev, n_tok)
-        n_heads = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=dtype, device=dev)
-        op, os_ = _rows(q_out, "q_out", dtype, dev, n_tok, n_heads)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rc = lib().qsa_rope_append(qp, qs, kp_, ks_, vp_, vs_, _TYPE[dtype], *rot, bool(interleaved), op, os_, kp, vp, ksp,
-                               vsp, sp, n_ppages, n_heads, n_kv, n_tok, _status_ptr(dev_status, dev),
-                               _raw_stream(stream, dev))
+            q_out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=dtype, device=k.device)
+        qp, op, qs_, os_ = q.data_ptr(), q_out.data_ptr(), _apart(qs, n_tok, n_heads), _apart(q_out.stride(), n_tok, n_heads)
+    rc = (_lib or lib()).qsa_rope_append(
+        qp, qs_, k.data_ptr(), _apart(ks, n_tok, n_kv), v.data_ptr(), _apart(vs, n_tok, n_kv), _TYPE[dtype],
+        *_rotation(positions, inv_freq, pair_axis, n_tok), bool(interleaved), op, os_, k_pool.data_ptr(), v_pool.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), k_pool.shape[0], n_heads, n_kv, n_tok,
+        _status_of(dev_status, dev), _stream_of(stream, dev))
     if rc != QSA_OK:
         raise QsaError("qsa_rope_append", rc)
     return q_out
+
+
+def _refuse_cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype, k_out, v_out):
+    dev = _here(k_pool, "k_pool")
+    _want_pool(k_pool, v_pool, k_scale, v_scale, dev)
+    _want(slots, "slots", (_I32,), dev)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [n_cell], got {tuple(slots.shape)}")
+    shape = (slots.shape[0], k_pool.shape[1], gen.HEAD_DIM)
+    if k_out is not None:
+        _want(k_out, "k_out", _OUT, dev, shape)
+    if v_out is not None:
+        _want(v_out, "v_out", _OUT if k_out is None else (k_out.dtype,), dev, shape)
+    if k_out is None and v_out is None and dtype not in _OUT:
+        raise TypeError(f"dtype {dtype} is none of {_OUT}")
 
 
 def cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype: torch.dtype = torch.bfloat16,
@@ -451,20 +560,26 @@ def cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype: torch.dtype = t
                  dev_status: Optional[torch.Tensor] = None, stream=None):
     """Cells read back as the values they stand for (qsa_cache_gather): slots int32 [n_cell] -> (k, v)
     [n_cell, n_kv, 128] of `dtype`, or of the given outputs' type."""
-    dev = _here(k_pool, "k_pool")
-    kp, vp, ksp, vsp, n_ppages, n_kv = _pool_ptrs(k_pool, v_pool, k_scale, v_scale, dev)
-    sp = _want(slots, "slots", _I32, dev)
-    if slots.dim() != 1:
-        raise ValueError(f"slots must be [n_cell], got {tuple(slots.shape)}")
-    shape = (slots.shape[0], n_kv, gen.HEAD_DIM)
+    try:
+        dev, cells, n_kv = k_pool.get_device(), slots.shape, k_pool.shape[1]
+        shape = (cells[0], n_kv, 128)
+        kind = dtype if k_out is None and v_out is None else v_out.dtype if k_out is None else k_out.dtype
+        good = (dev >= 0 and dev == _current() and _pool_ok(k_pool, v_pool, k_scale, v_scale, dev) and len(cells) == 1
+                and _ok(slots, _I32, dev, cells) and kind in _OUT
+                and (k_out is None or _ok(k_out, kind, dev, shape)) and (v_out is None or _ok(v_out, kind, dev, shape)))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype, k_out, v_out)
+        raise ValueError("cache_gather: arguments do not fit together")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=dev)
+        k_out = torch.empty(shape, dtype=kind, device=k_pool.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=dev)
-    ko = _want(k_out, "k_out", (torch.bfloat16, torch.float16, torch.float32), dev, shape)
-    vo = _want(v_out, "v_out", k_out.dtype, dev, shape)
-    rc = lib().qsa_cache_gather(kp, vp, ksp, vsp, sp, shape[0], n_ppages, n_kv, ko, vo, _TYPE[k_out.dtype],
-                                _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+        v_out = torch.empty(shape, dtype=kind, device=k_pool.device)
+    rc = (_lib or lib()).qsa_cache_gather(
+        k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), shape[0],
+        k_pool.shape[0], n_kv, k_out.data_ptr(), v_out.data_ptr(), _TYPE[kind], _status_of(dev_status, dev),
+        _stream_of(stream, dev))
     if rc != QSA_OK:
         raise QsaError("qsa_cache_gather", rc)
     return k_out, v_out
@@ -480,32 +595,57 @@ class StepTables(NamedTuple):
     free_head: torch.Tensor       # [1] pages of the free list that are taken now
 
 
+def _refuse_extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok, n_ppages, free_head, out):
+    dev = _here(seq_lens, "seq_lens")
+    if seq_lens.dim() != 1:
+        raise ValueError(f"seq_lens must be [n_seq], got {tuple(seq_lens.shape)}")
+    n_seq = seq_lens.shape[0]
+    _want(seq_lens, "seq_lens", (_I32,), dev)
+    _want(new_lens, "new_lens", (_I32,), dev, (n_seq,))
+    _want(page_tables, "page_tables", (_I32,), dev)
+    if page_tables.dim() != 2 or page_tables.shape[0] != n_seq:
+        raise ValueError(f"page_tables must be [{n_seq}, n_lpages], got {tuple(page_tables.shape)}")
+    if not (0 <= n_tok < 1 << 31 and 0 <= n_ppages < 1 << 31):
+        raise ValueError("n_tok and n_ppages must be non-negative 32-bit numbers")
+    _want(free_pages, "free_pages", (_I32,), dev)
+    if free_head is not None:
+        _want(free_head, "free_head", (_I32,), dev, (1,))
+    for t, name, n in zip(out or (), StepTables._fields, (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1)):
+        _want(t, f"out: {name}", (_I32,), dev, (n,))
+
+
 def extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok: int, n_ppages: int,
                   free_head: Optional[torch.Tensor] = None, out=None, dev_status: Optional[torch.Tensor] = None,
                   stream=None) -> StepTables:
     """Page tables extended in place and slots mapped for a step's new tokens (qsa_extend_tables): seq_lens and new_lens
     int32 [n_seq], page_tables int32 [n_seq, n_lpages], free_pages int32 [n_free] of which *free_head are taken, n_tok =
     length of the token arrays (at least the new tokens of all sequences).  `out`: six tensors as in StepTables to reuse."""
-    dev = _here(seq_lens, "seq_lens")
-    n_seq = seq_lens.shape[0]
-    sl, nl = _want(seq_lens, "seq_lens", _I32, dev, (n_seq,)), _want(new_lens, "new_lens", _I32, dev, (n_seq,))
-    tp = _want(page_tables, "page_tables", _I32, dev)
-    if page_tables.dim() != 2 or page_tables.shape[0] != n_seq:
-        raise ValueError(f"page_tables must be [{n_seq}, n_lpages], got {tuple(page_tables.shape)}")
-    width = page_tables.shape[1]
-    if not (0 <= n_tok < 1 << 31 and 0 <= n_ppages < 1 << 31):
-        raise ValueError("n_tok and n_ppages must be non-negative 32-bit numbers")
-    fp = _want(free_pages, "free_pages", _I32, dev)
+    try:
+        dev, lens, tables = seq_lens.get_device(), seq_lens.shape, page_tables.shape
+        n_seq, toks = lens[0], (n_tok,)
+        good = (dev >= 0 and dev == _current() and len(lens) == 1 and _ok(seq_lens, _I32, dev, lens)
+                and _ok(new_lens, _I32, dev, lens) and len(tables) == 2 and tables[0] == n_seq
+                and _ok(page_tables, _I32, dev, tables) and _ok(free_pages, _I32, dev, free_pages.shape)
+                and (free_head is None or _ok(free_head, _I32, dev, (1,)))
+                and 0 <= n_tok < 1 << 31 and 0 <= n_ppages < 1 << 31)
+        if out is not None:
+            slots, positions, token_seq, lens_out, cu, head_out = out
+            good = (good and _ok(slots, _I32, dev, toks) and _ok(positions, _I32, dev, toks)
+                    and _ok(token_seq, _I32, dev, toks) and _ok(lens_out, _I32, dev, lens)
+                    and _ok(cu, _I32, dev, (n_seq + 1,)) and _ok(head_out, _I32, dev, (1,)))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok, n_ppages, free_head, out)
+        raise ValueError("extend_tables: arguments do not fit together")
     if out is None:
-        out = [torch.empty(n, dtype=_I32, device=dev) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1)]
-    slots, positions, token_seq, lens_out, cu, head_out = out
-    rc = lib().qsa_extend_tables(
-        sl, nl, n_seq, tp, width, width, n_ppages, fp, free_pages.numel(),
-        None if free_head is None else _want(free_head, "free_head", _I32, dev, (1,)), n_tok,
-        _want(slots, "slots", _I32, dev, (n_tok,)), _want(positions, "positions", _I32, dev, (n_tok,)),
-        _want(token_seq, "token_seq", _I32, dev, (n_tok,)), _want(lens_out, "seq_lens_out", _I32, dev, (n_seq,)),
-        _want(cu, "cu_tokens", _I32, dev, (n_seq + 1,)), _want(head_out, "free_head_out", _I32, dev, (1,)),
-        _status_ptr(dev_status, dev), _raw_stream(stream, dev))
+        slots, positions, token_seq, lens_out, cu, head_out = (
+            torch.empty(n, dtype=_I32, device=seq_lens.device) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1))
+    rc = (_lib or lib()).qsa_extend_tables(
+        seq_lens.data_ptr(), new_lens.data_ptr(), n_seq, page_tables.data_ptr(), tables[1], tables[1], n_ppages,
+        free_pages.data_ptr(), free_pages.numel(), None if free_head is None else free_head.data_ptr(), n_tok,
+        slots.data_ptr(), positions.data_ptr(), token_seq.data_ptr(), lens_out.data_ptr(), cu.data_ptr(),
+        head_out.data_ptr(), _status_of(dev_status, dev), _stream_of(stream, dev))
     if rc != QSA_OK:
         raise QsaError("qsa_extend_tables", rc)
     return StepTables(slots, positions, token_seq, lens_out, cu, head_out)

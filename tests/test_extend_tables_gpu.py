@@ -108,6 +108,54 @@ def test_lengths_near_the_top_of_int32(qsa):
     assert check(qsa, lens, new, tables, perm, at, 9000, pool) & 256
 
 
+def test_refusals(qsa):
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    good = dict(seq_lens=i(3), new_lens=i(3), page_tables=i(3, 4), free_pages=i(9), n_tok=5, n_ppages=20)
+    out = [i(5), i(5), i(5), i(3), i(4), i(1)]
+    assert qsa.extend_tables(**good, out=out).slots is out[0]
+    for bad in (dict(seq_lens=i(3).cpu()), dict(seq_lens=i(3).long()), dict(new_lens=i(2)), dict(page_tables=i(4, 4)),
+                dict(page_tables=i(12)), dict(page_tables=i(3, 8)[:, ::2]), dict(free_pages=None), dict(free_head=i(2)), dict(n_tok=-1),
+                dict(n_ppages=1 << 31), dict(out=out[:3] + [i(4)] + out[4:]), dict(out=[i(4)] + out[1:])):
+        with pytest.raises((TypeError, ValueError)):
+            qsa.extend_tables(**{**good, **bad})
+    head = i(1)
+    with pytest.raises(qsa.QsaError):                          # the head's place cannot be read and written by one call
+        qsa.extend_tables(**good, free_head=head, out=out[:5] + [head])
+    with pytest.raises(qsa.QsaError):
+        qsa.extend_tables(**good, out=out[:3] + [good["new_lens"]] + out[4:])
+
+
+def test_captured_steps_follow_the_lengths(qsa):
+    """One captured step replayed: lengths, tables and the list's head advance on the device alone."""
+    n_seq, width, pool = 4, 6, 40
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    free = torch.randperm(pool, generator=torch.Generator().manual_seed(2)).int().cuda()
+    lens, new, tables, head = i([0, 63, 64, 130]), i([1, 1, 1, 1]), torch.full((n_seq, width), -1, dtype=torch.int32, device="cuda"), i([6])
+    held = [0, 1, 1, 3]
+    at = 0
+    for s, n in enumerate(held):
+        tables[s, :n] = free[at:at + n]
+        at += n
+    out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (8, 8, 8, n_seq, n_seq + 1, 1)]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    want_lens, want_tables, want_head = lens.cpu().numpy(), tables.cpu().numpy(), 6
+    with torch.cuda.graph(graph, stream=stream):
+        step = qsa.extend_tables(lens, new, tables, free, 8, pool, free_head=head, out=out)
+        lens.copy_(step.seq_lens)
+        head.copy_(step.free_head)
+    for _ in range(70):
+        graph.replay()
+        torch.cuda.synchronize()
+        want_tables, slots, pos, seq, want_lens, cu, want_head, bits = ref.extend_tables(
+            want_lens, [1] * n_seq, want_tables, free.cpu().numpy(), 8, pool, want_head)
+        assert bits == 0
+        assert step.slots.tolist() == slots.tolist() and step.positions.tolist() == pos.tolist()
+        assert lens.tolist() == want_lens.tolist() and head.tolist() == [want_head]
+        assert tables.cpu().numpy().tolist() == want_tables.tolist()
+
+
 def test_serving_steps_run_together(qsa):
     """A prompt step and three decode steps: tables extended, keys and values rotated and written, attention over the
     whole cache, all on one stream without the host reading anything; the output is checked against FP64 attention over
