@@ -252,7 +252,7 @@ struct Fetch {
                 ok = false;
             }
             if (ok) {
-                const long long row = ((long long)entry * a.n_kv + w.hk / c.tiles) * kPage;
+                const long long row = ((long long)entry * a.n_kv + (c.tiles == 1 ? w.hk : w.hk / c.tiles)) * kPage;
                 ksrc = a.k_pool + row * kHeadDim + 16 * lane;
                 vsrc = a.v_pool + row * kHeadDim + 16 * lane;
                 ssrc = (lane < 4 ? a.k_scale : a.v_scale) + row + 8 * (lane & 3);
@@ -525,7 +525,7 @@ __device__ __forceinline__ void convert_q(const RawQuery& raw, int type, Query& 
 
 // Rows of an item: the first one's number in q and out, and how many.
 __device__ __forceinline__ size_t first_row(const PagedArgs& a, const Ctx& c, int seq, int hk, int& rows) {
-    const int h = hk / c.tiles, tile = hk - h * c.tiles;
+    const int h = c.tiles == 1 ? hk : hk / c.tiles, tile = hk - h * c.tiles;
     rows = min(kRowsTile, c.group - kRowsTile * tile);
     return (size_t)seq * a.n_heads + h * c.group + kRowsTile * tile;
 }
@@ -687,35 +687,49 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         const size_t row0 = first_row(a, c, seq, hk, rows);
         Part* to = &ws.cta[blockIdx.x].cta[from_before ? 0 : 1];
         if (!complete && !from_before) rec = Rec{cta_of(total, end - 1, runs), seq, hk, 0};
-        for (int r = warp; r < rows; r += kWarps) {
-            float m[kWarps], l[kWarps], M = -INFINITY;
+        // rows warp, warp + 4, ..: two at a time, all their loads before the first is used
+        for (int r0 = warp; r0 < rows; r0 += 2 * kWarps) {
+            float m[2][kWarps], l[2][kWarps];
+            float4 o[2][kWarps];
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                m[k] = k < n ? part[k]->m[r] : -INFINITY;
-                l[k] = k < n ? part[k]->l[r] : 0.f;
-                M = fmaxf(M, m[k]);
-            }
-            float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                if (k >= n) continue;
-                const float wt = merge_weight(m[k], l[k], M);
-                const float4 o = *reinterpret_cast<const float4*>(&part[k]->o[r][col(r, 4 * lane)]);
-                L += wt * l[k];
-                x0 += wt * o.x;
-                x1 += wt * o.y;
-                x2 += wt * o.z;
-                x3 += wt * o.w;
-            }
-            if (complete) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
-                if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
-            } else {
-                *reinterpret_cast<float4*>(&to->o[r][col(r, 4 * lane)]) = make_float4(x0, x1, x2, x3);
-                if (lane == 0) {
-                    to->m[r] = M;
-                    to->l[r] = L;
+                for (int k = 0; k < kWarps; ++k) {
+                    const int r = r0 + j * kWarps;
+                    m[j][k] = -INFINITY;
+                    l[j][k] = 0.f;
+                    o[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < n && r < rows) {
+                        m[j][k] = part[k]->m[r];
+                        l[j][k] = part[k]->l[r];
+                        o[j][k] = *reinterpret_cast<const float4*>(&part[k]->o[r][col(r, 4 * lane)]);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = r0 + j * kWarps;
+                if (r >= rows) continue;
+                const float M = fmaxf(fmaxf(m[j][0], m[j][1]), fmaxf(m[j][2], m[j][3]));
+                float L = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    const float wt = merge_weight(m[j][k], l[j][k], M);
+                    L += wt * l[j][k];
+                    x0 += wt * o[j][k].x;
+                    x1 += wt * o[j][k].y;
+                    x2 += wt * o[j][k].z;
+                    x3 += wt * o[j][k].w;
+                }
+                if (complete) {
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    store4(a.out, a.out_type, (row0 + r) * kHeadDim + 4 * lane, x0 * inv, x1 * inv, x2 * inv, x3 * inv);
+                    if (lane == 0 && a.lse) a.lse[row0 + r] = lse_of(M, L);
+                } else {
+                    *reinterpret_cast<float4*>(&to->o[r][col(r, 4 * lane)]) = make_float4(x0, x1, x2, x3);
+                    if (lane == 0) {
+                        to->m[r] = M;
+                        to->l[r] = L;
+                    }
                 }
             }
         }
