@@ -247,7 +247,7 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  * natural logarithm, -infinity when no such cell exists.
  *   - q: [n_seq][n_heads][128] of q_type (QSA_BF16 or QSA_F16); out: the same
  *     shape of out_type (QSA_BF16, QSA_F16 or QSA_F32); lse: FP32 [n_seq][n_heads].
- *     n_heads is a multiple of n_kv.
+ *     n_heads is a multiple of n_kv.  out and lse must not overlap an input.
  *   - page_tables: sequence s's table is page_tables[s * pt_stride ...], n_lpages
  *     entries; pt_stride == 0 gives every sequence one shared table, otherwise
  *     pt_stride >= n_lpages.  Entries past the sequence's last cell, and cells
@@ -260,7 +260,7 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *     order: the same call gives the same bits.
  *   - Scores: Q rounded to FP16 after an exact power-of-two scaling of each row
  *     (exact for elements within 2^26 of the row's largest), K as the exact
- *     INT8 integers, FP32 sums.  Weights times V scales are rounded to FP16 once
+ *     INT8 integers, FP32 sums (of q (k + 128), from -128 times the sum of q).  Weights times V scales are rounded to FP16 once
  *     (relative 2^-11; a power of two per row keeps them in FP16's range, and what
  *     is below 2^-32 of the row's largest vanishes), V exact, FP32 sums.
  *   - workspace: device memory of at least qsa_paged_attn_workspace_bytes(n_kv,

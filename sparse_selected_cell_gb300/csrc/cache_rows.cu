@@ -88,7 +88,7 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     const bool turned = INTERLEAVED || 8 * l < a.n_pairs;
     const int p0 = turned ? l : l + a.n_pairs / 8;
     const int p1 = INTERLEAVED || !turned ? l + 8 : l + a.n_pairs / 8;
-    const int n_rows = a.n_heads + (a.k_pool ? 2 * a.n_kv : 0);   // query, key, value rows
+    const int n_rows = a.n_heads + (a.slots ? 2 * a.n_kv : 0);   // query, key, value rows
     constexpr int kTurn = 4 * WARPS;                 // a warp's turns: rows 4 warp .. 4 warp + 3, then kTurn further
     wait_for_stream();
 
@@ -142,7 +142,7 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         if (next < n_tok) pos = __ldg(pos_at + next);
     };
     form(0, blockIdx.x + stride);
-    int cell = a.k_pool ? __ldg(a.slots + blockIdx.x) : -1;
+    int cell = a.slots ? __ldg(a.slots + blockIdx.x) : -1;
 
     int slot = 0, buf = 0;
 #pragma unroll 1
@@ -156,7 +156,7 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
             if (page < a.n_ppages) cell_row = (long long)page * a.n_kv * kPage + (cell & (kPage - 1));
             else if (threadIdx.x == 0) report(a.dev_status, QSA_DEV_BAD_CELL);
         }
-        if (a.k_pool && tok + stride < n_tok) cell = __ldg(a.slots + tok + stride);
+        if (a.slots && tok + stride < n_tok) cell = __ldg(a.slots + tok + stride);
         float cs[8], sn[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -240,7 +240,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // few tokens: as many warps to a token as still fit the GPU together
-    const int rows = a.n_heads + (a.k_pool ? 2 * a.n_kv : 0), wide = sms * kRopeBlocks * kRopeWarps / kRopeWide;
+    const int rows = a.n_heads + (a.slots ? 2 * a.n_kv : 0), wide = sms * kRopeBlocks * kRopeWarps / kRopeWide;
     if (a.n_tok <= wide && rows > 4 * kRopeWarps)
         return launch_overlapped(rope_append_kernel<TYPE, INTERLEAVED, kRopeWide>, dim3((unsigned)a.n_tok), 32 * kRopeWide, 0,
                                  stream, a);
@@ -271,19 +271,20 @@ template <int TYPE>
 __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const __grid_constant__ GatherArgs a) {
     constexpr int kElems = TYPE == QSA_F32 ? 4 : 8, kLanes = kHeadDim / kElems, kRows = kGatherThreads / kLanes;
     const int l = threadIdx.x % kLanes;
-    const long long items = (long long)a.n_cell * a.n_kv;
-    const long long item0 = (long long)blockIdx.x * (kRows * kGatherItems) + threadIdx.x / kLanes;
+    const long long items = (long long)a.n_cell * a.n_kv, block0 = (long long)blockIdx.x * (kRows * kGatherItems);
+    // the block's first item by one wide division, its threads' from there in 32 bits
+    const unsigned cell0 = (unsigned)(block0 / a.n_kv), head0 = (unsigned)(block0 - (long long)cell0 * a.n_kv);
+    const unsigned local = threadIdx.x / kLanes;
     wait_for_stream();
     uint2 k[kGatherItems], v[kGatherItems];
     float ks[kGatherItems], vs[kGatherItems];
 #pragma unroll
     for (int j = 0; j < kGatherItems; ++j) {
-        const long long item = item0 + j * kRows;
         k[j] = v[j] = make_uint2(0u, 0u);
         ks[j] = vs[j] = 0.f;
-        if (item >= items) continue;
-        const int i = (int)(item / a.n_kv), h = (int)(item - (long long)i * a.n_kv);
-        const int slot = __ldg(a.slots + i), page = slot >> 6;
+        if (block0 + local + j * kRows >= items) continue;
+        const unsigned from = head0 + local + j * kRows, more = from / (unsigned)a.n_kv, h = from - more * (unsigned)a.n_kv;
+        const int slot = __ldg(a.slots + cell0 + more), page = slot >> 6;
         if (slot >= 0 && page < a.n_ppages) {
             const long long row = ((long long)page * a.n_kv + h) * kPage + (slot & (kPage - 1));
             if (TYPE == QSA_F32) {
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const __gr
     }
 #pragma unroll
     for (int j = 0; j < kGatherItems; ++j) {
-        const long long item = item0 + j * kRows;
+        const long long item = block0 + local + j * kRows;
         if (item >= items) continue;
         const size_t at = (size_t)item * kHeadDim + kElems * l;
         put_row<TYPE>(a.k_out, at, k[j], ks[j]);

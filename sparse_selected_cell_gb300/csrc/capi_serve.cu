@@ -67,6 +67,7 @@ int qsa_paged_attn(const void* q, int32_t q_type, const int8_t* k_pool, const in
     if (n_heads > kMaxHeads) return QSA_ERR_UNSUPPORTED;
     if (n_seq == 0) return QSA_OK;
     if (!q || !out || !seq_lens || !workspace || (n_lpages > 0 && !page_tables)) return QSA_ERR_ARG;
+    if (out == q) return QSA_ERR_ARG;   // rows are read by several blocks, at any time
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return QSA_ERR_ARG;
     const int rc = check_pool(k_pool, v_pool, k_scale, v_scale, n_ppages, n_kv);
     if (rc != QSA_OK) return rc;

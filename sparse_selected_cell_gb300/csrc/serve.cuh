@@ -87,11 +87,11 @@ struct RopeArgs {
     int n_pairs, interleaved;
     uint16_t* q_out;
     long long q_out_stride;
-    int8_t* k_pool;               // null: nothing is written to a cache
+    int8_t* k_pool;
     int8_t* v_pool;
     uint16_t* k_scale;
     uint16_t* v_scale;
-    const int32_t* slots;
+    const int32_t* slots;         // null: no keys and values, nothing is written to a cache
     int n_ppages, n_heads, n_kv, n_tok;
     int32_t* dev_status;
 };

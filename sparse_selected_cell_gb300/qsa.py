@@ -337,6 +337,17 @@ def _stream_of(stream, dev) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor allocated here for a call on `stream`: on that stream, so that its memory is neither still in use by
+    the current one nor handed out again before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_of(stream, device.index), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _status_of(dev_status, dev) -> Optional[int]:
     if dev_status is None:
         return None
@@ -375,7 +386,7 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
     """One new token per sequence over its whole paged cache, or its last `window` cells (qsa_paged_attn):
     q BF16 or FP16 [n_seq, n_heads, 128], page_tables int32 [n_seq, n_lpages], seq_lens int32 [n_seq] -> out
     [n_seq, n_heads, 128] (float32 unless an `out` of another type is given); lse float32 [n_seq, n_heads] is
-    written when given.  A workspace that is not given is allocated here."""
+    written when given.  A workspace that is not given is allocated here; out must not be q."""
     try:
         dev, shape, tables, n_kv = q.get_device(), q.shape, page_tables.shape, k_pool.shape[1]
         good = (dev >= 0 and dev == _current() and q.dtype in _T16 and q.is_contiguous()
@@ -393,9 +404,9 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
         _refuse_paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, out, lse, workspace)
         raise ValueError("paged_attn: arguments do not fit together")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = _empty(shape, torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(paged_attn_workspace_bytes(n_kv, shape[1]), dtype=torch.uint8, device=q.device)
+        workspace = _empty(paged_attn_workspace_bytes(n_kv, shape[1]), torch.uint8, q.device, stream)
     rc = (_lib or lib()).qsa_paged_attn(
         q.data_ptr(), _TYPE[q.dtype], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_tables.data_ptr(), tables[1], tables[1], k_pool.shape[0], n_kv, shape[1], seq_lens.data_ptr(), shape[0],
@@ -468,7 +479,7 @@ def rope(x, positions, inv_freq, pair_axis: Optional[torch.Tensor] = None, inter
     n_tok, n_heads = x.shape[0], x.shape[1]
     _want_rotation(positions, inv_freq, pair_axis, n_tok, dev)
     if out is None:
-        out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=x.dtype, device=x.device)
+        out = _empty((n_tok, n_heads, gen.HEAD_DIM), x.dtype, x.device, stream)
     _want_rows(out, "out", (x.dtype,), dev, n_tok, n_heads)
     rc = lib().qsa_rope(x.data_ptr(), _apart(x.stride(), n_tok, n_heads), _TYPE[x.dtype],
                         *_rotation(positions, inv_freq, pair_axis, n_tok), bool(interleaved), out.data_ptr(),
@@ -528,7 +539,7 @@ def rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale
     qs_ = os_ = 0
     if q is not None:
         if q_out is None:
-            q_out = torch.empty((n_tok, n_heads, gen.HEAD_DIM), dtype=dtype, device=k.device)
+            q_out = _empty((n_tok, n_heads, gen.HEAD_DIM), dtype, k.device, stream)
         qp, op, qs_, os_ = q.data_ptr(), q_out.data_ptr(), _apart(qs, n_tok, n_heads), _apart(q_out.stride(), n_tok, n_heads)
     rc = (_lib or lib()).qsa_rope_append(
         qp, qs_, k.data_ptr(), _apart(ks, n_tok, n_kv), v.data_ptr(), _apart(vs, n_tok, n_kv), _TYPE[dtype],
@@ -573,9 +584,9 @@ def cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype: torch.dtype = t
         _refuse_cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype, k_out, v_out)
         raise ValueError("cache_gather: arguments do not fit together")
     if k_out is None:
-        k_out = torch.empty(shape, dtype=kind, device=k_pool.device)
+        k_out = _empty(shape, kind, k_pool.device, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=kind, device=k_pool.device)
+        v_out = _empty(shape, kind, k_pool.device, stream)
     rc = (_lib or lib()).qsa_cache_gather(
         k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), shape[0],
         k_pool.shape[0], n_kv, k_out.data_ptr(), v_out.data_ptr(), _TYPE[kind], _status_of(dev_status, dev),
@@ -640,7 +651,7 @@ def extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok: int, n_ppa
         raise ValueError("extend_tables: arguments do not fit together")
     if out is None:
         slots, positions, token_seq, lens_out, cu, head_out = (
-            torch.empty(n, dtype=_I32, device=seq_lens.device) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1))
+            _empty(n, _I32, seq_lens.device, stream) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1))
     rc = (_lib or lib()).qsa_extend_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), n_seq, page_tables.data_ptr(), tables[1], tables[1], n_ppages,
         free_pages.data_ptr(), free_pages.numel(), None if free_head is None else free_head.data_ptr(), n_tok,

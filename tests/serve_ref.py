@@ -18,10 +18,12 @@ def make_cache(n_pages, n_kv, seed, lo=0.01, hi=0.03, device="cpu"):
     return [t.to(device) for t in (k, v, ks, vs)]
 
 
-def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_scale, window=0):
+def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_scale, window=0, bias=0):
     """-> (out, lse, mean |v|, reach, lengths): out and lse in FP64; mean |v| = the softmax-weighted mean of |v| (what a
     relative error of the weights scales with); reach = the largest sum over d of |q_d k_d| * |sm_scale| of a row's cells
-    (what the error of an FP32 score scales with)."""
+    (what the error of an FP32 score scales with); with `bias`, |k_d| is taken larger by that many of its row's scales
+    (for rows of small integers: the kernel sums q (k + 128) from -128 sum(q), so its FP32 roundings are of magnitudes up
+    to sum |q| (|k| + 128) + 128 |sum q|, that is of |k| larger by 256)."""
     n_seq, n_heads, _ = q.shape
     n_kv = k_pool.shape[1]
     group = n_heads // n_kv
@@ -46,7 +48,8 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
             out[s, rows] = p @ v
             mean[s, rows] = p @ v.abs()
             lse[s, rows] = torch.logsumexp(score, -1)
-            reach[s, rows] = (x.abs() @ k.abs().T).amax(-1) * abs(sm_scale)
+            size = k.abs() + bias * k_scale[page, h, c % PAGE].double()[:, None]
+            reach[s, rows] = (x.abs() @ size.T).amax(-1) * abs(sm_scale)
     return out, lse, mean, reach, torch.tensor([int(n) for n in seq_lens], dtype=torch.float64)
 
 

@@ -91,7 +91,8 @@ def step(n_tok, n_heads, n_kv, seed, dtype=torch.bfloat16):
     return qkv, ref.make_cache(pages, n_kv, seed), slots
 
 
-@pytest.mark.parametrize("n_tok,n_heads,n_kv", [(1, 12, 1), (1, 48, 4), (3, 1, 1), (66, 24, 2), (257, 7, 5), (40, 96, 8)])
+@pytest.mark.parametrize("n_tok,n_heads,n_kv", [(1, 12, 1), (1, 48, 4), (3, 1, 1), (66, 24, 2), (257, 7, 5), (40, 96, 8),
+                                                 (2000, 3, 1), (1700, 33, 3)])
 @pytest.mark.parametrize("pairs,axes,interleaved", [(64, 1, False), (64, 3, True), (32, 2, False)])
 def test_append(qsa, n_tok, n_heads, n_kv, pairs, axes, interleaved):
     qkv, cache, slots = step(n_tok, n_heads, n_kv, seed=n_tok)
@@ -179,6 +180,32 @@ def test_gather(qsa, n_cell, n_kv, dtype):
         want = pool[page, :, cell].float() * scale[page, :, cell].float()[..., None]
         want[slots < 0] = 0
         assert got.dtype == dtype and torch.equal(got.cpu(), want.to(dtype))
+
+
+def test_append_to_an_empty_pool(qsa):
+    """No page at all: nothing is written, every slot is reported, the queries are rotated."""
+    qkv, _, _ = step(6, 20, 2, seed=10)
+    d = qkv.cuda()
+    none = [torch.empty((0, 2, 64, 128), dtype=torch.int8, device="cuda")] * 2 + [torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")] * 2
+    pos, inv, axis = cuda(*rotation(6, 64, 1, 100, seed=11))
+    for slot, want in ((3, BAD_CELL), (-1, 0)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = qsa.rope_append(d[:, :20], d[:, 20:22], d[:, 22:], pos, inv, axis, *none, torch.full((6,), slot, dtype=torch.int32, device="cuda"),
+                              dev_status=status)
+        assert int(status.item()) == want
+        ref.check_turned(got, d[:, :20], ref.turned(d[:, :20], pos, inv, axis, False))
+
+
+def test_gather_many_cells(qsa):
+    """More cells than one block takes, an odd number of heads, the last block ragged."""
+    cache = ref.make_cache(40, 3, seed=12)
+    slots = torch.randint(-5, 40 * 64, (2311,), generator=torch.Generator().manual_seed(13)).int()
+    k, v = qsa.cache_gather(*cuda(*cache), slots.cuda(), dtype=torch.float32)
+    page, cell = slots.long().clamp(min=0) // 64, slots.long().clamp(min=0) % 64
+    for got, pool, scale in ((k, cache[0], cache[2]), (v, cache[1], cache[3])):
+        want = pool[page, :, cell].float() * scale[page, :, cell].float()[..., None]
+        want[slots < 0] = 0
+        assert torch.equal(got.cpu(), want)
 
 
 def test_gather_bad_slot_is_reported(qsa):

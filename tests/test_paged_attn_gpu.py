@@ -185,6 +185,17 @@ def test_many_small_weights_beside_a_large_one(qsa):
     ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, lens, SCALE))
 
 
+def test_keys_with_outliers(qsa):
+    """Rows whose scale one large dim sets: all other integers are 0 to 3, as channels with outliers leave them; queries
+    all positive, so that the biased sums are as large as they get."""
+    q, cache, tables, n = make([700, 3000, 64], 2, 12, seed=20)
+    q = q.abs()
+    cache[0][:] = cache[0] % 4
+    cache[0][..., 17] = 127
+    out, lse = run(qsa, q, cache, tables, n)
+    ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE, bias=256))
+
+
 def test_nan_scale_shows_in_its_own_sequence_only(qsa):
     """A key scale that is NaN poisons the rows that read it and no others."""
     q, cache, tables, n = make([500, 500, 300], 2, 12, seed=13)
@@ -264,6 +275,55 @@ def test_cold_caches_and_a_small_call_before(qsa):
         flush.fill_(k)
         qsa.paged_attn(*small)
         assert torch.equal(qsa.paged_attn(*d), first)
+
+
+@pytest.mark.parametrize("lens", [[900, 64, 2000], [40000, 3, 9000]])
+def test_another_stream_with_everything_allocated_here(qsa, lens):
+    """A call on a stream that is not the current one: output and workspace come from that stream's memory, so work that
+    the current stream still has, or starts meanwhile, cannot touch them."""
+    q, cache, tables, n = make(lens, 4, 12, seed=21)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    first = qsa.paged_attn(*d)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for k in range(10):
+        junk = [torch.full((9 << 20,), k, dtype=torch.uint8, device="cuda") for _ in range(3)]   # the current stream is busy
+        outs.append(qsa.paged_attn(*d, stream=side if k % 2 else side.cuda_stream))
+        del junk
+        torch.full((17 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, first)
+
+
+def test_captured_with_copies_and_a_fork(qsa):
+    """A capture in which the calls follow copies, a fork and a join of streams, not only kernels."""
+    q, cache, tables, n = make([9000, 70, 300], 4, 12, seed=22)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    want = qsa.paged_attn(*d)
+    held, out = torch.zeros_like(d[0]), torch.zeros(q.shape, device="cuda")
+    ws = torch.empty(qsa.paged_attn_workspace_bytes(4, 48), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(64 * 3, dtype=torch.int32, device="cuda")
+    k, v = qsa.cache_gather(*d[1:5], slots)
+    k2, v2, side = torch.zeros_like(k), torch.zeros_like(v), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held.copy_(d[0])
+        side.wait_stream(torch.cuda.current_stream())
+        qsa.paged_attn(held, *d[1:], out=out, workspace=ws)
+        with torch.cuda.stream(side):
+            qsa.cache_gather(*d[1:5], slots, k_out=k2, v_out=v2)
+        torch.cuda.current_stream().wait_stream(side)
+        qsa.paged_attn(held, *d[1:], out=out, workspace=ws)
+        held.zero_()
+    for _ in range(3):
+        out.fill_(NAN16)
+        k2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(k2, k) and torch.equal(v2, v) and not held.any()
 
 
 def test_refusals(qsa):

@@ -17,7 +17,7 @@ def lib():
 
 def paged(lib, **kw):
     a = dict(q=FAKE, q_type=0, k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, pt=FAKE, pt_stride=4, n_lpages=4, n_ppages=16, n_kv=2,
-             n_heads=8, lens=FAKE, n_seq=3, window=0, scale=0.1, out=FAKE, out_type=2, lse=None, ws=FAKE,
+             n_heads=8, lens=FAKE, n_seq=3, window=0, scale=0.1, out=ctypes.c_void_p(0x200000), out_type=2, lse=None, ws=FAKE,
              ws_bytes=lib.qsa_paged_attn_workspace_bytes(2, 8), status=None, stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
@@ -28,7 +28,7 @@ def paged(lib, **kw):
                                  dict(n_heads=7), dict(window=-1), dict(q_type=2), dict(q_type=-1), dict(out_type=3),
                                  dict(pt_stride=-1), dict(pt_stride=3), dict(q=None), dict(out=None), dict(lens=None),
                                  dict(ws=None), dict(pt=None), dict(k=None), dict(vs=None), dict(q=ODD), dict(out=ODD),
-                                 dict(k=ODD), dict(vs=ODD), dict(ws=ODD)])
+                                 dict(k=ODD), dict(vs=ODD), dict(ws=ODD), dict(out=FAKE)])
 def test_paged_attn_arguments(lib, bad):
     assert paged(lib, **bad) == ARG
 
