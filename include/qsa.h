@@ -235,7 +235,8 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *     qsa_extend_tables -> qsa_rope_append -> qsa_paged_attn or qsa_decode_attn
  * on one stream, with nothing read back by the host in between.  Here the query
  * heads of a KV head are n_heads / n_kv, any whole number (not only 12).
- * Scale arrays, like pools, must be 16-byte aligned.
+ * Scale arrays, like pools, must be 16-byte aligned; a pool whose rows (n_ppages *
+ * n_kv * 64) exceed 2^31 - 64 is QSA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------ */
 
 /* Attention of one new token per sequence over its whole paged cache: for
@@ -260,15 +261,15 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *     order: the same call gives the same bits.
  *   - Scores: Q rounded to FP16 after an exact power-of-two scaling of each row
  *     (exact for elements within 2^26 of the row's largest), K as the exact
- *     INT8 integers, FP32 sums (of q (k + 128), from -128 times the sum of q).  Weights times V scales are rounded to FP16 once
- *     (relative 2^-11; a power of two per row keeps them in FP16's range, and what
- *     is below 2^-32 of the row's largest vanishes), V exact, FP32 sums.
+ *     INT8 integers, FP32 sums (of q (k + 128), from -128 times the sum of q).
+ *     Weights times V scales are rounded to FP16 once (relative 2^-11; a power of
+ *     two per row keeps them in FP16's range, and what is below 2^-32 of the row's
+ *     largest vanishes), V exact, FP32 sums.
  *   - workspace: device memory of at least qsa_paged_attn_workspace_bytes(n_kv,
  *     n_heads) bytes, 256-byte aligned; its contents need not be set and are
  *     not kept.  Two calls that can overlap on the device need one each.
  *   - QSA_ERR_UNSUPPORTED when n_seq * n_lpages * n_kv * ceil(n_heads / n_kv / 16)
- *     exceeds 2^30 or n_ppages * n_kv * 64 exceeds 2^31 - 64; QSA_ERR_CAPACITY for
- *     too small a workspace.  n_seq == 0 returns QSA_OK with no launch. */
+ *     exceeds 2^30; QSA_ERR_CAPACITY for too small a workspace.  n_seq == 0 returns QSA_OK with no launch. */
 int qsa_paged_attn(const void* q, int32_t q_type, const int8_t* k_pool, const int8_t* v_pool,
                    const uint16_t* k_scale, const uint16_t* v_scale, const int32_t* page_tables,
                    int32_t pt_stride, int32_t n_lpages, int32_t n_ppages, int32_t n_kv, int32_t n_heads,
@@ -296,7 +297,8 @@ size_t qsa_paged_attn_workspace_bytes(int32_t n_kv, int32_t n_heads);
  *     when interleaved; dims from 2 n_pairs on pass through.  The angle is formed
  *     as a 64-bit fixed-point fraction of a turn, so positions far out lose nothing.
  *   - q_out: as q, q_out_stride elements between tokens; the rotated queries,
- *     rounded once.  q_out == q with equal strides is allowed.
+ *     rounded once.  q_out == q with equal strides is allowed; otherwise q_out
+ *     must not overlap an input.
  *   - Rotated keys are quantised from FP32, not rounded to 16 bits before.  A
  *     row's scale is max |x| / 127 rounded up to FP16 (at most 65504), its
  *     integers round(x / scale), ties to even, within [-127, 127].  A row that

@@ -14,8 +14,8 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA
 
 bool type16(int t) { return t == QSA_BF16 || t == QSA_F16; }
 
-// Rows of one pool (n_ppages * n_kv * 64) must stay below 2^31: they are TMA
-// coordinates, and a slot (page * 64 + cell) is an int32.
+// A slot (page * 64 + cell) is an int32; as everywhere in this library, so are the rows
+// of one pool, n_ppages * n_kv * 64.
 bool pool_fits(int32_t n_ppages, int32_t n_kv) {
     return (long long)n_ppages * n_kv <= ((1LL << 31) - 64) / qsa::kPage;
 }

@@ -29,8 +29,8 @@
 // 16-byte pieces XOR-swizzled by (row & 7) as they land (a bulk copy would leave every
 // row on the same banks, eightfold conflicts for V).  It computes on one step while the
 // other is in flight and refills it when it is used: 67 to 133 KB per SM are on the way
-// at any time (a third step measured 1 to 3 % slower).  A page's table entry is looked up a page ahead, an item's queries an item
-// ahead.
+// at any time (a third step measured 1 to 3 % slower).  A page's table entry is looked
+// up a page ahead, an item's queries an item ahead.
 //
 // The tensor work is mma.sync m16n8k16: 16 rows per tile (12 query heads) would fill an
 // eighth of a tcgen05.mma's 128 rows, whose operands would also have to be written back
@@ -147,7 +147,8 @@ __device__ __forceinline__ void store4(void* out, int type, size_t at, float a, 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
-// Weight of a partial state with reference m (log2) and sum l in a merge around M.  m = -inf: nothing was summed (l = 0), or only NaN (l = NaN, which must show).
+// Weight of a partial state with reference m (log2) and sum l in a merge around M.
+// m = -inf: nothing was summed (l = 0), or only NaN (l = NaN, which must show).
 __device__ __forceinline__ float merge_weight(float m, float l, float M) {
     return m == -INFINITY ? l : fast_exp2(m - M);
 }
@@ -958,13 +959,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         }
         const int np = __shfl_sync(0xffffffffu, seq & 1 ? n1 : n0, seq >> 1);
         const int start = before * n_hk + hk * np;
-        if (np == 0) return;
-        total *= n_hk;
-        const int runs = run_count(total, ctas);
-        c0 = cta_of(total, start, runs);
-        last = cta_of(total, start + np - 1, runs);
-        if (last == c0) return;           // all in one CTA: done there
-        wait_for_stream();
+        c0 = last = 0;
+        if (np > 0) {
+            total *= n_hk;
+            const int runs = run_count(total, ctas);
+            c0 = cta_of(total, start, runs);
+            last = cta_of(total, start + np - 1, runs);
+        }
+        wait_for_stream();                // every block: this grid's end has to mean the end of the one before
+        if (last == c0) return;           // no page, or all in one CTA: done there
     } else {
         wait_for_stream();
         c0 = blockIdx.x;

@@ -203,3 +203,39 @@ def test_serving_steps_run_together(qsa):
                 want = torch.stack(held)
                 # half a step of a scale that was rounded up by at most 2^-10, and FP32 rotation
                 assert ((got.double().cpu() - want).abs() <= want.abs().amax(-1, keepdim=True) / 127 * 0.502 + 1e-5).all()
+
+
+def test_a_step_on_another_stream(qsa):
+    """The calls of a step given a stream that is not the current one, with everything they return allocated by them:
+    the same bits as on the current stream, whatever the current stream allocates meanwhile."""
+    n_kv, n_heads, pool, new = 2, 24, 30, [70, 1, 300, 0, 64]
+    g = torch.Generator().manual_seed(7)
+    inv = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).cuda()
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    qkv = torch.randn((sum(new), n_heads + 2 * n_kv, 128), generator=g).bfloat16().cuda()
+    free, lens, add = torch.randperm(pool, generator=g).int().cuda(), i([0] * 5), i(new)
+    last = (torch.tensor(new).cumsum(0) - 1).clamp(min=0).cuda()
+
+    def step(stream):
+        cache = [t.cuda() for t in ref.make_cache(pool, n_kv, seed=8)]
+        tables = torch.full((5, 8), -1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        t = qsa.extend_tables(lens, add, tables, free, len(qkv), pool, stream=stream)
+        torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda")
+        q = qsa.rope_append(qkv[:, :n_heads], qkv[:, n_heads:n_heads + n_kv], qkv[:, n_heads + n_kv:], t.positions, inv,
+                            None, *cache, t.slots, stream=stream)
+        x = qsa.rope(qkv[:, :n_heads], t.positions, inv, stream=stream)
+        torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+        k, v = qsa.cache_gather(*cache, t.slots, stream=stream)
+        torch.cuda.synchronize()
+        held = q[last]
+        torch.cuda.synchronize()
+        out = qsa.paged_attn(held, *cache, tables, t.seq_lens, stream=stream)
+        torch.cuda.synchronize()
+        return [*t, q, x, k, v, out, tables]
+
+    want = step(None)
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream, 0):
+        for got, w in zip(step(stream), want):
+            assert torch.equal(got, w)
+    assert torch.equal(want[6], want[7])                       # queries are turned alike by both calls

@@ -326,6 +326,51 @@ def test_captured_with_copies_and_a_fork(qsa):
         assert torch.equal(out, want) and torch.equal(k2, k) and torch.equal(v2, v) and not held.any()
 
 
+@pytest.mark.parametrize("lens", [[128] * 16, [256] * 16, [0] * 15 + [256], [0] * 16, [64] * 200])
+def test_the_next_call_waits_for_all_of_it(qsa, lens):
+    """Calls whose items are not cut between blocks, so that there is nothing to join: the next call of the stream
+    reads the finished output all the same, eagerly and captured."""
+    q, cache, tables, n = make(lens, 4, 12, seed=23, width=80)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    want = qsa.paged_attn(*d, out=torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"))
+    pos = torch.arange(len(lens), dtype=torch.int32, device="cuda") + 5
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).cuda()
+    turned = qsa.rope(want, pos, freq)
+    outs = [torch.empty_like(want) for _ in range(8)]
+    ys = [torch.empty_like(want) for _ in range(8)]
+    ws = torch.empty(qsa.paged_attn_workspace_bytes(4, 48), dtype=torch.uint8, device="cuda")
+
+    def steps():
+        for out, y in zip(outs, ys):
+            qsa.paged_attn(*d, out=out, workspace=ws)
+            qsa.rope(out, pos, freq, out=y)
+
+    steps()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for run_all in (steps, graph.replay, graph.replay):
+        for t in outs + ys:
+            t.fill_(NAN16)
+        torch.cuda.synchronize()
+        run_all()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, want) for t in outs) and all(torch.equal(t, turned) for t in ys)
+
+
+def test_raw_streams(qsa):
+    """Streams given as plain handles, the default stream's 0 among them."""
+    q, cache, tables, n = make([300, 5000], 4, 12, seed=24)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    want = qsa.paged_attn(*d)
+    torch.cuda.synchronize()
+    for stream in (0, torch.cuda.Stream().cuda_stream, torch.cuda.current_stream()):
+        got = qsa.paged_attn(*d, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_refusals(qsa):
     q, cache, tables, n = make([100], 2, 12, seed=18)
     d = [t.cuda() for t in (q, *cache, tables, n)]
