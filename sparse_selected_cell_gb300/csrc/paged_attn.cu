@@ -69,7 +69,7 @@ constexpr int kDepth = 2;                          // steps of a warp's ring
 constexpr int kStepBytes = kStep * kHeadDim;       // of K, and of V
 constexpr int kStepScales = kStep * 2;             // bytes of K scales, and of V scales
 constexpr int kWarpBytes = kDepth * 2 * (kStepBytes + kStepScales);
-constexpr int kSmem = kWarps * kWarpBytes;
+constexpr int kRings = kWarps * kWarpBytes;
 constexpr int kMaxCtas = 320;                      // two per SM of 152, with room
 constexpr int kPBits = 7;                          // a row's largest |p v_scale| is set to 2^7 .. 2^8 when R moves
 constexpr float kPTop = 32768.f, kSumTop = 0x1p60f;
@@ -82,16 +82,18 @@ struct Part {
 };
 __device__ __forceinline__ int col(int r, int d) { return d ^ ((r & 1) << 4); }
 static_assert(sizeof(Part) <= kDepth * 2 * kStepBytes, "a part fits a warp's ring");
+// Shared memory: the warps' rings, then for each warp the part of an item that its run
+// begins inside and ends.  What a run ends with lies in its ring.
+constexpr int kSmem = kRings + kWarps * (int)sizeof(Part);
 
-// Workspace, per CTA: a record for the join; the parts of items that end inside a
-// warp's run; and the CTA's own two parts (0: of the item its run begins inside, 1: of
-// the item its run ends inside).
+// Workspace, per CTA: a record for the join, and two parts (0: of the item its run
+// begins inside, 1: of the item its run ends inside).
 struct Rec {
     int last;            // last CTA with a part of the item that this CTA begins and does not end; < 0: there is none
     int seq, hk, pad;
 };
 struct CtaSpace {
-    Part warp[kWarps], cta[2];
+    Part cta[2];
 };
 struct Ws {
     Rec* rec;
@@ -215,6 +217,7 @@ struct Walk {
 
 struct Ctx {
     uint8_t* ring;                        // this warp's steps in shared memory, 2 * kStepBytes each
+    Part* ended;                          // this warp's part of an item that ends inside its run
     uint8_t* scales;                      // and their scales, 2 * kStepScales each
     float* cols;                          // this warp's [2][32]: the step's K and V scales as the lanes need them
     int begin, end;                       // this warp's pages
@@ -533,8 +536,8 @@ __device__ __forceinline__ size_t first_row(const PagedArgs& a, const Ctx& c, in
 
 // What a warp leaves for the CTA's merge.
 struct Left {
-    int first;           // its run begins inside an item (seq, hk), and that: 1 = ends in the run (part in the
-    int seq, hk;         // workspace), 2 = goes on behind it, 3 = ends with it (part in the ring); 0: no such item
+    int first;           // its run begins inside an item (seq, hk), and that: 1 = ends in the run (part in
+    int seq, hk;         // `ended`), 2 = goes on behind it, 3 = ends with it (part in the ring); 0: no such item
     int open;            // its run ends inside an item begun in it (part in the ring): that item and its pages' end
     int oseq, ohk, oend;
 };
@@ -543,7 +546,7 @@ struct Left {
 // them stays in the ring.
 template <bool SMALL>
 __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk w, Left& left) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const float kmul = a.sm_scale * kLog2e * 0x1p24f;   // scores come in units of 2^-24
     left = Left{0, w.s, w.hk, 0, 0, 0, 0};
@@ -619,7 +622,7 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
                 __syncwarp();
                 part = reinterpret_cast<Part*>(c.ring);
             } else {
-                part = &workspace_of(a.workspace).cta[blockIdx.x].warp[warp];
+                part = c.ended;
             }
         }
 #pragma unroll
@@ -651,9 +654,13 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
 
 // Merges the parts that the CTA's warps have left, item by item, a row to a warp.  The
 // warps' runs follow one another, so an item's parts are those of consecutive warps.
-__device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, const Left* s_left, uint8_t* rings, int total,
-                                          int runs) {
+__device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, const Left* s_left, const uint8_t* smem,
+                                          int total, int runs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto part_of = [&](int w) {
+        return reinterpret_cast<const Part*>(s_left[w].first == 1 ? smem + kRings + w * sizeof(Part)
+                                                                  : smem + w * kDepth * 2 * kStepBytes);
+    };
     const Ws ws = workspace_of(a.workspace);
     Rec rec{-1, 0, 0, 0};
     for (int w0 = 0, skip_first = 0; w0 < kWarps;) {
@@ -670,17 +677,14 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         const Part* part[kWarps];
         int n = 0, w1 = w0;
         bool closed = false;
-        part[n++] = from_before && x.first == 1 ? &ws.cta[blockIdx.x].warp[w0]
-                                                : reinterpret_cast<const Part*>(rings + w0 * kDepth * 2 * kStepBytes);
+        part[n++] = from_before ? part_of(w0) : reinterpret_cast<const Part*>(smem + w0 * kDepth * 2 * kStepBytes);
         if (from_before && x.first != 2) closed = true;
         while (!closed && w1 + 1 < kWarps && s_left[w1 + 1].first != 0) {
             ++w1;
             closed = s_left[w1].first != 2;
 #pragma unroll
             for (int k = 1; k < kWarps; ++k)
-                if (k == n)
-                    part[k] = s_left[w1].first == 1 ? &ws.cta[blockIdx.x].warp[w1]
-                                                    : reinterpret_cast<const Part*>(rings + w1 * kDepth * 2 * kStepBytes);
+                if (k == n) part[k] = part_of(w1);
             ++n;
         }
         const bool complete = closed && !from_before;
@@ -751,6 +755,7 @@ __device__ __forceinline__ Ctx context(const PagedArgs& a, uint8_t* smem, float*
     Ctx c;
     c.ring = smem + warp * kDepth * 2 * kStepBytes;
     c.scales = smem + kWarps * kDepth * 2 * kStepBytes + warp * kDepth * 2 * kStepScales;
+    c.ended = reinterpret_cast<Part*>(smem + kRings) + warp;
     c.cols = cols;
     c.group = a.n_heads / a.n_kv;
     c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
@@ -1056,9 +1061,9 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     // of 1,024 cells 7.1 / 10.6, of 4,096 9.4 / 11.4, of 8,192 13.5 / 12.6; 32 items of 1,024 7.9 / 12.1, of 8,192 18.7 /
     // 22.7; 64 items (two waves) of 256 14.6 / 9.3.
     if (items <= kSmallItems && a.n_lpages <= 64 + 2 * items) {
-        e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings);
         if (e != cudaSuccess) return e;
-        return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kSmem, stream, a);
+        return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kRings, stream, a);
     }
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);
