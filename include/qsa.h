@@ -268,8 +268,8 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *   - workspace: device memory of at least qsa_paged_attn_workspace_bytes(n_kv,
  *     n_heads) bytes, 256-byte aligned; its contents need not be set and are
  *     not kept.  Two calls that can overlap on the device need one each.
- *   - QSA_ERR_UNSUPPORTED when n_seq * n_lpages * n_kv * ceil(n_heads / n_kv / 16)
- *     exceeds 2^30; QSA_ERR_CAPACITY for too small a workspace.  n_seq == 0 returns QSA_OK with no launch. */
+ *   - QSA_ERR_UNSUPPORTED when n_seq * (n_lpages + 1) * n_kv * ceil(n_heads / n_kv /
+ *     16) exceeds 2^30; QSA_ERR_CAPACITY for too small a workspace.  n_seq == 0 returns QSA_OK with no launch. */
 int qsa_paged_attn(const void* q, int32_t q_type, const int8_t* k_pool, const int8_t* v_pool,
                    const uint16_t* k_scale, const uint16_t* v_scale, const int32_t* page_tables,
                    int32_t pt_stride, int32_t n_lpages, int32_t n_ppages, int32_t n_kv, int32_t n_heads,

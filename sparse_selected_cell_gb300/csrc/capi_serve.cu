@@ -73,8 +73,8 @@ int qsa_paged_attn(const void* q, int32_t q_type, const int8_t* k_pool, const in
     if (rc != QSA_OK) return rc;
     const long long tiles = (n_heads / n_kv + 15) / 16;
     if ((long long)n_lpages * qsa::kPage > (1LL << 31) - 64) return QSA_ERR_UNSUPPORTED;
-    // pages of all (sequence, KV head, row tile) items: the kernel numbers them in int32
-    if ((long long)n_seq * n_lpages > (1LL << 30) / (n_kv * tiles)) return QSA_ERR_UNSUPPORTED;
+    // pages of all (sequence, KV head, row tile) items and a place for each item: the kernel numbers them in int32
+    if (n_lpages > 0 && (long long)n_seq * (n_lpages + 1LL) > (1LL << 30) / (n_kv * tiles)) return QSA_ERR_UNSUPPORTED;
     if (workspace_bytes < qsa::paged_attn_workspace(n_kv, n_heads)) return QSA_ERR_CAPACITY;
     const qsa::PagedArgs a{q, q_type, k_pool, v_pool, k_scale, v_scale, page_tables, pt_stride, n_lpages, n_ppages,
                            n_kv, n_heads, seq_lens, n_seq, window, sm_scale, out, out_type, lse,

@@ -176,20 +176,30 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
     return q;
 }
 
-// The runs: run i of `runs` begins at page total i / runs, so that any two differ by a
-// page at most, and none is empty (fewer pages than warps: a page to each of the first);
-// and the CTA whose runs hold a page.
+// Places are counted with kItemPlaces before every item's first page, which stand for the
+// time that a warp takes from one item to the next.
+constexpr int kItemPlaces = 1;
+__device__ __forceinline__ int places(int np) { return np > 0 ? np + kItemPlaces : 0; }
+
+// The runs: run i of `runs` begins at place total i / runs, so that any two differ by a
+// place at most (a run may hold no page, but not inside an item); and the CTA whose runs
+// hold a place.
 __device__ __forceinline__ int run_begin(int total, int i, int runs) {
     i = min(i, runs);                     // total i / runs, in 32 bits: runs^2 < 2^31
     const int q = total / runs, r = total - q * runs;
     return q * i + r * i / runs;
 }
-__device__ __forceinline__ int cta_of(int total, int page, int runs) {
-    return (int)((((long long)page + 1) * runs - 1) / total) / kWarps;
+__device__ __forceinline__ int cta_of(int total, int place, int runs) {
+    return (int)((((long long)place + 1) * runs - 1) / total) / kWarps;
 }
 __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas * kWarps, total)); }
 
-// A place in the laid-out pages: sequence, item within it, page within the item.
+// Where a run begins: the sequence, the place among its items' places, the sequence's
+// pages and the pages of one KV head's items before it.
+struct Start {
+    int s, place, np, pages;
+};
+// A page on the way: sequence, item within it, page within the item.
 struct Walk {
     int s, hk, off;
     Seq q;
@@ -220,7 +230,7 @@ struct Ctx {
     Part* ended;                          // this warp's part of an item that ends inside its run
     uint8_t* scales;                      // and their scales, 2 * kStepScales each
     float* cols;                          // this warp's [2][32]: the step's K and V scales as the lanes need them
-    int begin, end;                       // this warp's pages
+    int n;                                // this warp's pages
     int n_hk, tiles, group;
 };
 
@@ -241,7 +251,7 @@ struct Fetch {
 
     __device__ __forceinline__ void look(const PagedArgs& a, const Ctx& c, int page) {
         idx = page;
-        if (c.begin + idx >= c.end) return;
+        if (idx >= c.n) return;
         w.advance(a, c.n_hk, idx - at);
         at = idx;
         entry = __ldg(a.page_tables + (size_t)w.s * a.pt_stride + w.q.p0 + w.off);
@@ -250,7 +260,7 @@ struct Fetch {
     __device__ __forceinline__ void put(const PagedArgs& a, const Ctx& c, int slot) {
         const int lane = threadIdx.x & 31;
         if (!second) {                    // a new page
-            ok = c.begin + idx < c.end && entry >= 0;
+            ok = idx < c.n && entry >= 0;
             if (ok && entry >= a.n_ppages) {
                 if (lane == 0) report(a.dev_status, QSA_DEV_BAD_PAGE);
                 ok = false;
@@ -264,7 +274,7 @@ struct Fetch {
             const int cell0 = (w.q.p0 + w.off) * kPage;
             lo = w.q.first - cell0;
             hi = w.q.n - cell0;
-            if (c.begin + idx < c.end) look(a, c, idx + 1);
+            if (idx < c.n) look(a, c, idx + 1);
         }
         second = !second;
         resident = ok ? resident | (1u << slot) : resident & ~(1u << slot);
@@ -538,8 +548,8 @@ __device__ __forceinline__ size_t first_row(const PagedArgs& a, const Ctx& c, in
 struct Left {
     int first;           // its run begins inside an item (seq, hk), and that: 1 = ends in the run (part in
     int seq, hk;         // `ended`), 2 = goes on behind it, 3 = ends with it (part in the ring); 0: no such item
-    int open;            // its run ends inside an item begun in it (part in the ring): that item and its pages' end
-    int oseq, ohk, oend;
+    int open;            // its run ends inside an item begun in it (part in the ring): that item, and how many of its
+    int oseq, ohk, rest; // pages are behind the run
 };
 
 // One warp's pages, from place w on.  SMALL: they are all one item's, and what comes of
@@ -568,15 +578,15 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
     for (int k = 0; k < kDepth; ++k) f.put(a, c, k);
     int slot = 0;                         // where the next step is
 #pragma unroll 1
-    for (int pos = c.begin; pos < c.end;) {
-        const int n = min(w.q.np - w.off, c.end - pos);
+    for (int pos = 0; pos < c.n;) {
+        const int n = min(w.q.np - w.off, c.n - pos);
         Query query;
         convert_q(raw, a.q_type, query);
         // the item after this one: its queries are on their way while this one is worked on
         const Walk here = w;
         const size_t here0 = row0;
         const int here_rows = rows;
-        if (pos + n < c.end) {
+        if (pos + n < c.n) {
             w.next_item(a, c.n_hk);
             row0 = first_row(a, c, w.s, w.hk, rows);
             load_q(a, row0, rows, lane, raw);
@@ -613,11 +623,11 @@ __device__ __forceinline__ void walk_run(const PagedArgs& a, const Ctx& c, Walk 
                 left.open = 1;
                 left.oseq = here.s;
                 left.ohk = here.hk;
-                left.oend = pos - n + here.q.np;
+                left.rest = here.q.np - n;
             } else {
-                left.first = !ends ? 2 : pos < c.end ? 1 : 3;
+                left.first = !ends ? 2 : pos < c.n ? 1 : 3;
             }
-            if (SMALL || pos == c.end) {  // the run is over: its ring is free
+            if (SMALL || pos == c.n) {  // the run is over: its ring is free
                 copies_wait<0>();
                 __syncwarp();
                 part = reinterpret_cast<Part*>(c.ring);
@@ -673,7 +683,7 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
             skip_first = 0;
             continue;
         }
-        const int seq = from_before ? x.seq : x.oseq, hk = from_before ? x.hk : x.ohk, end = x.oend;
+        const int seq = from_before ? x.seq : x.oseq, hk = from_before ? x.hk : x.ohk;
         const Part* part[kWarps];
         int n = 0, w1 = w0;
         bool closed = false;
@@ -691,7 +701,8 @@ __device__ __forceinline__ void merge_cta(const PagedArgs& a, const Ctx& c, cons
         int rows;
         const size_t row0 = first_row(a, c, seq, hk, rows);
         Part* to = &ws.cta[blockIdx.x].cta[from_before ? 0 : 1];
-        if (!complete && !from_before) rec = Rec{cta_of(total, end - 1, runs), seq, hk, 0};
+        if (!complete && !from_before)
+            rec = Rec{cta_of(total, run_begin(total, blockIdx.x * kWarps + w0 + 1, runs) + x.rest - 1, runs), seq, hk, 0};
         // rows warp, warp + 4, ..: two at a time, all their loads before the first is used
         for (int r0 = warp; r0 < rows; r0 += 2 * kWarps) {
             float m[2][kWarps], l[2][kWarps];
@@ -760,7 +771,7 @@ __device__ __forceinline__ Ctx context(const PagedArgs& a, uint8_t* smem, float*
     c.group = a.n_heads / a.n_kv;
     c.tiles = (c.group + kRowsTile - 1) / kRowsTile;
     c.n_hk = a.n_kv * c.tiles;
-    c.begin = c.end = 0;
+    c.n = 0;
     return c;
 }
 
@@ -787,7 +798,8 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& before) {
 
 __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ int s_warp[kWarps], s_start[kWarps][2];
+    __shared__ int s_warp[2][kWarps];
+    __shared__ Start s_start[kWarps + 1];
     __shared__ Left s_left[kWarps];
     __shared__ __align__(16) float s_cols[kWarps][2 * kStep];
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -799,34 +811,49 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     // ---- the warps' runs of the pages of all items
     const int per = (a.n_seq + kThreads - 1) / kThreads;   // consecutive sequences per thread
     const int s_lo = min(tid * per, a.n_seq), s_hi = min(s_lo + per, a.n_seq);
-    int sum = 0, before;
-    for (int s = s_lo; s < s_hi; ++s) sum += seq_of(a, s, blockIdx.x == 0).np;
-    const int total = block_scan(sum, s_warp, before) * c.n_hk;   // at most 2^30, checked on the host
-    const int runs = run_count(total, (int)gridDim.x);
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        // the one thread whose sequences hold warp k's first page
-        const int first = run_begin(total, blockIdx.x * kWarps + k, runs);
-        if (first < before * c.n_hk || first >= (before + sum) * c.n_hk) continue;
-        int at = before, s = s_lo;
-        for (;; ++s) {
-            const int np = seq_of(a, s, false).np;
-            if (first < (at + np) * c.n_hk) break;
-            at += np;
-        }
-        s_start[k][0] = s;
-        s_start[k][1] = first - at * c.n_hk;
+    int pages = 0, sum = 0, pages_before, before;
+    for (int s = s_lo; s < s_hi; ++s) {
+        const int np = seq_of(a, s, blockIdx.x == 0).np;
+        pages += np;
+        sum += places(np);
     }
-    c.begin = run_begin(total, blockIdx.x * kWarps + warp, runs);
-    c.end = run_begin(total, blockIdx.x * kWarps + warp + 1, runs);
+    const int all_pages = block_scan(pages, s_warp[0], pages_before);
+    const int total = block_scan(sum, s_warp[1], before) * c.n_hk;   // at most 2^30, checked on the host
+    const int runs = run_count(total, (int)gridDim.x);
+    {
+        int at = before, at_page = pages_before, s = s_lo, np = -1;
+#pragma unroll
+        for (int k = 0; k <= kWarps; ++k) {
+            // the one thread whose sequences hold the place where warp k begins
+            const int first = run_begin(total, blockIdx.x * kWarps + k, runs);
+            if (first >= total && tid == 0) s_start[k] = Start{0, 0, 1, all_pages};
+            if (first < before * c.n_hk || first >= (before + sum) * c.n_hk) continue;
+            for (;;) {
+                if (np < 0) np = seq_of(a, s, false).np;
+                if (first < (at + places(np)) * c.n_hk) break;
+                at += places(np);
+                at_page += np;
+                ++s;
+                np = -1;
+            }
+            s_start[k] = Start{s, first - at * c.n_hk, np, at_page};
+        }
+    }
     __syncthreads();
     Left left{0, 0, 0, 0, 0, 0, 0};
-    if (c.begin < c.end) {
-        Walk w;
-        w.s = s_start[warp][0];
+    Walk w;
+    {
+        // even lanes: where this warp begins, odd ones: where the next does
+        const Start st = s_start[warp + (tid & 1)];
+        const int hk = st.place / places(st.np), off = max(st.place - hk * places(st.np) - kItemPlaces, 0);
+        const int page = st.pages * c.n_hk + hk * st.np + off;
+        c.n = __shfl_sync(0xffffffffu, page, 1) - __shfl_sync(0xffffffffu, page, 0);
+        w.s = __shfl_sync(0xffffffffu, st.s, 0);
+        w.hk = __shfl_sync(0xffffffffu, hk, 0);
+        w.off = __shfl_sync(0xffffffffu, off, 0);
+    }
+    if (c.n > 0) {
         w.q = seq_of(a, w.s, false);
-        w.hk = s_start[warp][1] / w.q.np;
-        w.off = s_start[warp][1] - w.hk * w.q.np;
         walk_run<false>(a, c, w, left);
     }
     if ((tid & 31) == 0) s_left[warp] = left;
@@ -866,11 +893,10 @@ paged_small_kernel(const __grid_constant__ PagedArgs a) {
     w.hk = item - w.s * c.n_hk;
     w.q = seq_of(a, w.s, rank == 0 && tid == 0 && w.hk == 0);
     const int i = rank * kWarps + warp, all = kCluster * kWarps;
-    c.begin = (int)((long long)w.q.np * i / all);
-    c.end = (int)((long long)w.q.np * (i + 1) / all);
-    w.off = c.begin;
+    w.off = (int)((long long)w.q.np * i / all);
+    c.n = (int)((long long)w.q.np * (i + 1) / all) - w.off;
     Left left{0, 0, 0, 0, 0, 0, 0};
-    if (c.begin < c.end) walk_run<true>(a, c, w, left);
+    if (c.n > 0) walk_run<true>(a, c, w, left);
     if (lane == 0) s_has[warp] = left.open;
     int rows;
     const size_t row0 = first_row(a, c, w.s, w.hk, rows);
@@ -956,14 +982,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         // two sequences per lane: at most 64 items
         const int n0 = 2 * lane < a.n_seq ? seq_of(a, 2 * lane, false).np : 0;
         const int n1 = 2 * lane + 1 < a.n_seq ? seq_of(a, 2 * lane + 1, false).np : 0;
-        int before = (2 * lane < seq ? n0 : 0) + (2 * lane + 1 < seq ? n1 : 0), total = n0 + n1;
+        int before = (2 * lane < seq ? places(n0) : 0) + (2 * lane + 1 < seq ? places(n1) : 0);
+        int total = places(n0) + places(n1);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             before += __shfl_xor_sync(0xffffffffu, before, o);
             total += __shfl_xor_sync(0xffffffffu, total, o);
         }
         const int np = __shfl_sync(0xffffffffu, seq & 1 ? n1 : n0, seq >> 1);
-        const int start = before * n_hk + hk * np;
+        const int start = before * n_hk + hk * places(np) + kItemPlaces;   // its first page
         c0 = last = 0;
         if (np > 0) {
             total *= n_hk;
