@@ -1,4 +1,5 @@
-"""Selected-cell (QSA union) prompt attention for GB300 (sm_103a).
+"""Selected-cell (QSA union) prompt attention for GB300 (sm_103a), and the serving
+operators around its paged INT8 cache.
 
 The compute path lives in ``libqsa.so`` (CUDA kernels behind a C ABI); the
 ``qsa`` module is a thin ctypes binding over it and ``gen`` draws the seeded

@@ -20,6 +20,11 @@
 // token's rows are read and written by one block at about the same time because that is
 // what DRAM pages like (a token to a warp, every warp in a page of its own, copied at 5.2
 // of the 6.5 TB/s of a plain copy).
+//
+// Measured (4 KV heads x 12, BF16, calls in a row): 8,192 tokens on three axes, written and
+// read back, 243 MB in 42.8 us, 5.7 TB/s; 40,960 cells of 8 KV heads read back alone, 253
+// MB in 41.8 us, 6.06 TB/s.  Small steps are latency: one token's write and read 8.3 us,
+// 256 tokens' 9.7 us as a replayed graph.
 #include "serve.cuh"
 
 namespace qsa {
