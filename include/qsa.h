@@ -367,6 +367,79 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
                       int32_t* positions, int32_t* token_seq, int32_t* seq_lens_out, int32_t* cu_tokens,
                       int32_t* free_head_out, int32_t* dev_status, void* stream);
 
+/* The same calls with their arguments in one struct, in the order of the
+ * parameters, for callers to whom converting each argument costs more than the call
+ * (interpreters).  Statuses and results are those of the calls; NULL is QSA_ERR_ARG. */
+typedef struct {
+    const void* q;
+    int32_t q_type;
+    const int8_t *k_pool, *v_pool;
+    const uint16_t *k_scale, *v_scale;
+    const int32_t* page_tables;
+    int32_t pt_stride, n_lpages, n_ppages, n_kv, n_heads;
+    const int32_t* seq_lens;
+    int32_t n_seq, window;
+    float sm_scale;
+    void* out;
+    int32_t out_type;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* dev_status;
+    void* stream;
+} qsa_paged_attn_args;
+int qsa_paged_attn_packed(const qsa_paged_attn_args* args);
+
+typedef struct {
+    const void* q;
+    int64_t q_stride;
+    const void* k;
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    int32_t type;
+    const int32_t* positions;
+    int32_t n_axes, pos_stride;
+    const double* inv_freq;
+    const int32_t* pair_axis;
+    int32_t n_pairs, interleaved;
+    void* q_out;
+    int64_t q_out_stride;
+    int8_t *k_pool, *v_pool;
+    uint16_t *k_scale, *v_scale;
+    const int32_t* slots;
+    int32_t n_ppages, n_heads, n_kv, n_tok;
+    int32_t* dev_status;
+    void* stream;
+} qsa_rope_append_args;
+int qsa_rope_append_packed(const qsa_rope_append_args* args);
+
+typedef struct {
+    const int8_t *k_pool, *v_pool;
+    const uint16_t *k_scale, *v_scale;
+    const int32_t* slots;
+    int32_t n_cell, n_ppages, n_kv;
+    void *k_out, *v_out;
+    int32_t out_type;
+    int32_t* dev_status;
+    void* stream;
+} qsa_cache_gather_args;
+int qsa_cache_gather_packed(const qsa_cache_gather_args* args);
+
+typedef struct {
+    const int32_t *seq_lens, *new_lens;
+    int32_t n_seq;
+    int32_t* page_tables;
+    int32_t pt_stride, n_lpages, n_ppages;
+    const int32_t* free_pages;
+    int32_t n_free;
+    const int32_t* free_head;
+    int32_t n_tok;
+    int32_t *slots, *positions, *token_seq, *seq_lens_out, *cu_tokens, *free_head_out, *dev_status;
+    void* stream;
+} qsa_extend_tables_args;
+int qsa_extend_tables_packed(const qsa_extend_tables_args* args);
+
 /* Self-test of the bounded waits (not part of the method: the pages have no
  * counterpart).  Every pipelined kernel here waits on mbarriers with a wall-time
  * limit and, when one runs out, records QSA_DEV_WAIT_TIMEOUT in *dev_status and

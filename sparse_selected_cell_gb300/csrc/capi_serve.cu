@@ -161,4 +161,32 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
     return cuda_status(qsa::launch_extend_tables(a, static_cast<cudaStream_t>(stream)));
 }
 
+int qsa_paged_attn_packed(const qsa_paged_attn_args* a) {
+    if (!a) return QSA_ERR_ARG;
+    return qsa_paged_attn(a->q, a->q_type, a->k_pool, a->v_pool, a->k_scale, a->v_scale, a->page_tables, a->pt_stride,
+                          a->n_lpages, a->n_ppages, a->n_kv, a->n_heads, a->seq_lens, a->n_seq, a->window, a->sm_scale,
+                          a->out, a->out_type, a->lse, a->workspace, a->workspace_bytes, a->dev_status, a->stream);
+}
+
+int qsa_rope_append_packed(const qsa_rope_append_args* a) {
+    if (!a) return QSA_ERR_ARG;
+    return qsa_rope_append(a->q, a->q_stride, a->k, a->k_stride, a->v, a->v_stride, a->type, a->positions, a->n_axes,
+                           a->pos_stride, a->inv_freq, a->pair_axis, a->n_pairs, a->interleaved, a->q_out,
+                           a->q_out_stride, a->k_pool, a->v_pool, a->k_scale, a->v_scale, a->slots, a->n_ppages,
+                           a->n_heads, a->n_kv, a->n_tok, a->dev_status, a->stream);
+}
+
+int qsa_cache_gather_packed(const qsa_cache_gather_args* a) {
+    if (!a) return QSA_ERR_ARG;
+    return qsa_cache_gather(a->k_pool, a->v_pool, a->k_scale, a->v_scale, a->slots, a->n_cell, a->n_ppages, a->n_kv,
+                            a->k_out, a->v_out, a->out_type, a->dev_status, a->stream);
+}
+
+int qsa_extend_tables_packed(const qsa_extend_tables_args* a) {
+    if (!a) return QSA_ERR_ARG;
+    return qsa_extend_tables(a->seq_lens, a->new_lens, a->n_seq, a->page_tables, a->pt_stride, a->n_lpages, a->n_ppages,
+                             a->free_pages, a->n_free, a->free_head, a->n_tok, a->slots, a->positions, a->token_seq,
+                             a->seq_lens_out, a->cu_tokens, a->free_head_out, a->dev_status, a->stream);
+}
+
 }  // extern "C"

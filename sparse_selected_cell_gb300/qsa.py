@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -26,6 +27,11 @@ BF16, F16, F32 = 0, 1, 2          # element types (QSA_BF16, QSA_F16, QSA_F32)
 
 _lib = None
 _P, _I, _F, _S, _L = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+# The argument structs of the packed calls: one conversion of all arguments (0.3 us) instead of one each (2 to 3 us).
+_PAGED_ARGS = struct.Struct("PiPPPPPiiiiiPiifPiPPNPP").pack
+_APPEND_ARGS = struct.Struct("PqPqPqiPiiPPiiPqPPPPPiiiiPP").pack
+_GATHER_ARGS = struct.Struct("PPPPPiiiPPiPP").pack
+_TABLES_ARGS = struct.Struct("PPiPiiiPiPiPPPPPPPP").pack
 
 
 class QsaError(RuntimeError):
@@ -78,6 +84,9 @@ def lib():
         L.qsa_cache_gather.restype = ctypes.c_int
         L.qsa_extend_tables.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]
         L.qsa_extend_tables.restype = ctypes.c_int
+        for f in (L.qsa_paged_attn_packed, L.qsa_rope_append_packed, L.qsa_cache_gather_packed, L.qsa_extend_tables_packed):
+            f.argtypes = [ctypes.c_char_p]
+            f.restype = ctypes.c_int
         L.qsa_wait_selftest.argtypes = [_I, _P, _P]
         L.qsa_wait_selftest.restype = ctypes.c_int
         _lib = L
@@ -348,9 +357,9 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _status_of(dev_status, dev) -> Optional[int]:
+def _status_of(dev_status, dev) -> int:
     if dev_status is None:
-        return None
+        return 0
     _want(dev_status, "dev_status", (_I32,), dev)
     return dev_status.data_ptr()
 
@@ -407,12 +416,12 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
         out = _empty(shape, torch.float32, q.device, stream)
     if workspace is None:
         workspace = _empty(paged_attn_workspace_bytes(n_kv, shape[1]), torch.uint8, q.device, stream)
-    rc = (_lib or lib()).qsa_paged_attn(
+    rc = (_lib or lib()).qsa_paged_attn_packed(_PAGED_ARGS(
         q.data_ptr(), _TYPE[q.dtype], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_tables.data_ptr(), tables[1], tables[1], k_pool.shape[0], n_kv, shape[1], seq_lens.data_ptr(), shape[0],
-        min(window, 0x7FFFFFFF), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _TYPE[out.dtype],
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev),
-        _stream_of(stream, dev))
+        max(-1, min(window, 0x7FFFFFFF)), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _TYPE[out.dtype],
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev),
+        _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_paged_attn", rc)
     return out
@@ -464,10 +473,10 @@ def _want_rotation(positions, inv_freq, pair_axis, n_tok, dev):
 def _rotation(positions, inv_freq, pair_axis, n_tok):
     """(positions, n_axes, pos_stride, inv_freq, pair_axis, n_pairs) of a rotation; inv_freq None: none."""
     if inv_freq is None:
-        return None, 0, 0, None, None, 0
+        return 0, 0, 0, 0, 0, 0
     at = positions.shape
     return (positions.data_ptr(), at[0] if len(at) == 2 else 1, n_tok, inv_freq.data_ptr(),
-            None if pair_axis is None else pair_axis.data_ptr(), inv_freq.shape[0])
+            0 if pair_axis is None else pair_axis.data_ptr(), inv_freq.shape[0])
 
 
 def rope(x, positions, inv_freq, pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -535,17 +544,16 @@ def rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale
     if not good:
         _refuse_rope_append(q, k, v, positions, inv_freq, pair_axis, k_pool, v_pool, k_scale, v_scale, slots, q_out)
         raise ValueError("rope_append: arguments do not fit together")
-    qp = op = None
-    qs_ = os_ = 0
+    qp = op = qs_ = os_ = 0
     if q is not None:
         if q_out is None:
             q_out = _empty((n_tok, n_heads, gen.HEAD_DIM), dtype, k.device, stream)
         qp, op, qs_, os_ = q.data_ptr(), q_out.data_ptr(), _apart(qs, n_tok, n_heads), _apart(q_out.stride(), n_tok, n_heads)
-    rc = (_lib or lib()).qsa_rope_append(
+    rc = (_lib or lib()).qsa_rope_append_packed(_APPEND_ARGS(
         qp, qs_, k.data_ptr(), _apart(ks, n_tok, n_kv), v.data_ptr(), _apart(vs, n_tok, n_kv), _TYPE[dtype],
         *_rotation(positions, inv_freq, pair_axis, n_tok), bool(interleaved), op, os_, k_pool.data_ptr(), v_pool.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), k_pool.shape[0], n_heads, n_kv, n_tok,
-        _status_of(dev_status, dev), _stream_of(stream, dev))
+        _status_of(dev_status, dev), _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_rope_append", rc)
     return q_out
@@ -587,10 +595,10 @@ def cache_gather(k_pool, v_pool, k_scale, v_scale, slots, dtype: torch.dtype = t
         k_out = _empty(shape, kind, k_pool.device, stream)
     if v_out is None:
         v_out = _empty(shape, kind, k_pool.device, stream)
-    rc = (_lib or lib()).qsa_cache_gather(
+    rc = (_lib or lib()).qsa_cache_gather_packed(_GATHER_ARGS(
         k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slots.data_ptr(), shape[0],
         k_pool.shape[0], n_kv, k_out.data_ptr(), v_out.data_ptr(), _TYPE[kind], _status_of(dev_status, dev),
-        _stream_of(stream, dev))
+        _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_cache_gather", rc)
     return k_out, v_out
@@ -652,11 +660,11 @@ def extend_tables(seq_lens, new_lens, page_tables, free_pages, n_tok: int, n_ppa
     if out is None:
         slots, positions, token_seq, lens_out, cu, head_out = (
             _empty(n, _I32, seq_lens.device, stream) for n in (n_tok, n_tok, n_tok, n_seq, n_seq + 1, 1))
-    rc = (_lib or lib()).qsa_extend_tables(
+    rc = (_lib or lib()).qsa_extend_tables_packed(_TABLES_ARGS(
         seq_lens.data_ptr(), new_lens.data_ptr(), n_seq, page_tables.data_ptr(), tables[1], tables[1], n_ppages,
-        free_pages.data_ptr(), free_pages.numel(), None if free_head is None else free_head.data_ptr(), n_tok,
+        free_pages.data_ptr(), free_pages.numel(), 0 if free_head is None else free_head.data_ptr(), n_tok,
         slots.data_ptr(), positions.data_ptr(), token_seq.data_ptr(), lens_out.data_ptr(), cu.data_ptr(),
-        head_out.data_ptr(), _status_of(dev_status, dev), _stream_of(stream, dev))
+        head_out.data_ptr(), _status_of(dev_status, dev), _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_extend_tables", rc)
     return StepTables(slots, positions, token_seq, lens_out, cu, head_out)

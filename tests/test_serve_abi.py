@@ -116,3 +116,28 @@ def test_extend_tables_limits(lib):
     assert tables(lib, n_ppages=1 << 25) == UNSUPPORTED
     assert tables(lib, n_tok=(1 << 30) + 1) == UNSUPPORTED
     assert tables(lib, n_lpages=1 << 25, pt_stride=1 << 25) == UNSUPPORTED
+
+
+def test_packed_calls_refuse_alike(lib):
+    """The calls with their arguments in one struct: every field arrives where the call's own parameter is."""
+    from sparse_selected_cell_gb300 import qsa
+
+    class Packed:                                              # the library with the packed calls behind the plain names
+        qsa_paged_attn_workspace_bytes = staticmethod(lib.qsa_paged_attn_workspace_bytes)
+
+    def through(name, pack):
+        def call(*args):
+            return getattr(lib, name)(pack(*[0 if x is None else getattr(x, "value", x) for x in args]))
+        return call
+
+    Packed.qsa_paged_attn = staticmethod(through("qsa_paged_attn_packed", qsa._PAGED_ARGS))
+    Packed.qsa_rope_append = staticmethod(through("qsa_rope_append_packed", qsa._APPEND_ARGS))
+    Packed.qsa_cache_gather = staticmethod(through("qsa_cache_gather_packed", qsa._GATHER_ARGS))
+    Packed.qsa_extend_tables = staticmethod(through("qsa_extend_tables_packed", qsa._TABLES_ARGS))
+    for test in (test_paged_attn_arguments, test_rope_append_arguments, test_gather_arguments, test_extend_tables_arguments):
+        for bad in test.pytestmark[0].args[1]:
+            test(Packed, bad)
+    for test in (test_paged_attn_limits, test_rope_append_limits, test_extend_tables_limits):
+        test(Packed)
+    for name in ("qsa_paged_attn_packed", "qsa_rope_append_packed", "qsa_cache_gather_packed", "qsa_extend_tables_packed"):
+        assert getattr(lib, name)(None) == ARG
