@@ -262,9 +262,10 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *   - Scores: Q rounded to FP16 after an exact power-of-two scaling of each row
  *     (exact for elements within 2^26 of the row's largest), K as the exact
  *     INT8 integers, FP32 sums (of q (k + 128), from -128 times the sum of q).
- *     Weights times V scales are rounded to FP16 once (relative 2^-11; a power of
- *     two per row keeps them in FP16's range, and what is below 2^-32 of the row's
- *     largest vanishes), V exact, FP32 sums.
+ *     Weights times V scales are rounded to FP16 once (relative 2^-11, whatever the
+ *     type of out; a power of two per row keeps them in FP16's range, and what is
+ *     below 2^-32 of the row's largest product, or 2^-78 of its largest weight, loses
+ *     bits), V exact, FP32 sums.
  *   - workspace: device memory of at least qsa_paged_attn_workspace_bytes(n_kv,
  *     n_heads) bytes, 256-byte aligned; its contents need not be set and are
  *     not kept.  Two calls that can overlap on the device need one each.

@@ -58,9 +58,11 @@
 //     score + log2 |v_scale|, less 7 to 15: the product p * v_scale, which enters O += P V
 //     in FP16, then is at most 2^15 and its largest so far at least 2^7, so P keeps
 //     FP16's 11 bits however scores and V scales lie, and what is below 2^-32 of the
-//     largest vanishes (2^20 such cells weigh 2^-12).  R moves, and O and the row sum
-//     with it, only when a product would pass 2^15 (or the sum 2^60, with V scales of
-//     zero): one vote a step.  V goes from the INT8 rows to the B operands by
+//     largest product vanishes (2^20 such cells weigh 2^-12).  Where cells without values (V
+//     scales of zero, or close to it) take nearly all of the weight, R stays 64 below their
+//     scores: p is FP32, and products down to 2^-78 of the largest weight are normal in FP16.
+//     R moves, and O and the row sum with it, only when a product would pass 2^15 (or the
+//     sum 2^76): one vote a step.  V goes from the INT8 rows to the B operands by
 //     ldmatrix.trans on byte pairs.
 #include <cooperative_groups.h>
 
@@ -80,7 +82,10 @@ constexpr int kWarpBytes = kDepth * 2 * (kStepBytes + kStepScales);
 constexpr int kRings = kWarps * kWarpBytes;
 constexpr int kMaxCtas = 320;                      // two per SM of 152, with room
 constexpr int kPBits = 7;                          // a row's largest |p v_scale| is set to 2^7 .. 2^8 when R moves
-constexpr float kPTop = 32768.f, kSumTop = 0x1p60f;
+constexpr int kPMost = 64;                         // and no weight p above 2^64 then, whatever its v_scale is
+// A run's 2^21 steps at most (2^30 pages over the warps) then sum to 2^99; what a change of reference or a merge flushes
+// (factors below 2^-126) is below 2^-27, beside sums of 2^-9 or more.
+constexpr float kPTop = 32768.f, kSumTop = 0x1p76f;
 
 // A part of an item's result: rows relative to their reference m (log2).  The
 // 16-float pieces of odd rows are swapped in pairs (see col()).
@@ -355,9 +360,10 @@ __device__ __forceinline__ void weigh(const float (&sc)[4][4], float (&pv)[4][4]
 }
 
 // A new reference for a row: the largest score mx of the step (log2), and the largest
-// |2^(score - mx) * v_scale|, both over the row.
+// |2^(score - mx) * v_scale|, both over the row.  R never falls, so a step without values
+// (top = 0) must not put it near mx: the products that come later may lie far below.
 __device__ __forceinline__ float new_reference(float r, float mx, float top) {
-    const int e = top > 0.f ? max(f32_exponent(top), -33) : 0;
+    const int e = max(top > 0.f ? f32_exponent(top) : -127, kPBits - kPMost);
     return fmaxf(r, mx + (float)(e - kPBits));
 }
 
