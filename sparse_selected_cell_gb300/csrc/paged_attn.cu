@@ -363,7 +363,7 @@ __device__ __forceinline__ void weigh(const float (&sc)[4][4], float (&pv)[4][4]
 // |2^(score - mx) * v_scale|, both over the row.  R never falls, so a step without values
 // (top = 0) must not put it near mx: the products that come later may lie far below.
 __device__ __forceinline__ float new_reference(float r, float mx, float top) {
-    const int e = max(top > 0.f ? f32_exponent(top) : -127, kPBits - kPMost);
+    const int least = kPBits - kPMost, e = top > 0.f ? max(f32_exponent(top), least) : least;
     return fmaxf(r, mx + (float)(e - kPBits));
 }
 
