@@ -129,25 +129,24 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     const bool has = pair < a.n_pairs;
     const int32_t* pos_at = a.positions;
     unsigned long long f = 0;
-    int pos = 0;
+    int pos = 0, cell = a.slots ? a.slots[blockIdx.x] : -1;
     if (has) {
-        int axis = a.pair_axis ? __ldg(a.pair_axis + pair) : 0;
+        int axis = a.pair_axis ? a.pair_axis[pair] : 0;
+        f = turn_fraction(a.inv_freq[pair]);
         if (axis < 0 || axis >= a.n_axes) {
             report(a.dev_status, QSA_DEV_BAD_AXIS);
             axis = 0;
         }
         pos_at += (size_t)axis * a.pos_stride;
-        f = turn_fraction(__ldg(a.inv_freq + pair));
-        pos = __ldg(pos_at + blockIdx.x);
+        pos = pos_at[blockIdx.x];
     }
     auto form = [&](int buf, unsigned next) {        // the sines of the token that pos is of; then the next one's position
         if (!has) return;
         const int turn = (int)(((unsigned long long)(long long)pos * f) >> 32);   // [-1/2, 1/2) turns, 2^-32 each
         sincospif((float)turn * 0x1p-31f, &s_sin[buf][pair], &s_cos[buf][pair]);
-        if (next < n_tok) pos = __ldg(pos_at + next);
+        if (next < n_tok) pos = pos_at[next];
     };
     form(0, blockIdx.x + stride);
-    int cell = a.slots ? __ldg(a.slots + blockIdx.x) : -1;
 
     int slot = 0, buf = 0;
 #pragma unroll 1
@@ -161,7 +160,7 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
             if (page < a.n_ppages) cell_row = (long long)page * a.n_kv * kPage + (cell & (kPage - 1));
             else if (threadIdx.x == 0) report(a.dev_status, QSA_DEV_BAD_CELL);
         }
-        if (a.slots && tok + stride < n_tok) cell = __ldg(a.slots + tok + stride);
+        if (a.slots && tok + stride < n_tok) cell = a.slots[tok + stride];
         float cs[8], sn[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -289,18 +288,18 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const __gr
         ks[j] = vs[j] = 0.f;
         if (block0 + local + j * kRows >= items) continue;
         const unsigned from = head0 + local + j * kRows, more = from / (unsigned)a.n_kv, h = from - more * (unsigned)a.n_kv;
-        const int slot = __ldg(a.slots + cell0 + more), page = slot >> 6;
+        const int slot = a.slots[cell0 + more], page = slot >> 6;
         if (slot >= 0 && page < a.n_ppages) {
             const long long row = ((long long)page * a.n_kv + h) * kPage + (slot & (kPage - 1));
             if (TYPE == QSA_F32) {
-                k[j].x = __ldg(reinterpret_cast<const uint32_t*>(a.k_pool + row * kHeadDim) + l);
-                v[j].x = __ldg(reinterpret_cast<const uint32_t*>(a.v_pool + row * kHeadDim) + l);
+                k[j].x = reinterpret_cast<const uint32_t*>(a.k_pool + row * kHeadDim)[l];
+                v[j].x = reinterpret_cast<const uint32_t*>(a.v_pool + row * kHeadDim)[l];
             } else {
-                k[j] = __ldg(reinterpret_cast<const uint2*>(a.k_pool + row * kHeadDim) + l);
-                v[j] = __ldg(reinterpret_cast<const uint2*>(a.v_pool + row * kHeadDim) + l);
+                k[j] = reinterpret_cast<const uint2*>(a.k_pool + row * kHeadDim)[l];
+                v[j] = reinterpret_cast<const uint2*>(a.v_pool + row * kHeadDim)[l];
             }
-            ks[j] = __half2float(__ushort_as_half(__ldg(a.k_scale + row)));
-            vs[j] = __half2float(__ushort_as_half(__ldg(a.v_scale + row)));
+            ks[j] = __half2float(__ushort_as_half(a.k_scale[row]));
+            vs[j] = __half2float(__ushort_as_half(a.v_scale[row]));
         } else if (slot >= 0 && l == 0) {
             report(a.dev_status, QSA_DEV_BAD_CELL);
         }

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablesArg
     const unsigned n_tok = (unsigned)a.n_tok;
     wait_for_stream();
     const unsigned lo = blockIdx.x * (unsigned)kTile, hi = min(lo + kTile, n_tok);
-    int head = a.free_head ? __ldg(a.free_head) : 0;
+    int head = a.free_head ? a.free_head[0] : 0;
     if (head < 0 || head > a.n_free) {
         if (blockIdx.x == 0 && tid == 0) report(a.dev_status, QSA_DEV_NO_PAGE);
         head = head < 0 ? 0 : a.n_free;
@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablesArg
             const int s = base + tid * kPer + j;
             old[j] = add[j] = 0;
             if (s < a.n_seq) {
-                old[j] = __ldg(a.seq_lens + s);
-                add[j] = __ldg(a.new_lens + s);
+                old[j] = a.seq_lens[s];
+                add[j] = a.new_lens[s];
             }
         }
 #pragma unroll
@@ -161,39 +161,41 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablesArg
     for (int w = 0; w < 8; ++w)
         if (w < warp) before = max(before, s_max[w]);
     const unsigned total = min(tok0, n_tok);
-    int slot[kPer], pos[kPer], seq[kPer];
+    int slot[kPer], pos[kPer], seq[kPer], page[kPer];
+    bool held[kPer], listed[kPer];         // on a page that the sequence had, or on one that the free list holds
+    int32_t* entry[kPer];                  // where a new page's number goes, from the token on its first cell
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < kPer; ++j) {       // all loads before the first store: entries read are not those written
         const int place = tid * kPer + j;
-        slot[j] = -1;
         pos[j] = 0;
-        seq[j] = -1;
+        seq[j] = page[j] = -1;
+        held[j] = listed[j] = false;
+        entry[j] = nullptr;
         const int m = max(at[j], before);
         if (lo + place >= total || m < 0) continue;
         const Mark mk = s_mark[m];
         pos[j] = mk.pos + (place - m);
         seq[j] = mk.seq;
-        const int lp = pos[j] >> 6;
-        int32_t* entry = a.page_tables + (size_t)mk.seq * a.pt_stride + lp;
-        int page;
-        if (lp < (mk.old + kPage - 1) / kPage) {
-            page = *entry;
-            if (page < 0) report(a.dev_status, QSA_DEV_NO_PAGE);
-            if (page >= a.n_ppages) {
-                report(a.dev_status, QSA_DEV_BAD_PAGE);
-                page = -1;
-            }
-        } else {
-            const int idx = mk.base + lp;
-            page = idx < a.n_free ? __ldg(a.free_pages + idx) : -1;
-            if (idx >= a.n_free) report(a.dev_status, QSA_DEV_NO_PAGE);
-            else if (page < 0 || page >= a.n_ppages) {
-                report(a.dev_status, QSA_DEV_BAD_PAGE);
-                page = -1;
-            }
-            if ((pos[j] & (kPage - 1)) == 0) *entry = page;
+        const int lp = pos[j] >> 6, idx = mk.base + lp;
+        int32_t* at_table = a.page_tables + (size_t)mk.seq * a.pt_stride + lp;
+        held[j] = lp < (mk.old + kPage - 1) / kPage;
+        listed[j] = !held[j] && idx < a.n_free;
+        if (held[j]) page[j] = *at_table;
+        else if (listed[j]) page[j] = a.free_pages[idx];
+        if (!held[j] && (pos[j] & (kPage - 1)) == 0) entry[j] = at_table;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        slot[j] = -1;
+        if (seq[j] < 0) continue;
+        if (held[j] ? page[j] < 0 : !listed[j]) {
+            report(a.dev_status, QSA_DEV_NO_PAGE);
+        } else if (page[j] < 0 || page[j] >= a.n_ppages) {
+            report(a.dev_status, QSA_DEV_BAD_PAGE);
+            page[j] = -1;
         }
-        if (page >= 0) slot[j] = page * kPage + (pos[j] & (kPage - 1));
+        if (entry[j]) *entry[j] = page[j];
+        if (page[j] >= 0) slot[j] = page[j] * kPage + (pos[j] & (kPage - 1));
     }
     const unsigned t0 = lo + tid * kPer;
     if (t0 + kPer <= hi) {

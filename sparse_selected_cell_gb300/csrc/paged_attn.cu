@@ -174,8 +174,7 @@ struct Seq {
     int n, first;    // cells first .. n-1
     int p0, np;      // pages p0 .. p0 + np - 1
 };
-__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
-    int n = __ldg(a.seq_lens + s);
+__device__ __forceinline__ Seq seq_from(const PagedArgs& a, int n, bool tell) {
     const int cap = a.n_lpages * kPage;
     if (n < 0 || n > cap) {
         if (tell) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
@@ -188,6 +187,7 @@ __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) {
     q.np = (n + kPage - 1) / kPage - q.p0;
     return q;
 }
+__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s, bool tell) { return seq_from(a, a.seq_lens[s], tell); }
 
 // Places are counted with kItemPlaces before every item's first page, which stand for the
 // time that a warp takes from one item to the next (64 sequences of 1 to 8,192 cells 59.2
@@ -269,7 +269,7 @@ struct Fetch {
         if (idx >= c.n) return;
         w.advance(a, c.n_hk, idx - at);
         at = idx;
-        entry = __ldg(a.page_tables + (size_t)w.s * a.pt_stride + w.q.p0 + w.off);
+        entry = a.page_tables[(size_t)w.s * a.pt_stride + w.q.p0 + w.off];
     }
     // The next step into slot `slot` of the ring; one group, empty behind the run's end.
     __device__ __forceinline__ void put(const PagedArgs& a, const Ctx& c, int slot) {
@@ -503,9 +503,9 @@ __device__ __forceinline__ void load_q(const PagedArgs& a, size_t row0, int rows
         for (int j = 0; j < 4; ++j) {
             raw.w[half][j] = make_uint4(0u, 0u, 0u, 0u);
             if (g + 8 * half < rows)
-                raw.w[half][j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                      (row0 + g + 8 * half) * kHeadDim + 64 * (j >> 1) +
-                                                                      16 * t + 8 * (j & 1)));
+                raw.w[half][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                 (row0 + g + 8 * half) * kHeadDim + 64 * (j >> 1) + 16 * t +
+                                                                 8 * (j & 1));
         }
 }
 // Largest |x| of packed 16-bit pairs, still packed.
@@ -987,9 +987,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const int n_hk = a.n_kv * tiles;
         seq = blockIdx.x / n_hk;
         hk = blockIdx.x - seq * n_hk;
-        // two sequences per lane: at most 64 items
-        const int n0 = 2 * lane < a.n_seq ? seq_of(a, 2 * lane, false).np : 0;
-        const int n1 = 2 * lane + 1 < a.n_seq ? seq_of(a, 2 * lane + 1, false).np : 0;
+        // two sequences per lane: at most 64 items.  The lengths are final although this is before the wait: the attention
+        // lets this grid start only after its own wait, behind all that came before it, and does not write them.
+        const int n0 = 2 * lane < a.n_seq ? seq_from(a, __ldcg(a.seq_lens + 2 * lane), false).np : 0;
+        const int n1 = 2 * lane + 1 < a.n_seq ? seq_from(a, __ldcg(a.seq_lens + 2 * lane + 1), false).np : 0;
         int before = (2 * lane < seq ? places(n0) : 0) + (2 * lane + 1 < seq ? places(n1) : 0);
         int total = places(n0) + places(n1);
 #pragma unroll

@@ -32,7 +32,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, int type) {
 // These kernels are launched so that their blocks may be set up while the kernel before
 // them in the stream still drains; each waits here, before its first read, until that
 // kernel has finished and its writes are visible.  Whatever was launched before, and
-// whatever follows, sees plain stream order.
+// whatever follows, sees plain stream order.  What they read may be written while they are
+// already resident, so they read it by ordinary loads, which stay behind this wait, and
+// never by non-coherent ones, which are for data that nothing writes in a kernel's lifetime
+// and may be moved.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>
