@@ -292,8 +292,11 @@ _I8, _I32, _F64, _BF = torch.int8, torch.int32, torch.float64, torch.bfloat16
 _T16 = (torch.bfloat16, torch.float16)
 _OUT = (torch.bfloat16, torch.float16, torch.float32)
 _SCALE = (torch.float16, torch.int16, torch.uint16)
-_current = torch._C._cuda_getDevice                 # torch.cuda.current_device() without its checks
-_raw_stream = torch._C._cuda_getCurrentRawStream    # torch.cuda.current_stream(dev).cuda_stream without the object
+# torch.cuda.current_device() without its checks, and torch.cuda.current_stream(dev).cuda_stream without the object, where
+# this torch has them (one built without CUDA has neither, and imports this module all the same)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _want(t, name: str, dtypes, dev, shape=None, contiguous: bool = True):
