@@ -882,7 +882,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 // CTA merges its warps' parts into one, then CTA r of the cluster joins all eight CTAs'
 // rows r and r + 8.
 constexpr int kCluster = 8;
-constexpr int kSmallItems = 38;           // 304 CTAs: all at once
+// As many clusters as run at once: two CTAs per SM, but a cluster stays within one of the GPU's processing clusters, and 152
+// SMs of them hold between 32 (each a cluster short of 2 n / 8) and 38; beyond 32 the occupancy query says (0.8 us).
+constexpr int kSmallItems = 38, kSmallSure = 32;
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
 paged_small_kernel(const __grid_constant__ PagedArgs a) {
@@ -1092,14 +1094,25 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     const int group = a.n_heads / a.n_kv, rows = group < kRowsTile ? group : kRowsTile;
     const long long items = (long long)a.n_seq * a.n_kv * ((group + kRowsTile - 1) / kRowsTile);
     cudaError_t e;
-    // A cluster per item while all of them run at once and an item is not too long for one: tables of up to 64 pages,
-    // and two more for each item that keeps the GPU busy beside it.  Measured, us, cluster against runs and join: 4 items
-    // of 1,024 cells 7.1 / 10.6, of 4,096 9.4 / 11.4, of 8,192 13.5 / 12.6; 32 items of 1,024 7.9 / 12.1, of 8,192 18.7 /
-    // 22.7; 64 items (two waves) of 256 14.6 / 9.3.
+    // A cluster per item while all of them run at once and tables are not too wide: up to 64 pages, and two more for each
+    // item that keeps the GPU busy beside it.  The width stands for the lengths, which only the device knows: a short
+    // sequence under a wide table takes the runs (1 x 1,021 cells, 4 KV heads: 7.0 us under 16 entries, 11.5 under 512).
+    // Measured, us, cluster against runs and join: 4 items of 1,024 cells 7.1 / 10.6, of 4,096 9.4 / 11.4, of 8,192 13.5 /
+    // 12.6; 32 items of 1,024 7.9 / 12.1, of 8,192 16.5 / 20.4; 36 items (the most at once here) of 1,021 8.1 / 12.4, of
+    // 4,096 11.6 / 16.2; 37 items (two waves) of 1,021 13.2 / 11.8; 38 of 4,096 19.6 / 17.0.
     if (items <= kSmallItems && a.n_lpages <= 64 + 2 * items) {
         e = cudaFuncSetAttribute(paged_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRings);
+        int at_once = kSmallSure;
+        if (e == cudaSuccess && items > kSmallSure) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)items * kCluster);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kRings;
+            e = cudaOccupancyMaxActiveClusters(&at_once, paged_small_kernel, &cfg);
+        }
         if (e != cudaSuccess) return e;
-        return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kRings, stream, a);
+        if (items <= at_once)
+            return launch_overlapped(paged_small_kernel, dim3((unsigned)items * kCluster), kThreads, kRings, stream, a);
     }
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);

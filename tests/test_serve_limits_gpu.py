@@ -2,8 +2,9 @@
 import pytest
 
 torch = pytest.importorskip("torch")
+import serve_ref as ref  # noqa: E402
 from test_cache_rows_gpu import cuda, rotation, step  # noqa: E402
-from test_paged_attn_gpu import qsa  # noqa: E402, F401
+from test_paged_attn_gpu import SCALE, make, qsa, run  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +24,19 @@ def test_write_of_so_many_tokens_is_that_of_each_alone(qsa, n_tok):  # noqa: F81
 
     for got, want in zip(write([(0, n_tok)]), write([(k, min(k + 100, n_tok)) for k in range(0, n_tok, 100)])):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("items", [1, 31, 32, 33, 35, 36, 37, 38, 39, 40, 64, 65])
+def test_attention_with_so_many_items(qsa, items):  # noqa: F811
+    """One KV head, so an item a sequence: clusters, runs with few items and with many."""
+    q, cache, tables, n = make([(997 * k) % 700 for k in range(1, items + 1)], 1, 12, seed=items)
+    out, lse = run(qsa, q, cache, tables, n)
+    ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE))
+
+
+@pytest.mark.parametrize("width", [65, 66, 67, 128, 512])
+def test_attention_under_tables_of_any_width(qsa, width):  # noqa: F811
+    """Tables wider than the sequences: one item takes clusters up to 66 pages, and runs from there."""
+    q, cache, tables, n = make([1021], 1, 12, seed=1, width=width)
+    out, lse = run(qsa, q, cache, tables, n)
+    ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE))
