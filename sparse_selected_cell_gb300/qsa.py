@@ -394,11 +394,12 @@ def _refuse_paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_len
 def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_scale: Optional[float] = None,
                window: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
+               stream=None, n_lpages: Optional[int] = None) -> torch.Tensor:
     """One new token per sequence over its whole paged cache, or its last `window` cells (qsa_paged_attn):
-    q BF16 or FP16 [n_seq, n_heads, 128], page_tables int32 [n_seq, n_lpages], seq_lens int32 [n_seq] -> out
+    q BF16 or FP16 [n_seq, n_heads, 128], page_tables int32 [n_seq, width], seq_lens int32 [n_seq] -> out
     [n_seq, n_heads, 128] (float32 unless an `out` of another type is given); lse float32 [n_seq, n_heads] is
-    written when given.  A workspace that is not given is allocated here; out must not be q."""
+    written when given.  The first n_lpages entries of a table's row are in use (None: all); short sequences are
+    fastest when that is no more than they need.  A workspace that is not given is allocated here; out must not be q."""
     try:
         dev, shape, tables, n_kv = q.get_device(), q.shape, page_tables.shape, k_pool.shape[1]
         good = (dev >= 0 and dev == _current() and q.dtype in _T16 and q.is_contiguous()
@@ -421,8 +422,9 @@ def paged_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, seq_lens, sm_sc
         workspace = _empty(paged_attn_workspace_bytes(n_kv, shape[1]), torch.uint8, q.device, stream)
     rc = (_lib or lib()).qsa_paged_attn_packed(_PAGED_ARGS(
         q.data_ptr(), _TYPE[q.dtype], k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        page_tables.data_ptr(), tables[1], tables[1], k_pool.shape[0], n_kv, shape[1], seq_lens.data_ptr(), shape[0],
-        max(-1, min(window, 0x7FFFFFFF)), gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _TYPE[out.dtype],
+        page_tables.data_ptr(), tables[1], tables[1] if n_lpages is None else n_lpages, k_pool.shape[0], n_kv, shape[1],
+        seq_lens.data_ptr(), shape[0], max(-1, min(window, 0x7FFFFFFF)),
+        gen.HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), _TYPE[out.dtype],
         0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev),
         _stream_of(stream, dev)))
     if rc != QSA_OK:

@@ -40,3 +40,19 @@ def test_attention_under_tables_of_any_width(qsa, width):  # noqa: F811
     q, cache, tables, n = make([1021], 1, 12, seed=1, width=width)
     out, lse = run(qsa, q, cache, tables, n)
     ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE))
+
+
+def test_part_of_a_wide_table(qsa):  # noqa: F811
+    """n_lpages below the tables' width: the bits of tables cut to it; longer sequences are clamped to it and reported."""
+    q, cache, tables, n = make([1021, 64, 700], 2, 12, seed=2, width=512)
+    cut = tables[:, :16].contiguous()
+    want = run(qsa, q, cache, cut, n)
+    ref.check_attn(*want, ref.paged_attn(q, *cache, tables, n, SCALE))
+    for got, w in zip(run(qsa, q, cache, tables, n, n_lpages=16), want):
+        assert torch.equal(got, w)
+    for got, w in zip(run(qsa, q, cache, tables, n, n_lpages=11, want_status=64),
+                      run(qsa, q, cache, cut, torch.tensor([11 * 64, 64, 700], dtype=torch.int32))):
+        assert torch.equal(got, w)
+    for bad in (513, -1):
+        with pytest.raises(qsa.QsaError):
+            run(qsa, q, cache, tables, n, n_lpages=bad)
