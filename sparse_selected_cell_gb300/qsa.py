@@ -470,7 +470,9 @@ def _want_rotation(positions, inv_freq, pair_axis, n_tok, dev):
     _want(positions, "positions", (_I32,), dev)
     if positions.dim() not in (1, 2) or positions.shape[-1] != n_tok:
         raise ValueError(f"positions must be [n_axes, {n_tok}] or [{n_tok}], got {tuple(positions.shape)}")
-    _want(inv_freq, "inv_freq", (_F64,), dev, (inv_freq.numel(),))
+    _want(inv_freq, "inv_freq", (_F64,), dev)
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be [n_pairs], got {tuple(inv_freq.shape)}")
     if pair_axis is not None:
         _want(pair_axis, "pair_axis", (_I32,), dev, inv_freq.shape)
 

@@ -1,4 +1,5 @@
-"""Forms of the serving calls beside the usual ones: FP16 rows written, and pools past 2^31 bytes."""
+"""Forms of the serving calls beside the usual ones: FP16 rows written, pools past 2^31 bytes; and every argument that does
+not fit refused with a message of its own."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -101,3 +102,53 @@ def test_pool_past_2_31_bytes(qsa):  # noqa: F811
     for big, t in zip(large, small):
         assert torch.equal(big[far.cuda()], t)
     ref.check_attn(results[0][-1], None, ref.paged_attn(results[0][0][:2].cpu(), *[t.cpu() for t in small], tables, lens.cpu(), SCALE))
+
+
+# ---------------------------------------------------------------- arguments that do not fit
+
+def spoiled(t):
+    """What an argument that has to be the tensor t must not be."""
+    yield "a list", t.tolist()
+    yield "on the host", t.cpu()
+    yield "complex", t.to(torch.complex64)
+    yield "one dim more", t[None]
+    yield "flat", t.reshape(-1) if t.dim() > 1 else t[:, None]
+    yield "strided", torch.stack((t, t), -1)[..., 0]
+    if t.shape[0] > 1:
+        yield "shorter", t[:-1].contiguous()
+    if t.dim() > 1:
+        yield "narrower", t[..., :-1].contiguous()
+
+
+def refused(call, args, names, skip=()):
+    call(**args)                                               # as they are, they fit
+    for name in names:
+        for what, bad in spoiled(args[name]):
+            if (name, what) in skip:
+                continue
+            with pytest.raises((TypeError, ValueError)) as e:
+                call(**{**args, name: bad})
+            assert "do not fit together" not in str(e.value), f"{name}: {what}"
+            assert "must" in str(e.value) or "expected" in str(e.value) or "heads" in str(e.value), f"{name}: {what}: {e.value}"
+
+
+def test_every_refusal_says_what_is_wrong(qsa):  # noqa: F811
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    b = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    k, v, ks, vs = cuda(*ref.make_cache(4, 2, seed=1))
+    pools = dict(k_pool=k, v_pool=v, k_scale=ks, v_scale=vs)
+    attn = dict(q=b(3, 8, 128), **pools, page_tables=i(3, 4), seq_lens=i(3), out=b(3, 8, 128),
+                lse=torch.zeros((3, 8), device="cuda"))
+    refused(qsa.paged_attn, attn, list(attn), skip={("page_tables", "narrower")})
+    freq = torch.ones(64, dtype=torch.float64, device="cuda")
+    turn = dict(positions=i(2, 5), inv_freq=freq, pair_axis=i(64))
+    write = dict(q=b(5, 8, 128), k=b(5, 2, 128), v=b(5, 2, 128), **turn, **pools, slots=i(5) - 1, q_out=b(5, 8, 128))
+    refused(qsa.rope_append, write, list(write), skip={("positions", "shorter")})          # fewer axes
+    refused(qsa.rope, dict(x=b(5, 8, 128), **turn, out=b(5, 8, 128)), ["x", "positions", "inv_freq", "pair_axis", "out"],
+            skip={("positions", "shorter")})
+    read = dict(**pools, slots=i(5), k_out=b(5, 2, 128), v_out=b(5, 2, 128))
+    refused(qsa.cache_gather, read, list(read))
+    tables = dict(seq_lens=i(3), new_lens=i(3), page_tables=i(3, 4) - 1, free_pages=i(9), n_tok=5, n_ppages=4, free_head=i(1))
+    refused(qsa.extend_tables, tables, ["seq_lens", "new_lens", "page_tables", "free_pages", "free_head"],
+            skip={("page_tables", "narrower"), ("free_pages", "shorter"), ("free_pages", "one dim more"), ("free_pages", "flat"),
+                  ("free_head", "strided")})                   # (one element lies as it should whatever its stride)
