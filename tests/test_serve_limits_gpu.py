@@ -34,6 +34,22 @@ def test_attention_with_so_many_items(qsa, items):  # noqa: F811
     ref.check_attn(out, lse, ref.paged_attn(q, *cache, tables, n, SCALE))
 
 
+@pytest.mark.parametrize("items", [32, 33, 36, 37])
+def test_so_many_items_captured(qsa, items):  # noqa: F811
+    """The choice is made while the stream is being captured."""
+    q, cache, tables, n = make([(997 * k) % 700 for k in range(1, items + 1)], 1, 12, seed=items)
+    d = [t.cuda() for t in (q, *cache, tables, n)]
+    want = qsa.paged_attn(*d)
+    out = torch.zeros_like(want)
+    ws = torch.empty(qsa.paged_attn_workspace_bytes(1, 12), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qsa.paged_attn(*d, out=out, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("width", [65, 66, 67, 128, 512])
 def test_attention_under_tables_of_any_width(qsa, width):  # noqa: F811
     """Tables wider than the sequences: one item takes clusters up to 66 pages, and runs from there."""
