@@ -22,9 +22,10 @@
 // of the 6.5 TB/s of a plain copy).
 //
 // Measured (4 KV heads x 12, BF16, calls in a row): 8,192 tokens on three axes, written and
-// read back, 243 MB in 42.8 us, 5.7 TB/s; 40,960 cells of 8 KV heads read back alone, 253
-// MB in 41.8 us, 6.06 TB/s.  Small steps are latency: one token's write and read 8.3 us,
-// 256 tokens' 9.7 us as a replayed graph.
+// read back, 243 MB in 43.4 us, 5.6 TB/s; written alone, 227 MB in 37.7 (interleaved pairs
+// 38.1, FP16 37.9); 40,960 cells of 8 KV heads read back alone, 253 MB in 42.3 us, 6.0 TB/s
+// (FP32 421 MB in 71.9).  Small steps are latency: inside a captured graph one token's write
+// and read take 3.8 us, 256 tokens' 5.7.
 #include "serve.cuh"
 
 namespace qsa {

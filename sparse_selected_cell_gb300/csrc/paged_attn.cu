@@ -33,9 +33,9 @@
 // up a page ahead, an item's queries an item ahead.
 //
 // Measured (12 heads to a KV head, BF16, calls in a row): 96 sequences of 16,000 to
-// 20,000 cells, 4 KV heads, 1.80 GB: 268 us, 6.72 TB/s, the rate of a plain copy; one of
-// 262,149, 8 KV heads, 545 MB: 90 us, 6.0 TB/s; 64 of 1 to 8,192, 4 KV heads, 274 MB: 53
-// us, 5.2 TB/s.  Beside the bytes there are 2 us until the lengths are summed, 3 until the
+// 20,000 cells, 4 KV heads, 1.81 GB: 271 us, 6.69 TB/s, the rate of a plain copy; one of
+// 262,149, 8 KV heads, 545 MB: 90 us, 6.05 TB/s; 64 of 1 to 8,192, 4 KV heads, 316 MB:
+// 60.6 us, 5.2 TB/s.  Beside the bytes there are 2 us until the lengths are summed, 3 until the
 // first rows are there, 4 to 8 in which some runs are over and others not (they hold as
 // many bytes, DRAM does not serve them alike; next pages prefetched into L2 made it 1 to 2
 // % slower), 1 to 3 for the merge and 3 for the join.
