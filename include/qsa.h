@@ -260,7 +260,7 @@ int qsa_decode_attn(const uint16_t* q, const int8_t* k_pool, const int8_t* v_poo
  *   - Only the device knows the lengths; the kernels are chosen by n_seq, the head counts
  *     and n_lpages.  A batch of a few short sequences is fastest when n_lpages is no
  *     larger than they need, whatever the tables' width pt_stride (one sequence of
- *     1,021 cells: 7.0 us with 16, 11.5 with 512).
+ *     1,021 cells: 6.9 us with 16, 11.1 with 512).
  *   - The cache's length is split over the GPU and the parts joined in a fixed
  *     order: the same call gives the same bits.
  *   - Scores: Q rounded to FP16 after an exact power-of-two scaling of each row

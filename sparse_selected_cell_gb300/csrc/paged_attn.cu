@@ -1096,7 +1096,7 @@ cudaError_t launch_paged_attn(const PagedArgs& a, cudaStream_t stream) {
     cudaError_t e;
     // A cluster per item while all of them run at once and tables are not too wide: up to 64 pages, and two more for each
     // item that keeps the GPU busy beside it.  The width stands for the lengths, which only the device knows: a short
-    // sequence under a wide table takes the runs (1 x 1,021 cells, 4 KV heads: 7.0 us under 16 entries, 11.5 under 512).
+    // sequence under a wide table takes the runs (1 x 1,021 cells, 4 KV heads: 6.9 us under 16 entries, 11.1 under 512).
     // Measured, us, cluster against runs and join: 4 items of 1,024 cells 7.1 / 10.6, of 4,096 9.4 / 11.4, of 8,192 13.5 /
     // 12.6; 32 items of 1,024 7.9 / 12.1, of 8,192 16.5 / 20.4; 36 items (the most at once here) of 1,021 8.1 / 12.4, of
     // 4,096 11.6 / 16.2; 37 items (two waves) of 1,021 13.2 / 11.8; 38 of 4,096 19.6 / 17.0.
