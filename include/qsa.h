@@ -74,7 +74,8 @@ enum {
     QSA_DEV_BAD_SEQ_LEN = 64,      /* a length that is negative or longer than its page table (clamped) */
     QSA_DEV_NO_PAGE = 128,         /* the free list ran out, or a token's page is not resident (slot -1) */
     QSA_DEV_TOKEN_OVERFLOW = 256,  /* more new tokens than the token arrays hold (the rest is not mapped) */
-    QSA_DEV_BAD_AXIS = 512         /* a pair's axis outside [0, n_axes) (axis 0 is used) */
+    QSA_DEV_BAD_AXIS = 512,        /* a pair's axis outside [0, n_axes) (axis 0 is used) */
+    QSA_DEV_BAD_STATE = 1024       /* a state slot past the pool (its sequence is left out) */
 };
 
 /* Element types of the 16- and 32-bit tensors that more than one type is allowed for. */
@@ -372,6 +373,105 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
                       int32_t* positions, int32_t* token_seq, int32_t* seq_lens_out, int32_t* cu_tokens,
                       int32_t* free_head_out, int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------- layers with a state
+ * Models that select cells in some layers have layers of another kind between them,
+ * which keep a state of fixed size per sequence in place of a cache: a short
+ * convolution, the gated delta rule, and a norm of its heads.  The calls below are
+ * those layers' step.  They share the serving calls' conventions, and
+ *   - the step's new tokens of all sequences lie end to end, sequence s holding
+ *     tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32 [n_seq + 1], from 0 up and
+ *     nowhere falling; qsa_extend_tables writes it).  n_tok is what the token arrays
+ *     hold; tokens from cu_tokens[n_seq] on belong to nobody: nothing of theirs is
+ *     used, and their rows of the outputs stay as they are.  Bounds that fall or lie
+ *     outside [0, n_tok] are clamped and reported (QSA_DEV_BAD_SEQ_LEN).
+ *   - state_slots: int32 [n_seq], the sequence's place in the state pool, or < 0: the
+ *     sequence is left out, nothing of it is read and its rows of the outputs stay
+ *     as they are (padding of a batch).  A slot past the pool is treated alike and
+ *     reported (QSA_DEV_BAD_STATE).  Slots >= 0 must be distinct.
+ *   - old_lens: int32 [n_seq], how many tokens the sequence had before this step
+ *     (qsa_extend_tables' seq_lens).  Where it is <= 0 the state starts from zeros
+ *     and the pool's contents are not read.  NULL: every sequence goes on.
+ *   - After the call the pool holds each sequence's state after its last token;
+ *     other slots are not touched. */
+
+/* Activations. */
+enum { QSA_ACT_NONE = 0, QSA_ACT_SILU = 1 };
+
+/* Causal depthwise convolution over the last `width` inputs of a sequence:
+ *     out[t][c] = act(bias[c] + sum_j weight[c][j] x[t - (width - 1) + j][c]),
+ * inputs from before the step taken from the state, FP32 sums, rounded once.
+ *   - x: [n_tok][n_ch] of `type` (QSA_BF16 or QSA_F16), tokens x_stride elements
+ *     apart; out likewise, out_stride; both strides multiples of 8, >= n_ch, both
+ *     16-byte aligned.  n_ch is a multiple of 8, width 2 to 4.  out must not overlap x.
+ *   - weight [n_ch][width], bias [n_ch] or NULL, of w_type: `type` or QSA_F32,
+ *     16-byte aligned.
+ *   - state: [n_slots][width - 1][n_ch] of `type`, the last inputs, oldest first;
+ *     16-byte aligned.
+ *   - cu_tokens NULL: one token to every sequence (n_seq == n_tok). */
+int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* weight, const void* bias,
+                   int32_t w_type, int32_t width, int32_t activation, void* state, const int32_t* state_slots,
+                   int32_t n_slots, const int32_t* old_lens, const int32_t* cu_tokens, int32_t n_seq,
+                   int32_t n_tok, int32_t n_ch, void* out, int64_t out_stride, int32_t* dev_status,
+                   void* stream);
+
+/* The gated delta rule over a step's tokens.  For value head h, with the key head
+ * h / (n_v / n_k), a state S (128 x 128, value by key) and token t:
+ *     g = -exp(a_log[h]) softplus(a[t][h] + dt_bias[h]),  beta = sigmoid(b[t][h]),
+ *     k = k_t / sqrt(|k_t|^2 + eps),  q = q_t scale / sqrt(|q_t|^2 + eps),
+ *     S = exp(g) S,  S = S + beta (v_t - S k) k^T,  out[t][h] = S q.
+ *   - q, k: [n_tok][n_k][128], v: [n_tok][n_v][128] of `type` (QSA_BF16 or QSA_F16),
+ *     tokens q_stride, k_stride, v_stride elements apart (multiples of 8; slices of
+ *     the convolution's output), 16-byte aligned; out as v, out_stride; out must
+ *     not overlap an input.  n_v is a multiple of n_k.
+ *   - a, b: [n_tok][n_v] of `type`, tokens a_stride and b_stride elements apart.
+ *     a_log, dt_bias: FP32 [n_v].  a_log = -infinity: no decay; b = infinity: beta = 1.
+ *   - eps >= 0; scale is finite.
+ *   - state: FP32 [n_slots][n_v][128][128], the key dim innermost, 16-byte aligned.
+ *   - Chunks of 64 tokens on the tensor cores; the state and all sums in FP32, the
+ *     state's and the new values' operands as pairs of FP16 (22 bits, with a power
+ *     of two per value dim).  The products that end in `out` alone are of FP16 factors
+ *     (relative 2^-11 each).  The same call gives the same bits; how a sequence is
+ *     split into steps changes its last bits.
+ *   - workspace: device memory of at least qsa_delta_prompt_workspace_bytes(n_tok,
+ *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept.  Two
+ *     calls that can overlap on the device need one each.
+ *   - n_seq == 0 returns QSA_OK with no launch. */
+int qsa_delta_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, int32_t type, const void* a, int64_t a_stride, const void* b,
+                     int64_t b_stride, const float* a_log, const float* dt_bias, float* state,
+                     const int32_t* state_slots, int32_t n_slots, const int32_t* old_lens,
+                     const int32_t* cu_tokens, int32_t n_seq, int32_t n_tok, int32_t n_k, int32_t n_v,
+                     float eps, float scale, void* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace of qsa_delta_prompt; 0 for sizes that it refuses. */
+size_t qsa_delta_prompt_workspace_bytes(int32_t n_tok, int32_t n_seq, int32_t n_k, int32_t n_v);
+
+/* The same for one token of every sequence (token s is sequence s's), FP32
+ * throughout: the decode step, one launch, no workspace. */
+int qsa_delta_step(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, int32_t type, const void* a, int64_t a_stride, const void* b,
+                   int64_t b_stride, const float* a_log, const float* dt_bias, float* state,
+                   const int32_t* state_slots, int32_t n_slots, const int32_t* old_lens, int32_t n_seq,
+                   int32_t n_k, int32_t n_v, float eps, float scale, void* out, int64_t out_stride,
+                   int32_t* dev_status, void* stream);
+
+/* Each group of `size` channels of each token normalised over itself, channels last:
+ *     y = (x - m) / sqrt(mean((x - m)^2) + eps) weight + bias,
+ * m the group's mean when centred, else 0; then out = y act(gate), or act(y) without a
+ * gate.  Statistics in FP32 (the mean first, then the squares), rounded once.
+ *   - x, gate (or NULL), out: [n_tok][n_groups][size] of `type` (QSA_BF16 or QSA_F16),
+ *     tokens x_stride, gate_stride, out_stride elements apart (multiples of 8),
+ *     16-byte aligned.  size is a multiple of 8 up to 8192.  out may be x or gate, with
+ *     equal strides; otherwise it must not overlap them.
+ *   - weight, bias: [size], or [n_groups][size] when per_group, or NULL (ones,
+ *     zeros), of w_type: `type` or QSA_F32, 16-byte aligned.
+ *   - eps >= 0. */
+int qsa_group_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, int32_t type,
+                   const void* weight, const void* bias, int32_t w_type, int32_t per_group, int32_t n_tok,
+                   int32_t n_groups, int32_t size, float eps, int32_t centred, int32_t activation, void* out,
+                   int64_t out_stride, void* stream);
+
 /* The same calls with their arguments in one struct, in the order of the
  * parameters, for callers to whom converting each argument costs more than the call
  * (interpreters).  Statuses and results are those of the calls; NULL is QSA_ERR_ARG. */
@@ -444,6 +544,94 @@ typedef struct {
     void* stream;
 } qsa_extend_tables_args;
 int qsa_extend_tables_packed(const qsa_extend_tables_args* args);
+
+typedef struct {
+    const void* x;
+    int64_t x_stride;
+    int32_t type;
+    const void *weight, *bias;
+    int32_t w_type, width, activation;
+    void* state;
+    const int32_t* state_slots;
+    int32_t n_slots;
+    const int32_t *old_lens, *cu_tokens;
+    int32_t n_seq, n_tok, n_ch;
+    void* out;
+    int64_t out_stride;
+    int32_t* dev_status;
+    void* stream;
+} qsa_short_conv_args;
+int qsa_short_conv_packed(const qsa_short_conv_args* args);
+
+typedef struct {
+    const void* q;
+    int64_t q_stride;
+    const void* k;
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    int32_t type;
+    const void* a;
+    int64_t a_stride;
+    const void* b;
+    int64_t b_stride;
+    const float *a_log, *dt_bias;
+    float* state;
+    const int32_t* state_slots;
+    int32_t n_slots;
+    const int32_t *old_lens, *cu_tokens;
+    int32_t n_seq, n_tok, n_k, n_v;
+    float eps, scale;
+    void* out;
+    int64_t out_stride;
+    void* workspace;
+    size_t workspace_bytes;
+    int32_t* dev_status;
+    void* stream;
+} qsa_delta_prompt_args;
+int qsa_delta_prompt_packed(const qsa_delta_prompt_args* args);
+
+typedef struct {
+    const void* q;
+    int64_t q_stride;
+    const void* k;
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    int32_t type;
+    const void* a;
+    int64_t a_stride;
+    const void* b;
+    int64_t b_stride;
+    const float *a_log, *dt_bias;
+    float* state;
+    const int32_t* state_slots;
+    int32_t n_slots;
+    const int32_t* old_lens;
+    int32_t n_seq, n_k, n_v;
+    float eps, scale;
+    void* out;
+    int64_t out_stride;
+    int32_t* dev_status;
+    void* stream;
+} qsa_delta_step_args;
+int qsa_delta_step_packed(const qsa_delta_step_args* args);
+
+typedef struct {
+    const void* x;
+    int64_t x_stride;
+    const void* gate;
+    int64_t gate_stride;
+    int32_t type;
+    const void *weight, *bias;
+    int32_t w_type, per_group, n_tok, n_groups, size;
+    float eps;
+    int32_t centred, activation;
+    void* out;
+    int64_t out_stride;
+    void* stream;
+} qsa_group_norm_args;
+int qsa_group_norm_packed(const qsa_group_norm_args* args);
 
 /* Self-test of the bounded waits (not part of the method: the pages have no
  * counterpart).  Every pipelined kernel here waits on mbarriers with a wall-time

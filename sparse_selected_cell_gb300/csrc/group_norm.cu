@@ -1,0 +1,131 @@
+// group_norm.cu -- groups of a token's channels normalised, weighted and gated (qsa_group_norm).
+//
+// Bytes are all: x and the gate read once, out written once.  A group is held in registers
+// by as many threads as it has 16-byte words, up to a warp (LANES, a power of two), each with
+// PIECES words, or by a block's eight warps where it has more than 128 words; so the mean is
+// taken first and the squares of what is left after it, in FP32, without a second read.
+#include "linear.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kNormThreads = 256;
+
+template <int LANES>
+__device__ __forceinline__ float sum_over(float x, float* s_part) {
+#pragma unroll
+    for (int o = 1; o < (LANES < 32 ? LANES : 32); o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (LANES <= 32) return x;
+    __syncthreads();                                 // the sums of the round before have been read
+    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) x += s_part[i];
+    return x;
+}
+
+template <int TYPE, int LANES, int PIECES>
+__global__ void __launch_bounds__(kNormThreads) group_norm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float s_part[kNormThreads / 32];
+    const int l = threadIdx.x % LANES, words = a.size / 8;
+    const long long item = (long long)blockIdx.x * (kNormThreads / LANES) + threadIdx.x / LANES;
+    const bool live = item < (long long)a.n_tok * a.n_groups;
+    const long long t = live ? item / a.n_groups : 0;
+    const int g = live ? (int)(item - t * a.n_groups) : 0;
+    wait_for_stream();
+    const uint16_t* x = a.x + t * a.x_stride + (size_t)g * a.size;
+    const uint16_t* z = a.gate ? a.gate + t * a.gate_stride + (size_t)g * a.size : nullptr;
+    uint4 rx[PIECES], rz[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int w = l + i * LANES;
+        rx[i] = rz[i] = make_uint4(0, 0, 0, 0);
+        if (live && w < words) {
+            rx[i] = *reinterpret_cast<const uint4*>(x + 8 * w);
+            if (z) rz[i] = *reinterpret_cast<const uint4*>(z + 8 * w);
+        }
+    }
+    float mean = 0.f;
+    if (a.centred) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            float f[8];
+            unpack8(rx[i], TYPE, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mean += f[j];
+        }
+        mean = __fdiv_rn(sum_over<LANES>(mean, s_part), (float)a.size);
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        float f[8];
+        unpack8(rx[i], TYPE, f);
+        if (l + i * LANES < words) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+        }
+    }
+    const float r = __frsqrt_rn(__fdiv_rn(sum_over<LANES>(sq, s_part), (float)a.size) + a.eps);
+    uint16_t* out = a.out + t * a.out_stride + (size_t)g * a.size;
+    const size_t w0 = a.per_group ? (size_t)g * a.size : 0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int w = l + i * LANES;
+        if (!live || w >= words) continue;
+        float y[8], p[8];
+        unpack8(rx[i], TYPE, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (y[j] - mean) * r;
+        if (a.weight) {
+            load8(a.weight, w0 + 8 * w, a.w_type, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= p[j];
+        }
+        if (a.bias) {
+            load8(a.bias, w0 + 8 * w, a.w_type, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += p[j];
+        }
+        if (z) {
+            unpack8(rz[i], TYPE, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= a.activation == QSA_ACT_SILU ? silu(p[j]) : p[j];
+        } else if (a.activation == QSA_ACT_SILU) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
+        }
+        *reinterpret_cast<uint4*>(out + 8 * w) = pack8(y, TYPE);
+    }
+}
+
+template <int TYPE, int LANES, int PIECES>
+cudaError_t launch_lanes(const NormArgs& a, cudaStream_t stream) {
+    const long long items = (long long)a.n_tok * a.n_groups, per = kNormThreads / LANES, grid = (items + per - 1) / per;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(group_norm_kernel<TYPE, LANES, PIECES>, dim3((unsigned)grid), kNormThreads, 0, stream, a);
+}
+
+template <int TYPE>
+cudaError_t launch_type(const NormArgs& a, cudaStream_t stream) {
+    const int words = a.size / 8;
+    if (words <= 1) return launch_lanes<TYPE, 1, 1>(a, stream);
+    if (words <= 2) return launch_lanes<TYPE, 2, 1>(a, stream);
+    if (words <= 4) return launch_lanes<TYPE, 4, 1>(a, stream);
+    if (words <= 8) return launch_lanes<TYPE, 8, 1>(a, stream);
+    if (words <= 16) return launch_lanes<TYPE, 16, 1>(a, stream);
+    if (words <= 32) return launch_lanes<TYPE, 32, 1>(a, stream);
+    if (words <= 64) return launch_lanes<TYPE, 32, 2>(a, stream);
+    if (words <= 128) return launch_lanes<TYPE, 32, 4>(a, stream);
+    if (words <= 512) return launch_lanes<TYPE, kNormThreads, 2>(a, stream);
+    return launch_lanes<TYPE, kNormThreads, 4>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t stream) {
+    return a.type == QSA_F16 ? launch_type<QSA_F16>(a, stream) : launch_type<QSA_BF16>(a, stream);
+}
+
+}  // namespace qsa

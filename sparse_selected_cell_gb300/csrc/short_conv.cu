@@ -1,0 +1,205 @@
+// short_conv.cu -- the causal depthwise convolution of layers with a state (qsa_short_conv).
+//
+// out[t][c] = act(bias[c] + sum_j w[c][j] x[t - (W - 1) + j][c]): 2 W flops an element, so
+// bytes are all: x read once, out written once, and the states of the sequences that go on.
+//
+// A thread owns eight channels (one 16-byte word a token) and a run of consecutive tokens,
+// the last W - 1 inputs in registers; a warp's accesses are 512 consecutive bytes.  Runs cut
+// sequences anywhere.  Inside a sequence a run's loads go out together; where sequences
+// begin, the tokens are taken one by one.
+//
+// States are updated in place without a block that waits for another: the block whose run
+// holds a sequence's first token (the last run, for sequences that begin behind it and so
+// have none) is the only one that touches its state.  It reads the old one, writes the new
+// one, whose inputs it reads again where they lie in another run, and computes the first
+// W - 1 tokens, the only ones that need the old state, even those past its run's end; the
+// next run leaves them out.
+#include "linear.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kConvThreads = 128;
+
+// The first sequence that begins at token t or later (n_seq: none), by the whole warp.
+__device__ __forceinline__ int first_from(const int32_t* cu_tokens, int n_seq, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n_seq;                         // the answer is in [lo, lo + len]
+    while (len > 0) {
+        const int step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const unsigned there = __ballot_sync(0xffffffffu, at >= lo + len || cu_tokens[at] >= t);
+        const int f = there ? __ffs(there) - 1 : 32;
+        const int from = min(lo + f * step, lo + len);
+        len = min(lo + f * step + step - 1, lo + len) - from;
+        lo = from;
+    }
+    return lo;
+}
+
+template <int TYPE, int W, int RUN>
+__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_constant__ ConvArgs a, const unsigned cols) {
+    const unsigned run = blockIdx.x / cols;          // the columns of one run side by side
+    const int c = (int)((blockIdx.x - run * cols) * kConvThreads + threadIdx.x) * 8;
+    const int t0 = (int)run * RUN, t1 = min(t0 + RUN, a.n_tok);
+    const bool live = c < a.n_ch, last = blockIdx.x >= gridDim.x - cols;
+    wait_for_stream();
+    const uint16_t* x = a.x + c;
+    uint16_t* out = a.out + c;
+    auto input = [&](int t) { return *reinterpret_cast<const uint4*>(x + (long long)t * a.x_stride); };
+    float w[W][8], bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {                // [channel][tap]: 8 W consecutive values
+            float flat[8];
+            load8(a.weight, (size_t)c * W + 8 * i, a.w_type, flat);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[(8 * i + j) % W][(8 * i + j) / W] = flat[j];
+        }
+        if (a.bias) load8(a.bias, (size_t)c, a.w_type, bias);
+    }
+    float win[W - 1][8];                             // inputs t - (W - 1) .. t - 1
+    auto token = [&](int t, const float (&in)[8], bool write) {
+        if (write) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[j] = bias[j];
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) y[j] = fmaf(w[i][j], win[i][j], y[j]);
+                y[j] = fmaf(w[W - 1][j], in[j], y[j]);
+                if (a.activation == QSA_ACT_SILU) y[j] = silu(y[j]);
+            }
+            *reinterpret_cast<uint4*>(out + (long long)t * a.out_stride) = pack8(y, TYPE);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int i = 0; i < W - 2; ++i) win[i][j] = win[i + 1][j];
+            win[W - 2][j] = in[j];
+        }
+    };
+
+    // the first sequence that begins here or later
+    const int owned = !a.cu_tokens ? t0 : t0 == 0 ? 0 : first_from(a.cu_tokens, a.n_seq, t0);
+    if (blockIdx.x == 0 && a.cu_tokens && a.dev_status)
+        for (int i = threadIdx.x; i < a.n_seq; i += kConvThreads)
+            if (tokens_bad(a.cu_tokens, i, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
+    if (!live) return;
+    int s = owned - 1, begin = 0, end = t0;          // the sequence that the run begins in
+    bool skip = true;
+    auto look = [&]() {
+        const int2 span = tokens_of(a.cu_tokens, s, a.n_tok);
+        const int slot = a.state_slots[s];
+        begin = span.x, end = span.y;
+        skip = slot < 0 || slot >= a.n_slots;
+        return slot;
+    };
+    if (a.cu_tokens && s >= 0) look();
+    const int following = owned < a.n_seq ? (a.cu_tokens ? a.cu_tokens[owned] : owned) : a.n_tok;
+    if (RUN > 1 && t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
+        if (skip) return;                            // the whole run inside one sequence
+        uint4 raw[RUN + W - 1];
+#pragma unroll
+        for (int i = 0; i < RUN + W - 1; ++i) raw[i] = input(t0 - (W - 1) + i);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) unpack8(raw[i], TYPE, win[i]);
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            float in[8];
+            unpack8(raw[i + W - 1], TYPE, in);
+            token(t0 + i, in, true);
+        }
+        return;
+    }
+
+    // Sequence s begins in this run: its state in, and out again as its tokens leave it.
+    auto enter = [&]() {
+        const int slot = look();
+        if (c == 0 && slot >= a.n_slots) report(a.dev_status, QSA_DEV_BAD_STATE);
+        if (skip) return;
+        const bool fresh = a.old_lens && a.old_lens[s] <= 0;
+        uint16_t* held = a.state + (size_t)slot * (W - 1) * a.n_ch + c;
+        const int n = end - begin;
+        uint4 old[W - 1], now[W - 1];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            old[i] = fresh ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(held + (size_t)i * a.n_ch);
+            unpack8(old[i], TYPE, win[i]);
+        }
+        if (n == 0 && !fresh) return;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {            // place i holds input n - (W - 1) + i: below 0, the old state's place i + n
+            if (n - (W - 1) + i >= 0) {
+                now[i] = input(begin + n - (W - 1) + i);
+            } else {
+                now[i] = old[i];
+#pragma unroll
+                for (int m = i + 1; m < W - 1; ++m)
+                    if (m == i + n) now[i] = old[m];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) *reinterpret_cast<uint4*>(held + (size_t)i * a.n_ch) = now[i];
+    };
+    // Up to W - 2 tokens past the run's end belong to a sequence that begins in it.
+    const int reach = min(t1 + W - 2, a.n_tok);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {                // the inputs before the run, as far as they are the sequence's own
+        const int t = t0 - (W - 1) + i;
+        unpack8(!skip && t >= begin && t < end ? input(t) : make_uint4(0, 0, 0, 0), TYPE, win[i]);
+    }
+    uint4 ahead = t0 < t1 ? input(t0) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int t = t0; t < reach; ++t) {
+        float in[8];
+        unpack8(ahead, TYPE, in);
+        if (t + 1 < reach) ahead = input(t + 1);
+        if (t < t1) {
+            while (s + 1 < a.n_seq && (a.cu_tokens ? a.cu_tokens[s + 1] : s + 1) <= t) {
+                ++s;
+                enter();
+            }
+        } else if (t >= end) {
+            break;
+        }
+        const bool first = t - begin < W - 1, mine = begin >= t0;
+        if (t >= t1 && !(mine && first)) break;
+        token(t, in, !skip && t < end && (mine || !first));
+    }
+    if (last)
+        while (s + 1 < a.n_seq) {
+            ++s;
+            enter();
+        }
+}
+
+template <int TYPE, int W, int RUN>
+cudaError_t launch_run(const ConvArgs& a, cudaStream_t stream) {
+    const long long cols = (a.n_ch / 8 + kConvThreads - 1) / kConvThreads;
+    const long long runs = a.n_tok > 0 ? (a.n_tok + RUN - 1LL) / RUN : 1;
+    if (cols * runs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(short_conv_kernel<TYPE, W, RUN>, dim3((unsigned)(cols * runs)), kConvThreads, 0, stream, a,
+                             (unsigned)cols);
+}
+
+template <int TYPE, int W>
+cudaError_t launch_width(const ConvArgs& a, cudaStream_t stream) {
+    if (!a.cu_tokens || a.n_tok < 4LL * a.n_seq) return launch_run<TYPE, W, 1>(a, stream);
+    return launch_run<TYPE, W, 16>(a, stream);
+}
+
+template <int TYPE>
+cudaError_t launch_type(const ConvArgs& a, cudaStream_t stream) {
+    return a.width == 4 ? launch_width<TYPE, 4>(a, stream) : a.width == 3 ? launch_width<TYPE, 3>(a, stream)
+                                                                          : launch_width<TYPE, 2>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t stream) {
+    return a.type == QSA_F16 ? launch_type<QSA_F16>(a, stream) : launch_type<QSA_BF16>(a, stream);
+}
+
+}  // namespace qsa

@@ -22,8 +22,9 @@ QSA_OK, QSA_ERR_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_CAPACITY, QSA_ERR_CUDA, QSA_ER
 ATTN_DEFAULT, ATTN_TCGEN05, ATTN_TCGEN05_SM = 0, 1, 2
 DEV_BITS = {1: "bad selection count", 2: "union overflow", 4: "bad cell", 8: "bad page-table entry",
             16: "bad union count", 32: "device wait timeout", 64: "bad sequence length", 128: "no page",
-            256: "token overflow", 512: "bad axis"}
+            256: "token overflow", 512: "bad axis", 1024: "bad state slot"}
 BF16, F16, F32 = 0, 1, 2          # element types (QSA_BF16, QSA_F16, QSA_F32)
+ACTIVATIONS = {"none": 0, "silu": 1}   # QSA_ACT_*
 
 _lib = None
 _P, _I, _F, _S, _L = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
@@ -32,6 +33,10 @@ _PAGED_ARGS = struct.Struct("PiPPPPPiiiiiPiifPiPPNPP").pack
 _APPEND_ARGS = struct.Struct("PqPqPqiPiiPPiiPqPPPPPiiiiPP").pack
 _GATHER_ARGS = struct.Struct("PPPPPiiiPPiPP").pack
 _TABLES_ARGS = struct.Struct("PPiPiiiPiPiPPPPPPPP").pack
+_CONV_ARGS = struct.Struct("PqiPPiiiPPiPPiiiPqPP").pack
+_PROMPT_ARGS = struct.Struct("PqPqPqiPqPqPPPPiPPiiiiffPqPNPP").pack
+_STEP_ARGS = struct.Struct("PqPqPqiPqPqPPPPiPiiiffPqPP").pack
+_NORM_ARGS = struct.Struct("PqPqiPPiiiiifiiPqP").pack
 
 
 class QsaError(RuntimeError):
@@ -84,7 +89,20 @@ def lib():
         L.qsa_cache_gather.restype = ctypes.c_int
         L.qsa_extend_tables.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]
         L.qsa_extend_tables.restype = ctypes.c_int
-        for f in (L.qsa_paged_attn_packed, L.qsa_rope_append_packed, L.qsa_cache_gather_packed, L.qsa_extend_tables_packed):
+        L.qsa_short_conv.argtypes = [_P, _L, _I, _P, _P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _I, _I, _P, _L, _P, _P]
+        L.qsa_short_conv.restype = ctypes.c_int
+        L.qsa_delta_prompt.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I,
+                                       _F, _F, _P, _L, _P, _S, _P, _P]
+        L.qsa_delta_prompt.restype = ctypes.c_int
+        L.qsa_delta_prompt_workspace_bytes.argtypes = [_I, _I, _I, _I]
+        L.qsa_delta_prompt_workspace_bytes.restype = _S
+        L.qsa_delta_step.argtypes = [_P, _L, _P, _L, _P, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, _I, _P, _I, _I, _I, _F, _F,
+                                     _P, _L, _P, _P]
+        L.qsa_delta_step.restype = ctypes.c_int
+        L.qsa_group_norm.argtypes = [_P, _L, _P, _L, _I, _P, _P, _I, _I, _I, _I, _I, _F, _I, _I, _P, _L, _P]
+        L.qsa_group_norm.restype = ctypes.c_int
+        for f in (L.qsa_paged_attn_packed, L.qsa_rope_append_packed, L.qsa_cache_gather_packed, L.qsa_extend_tables_packed,
+                  L.qsa_short_conv_packed, L.qsa_delta_prompt_packed, L.qsa_delta_step_packed, L.qsa_group_norm_packed):
             f.argtypes = [ctypes.c_char_p]
             f.restype = ctypes.c_int
         L.qsa_wait_selftest.argtypes = [_I, _P, _P]
@@ -715,6 +733,276 @@ def to_device(wl: "gen.Workload", device="cuda") -> dict:
     return dict(q=t(wl.q, np.int16), k_pool=t(wl.k_pool), v_pool=t(wl.v_pool),
                 k_scale=t(wl.k_scale.view(np.int16)), v_scale=t(wl.v_scale.view(np.int16)),
                 page_table=t(wl.page_table), sel=t(wl.sel), sel_count=t(wl.sel_count))
+
+
+# ---------------------------------------------------------------- layers with a state
+# Layers that keep a state of fixed size per sequence in place of a cache (include/qsa.h,
+# "layers with a state").  A step is short_conv -> delta_prompt or delta_step -> group_norm;
+# cu_tokens and old_lens are extend_tables' cu_tokens and the seq_lens it was given.
+
+
+def _flat_ok(t, dtype, dev, n_tok, width, stride) -> bool:
+    """A [n_tok, width] tensor whose tokens may lie apart."""
+    return (t.dtype is dtype and t.shape == (n_tok, width) and t.get_device() == dev and (stride[1] == 1 or width == 1))
+
+
+def _want_flat(t, name: str, dtypes, dev, n_tok=None, width=None):
+    _want(t, name, dtypes, dev, contiguous=False)
+    if t.dim() != 2 or (n_tok is not None and t.shape[0] != n_tok) or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be [{'n_tok' if n_tok is None else n_tok}, {'width' if width is None else width}], "
+                         f"got {tuple(t.shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: a token's channels must lie side by side")
+
+
+def _seqs_ok(state_slots, old_lens, cu_tokens, dev):
+    """Whether the sequences' arrays fit together; state_slots says how many they are."""
+    at = state_slots.shape
+    return (len(at) == 1 and _ok(state_slots, _I32, dev, at) and (old_lens is None or _ok(old_lens, _I32, dev, at))
+            and (cu_tokens is None or _ok(cu_tokens, _I32, dev, (at[0] + 1,))))
+
+
+def _want_seqs(state_slots, old_lens, cu_tokens, dev):
+    _want(state_slots, "state_slots", (_I32,), dev)
+    if state_slots.dim() != 1:
+        raise ValueError(f"state_slots must be [n_seq], got {tuple(state_slots.shape)}")
+    if old_lens is not None:
+        _want(old_lens, "old_lens", (_I32,), dev, state_slots.shape)
+    if cu_tokens is not None:
+        _want(cu_tokens, "cu_tokens", (_I32,), dev, (state_slots.shape[0] + 1,))
+
+
+def _act(activation) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is none of {tuple(ACTIVATIONS)}")
+    return ACTIVATIONS[activation]
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _refuse_short_conv(x, weight, state, state_slots, old_lens, cu_tokens, bias, out):
+    dev = _here(x, "x")
+    _want_flat(x, "x", _T16, dev)
+    n_tok, n_ch = x.shape
+    _want(weight, "weight", (x.dtype, torch.float32), dev)
+    if weight.dim() != 2 or weight.shape[0] != n_ch:
+        raise ValueError(f"weight must be [{n_ch}, width], got {tuple(weight.shape)}")
+    if bias is not None:
+        _want(bias, "bias", (weight.dtype,), dev, (n_ch,))
+    _want(state, "state", (x.dtype,), dev)
+    if state.dim() != 3 or state.shape[1:] != (weight.shape[1] - 1, n_ch):
+        raise ValueError(f"state must be [n_slots, {weight.shape[1] - 1}, {n_ch}], got {tuple(state.shape)}")
+    _want_seqs(state_slots, old_lens, cu_tokens, dev)
+    if cu_tokens is None and state_slots.shape[0] != n_tok:
+        raise ValueError(f"without cu_tokens there is one token to a sequence: {n_tok} tokens, {state_slots.shape[0]} sequences")
+    if out is not None:
+        _want_flat(out, "out", (x.dtype,), dev, n_tok, n_ch)
+
+
+def short_conv(x, weight, state, state_slots, old_lens: Optional[torch.Tensor] = None,
+               cu_tokens: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, activation: str = "silu",
+               out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal depthwise convolution of a step's new tokens (qsa_short_conv): x BF16 or FP16 [n_tok, n_ch], tokens any
+    multiple of 8 elements apart; weight [n_ch, width] and bias [n_ch] of x's type or float32, width 2 to 4; state
+    [n_slots, width - 1, n_ch] (the last inputs, updated in place); state_slots int32 [n_seq], < 0 = left out; old_lens int32
+    [n_seq], 0 = from zeros (None: all go on); cu_tokens int32 [n_seq + 1] (None: one token each) -> out [n_tok, n_ch]."""
+    try:
+        dev, dtype, xs, shape = x.get_device(), x.dtype, x.stride(), x.shape
+        n_tok, n_ch = shape
+        width = weight.shape[1]
+        n_seq = state_slots.shape[0]
+        wt = weight.dtype
+        good = (dev >= 0 and dev == _current() and dtype in _T16 and _flat_ok(x, dtype, dev, n_tok, n_ch, xs)
+                and (wt is dtype or wt is torch.float32) and _ok(weight, wt, dev, (n_ch, width))
+                and (bias is None or _ok(bias, wt, dev, (n_ch,)))
+                and _ok(state, dtype, dev, (state.shape[0], width - 1, n_ch))
+                and _seqs_ok(state_slots, old_lens, cu_tokens, dev) and (cu_tokens is not None or n_seq == n_tok)
+                and (out is None or _flat_ok(out, dtype, dev, n_tok, n_ch, out.stride())))
+    except (AttributeError, IndexError, ValueError):
+        good = False
+    if not good:
+        _refuse_short_conv(x, weight, state, state_slots, old_lens, cu_tokens, bias, out)
+        raise ValueError("short_conv: arguments do not fit together")
+    if out is None:
+        out = _empty(shape, dtype, x.device, stream)
+    rc = (_lib or lib()).qsa_short_conv_packed(_CONV_ARGS(
+        x.data_ptr(), xs[0] if n_tok > 1 else n_ch, _TYPE[dtype], weight.data_ptr(), _at(bias), _TYPE[wt], width,
+        _act(activation), state.data_ptr(), state_slots.data_ptr(), state.shape[0], _at(old_lens), _at(cu_tokens), n_seq, n_tok,
+        n_ch, out.data_ptr(), out.stride(0) if n_tok > 1 else n_ch, _status_of(dev_status, dev), _stream_of(stream, dev)))
+    if rc != QSA_OK:
+        raise QsaError("qsa_short_conv", rc)
+    return out
+
+
+def delta_prompt_workspace_bytes(n_tok: int, n_seq: int, n_k: int, n_v: int) -> int:
+    """Bytes of workspace delta_prompt needs for n_tok tokens of n_seq sequences, n_k key heads and n_v value heads."""
+    return int(lib().qsa_delta_prompt_workspace_bytes(int(n_tok), int(n_seq), int(n_k), int(n_v)))
+
+
+def _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, n_tok, n_k, n_v):
+    return (dev >= 0 and dev == _current() and dtype in _T16 and _rows_ok(q, dtype, dev, n_tok, n_k, q.stride())
+            and _rows_ok(k, dtype, dev, n_tok, n_k, k.stride()) and _rows_ok(v, dtype, dev, n_tok, n_v, v.stride())
+            and n_k > 0 and n_v > 0 and n_v % n_k == 0 and _flat_ok(a, dtype, dev, n_tok, n_v, a.stride())
+            and _flat_ok(b, dtype, dev, n_tok, n_v, b.stride()) and _ok(a_log, torch.float32, dev, (n_v,))
+            and _ok(dt_bias, torch.float32, dev, (n_v,)) and _ok(state, torch.float32, dev, (state.shape[0], n_v, 128, 128))
+            and _seqs_ok(state_slots, old_lens, cu_tokens, dev)
+            and (out is None or _rows_ok(out, dtype, dev, n_tok, n_v, out.stride())))
+
+
+def _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out):
+    dev = _here(q, "q")
+    _want_rows(q, "q", _T16, dev)
+    n_tok, n_k = q.shape[0], q.shape[1]
+    _want_rows(k, "k", (q.dtype,), dev, n_tok, n_k)
+    _want_rows(v, "v", (q.dtype,), dev, n_tok)
+    n_v = v.shape[1]
+    if n_k == 0 or n_v == 0 or n_v % n_k:
+        raise ValueError(f"the value heads must be a multiple of the key heads, got {n_v} and {n_k}")
+    _want_flat(a, "a", (q.dtype,), dev, n_tok, n_v)
+    _want_flat(b, "b", (q.dtype,), dev, n_tok, n_v)
+    _want(a_log, "a_log", (torch.float32,), dev, (n_v,))
+    _want(dt_bias, "dt_bias", (torch.float32,), dev, (n_v,))
+    _want(state, "state", (torch.float32,), dev)
+    if state.dim() != 4 or state.shape[1:] != (n_v, 128, 128):
+        raise ValueError(f"state must be [n_slots, {n_v}, 128, 128], got {tuple(state.shape)}")
+    _want_seqs(state_slots, old_lens, cu_tokens, dev)
+    if out is not None:
+        _want_rows(out, "out", (q.dtype,), dev, n_tok, n_v)
+
+
+def delta_prompt(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, eps: float = 1e-6,
+                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The gated delta rule over a step's new tokens (qsa_delta_prompt): q, k [n_tok, n_k, 128], v [n_tok, n_v, 128], a, b
+    [n_tok, n_v], all BF16 or all FP16, tokens any distance apart that is a multiple of 8 elements (a and b: any); a_log,
+    dt_bias float32 [n_v]; state float32 [n_slots, n_v, 128, 128] (value by key, updated in place); state_slots, old_lens
+    (None: all go on), cu_tokens as in short_conv -> out [n_tok, n_v, 128].  A workspace that is not given is allocated."""
+    try:
+        dev, dtype = q.get_device(), q.dtype
+        n_tok, n_k, n_v, n_seq = q.shape[0], q.shape[1], v.shape[1], state_slots.shape[0]
+        good = (cu_tokens is not None
+                and _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, n_tok,
+                              n_k, n_v)
+                and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out)
+        if workspace is not None:
+            _want(workspace, "workspace", (getattr(workspace, "dtype", None),), q.get_device())
+        raise ValueError("delta_prompt: arguments do not fit together")
+    if out is None:
+        out = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream)
+    if workspace is None:
+        workspace = _empty(delta_prompt_workspace_bytes(n_tok, n_seq, n_k, n_v), torch.uint8, q.device, stream)
+    rc = (_lib or lib()).qsa_delta_prompt_packed(_PROMPT_ARGS(
+        q.data_ptr(), _apart(q.stride(), n_tok, n_k), k.data_ptr(), _apart(k.stride(), n_tok, n_k), v.data_ptr(),
+        _apart(v.stride(), n_tok, n_v), _TYPE[dtype], a.data_ptr(), a.stride(0) if n_tok > 1 else n_v, b.data_ptr(),
+        b.stride(0) if n_tok > 1 else n_v, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(),
+        state.shape[0], _at(old_lens), cu_tokens.data_ptr(), n_seq, n_tok, n_k, n_v, eps,
+        gen.HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), _apart(out.stride(), n_tok, n_v),
+        workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev), _stream_of(stream, dev)))
+    if rc != QSA_OK:
+        raise QsaError("qsa_delta_prompt", rc)
+    return out
+
+
+def delta_step(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens: Optional[torch.Tensor] = None,
+               eps: float = 1e-6, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+               dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated delta rule for one token of every sequence (qsa_delta_step): as delta_prompt, token s being sequence s's
+    -> out [n_seq, n_v, 128]."""
+    try:
+        dev, dtype = q.get_device(), q.dtype
+        n_tok, n_k, n_v = q.shape[0], q.shape[1], v.shape[1]
+        good = (_delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, None, out, dev, dtype, n_tok, n_k, n_v)
+                and state_slots.shape[0] == n_tok)
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, None, out)
+        raise ValueError("delta_step: arguments do not fit together (one token to a sequence)")
+    if out is None:
+        out = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream)
+    rc = (_lib or lib()).qsa_delta_step_packed(_STEP_ARGS(
+        q.data_ptr(), _apart(q.stride(), n_tok, n_k), k.data_ptr(), _apart(k.stride(), n_tok, n_k), v.data_ptr(),
+        _apart(v.stride(), n_tok, n_v), _TYPE[dtype], a.data_ptr(), a.stride(0) if n_tok > 1 else n_v, b.data_ptr(),
+        b.stride(0) if n_tok > 1 else n_v, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(),
+        state.shape[0], _at(old_lens), n_tok, n_k, n_v, eps, gen.HEAD_DIM ** -0.5 if scale is None else scale,
+        out.data_ptr(), _apart(out.stride(), n_tok, n_v), _status_of(dev_status, dev), _stream_of(stream, dev)))
+    if rc != QSA_OK:
+        raise QsaError("qsa_delta_step", rc)
+    return out
+
+
+def _groups_ok(t, dtype, dev, shape, stride) -> bool:
+    """A [n_tok, n_groups, size] tensor whose tokens may lie apart."""
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == dev and (stride[2] == 1 or shape[2] == 1)
+            and (stride[1] == shape[2] or shape[1] == 1))
+
+
+def _want_groups(t, name: str, dtypes, dev, shape=None):
+    _want(t, name, dtypes, dev, shape, contiguous=False)
+    if t.dim() != 3 or t.shape[1] == 0:
+        raise ValueError(f"{name} must be [n_tok, n_groups, size], got {tuple(t.shape)}")
+    s = t.stride()
+    if (s[2] != 1 and t.shape[2] > 1) or (s[1] != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: a token's channels must lie side by side")
+
+
+def _refuse_group_norm(x, weight, bias, gate, out):
+    dev = _here(x, "x")
+    _want_groups(x, "x", _T16, dev)
+    shape = x.shape
+    first = weight if weight is not None else bias
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _want(t, name, (x.dtype, torch.float32) if t is first else (first.dtype,), dev)
+            if t.shape not in (shape[1:], shape[2:]) or t.shape != first.shape:
+                raise ValueError(f"{name} must be {tuple(shape[2:])} or {tuple(shape[1:])}, weight and bias alike, "
+                                 f"got {tuple(t.shape)}")
+    if gate is not None:
+        _want_groups(gate, "gate", (x.dtype,), dev, shape)
+    if out is not None:
+        _want_groups(out, "out", (x.dtype,), dev, shape)
+
+
+def group_norm(x, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, eps: float = 1e-6, centred: bool = False,
+               activation: Optional[str] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each group of a token's channels normalised over itself (qsa_group_norm): x BF16 or FP16 [n_tok, n_groups, size],
+    tokens any multiple of 8 elements apart; weight and bias [size] or [n_groups, size], of x's type or float32; by the root
+    mean square, or when centred by the standard deviation about the mean; then times activation(gate), or the activation of
+    the result without a gate (None: SiLU with a gate, none without) -> out as x (may be x or the gate)."""
+    try:
+        dev, dtype, shape, xs = x.get_device(), x.dtype, x.shape, x.stride()
+        first = weight if weight is not None else bias
+        wt, at = (dtype, None) if first is None else (first.dtype, first.shape)
+        good = (dev >= 0 and dev == _current() and dtype in _T16 and len(shape) == 3 and _groups_ok(x, dtype, dev, shape, xs)
+                and shape[1] > 0 and (wt is dtype or wt is torch.float32) and (at is None or at == shape[2:] or at == shape[1:])
+                and (weight is None or _ok(weight, wt, dev, at)) and (bias is None or _ok(bias, wt, dev, at))
+                and (gate is None or _groups_ok(gate, dtype, dev, shape, gate.stride()))
+                and (out is None or _groups_ok(out, dtype, dev, shape, out.stride())))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _refuse_group_norm(x, weight, bias, gate, out)
+        raise ValueError("group_norm: arguments do not fit together")
+    if out is None:
+        out = _empty(shape, dtype, x.device, stream)
+    n_tok, n_groups, size = shape
+    row = n_groups * size
+    act = _act(activation) if activation is not None else int(gate is not None)
+    rc = (_lib or lib()).qsa_group_norm_packed(_NORM_ARGS(
+        x.data_ptr(), xs[0] if n_tok > 1 else row, _at(gate), (gate.stride(0) if n_tok > 1 else row) if gate is not None else 0,
+        _TYPE[dtype], _at(weight), _at(bias), _TYPE[wt], at is not None and len(at) == 2, n_tok, n_groups, size, eps,
+        bool(centred), act, out.data_ptr(), out.stride(0) if n_tok > 1 else row, _stream_of(stream, dev)))
+    if rc != QSA_OK:
+        raise QsaError("qsa_group_norm", rc)
+    return out
 
 
 def decode_status(word: int) -> list:
