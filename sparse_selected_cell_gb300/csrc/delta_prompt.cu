@@ -1,94 +1,836 @@
 // delta_prompt.cu -- the gated delta rule over the new tokens of several sequences (qsa_delta_prompt).
 //
-// The simplest form: a block to (sequence, value head, quarter of the value dims) holds its
-// part of the state in registers and goes through the tokens one by one,
-//     new = beta (v - alpha S k),  S = alpha S + new k^T,  out = S q.
-// Eight threads to a state row, 16 key dims each.  Bound by the chain of tokens.
+// The rule token by token,
+//     S_t = alpha_t S_{t-1} + v'_t k_t^T,  v'_t = beta_t (v_t - alpha_t S_{t-1} k_t),  o_t = S_t q_t,
+// solved for chunks of C = 64 tokens.  With G_i the sum of log alpha over the chunk's tokens up
+// to i, D_ij = exp(G_i - G_j) for i >= j (never above 1), and rows of V', V, K, Q by token,
+//     V' = (I + A)^-1 diag(beta) X,   X = V - exp(G) (K S^T),   A_ij = beta_i D_ij k_i.k_j (i > j),
+//     O  = exp(G) (Q S^T) + P V',     P_ij = D_ij q_i.k_j (i >= j),
+//     S' = exp(G_C) S + sum_j exp(G_C - G_j) v'_j k_j^T.
+// The first kernel (delta_prep_kernel) forms what does not need the state, for all chunks at
+// once: T = (I + A)^-1 diag(beta), P, the keys and queries as FP16 operands, and the factors
+// of each token.  The second (delta_chunk_kernel) goes through a sequence's chunks.
+//
+// Numbers.  Keys and queries enter as their FP16 selves times a power of two for each row
+// (exact but for elements 2^-33 of the row's largest); their lengths, 1 / |k|, are factors of
+// columns and rows in FP32.  The state, X, V' and T are pairs of FP16, hi + lo (22 bits), in
+// products of which lo lo is left out; the state itself stays in FP32 registers.  All products
+// are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
+// the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
+// passes FP16's range and what counts stays in its upper bits.  P and V' in P V' are single FP16.
 #include "linear.cuh"
+#include "tc_ptx.cuh"
 
 namespace qsa {
 namespace {
 
-__device__ __forceinline__ float sum8(float x) {
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+constexpr int kC = 64;                               // tokens of a chunk
+
+// ---------------------------------------------------------------- workspace
+// Chunk c of sequence s has place first / 64 + s + c, first being the sequence's first token:
+// places never meet, and none passes n_tok / 64 + n_seq.
+constexpr uint32_t kKqBytes = 2 * kC * kHeadDim * 2; // keys, then queries: two 64-dim halves of 128 rows, 128-byte swizzle
+constexpr uint32_t kTriBytes = kC * kC * 2;          // a 64 x 64 FP16 matrix, 128-byte swizzle
+constexpr uint32_t kOffTlo = kTriBytes, kOffP = 2 * kTriBytes, kOffScal = 3 * kTriBytes;
+constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T hi, T lo, P, the factors of each token
+constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
+constexpr float kKeyUnit = 16384.f;                  // and exp(G_C - G) / |k| of a stored key times this: 2 at most
+constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC;   // exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
+
+__device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
+
+struct Blobs {
+    uint8_t* kq;                                     // [place][n_k][kKqBytes]
+    uint8_t* head;                                   // [place][n_v][kHeadBytes]
+};
+__host__ __device__ __forceinline__ size_t places(int n_tok, int n_seq) { return (size_t)n_tok / kC + n_seq; }
+__device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
+    return Blobs{a.workspace, a.workspace + places(a.n_tok, a.n_seq) * a.n_k * kKqBytes};
 }
 
-constexpr int kWarps = 4, kRows = 32;
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
+// Two FP32 at a time.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// x + y i as FP16 pairs: hi the nearest, lo the nearest of what is left (exact before its rounding).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_f16x2(x, y);
+    float dx, dy;                                    // hi - x, one operand FP16
+    asm("{\n .reg .b16 h, l;\n mov.b32 {l, h}, %2;\n sub.rn.f32.f16 %0, l, %3;\n sub.rn.f32.f16 %1, h, %4;\n}"
+        : "=f"(dx), "=f"(dy) : "r"(hi), "f"(x), "f"(y));
+    lo = pack_f16x2(-dx, -dy);
+}
+
+// Byte offset of 16-byte word j of row r in a tile of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// ================================================================ what does not need the state
+constexpr int kPrepThreads = 128;
+constexpr int kAStride = 68;                         // floats to a row of A
+constexpr uint32_t kPrepA = kKqBytes, kPrepVec = kPrepA + 2 * kC * kAStride * 4;
+constexpr uint32_t kPrepBytes = kPrepVec + (2 * kC + 2 * 3 * kC) * 4 + 1024;
+
+// Column `col` of (I + A)^-1 of an N x N block of A (strictly lower, rows kAStride apart), by substitution.
+template <int N>
+__device__ __forceinline__ void solve(const float* A, int col, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        f2 acc[2] = {0ull, 0ull};
+        float rest = 0.f;
+#pragma unroll
+        for (int j = 0; j + 3 < i; j += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(A + i * kAStride + j);
+            acc[0] = fma2(pair(w.x, w.y), pair(x[j], x[j + 1]), acc[0]);
+            acc[1] = fma2(pair(w.z, w.w), pair(x[j + 2], x[j + 3]), acc[1]);
+        }
+#pragma unroll
+        for (int j = i & ~3; j < i; ++j) rest = fmaf(A[i * kAStride + j], x[j], rest);
+        float a0, a1, b0, b1;
+        unpair(acc[0], a0, a1);
+        unpair(acc[1], b0, b1);
+        x[i] = (i == col ? 1.f : 0.f) - ((a0 + a1) + (b0 + b1) + rest);
+    }
+}
 
 template <int TYPE>
-__global__ void __launch_bounds__(32 * kWarps) delta_prompt_kernel(const __grid_constant__ DeltaArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7;
-    const unsigned item = blockIdx.x / 4, s = item / (unsigned)a.n_v, h = item - s * (unsigned)a.n_v;
-    const int row0 = (int)(blockIdx.x & 3) * kRows + warp * 8 + (lane >> 3);
+__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_u - raw_u);
+    float* s_A = reinterpret_cast<float*>(base + kPrepA);
+    float* s_r = reinterpret_cast<float*>(base + kPrepVec);          // 1 / |k|, 1 / |q| of the FP16 rows
+    float* s_g = s_r + 2 * kC;                                       // [head of the pair][hi, lo of G in powers of two; beta][kC]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int place = (int)(blockIdx.x / (unsigned)a.n_k), kh = (int)(blockIdx.x - (unsigned)place * (unsigned)a.n_k);
     wait_for_stream();
+    // the last sequence whose places begin here or before (every warp for itself)
+    int s;
+    {
+        int lo = 0, len = a.n_seq;                   // the first sequence whose places begin behind this one: in [lo, lo + len]
+        while (len > 0) {
+            const int step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
+            const bool behind = at >= lo + len || place_of(min(max(a.cu_tokens[at], 0), a.n_tok), at) > place;
+            const unsigned there = __ballot_sync(0xffffffffu, behind);
+            const int f = there ? __ffs(there) - 1 : 32;
+            const int from = min(lo + f * step, lo + len);
+            len = min(lo + f * step + step - 1, lo + len) - from;
+            lo = from;
+        }
+        s = lo - 1;
+    }
+    if (s < 0) return;
     const int slot = a.state_slots[s];
-    const int2 span = tokens_of(a.cu_tokens, (int)s, a.n_tok);
-    if (h == 0 && (blockIdx.x & 3) == 0 && threadIdx.x == 0) {
-        if (tokens_bad(a.cu_tokens, (int)s, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
-        if (slot >= a.n_slots) report(a.dev_status, QSA_DEV_BAD_STATE);
-    }
     if (slot < 0 || slot >= a.n_slots) return;
-    const bool fresh = a.old_lens && a.old_lens[s] <= 0;
-    const int kh = (int)h / (a.n_v / a.n_k);
-    float* state = a.state + ((size_t)slot * a.n_v + h) * kHeadDim * kHeadDim;
-    float st[2][16];
+    const int2 span = tokens_of(a.cu_tokens, s, a.n_tok);
+    const int first = span.x + (place - place_of(span.x, s)) * kC, n = min(kC, span.y - first);
+    if (first < span.x || n <= 0) return;
+    const Blobs w = blobs_of(a);
+    uint8_t* kq = w.kq + ((size_t)place * a.n_k + kh) * kKqBytes;
+
+    // ---- keys and queries to FP16 rows, each times the power of two that puts its length in [2^13, 2^14)
+    {
+        const int l = lane & 15;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+        for (int half = 0; half < 2; ++half) {
+            uint4 raw[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[p][i] = fresh ? 0.f : state[(row0 + 4 * p) * kHeadDim + 16 * l + i];
-    for (long long t = span.x; t < span.y; ++t) {
-        float k[16], q[16], kk = 0.f, qq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            k[i] = to_f32(a.k[t * a.k_stride + (size_t)kh * kHeadDim + 16 * l + i], TYPE);
-            q[i] = to_f32(a.q[t * a.q_stride + (size_t)kh * kHeadDim + 16 * l + i], TYPE);
-            kk = fmaf(k[i], k[i], kk);
-            qq = fmaf(q[i], q[i], qq);
-        }
-        const float rk = __frsqrt_rn(sum8(kk) + a.eps), rq = __frsqrt_rn(sum8(qq) + a.eps) * a.scale;
-        const float alpha = expf(log_decay(to_f32(a.a[t * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]));
-        const float beta = sigmoid(to_f32(a.b[t * a.b_stride + h], TYPE));
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float sk = 0.f, sq = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                st[p][i] *= alpha;
-                sk = fmaf(st[p][i], k[i], sk);
+            for (int p = 0; p < 8; ++p) {
+                const int r = 2 * (4 * (8 * half + p) + warp) + (lane >> 4), t = r & (kC - 1);   // rows 0..63 keys, 64.. queries
+                const uint16_t* src = r < kC ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
+                raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * l) : make_uint4(0, 0, 0, 0);
             }
-            const float v = to_f32(a.v[t * a.v_stride + (size_t)h * kHeadDim + row0 + 4 * p], TYPE);
-            const float fresh_v = beta * (v - sum8(sk) * rk) * rk;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                st[p][i] = fmaf(fresh_v, k[i], st[p][i]);
-                sq = fmaf(st[p][i], q[i], sq);
+            for (int p = 0; p < 8; ++p) {
+                const int r = 2 * (4 * (8 * half + p) + warp) + (lane >> 4), t = r & (kC - 1);
+                float x[8], m = 0.f, ss = 0.f;
+                unpack8(raw[p], TYPE, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                // (a row of zeros is any power of two of itself: one that leaves 1 / |k| small)
+                const float pre = m < 0x1p-100f ? 0x1p40f : 1.f;
+                int e = m > 0.f ? 13 - f32_exponent(m * pre) : 60;
+                const float up = exp2i(e);
+                if (pre != 1.f) e += 40;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[j] *= pre, x[j] *= up;
+                    ss = fmaf(x[j], x[j], ss);
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const int less = ss >= 0x1p28f ? (f32_exponent(ss) >> 1) - 13 : 0;   // the largest element is in [2^13, 2^14)
+                e -= less;
+                ss *= exp2i(-2 * less);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= exp2i(-less);
+                const uint4 h = pack8(x, QSA_F16);
+                const uint32_t at = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r, l & 7);
+                *reinterpret_cast<uint4*>(base + at) = h;
+                *reinterpret_cast<uint4*>(kq + at) = h;
+                if (l == 0) s_r[r] = t < n ? __frsqrt_rn(ss + ldexpf(a.eps, 2 * e)) : 0.f;
             }
-            sq = sum8(sq) * rq;
-            if (l == 0) a.out[t * a.out_stride + (size_t)h * kHeadDim + row0 + 4 * p] = (uint16_t)pack2(sq, 0.f, TYPE);
         }
     }
-    if (span.x == span.y && !fresh) return;
+    __syncthreads();
+    // ---- K K^T and Q K^T: a warp has rows 16 warp .. + 15 of both, columns up to the diagonal
+    float kk[8][4], qk[8][4];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) state[(row0 + 4 * p) * kHeadDim + 16 * l + i] = st[p][i];
+        for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t tile = base_u + (uint32_t)(k >> 2) * (kKqBytes / 2);
+        uint32_t ak[4], aq[4];
+        ldmatrix4(tile + swz(16 * warp + (lane & 15), 2 * (k & 3) + (lane >> 4)), ak);
+        ldmatrix4(tile + swz(kC + 16 * warp + (lane & 15), 2 * (k & 3) + (lane >> 4)), aq);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p > warp) continue;
+            uint32_t b[4];
+            ldmatrix4(tile + swz(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * (k & 3) + ((lane >> 3) & 1)), b);
+            mma16816(kk[2 * p], ak, b[0], b[1]);
+            mma16816(kk[2 * p + 1], ak, b[2], b[3]);
+            mma16816(qk[2 * p], aq, b[0], b[1]);
+            mma16816(qk[2 * p + 1], aq, b[2], b[3]);
+        }
+    }
+    // ---- two value heads at a time
+    const int rep = a.n_v / a.n_k;
+    for (int h0 = 0; h0 < rep; h0 += 2) {
+        const int mine = h0 + (warp >> 1);           // the head whose gates and inverse this warp has
+        const int h = kh * rep + mine;
+        uint8_t* blob = w.head + ((size_t)place * a.n_v + h) * kHeadBytes;
+        if (mine < rep && (warp & 1) == 0) {
+            // two tokens to a lane; G in powers of two, summed in FP64, clamped where a factor is long zero
+            double g[2];
+            float beta[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                g[i] = 0.0, beta[i] = 0.f;
+                if (t < n) {
+                    const long long at = first + t;
+                    const float x = log_decay(to_f32(a.a[at * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]);
+                    g[i] = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
+                    beta[i] = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
+                }
+            }
+            double sum = g[0] + g[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            const double G[2] = {sum - g[1], sum}, last = __shfl_sync(0xffffffffu, sum, 31);
+            float* scal = reinterpret_cast<float*>(blob + kOffScal);
+            float* vec = s_g + (warp >> 1) * 3 * kC;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const float hi = (float)G[i], lo = (float)(G[i] - (double)hi), from = exp2f(hi) * (1.f + lo * 0.69314718f);
+                vec[t] = hi, vec[kC + t] = lo, vec[2 * kC + t] = beta[i];
+                scal[kScalF + t] = from * s_r[t];
+                scal[kScalD + t] = exp2f((float)(last - G[i])) * s_r[t] * kKeyUnit;
+                scal[kScalO + t] = from * s_r[kC + t];
+            }
+            if (lane == 0) scal[kScalG] = exp2f((float)last);
+        }
+        __syncthreads();                             // also: every warp has read the keys and queries in shared memory
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            if (h0 + hh >= rep) continue;
+            const float* vec = s_g + hh * 3 * kC;
+            float* A = s_A + hh * kC * kAStride;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 16 * warp + (lane >> 2) + 8 * e;
+                const float ghi = vec[i], glo = vec[kC + i], ka = vec[2 * kC + i] * s_r[i], qa = s_r[kC + i] * kTriUnit;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if (t > 2 * warp + 1) continue;
+                    float av[2], pv[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = 8 * t + 2 * (lane & 3) + u;
+                        const float d = fast_exp2((ghi - vec[j]) + (glo - vec[kC + j])) * s_r[j];
+                        av[u] = j < i ? kk[t][2 * e + u] * ka * d : 0.f;
+                        pv[u] = j <= i ? qk[t][2 * e + u] * qa * d : 0.f;
+                    }
+                    const int j = 8 * t + 2 * (lane & 3);
+                    *reinterpret_cast<float2*>(A + i * kAStride + j) = make_float2(av[0], av[1]);
+                    *reinterpret_cast<uint32_t*>(base + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) = pack_f16x2(pv[0], pv[1]);
+                }
+            }
+        }
+        tc::fence_proxy_async();
+        __syncthreads();
+        if (tid == 0) {
+            for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + hh * kTriBytes, kTriBytes);
+            bulk_commit();
+        }
+        const int col = 32 * (warp & 1) + lane;
+        const float* A = s_A + (warp >> 1) * kC * kAStride;
+        const float bc = s_g[(warp >> 1) * 3 * kC + 2 * kC + col] * kTriUnit;
+        uint8_t* T = base + (warp >> 1) * 2 * kTriBytes;
+        auto put = [&](int i, float x) {
+            const __half hi = __float2half_rn(x * bc), lo = __float2half_rn(x * bc - __half2float(hi));
+            const uint32_t at = swz(i, col >> 3) + 2 * (col & 7);
+            *reinterpret_cast<__half*>(T + at) = hi;
+            *reinterpret_cast<__half*>(T + kOffTlo + at) = lo;
+        };
+        if (warp & 1) {                              // columns from 32 on: rows from 32 on
+            float x[kC / 2];
+            if (mine < rep) solve<kC / 2>(A + (kC / 2) * kAStride + kC / 2, lane, x);
+            if (tid == 0) bulk_wait_read();
+            __syncthreads();                         // P has left
+            if (mine < rep) {
+#pragma unroll
+                for (int i = 0; i < kC / 2; ++i) put(kC / 2 + i, x[i]);
+            }
+        } else {
+            float x[kC];
+            if (mine < rep) solve<kC>(A, lane, x);
+            if (tid == 0) bulk_wait_read();
+            __syncthreads();
+            if (mine < rep) {
+#pragma unroll
+                for (int i = 0; i < kC; ++i) put(i, x[i]);
+            }
+        }
+        tc::fence_proxy_async();
+        __syncthreads();
+        if (tid == 0) {
+            for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * 2 * kTriBytes, 2 * kTriBytes);
+            bulk_commit();
+            if (h0 + 2 < rep) bulk_wait_read();
+        }
+        if (h0 + 2 < rep) __syncthreads();           // T has left, the gates have been read
+    }
+    if (tid == 0) bulk_wait();
+}
+
+// ================================================================ the chunks of a sequence
+//
+// A block has one sequence and value head.  Everything is transposed: the 128 value dims are
+// the tensor core's rows (Tensor Memory's lanes), tokens or key dims its columns, so that a
+// thread of the state warps owns a value dim: its state row stays in the thread's registers,
+// and whatever passes from one product to the next is a thread's own row, read from the
+// accumulator and written back as the next one's A operand, with no exchange at all.
+//   state warps (0-3)     S (FP32 registers) -> pair;  X^T = V^T - (S K^T) f -> pair;
+//                         V'^T -> pair with each token's decay, and once in FP16;  S = g S + D
+//   output warps (4-7)    O^T = (S Q^T) o + V'^T P^T, to the type, to rows of tokens
+//   warp 8                issues all products:  S K^T (hi, lo), S Q^T (hi, lo), V'^T = X^T T^T (hi hi, lo hi, hi lo),
+//                         D = V'^T K (hi, lo), V'^T P^T
+//   warp 9                copies a chunk's operands ahead, two stages
+// The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
+// the first quarter of its operand is there.
+constexpr int kChunkThreads = 384;
+constexpr int kStages = 2;
+constexpr uint32_t kStageV = kKqBytes + kHeadBytes, kStageBytes = kStageV + kC * kHeadDim * 2;
+constexpr uint32_t kOffOut = kStages * kStageBytes;                  // [output warp][token][32 dims]
+constexpr uint32_t kOffPow = kOffOut + 4 * kC * 64;                  // [chunk & 1][value dim]: 1 / the units of S Q^T and of V' P^T
+constexpr uint32_t kOffBar = kOffPow + 2 * kHeadDim * 8;
+enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_S = BAR_EMPTY + kStages, BAR_X = BAR_S + 4, BAR_D = BAR_X + 4, BAR_KS = BAR_D + 4,
+       BAR_V, BAR_U, BAR_H, BAR_O, BAR_OFREE, BAR_DRAIN, NUM_BARS };
+constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
+constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
+static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
+constexpr uint64_t kWaitNs = 1000000000ull;
+// Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo; D, a chunk's addition to the
+// state, comes to the same columns once the products with S are done.  X and, after V' is formed, V' with decays: hi, lo.
+constexpr uint32_t kTmS = 0, kTmKs = 128, kTmQs = 192, kTmX = 256, kTmH = 320, kTmPv = 352, kTmV = 416;
+
+struct Block {
+    const DeltaArgs* a;
+    uint8_t* base;
+    uint32_t base_u, tmem;
+    volatile int* abort_flag;
+    int s, h, slot, first, n_tok, n_chunks;
+    bool fresh;
+};
+__device__ __forceinline__ uint32_t bar(const Block& c, int i) { return c.base_u + kOffBar + 8u * i; }
+__device__ __forceinline__ bool wait(const Block& c, int i, int parity) {
+    // inline, without a call: the groups of warps have registers of their own number
+    if (tc::mbar_try_wait(bar(c, i), (uint32_t)parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        if (tc::mbar_try_wait(bar(c, i), (uint32_t)parity)) return true;
+        if ((n & 15u) == 0 && (*c.abort_flag || tc::globaltimer_ns() - t0 > kWaitNs)) break;
+    }
+    *c.abort_flag = 1;
+    report(c.a->dev_status, QSA_DEV_WAIT_TIMEOUT);
+    return false;
+}
+// The warp's stores to Tensor Memory, and its loads from it, are done: tell whoever waits on `i`.
+__device__ __forceinline__ void tell(const Block& c, int i) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, i));
+}
+
+__device__ void copy_role(const Block& c, int lane) {
+    const DeltaArgs& a = *c.a;
+    const int kh = c.h / (a.n_v / a.n_k), place0 = place_of(c.first, c.s);
+    const Blobs w = blobs_of(a);
+    int done = 0;
+    for (int i = 0; i < c.n_chunks; ++i, ++done) {
+        const int st = i % kStages;
+        if (i >= kStages && !wait(c, BAR_EMPTY + st, (i / kStages - 1) & 1)) break;
+        const int n = min(kC, c.n_tok - i * kC);
+        const uint32_t to = c.base_u + st * kStageBytes;
+        // the last chunk's missing tokens have values of zero (their factors are zero, but what lies there might be no number)
+        for (int p = lane + n * 16; p < kC * 16; p += 32)
+            *reinterpret_cast<uint4*>(c.base + st * kStageBytes + kStageV + 16 * p) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (lane == 0) {
+            mbar_expect(bar(c, BAR_FULL + st), kKqBytes + kHeadBytes + (uint32_t)n * kHeadDim * 2);
+            bulk_load(to, w.kq + ((size_t)(place0 + i) * a.n_k + kh) * kKqBytes, kKqBytes, bar(c, BAR_FULL + st));
+            bulk_load(to + kKqBytes, w.head + ((size_t)(place0 + i) * a.n_v + c.h) * kHeadBytes, kHeadBytes, bar(c, BAR_FULL + st));
+        }
+        __syncwarp();
+        for (int r = lane; r < n; r += 32)
+            bulk_load(to + kStageV + r * kHeadDim * 2, a.v + (long long)(c.first + i * kC + r) * a.v_stride + (size_t)c.h * kHeadDim,
+                      kHeadDim * 2, bar(c, BAR_FULL + st));
+    }
+    // no copy may be on its way into shared memory when the block ends
+    for (int i = max(0, done - kStages); i < done; ++i)
+        if (!tc::mbar_wait_drain(bar(c, BAR_FULL + i % kStages), (uint32_t)(i / kStages) & 1u, kWaitNs)) report(a.dev_status, QSA_DEV_WAIT_TIMEOUT);
+}
+
+__device__ void product_role(const Block& c) {
+    // FP16 operands: the type fields (bits 7 to 12) zero
+    constexpr uint32_t kTypes = ~((7u << 7) | (7u << 10));
+    constexpr uint32_t id64 = tc::idesc_bf16(128, 64, false, false) & kTypes;
+    constexpr uint32_t idD = tc::idesc_bf16(128, kHeadDim, false, true) & kTypes;       // B = keys, key dims along the row
+    const uint64_t dkq0 = tc::smem_desc(c.base_u, 16, 1024, 2), dkt0 = tc::smem_desc(c.base_u, kKqBytes / 2, 1024, 2);
+    bool ok = true;
+    for (int i = 0; i < c.n_chunks && ok; ++i) {
+        const int st = i % kStages, par = i & 1;
+        const uint64_t stage = (uint64_t)(st * kStageBytes) >> 4, tri = stage + (kKqBytes >> 4);
+        if (!(ok = wait(c, BAR_FULL + st, (i / kStages) & 1))) break;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (!(ok = wait(c, BAR_S + b, par))) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int k = 2 * b; k < 2 * b + 2; ++k) {
+                const uint64_t d = dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + (k & 3) * 32) >> 4);
+                const uint32_t at = c.tmem + kTmS + 16 * k;
+                tc::mma_ts(c.tmem + kTmKs, at, d, id64, k > 0);
+                tc::mma_ts(c.tmem + kTmKs, at + 8, d, id64, 1);
+            }
+        }
+        if (!ok) break;
+        tc::commit(bar(c, BAR_KS));
+        if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint64_t d = dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + kC * 128 + (k & 3) * 32) >> 4);
+            const uint32_t at = c.tmem + kTmS + 16 * k;
+            tc::mma_ts(c.tmem + kTmQs, at, d, id64, k > 0);
+            tc::mma_ts(c.tmem + kTmQs, at + 8, d, id64, 1);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
+            if (!(ok = wait(c, BAR_X + b, par))) break;
+            tc::fence_after_sync();
+            const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
+            const uint64_t d = dkq0 + tri + ((b * 2048 + b * 32) >> 4);
+            const uint32_t at = c.tmem + kTmX + 8 * b, to = c.tmem + kTmV + 16 * b;
+            tc::mma_ts(to, at, d, id, b > 0);
+            tc::mma_ts(to, at + 32, d, id, 1);
+            tc::mma_ts(to, at, d + (kOffTlo >> 4), id, 1);
+        }
+        if (!ok) break;
+        tc::commit(bar(c, BAR_V));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (!(ok = wait(c, BAR_D + b, par))) break;
+            tc::fence_after_sync();
+            const uint64_t d = dkt0 + stage + ((b * 2048) >> 4);
+            tc::mma_ts(c.tmem + kTmS, c.tmem + kTmX + 8 * b, d, idD, b > 0);
+            tc::mma_ts(c.tmem + kTmS, c.tmem + kTmX + 32 + 8 * b, d, idD, 1);
+        }
+        if (!ok) break;
+        tc::commit(bar(c, BAR_U));
+        if (!(ok = wait(c, BAR_H, par))) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
+            tc::mma_ts(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4), id, b > 0);
+        }
+        tc::commit(bar(c, BAR_O));
+        tc::commit(bar(c, BAR_EMPTY + st));
+    }
+    // every product issued above must be complete before Tensor Memory is released
+    tc::commit(bar(c, BAR_DRAIN));
+    if (!tc::mbar_wait_drain(bar(c, BAR_DRAIN), 0, kWaitNs)) report(c.a->dev_status, QSA_DEV_WAIT_TIMEOUT);
+}
+
+// This thread's value dim of a chunk's values, two tokens to a word, and the largest of them.
+template <int TYPE>
+__device__ __forceinline__ float read_values(const uint8_t* stage, int r, uint32_t (&v)[32]) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(stage + kStageV) + r;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint32_t x = p[(2 * j) * kHeadDim], y = p[(2 * j + 1) * kHeadDim];
+        v[j] = x | (y << 16);
+        m = fmax3(m, fabsf(to_f32((uint16_t)x, TYPE)), fabsf(to_f32((uint16_t)y, TYPE)));
+    }
+    return m;
+}
+template <int TYPE>
+__device__ __forceinline__ void both(uint32_t w, float& x, float& y) {
+    x = to_f32((uint16_t)(w & 0xFFFFu), TYPE);
+    y = to_f32((uint16_t)(w >> 16), TYPE);
+}
+
+// 2^(14 - e) for x in [2^e, 2^(e+1)): what brings x below 2^15.
+__device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_exponent(x), -100)); }
+
+template <int TYPE>
+__device__ void state_role(const Block& c, int r, uint32_t lanes) {
+    const DeltaArgs& a = *c.a;
+    float* row = a.state + (((size_t)c.slot * a.n_v + c.h) * kHeadDim + r) * kHeadDim;
+    float2* pows = reinterpret_cast<float2*>(c.base + kOffPow) + r;
+    f2 s[64];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float4 x = c.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(row)[i];
+        s[2 * i] = pair(x.x, x.y);
+        s[2 * i + 1] = pair(x.z, x.w);
+    }
+    if (!wait(c, BAR_FULL, 0)) return;
+    uint32_t v[32];
+    float vm = read_values<TYPE>(c.base, r, v);
+    float gc = 1.f, v_up = 0.f;                      // the chunk's decay, and 1 / the unit of its new values
+    const uint32_t tm = c.tmem + lanes;
+    for (int i = 0; i < c.n_chunks; ++i) {
+        const int st = i % kStages, par = i & 1;
+        const uint8_t* stage = c.base + st * kStageBytes;
+        // ---- the state after the chunk before
+        if (i > 0) {
+            const f2 g2 = pair(gc, gc), u2 = pair(v_up, v_up);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                uint32_t d[16];
+                tc::tmem_ld16(tm + kTmS + 16 * b, d);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[8 * b + j] = fma2(u2, pair(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), mul2(g2, s[8 * b + j]));
+            }
+        }
+        float sm = 0.f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            float x, y;
+            unpair(s[j], x, y);
+            sm = fmax3(sm, fabsf(x), fabsf(y));
+        }
+        // ---- the powers of two of this chunk: for S; for X, |x| <= |v| + |S|; for V', |v'| <= |v| + |S| + the values before
+        const float s_unit = unit_of(sm), x_unit = unit_of(fmaf(12.f, sm, vm)), v_unit = 0.5f * unit_of(fmaf(12.f, sm, 66.f * vm));
+        const f2 s2 = pair(s_unit, s_unit);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float x, y;
+                    unpair(mul2(s2, s[16 * b + 8 * e + j]), x, y);
+                    split2(x, y, hi[j], lo[j]);
+                }
+                tmem_st8(tm + kTmS + 32 * b + 16 * e, hi);
+                tmem_st8(tm + kTmS + 32 * b + 16 * e + 8, lo);
+            }
+            tc::tmem_wait_st();
+            tell(c, BAR_S + b);
+        }
+        const float* scal = reinterpret_cast<const float*>(stage + kKqBytes + kOffScal);
+        gc = scal[kScalG];
+        const float s_up = 1.f / s_unit, xs = -(x_unit * s_up), vx = v_unit / x_unit * (1.f / kTriUnit);
+        pows[(i & 1) * kHeadDim] = make_float2(s_up, 1.f / v_unit * (1.f / kTriUnit));
+        v_up = 1.f / v_unit * (1.f / kKeyUnit);
+        // ---- X = V - f (S K^T)
+        if (!wait(c, BAR_KS, par)) return;
+        tc::fence_after_sync();
+        const f2 xs2 = pair(xs, xs), xu2 = pair(x_unit, x_unit);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t ks[16], hi[8], lo[8];
+            tc::tmem_ld16(tm + kTmKs + 16 * b, ks);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const f2 f = *reinterpret_cast<const f2*>(scal + kScalF + 16 * b + 2 * j);
+                float x, y;
+                both<TYPE>(v[8 * b + j], x, y);
+                const f2 t = fma2(mul2(f, xs2), pair(__uint_as_float(ks[2 * j]), __uint_as_float(ks[2 * j + 1])), mul2(pair(x, y), xu2));
+                unpair(t, x, y);
+                split2(x, y, hi[j], lo[j]);
+            }
+            tmem_st8(tm + kTmX + 8 * b, hi);
+            tmem_st8(tm + kTmX + 32 + 8 * b, lo);
+            tc::tmem_wait_st();
+            tell(c, BAR_X + b);
+        }
+        // ---- V', with each token's decay to the chunk's end
+        if (!wait(c, BAR_V, par)) return;
+        tc::fence_after_sync();
+        const f2 vx2 = pair(vx, vx);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t w[16], hi[8], lo[8], one[8];
+            tc::tmem_ld16(tm + kTmV + 16 * b, w);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const f2 d = *reinterpret_cast<const f2*>(scal + kScalD + 16 * b + 2 * j);
+                const f2 p = mul2(vx2, pair(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])));
+                float x, y;
+                unpair(p, x, y);
+                one[j] = pack_f16x2(x, y);
+                unpair(mul2(p, d), x, y);
+                split2(x, y, hi[j], lo[j]);
+            }
+            tmem_st8(tm + kTmX + 8 * b, hi);
+            tmem_st8(tm + kTmX + 32 + 8 * b, lo);
+            tmem_st8(tm + kTmH + 8 * b, one);
+            tc::tmem_wait_st();
+            tell(c, BAR_D + b);
+        }
+        tell(c, BAR_H);
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));   // this chunk's values and factors have been read
+        // ---- the next chunk's values, while the products run
+        if (i + 1 < c.n_chunks) {
+            const int nx = (i + 1) % kStages;
+            if (!wait(c, BAR_FULL + nx, ((i + 1) / kStages) & 1)) return;
+            vm = read_values<TYPE>(c.base + nx * kStageBytes, r, v);
+        }
+        if (!wait(c, BAR_U, par)) return;
+        tc::fence_after_sync();
+    }
+    const f2 g2 = pair(gc, gc), u2 = pair(v_up, v_up);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        uint32_t d[16];
+        tc::tmem_ld16(tm + kTmS + 16 * b, d);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float4 o;
+            unpair(fma2(u2, pair(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1])), mul2(g2, s[8 * b + 2 * j])), o.x, o.y);
+            unpair(fma2(u2, pair(__uint_as_float(d[4 * j + 2]), __uint_as_float(d[4 * j + 3])), mul2(g2, s[8 * b + 2 * j + 1])), o.z, o.w);
+            reinterpret_cast<float4*>(row)[4 * b + j] = o;
+        }
+    }
+}
+
+template <int TYPE>
+__device__ void output_role(const Block& c, int q, int lane) {
+    const DeltaArgs& a = *c.a;
+    uint16_t* mine = reinterpret_cast<uint16_t*>(c.base + kOffOut) + q * kC * 32;
+    const float2* pows = reinterpret_cast<const float2*>(c.base + kOffPow) + 32 * q + lane;
+    const uint32_t tm = c.tmem + ((uint32_t)q << 21);
+    for (int i = 0; i < c.n_chunks; ++i) {
+        const int st = i % kStages, par = i & 1;
+        const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + kScalO;
+        if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_H, par) || !wait(c, BAR_O, par)) return;
+        tc::fence_after_sync();
+        const float2 unit = pows[(i & 1) * kHeadDim];
+        const float us = unit.x * a.scale, uv = unit.y * a.scale;
+        uint32_t out[32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t qs[16], pv[16];
+            tc::tmem_ld16(tm + kTmQs + 16 * b, qs);
+            tc::tmem_ld16(tm + kTmPv + 16 * b, pv);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 o = *reinterpret_cast<const float2*>(scal + 16 * b + 2 * j);
+                out[8 * b + j] = pack2(fmaf(o.x * us, __uint_as_float(qs[2 * j]), uv * __uint_as_float(pv[2 * j])),
+                                       fmaf(o.y * us, __uint_as_float(qs[2 * j + 1]), uv * __uint_as_float(pv[2 * j + 1])), TYPE);
+            }
+        }
+        tell(c, BAR_OFREE);
+        if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            mine[(2 * j) * 32 + lane] = (uint16_t)(out[j] & 0xFFFFu);
+            mine[(2 * j + 1) * 32 + lane] = (uint16_t)(out[j] >> 16);
+        }
+        __syncwarp();
+        const int n = min(kC, c.n_tok - i * kC);
+        uint16_t* to = a.out + (long long)(c.first + i * kC) * a.out_stride + (size_t)c.h * kHeadDim + 32 * q + 8 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int t = 8 * j + (lane >> 2);
+            if (t < n) *reinterpret_cast<uint4*>(to + (long long)t * a.out_stride) = *reinterpret_cast<const uint4*>(mine + t * 32 + 8 * (lane & 3));
+        }
+        __syncwarp();
+    }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
+    Block c;
+    c.a = &a;
+    c.base = smem_raw + (base_u - raw_u);
+    c.base_u = base_u;
+    c.abort_flag = reinterpret_cast<volatile int*>(c.base + kOffMisc + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    c.s = (int)(blockIdx.x / (unsigned)a.n_v);
+    c.h = (int)(blockIdx.x - (unsigned)c.s * (unsigned)a.n_v);
+    wait_for_stream();
+    c.slot = a.state_slots[c.s];
+    const int2 span = tokens_of(a.cu_tokens, c.s, a.n_tok);
+    if (c.h == 0 && tid == 0) {
+        if (tokens_bad(a.cu_tokens, c.s, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
+        if (c.slot >= a.n_slots) report(a.dev_status, QSA_DEV_BAD_STATE);
+    }
+    if (c.slot < 0 || c.slot >= a.n_slots) return;
+    c.first = span.x;
+    c.n_tok = span.y - span.x;
+    c.n_chunks = (c.n_tok + kC - 1) / kC;
+    c.fresh = a.old_lens && a.old_lens[c.s] <= 0;
+    if (c.n_chunks == 0) {
+        if (c.fresh) {
+            float4* st = reinterpret_cast<float4*>(a.state + ((size_t)c.slot * a.n_v + c.h) * kHeadDim * kHeadDim);
+            for (int i = tid; i < kHeadDim * kHeadDim / 4; i += kChunkThreads) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(c.base + kOffMisc);
+    if (tid == 0) {
+        for (int st = 0; st < kStages; ++st) {
+            tc::mbar_init(bar(c, BAR_FULL + st), 1);
+            tc::mbar_init(bar(c, BAR_EMPTY + st), 9);          // the products', the state warps' and the output warps' last use
+        }
+        for (int b = 0; b < 4; ++b) {
+            tc::mbar_init(bar(c, BAR_S + b), 4);
+            tc::mbar_init(bar(c, BAR_X + b), 4);
+            tc::mbar_init(bar(c, BAR_D + b), 4);
+        }
+        tc::mbar_init(bar(c, BAR_KS), 1);
+        tc::mbar_init(bar(c, BAR_V), 1);
+        tc::mbar_init(bar(c, BAR_U), 1);
+        tc::mbar_init(bar(c, BAR_H), 4);
+        tc::mbar_init(bar(c, BAR_O), 1);
+        tc::mbar_init(bar(c, BAR_OFREE), 4);
+        tc::mbar_init(bar(c, BAR_DRAIN), 1);
+        *c.abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 8) {
+        tc::tmem_alloc(smem_u32(tmem_holder), 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    c.tmem = *tmem_holder;
+    // registers from the launch's 384 x 168: 248 + 112 + 80 for the three groups of four warps
+    if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 248;");
+        state_role<TYPE>(c, tid, (uint32_t)warp << 21);
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        output_role<TYPE>(c, warp - 4, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 8) {
+            if (lane == 0) product_role(c);
+        } else if (warp == 9) {
+            copy_role(c, lane);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(c.tmem, 512);
+    }
+}
+
+template <int TYPE>
+cudaError_t launch(const DeltaArgs& a, cudaStream_t stream) {
+    const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, chunks = (long long)a.n_seq * a.n_v;
+    if (prep > 0x7fffffffLL || chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_chunk_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkBytes);
+    if (e != cudaSuccess) return e;
+    if (a.n_tok > 0) {
+        e = launch_overlapped(delta_prep_kernel<TYPE>, dim3((unsigned)prep), kPrepThreads, kPrepBytes, stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(delta_chunk_kernel<TYPE>, dim3((unsigned)chunks), kChunkThreads, kChunkBytes, stream, a);
 }
 
 }  // namespace
 
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v) {
-    const size_t chunks = (size_t)n_tok / 64 + n_seq + 1;
-    return chunks * ((size_t)n_k * 32768 + (size_t)n_v * 28672) + 256;
+    return places(n_tok, n_seq) * ((size_t)n_k * kKqBytes + (size_t)n_v * kHeadBytes) + 256;
 }
 
 cudaError_t launch_delta_prompt(const DeltaArgs& a, cudaStream_t stream) {
-    const long long grid = (long long)a.n_seq * a.n_v * 4;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (a.type == QSA_F16)
-        return launch_overlapped(delta_prompt_kernel<QSA_F16>, dim3((unsigned)grid), 32 * kWarps, 0, stream, a);
-    return launch_overlapped(delta_prompt_kernel<QSA_BF16>, dim3((unsigned)grid), 32 * kWarps, 0, stream, a);
+    return a.type == QSA_F16 ? launch<QSA_F16>(a, stream) : launch<QSA_BF16>(a, stream);
 }
 
 }  // namespace qsa
