@@ -35,7 +35,7 @@ constexpr uint32_t kOffTlo = kTriBytes, kOffP = 2 * kTriBytes, kOffScal = 3 * kT
 constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T hi, T lo, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
 constexpr float kKeyUnit = 16384.f;                  // and exp(G_C - G) / |k| of a stored key times this: 2 at most
-constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC;   // exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
+constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC;   // -exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
 
 __device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
 
@@ -95,14 +95,29 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     return r;
 }
 
-// x + y i as FP16 pairs: hi the nearest, lo the nearest of what is left (exact before its rounding).
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = pack_f16x2(x, y);
-    float dx, dy;                                    // hi - x, one operand FP16
-    asm("{\n .reg .b16 h, l;\n mov.b32 {l, h}, %2;\n sub.rn.f32.f16 %0, l, %3;\n sub.rn.f32.f16 %1, h, %4;\n}"
-        : "=f"(dx), "=f"(dy) : "r"(hi), "f"(x), "f"(y));
-    lo = pack_f16x2(-dx, -dy);
+// D (+)= A B^T, A in Tensor Memory, issued by the lane that has `leader` set (one of a converged warp).
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add, uint32_t leader) {
+    if (add)
+        asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+                     " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
+                     ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader) : "memory");
+    else
+        asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 t, 0, 0;\n"
+                     " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
+                     ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader) : "memory");
 }
+
+// x and y as FP16 pairs: hi the nearest, lo the nearest of what is left (x - hi is exact).
+__device__ __forceinline__ void split2(f2 p, uint32_t& hi, uint32_t& lo) {
+    float x, y;
+    unpair(p, x, y);
+    hi = pack_f16x2(x, y);
+    asm("{\n .reg .b16 h, l, m;\n mov.b32 {l, h}, %2;\n mov.b16 m, 0xBC00;\n"
+        " fma.rn.f32.f16 %0, l, m, %3;\n fma.rn.f32.f16 %1, h, m, %4;\n}"
+        : "=f"(x), "=f"(y) : "r"(hi), "f"(x), "f"(y));
+    lo = pack_f16x2(x, y);
+}
+__device__ __forceinline__ f2 pair_of(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
 
 // Byte offset of 16-byte word j of row r in a tile of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
                 const int t = 2 * lane + i;
                 const float hi = (float)G[i], lo = (float)(G[i] - (double)hi), from = exp2f(hi) * (1.f + lo * 0.69314718f);
                 vec[t] = hi, vec[kC + t] = lo, vec[2 * kC + t] = beta[i];
-                scal[kScalF + t] = from * s_r[t];
+                scal[kScalF + t] = -from * s_r[t];
                 scal[kScalD + t] = exp2f((float)(last - G[i])) * s_r[t] * kKeyUnit;
                 scal[kScalO + t] = from * s_r[kC + t];
             }
@@ -364,29 +379,35 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
 // thread of the state warps owns a value dim: its state row stays in the thread's registers,
 // and whatever passes from one product to the next is a thread's own row, read from the
 // accumulator and written back as the next one's A operand, with no exchange at all.
-//   state warps (0-3)     S (FP32 registers) -> pair;  X^T = V^T - (S K^T) f -> pair;
+//   state warps (0-7)     two warps to 32 value dims, each with half the key dims and half the tokens:
+//                         S (FP32 registers) -> pair;  X^T = V^T - (S K^T) f -> pair;
 //                         V'^T -> pair with each token's decay, and once in FP16;  S = g S + D
-//   output warps (4-7)    O^T = (S Q^T) o + V'^T P^T, to the type, to rows of tokens
-//   warp 8                issues all products:  S K^T (hi, lo), S Q^T (hi, lo), V'^T = X^T T^T (hi hi, lo hi, hi lo),
+//   output warps (8-11)   O^T = (S Q^T) o + V'^T P^T, to the type, to rows of tokens
+//   warp 12               issues all products:  S K^T (hi, lo), S Q^T (hi, lo), V'^T = X^T T^T (hi hi, lo hi, hi lo),
 //                         D = V'^T K (hi, lo), V'^T P^T
-//   warp 9                copies a chunk's operands ahead, two stages
+//   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
-// the first quarter of its operand is there.
-constexpr int kChunkThreads = 384;
-constexpr int kStages = 2;
-constexpr uint32_t kStageV = kKqBytes + kHeadBytes, kStageBytes = kStageV + kC * kHeadDim * 2;
-constexpr uint32_t kOffOut = kStages * kStageBytes;                  // [output warp][token][32 dims]
+// the first quarter of its operand is there, and S Q^T is issued in the pauses.
+constexpr int kChunkThreads = 512;
+constexpr int kStages = 3, kVStages = 2;
+constexpr uint32_t kStageBytes = kKqBytes + kHeadBytes, kVBytes = kC * kHeadDim * 2;
+constexpr uint32_t kOffV = kStages * kStageBytes;
+constexpr uint32_t kOffOut = kOffV + kVStages * kVBytes;             // [output warp][token][32 dims]
 constexpr uint32_t kOffPow = kOffOut + 4 * kC * 64;                  // [chunk & 1][value dim]: 1 / the units of S Q^T and of V' P^T
-constexpr uint32_t kOffBar = kOffPow + 2 * kHeadDim * 8;
-enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_S = BAR_EMPTY + kStages, BAR_X = BAR_S + 4, BAR_D = BAR_X + 4, BAR_KS = BAR_D + 4,
+constexpr uint32_t kOffTop = kOffPow + 2 * kHeadDim * 8;             // [chunk & 1][half][value dim]: largest value; then largest of S
+constexpr uint32_t kOffBar = kOffTop + 2 * 2 * 2 * kHeadDim * 4;
+enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kStages, BAR_VEMPTY = BAR_VFULL + kVStages,
+       BAR_S = BAR_VEMPTY + kVStages, BAR_X = BAR_S + 4, BAR_D = BAR_X + 4, BAR_TOP = BAR_D + 4, BAR_KS = BAR_TOP + 4,
        BAR_V, BAR_U, BAR_H, BAR_O, BAR_OFREE, BAR_DRAIN, NUM_BARS };
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
 constexpr uint64_t kWaitNs = 1000000000ull;
-// Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo; D, a chunk's addition to the
-// state, comes to the same columns once the products with S are done.  X and, after V' is formed, V' with decays: hi, lo.
-constexpr uint32_t kTmS = 0, kTmKs = 128, kTmQs = 192, kTmX = 256, kTmH = 320, kTmPv = 352, kTmV = 416;
+// Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
+// products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' in FP16 lies where S K^T was, V' P^T where V' was.
+constexpr uint32_t kTmS = 0, kTmKs = 128, kTmH = 128, kTmQs = 192, kTmX = 256, kTmV = 320, kTmPv = 320, kTmD = 384;
+// The quarters of an operand in the order in which they are there: each half's first, each half's second.
+__device__ __forceinline__ constexpr int quarter(int i) { return i == 1 ? 2 : i == 2 ? 1 : i; }
 
 struct Block {
     const DeltaArgs* a;
@@ -425,27 +446,43 @@ __device__ void copy_role(const Block& c, int lane) {
     for (int i = 0; i < c.n_chunks; ++i, ++done) {
         const int st = i % kStages;
         if (i >= kStages && !wait(c, BAR_EMPTY + st, (i / kStages - 1) & 1)) break;
-        const int n = min(kC, c.n_tok - i * kC);
-        const uint32_t to = c.base_u + st * kStageBytes;
-        // the last chunk's missing tokens have values of zero (their factors are zero, but what lies there might be no number)
-        for (int p = lane + n * 16; p < kC * 16; p += 32)
-            *reinterpret_cast<uint4*>(c.base + st * kStageBytes + kStageV + 16 * p) = make_uint4(0, 0, 0, 0);
-        __syncwarp();
         if (lane == 0) {
-            mbar_expect(bar(c, BAR_FULL + st), kKqBytes + kHeadBytes + (uint32_t)n * kHeadDim * 2);
+            const uint32_t to = c.base_u + st * kStageBytes;
+            mbar_expect(bar(c, BAR_FULL + st), kStageBytes);
             bulk_load(to, w.kq + ((size_t)(place0 + i) * a.n_k + kh) * kKqBytes, kKqBytes, bar(c, BAR_FULL + st));
             bulk_load(to + kKqBytes, w.head + ((size_t)(place0 + i) * a.n_v + c.h) * kHeadBytes, kHeadBytes, bar(c, BAR_FULL + st));
         }
         __syncwarp();
-        for (int r = lane; r < n; r += 32)
-            bulk_load(to + kStageV + r * kHeadDim * 2, a.v + (long long)(c.first + i * kC + r) * a.v_stride + (size_t)c.h * kHeadDim,
-                      kHeadDim * 2, bar(c, BAR_FULL + st));
     }
     // no copy may be on its way into shared memory when the block ends
     for (int i = max(0, done - kStages); i < done; ++i)
         if (!tc::mbar_wait_drain(bar(c, BAR_FULL + i % kStages), (uint32_t)(i / kStages) & 1u, kWaitNs)) report(a.dev_status, QSA_DEV_WAIT_TIMEOUT);
 }
 
+// The values' rows lie a token's stride apart, 256 bytes each: by a warp's 16-byte copies (as 64 bulk copies a chunk they were
+// what the chain waited for, 6,000 instead of 4,000 cycles a chunk).
+__device__ void value_role(const Block& c, int lane) {
+    const DeltaArgs& a = *c.a;
+    const uint16_t* v = a.v + (long long)c.first * a.v_stride + (size_t)c.h * kHeadDim + 8 * (lane & 15);
+    for (int i = 0; i < c.n_chunks; ++i) {
+        const int vs = i % kVStages;
+        if (i >= kVStages && !wait(c, BAR_VEMPTY + vs, (i / kVStages - 1) & 1)) break;
+        const uint32_t to = c.base_u + kOffV + vs * kVBytes + lane * 16;
+#pragma unroll 8
+        for (int p = 0; p < kC / 2; ++p) {
+            // tokens that the last chunk does not have are filled with zeros (their factors are zero, but what lies there might be no number)
+            const int t = i * kC + 2 * p + (lane >> 4);
+            const bool there = t < c.n_tok;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(to + p * 512), "l"(v + (long long)(there ? t : 0) * a.v_stride), "r"(there ? 16 : 0) : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(c, BAR_VFULL + vs)) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The whole warp runs this, and one elected lane issues, so that descriptors and addresses stay in uniform registers: a
+// 64-column product then takes 35 cycles; issued by a thread alone, 53, whatever its columns.
 __device__ void product_role(const Block& c) {
     // FP16 operands: the type fields (bits 7 to 12) zero
     constexpr uint32_t kTypes = ~((7u << 7) | (7u << 10));
@@ -453,78 +490,82 @@ __device__ void product_role(const Block& c) {
     constexpr uint32_t idD = tc::idesc_bf16(128, kHeadDim, false, true) & kTypes;       // B = keys, key dims along the row
     const uint64_t dkq0 = tc::smem_desc(c.base_u, 16, 1024, 2), dkt0 = tc::smem_desc(c.base_u, kKqBytes / 2, 1024, 2);
     bool ok = true;
+    uint32_t leader;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(leader));
+    auto with_queries = [&](uint64_t stage, int lo) {       // S Q^T, of the hi or the lo
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            product(c.tmem + kTmQs, c.tmem + kTmS + 16 * k + lo,
+                             dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + kC * 128 + (k & 3) * 32) >> 4), id64, k > 0 || lo, leader);
+    };
     for (int i = 0; i < c.n_chunks && ok; ++i) {
         const int st = i % kStages, par = i & 1;
         const uint64_t stage = (uint64_t)(st * kStageBytes) >> 4, tri = stage + (kKqBytes >> 4);
         if (!(ok = wait(c, BAR_FULL + st, (i / kStages) & 1))) break;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (!(ok = wait(c, BAR_S + b, par))) break;
+        for (int n = 0; n < 4; ++n) {
+            if (!(ok = wait(c, BAR_S + quarter(n), par))) break;
             tc::fence_after_sync();
 #pragma unroll
-            for (int k = 2 * b; k < 2 * b + 2; ++k) {
+            for (int k = 2 * quarter(n); k < 2 * quarter(n) + 2; ++k) {
                 const uint64_t d = dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + (k & 3) * 32) >> 4);
-                const uint32_t at = c.tmem + kTmS + 16 * k;
-                tc::mma_ts(c.tmem + kTmKs, at, d, id64, k > 0);
-                tc::mma_ts(c.tmem + kTmKs, at + 8, d, id64, 1);
+                product(c.tmem + kTmKs, c.tmem + kTmS + 16 * k, d, id64, k > 0, leader);
+                product(c.tmem + kTmKs, c.tmem + kTmS + 16 * k + 8, d, id64, true, leader);
             }
         }
         if (!ok) break;
-        tc::commit(bar(c, BAR_KS));
+        tc::commit_elect(bar(c, BAR_KS));
         if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
         tc::fence_after_sync();
+        with_queries(stage, 0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint64_t d = dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + kC * 128 + (k & 3) * 32) >> 4);
-            const uint32_t at = c.tmem + kTmS + 16 * k;
-            tc::mma_ts(c.tmem + kTmQs, at, d, id64, k > 0);
-            tc::mma_ts(c.tmem + kTmQs, at + 8, d, id64, 1);
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
+        for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
+            const int b = quarter(n);
             if (!(ok = wait(c, BAR_X + b, par))) break;
             tc::fence_after_sync();
             const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
             const uint64_t d = dkq0 + tri + ((b * 2048 + b * 32) >> 4);
             const uint32_t at = c.tmem + kTmX + 8 * b, to = c.tmem + kTmV + 16 * b;
-            tc::mma_ts(to, at, d, id, b > 0);
-            tc::mma_ts(to, at + 32, d, id, 1);
-            tc::mma_ts(to, at, d + (kOffTlo >> 4), id, 1);
+            product(to, at, d, id, b > 0, leader);
+            product(to, at + 32, d, id, true, leader);
+            product(to, at, d + (kOffTlo >> 4), id, true, leader);
         }
         if (!ok) break;
-        tc::commit(bar(c, BAR_V));
+        tc::commit_elect(bar(c, BAR_V));
+        with_queries(stage, 8);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int n = 0; n < 4; ++n) {
+            const int b = quarter(n);
             if (!(ok = wait(c, BAR_D + b, par))) break;
             tc::fence_after_sync();
             const uint64_t d = dkt0 + stage + ((b * 2048) >> 4);
-            tc::mma_ts(c.tmem + kTmS, c.tmem + kTmX + 8 * b, d, idD, b > 0);
-            tc::mma_ts(c.tmem + kTmS, c.tmem + kTmX + 32 + 8 * b, d, idD, 1);
+            product(c.tmem + kTmD, c.tmem + kTmX + 8 * b, d, idD, true, leader);
+            product(c.tmem + kTmD, c.tmem + kTmX + 32 + 8 * b, d, idD, true, leader);
         }
         if (!ok) break;
-        tc::commit(bar(c, BAR_U));
+        tc::commit_elect(bar(c, BAR_U));
         if (!(ok = wait(c, BAR_H, par))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
-            tc::mma_ts(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4), id, b > 0);
+            product(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4), id, b > 0, leader);
         }
-        tc::commit(bar(c, BAR_O));
-        tc::commit(bar(c, BAR_EMPTY + st));
+        tc::commit_elect(bar(c, BAR_O));
+        tc::commit_elect(bar(c, BAR_EMPTY + st));
     }
     // every product issued above must be complete before Tensor Memory is released
-    tc::commit(bar(c, BAR_DRAIN));
+    tc::commit_elect(bar(c, BAR_DRAIN));
     if (!tc::mbar_wait_drain(bar(c, BAR_DRAIN), 0, kWaitNs)) report(c.a->dev_status, QSA_DEV_WAIT_TIMEOUT);
 }
 
-// This thread's value dim of a chunk's values, two tokens to a word, and the largest of them.
+// This thread's value dim of half a chunk's values, two tokens to a word, and the largest of them.
 template <int TYPE>
-__device__ __forceinline__ float read_values(const uint8_t* stage, int r, uint32_t (&v)[32]) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(stage + kStageV) + r;
+__device__ __forceinline__ float read_values(const uint8_t* values, int half, int r, uint32_t (&v)[16]) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(values) + half * (kC / 2) * kHeadDim + r;
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 16; ++j) {
         const uint32_t x = p[(2 * j) * kHeadDim], y = p[(2 * j + 1) * kHeadDim];
         v[j] = x | (y << 16);
         m = fmax3(m, fabsf(to_f32((uint16_t)x, TYPE)), fabsf(to_f32((uint16_t)y, TYPE)));
@@ -538,144 +579,193 @@ __device__ __forceinline__ void both(uint32_t w, float& x, float& y) {
 }
 
 // 2^(14 - e) for x in [2^e, 2^(e+1)): what brings x below 2^15.
-__device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_exponent(x), -100)); }
+__device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_exponent(x), -80)); }
 
 template <int TYPE>
-__device__ void state_role(const Block& c, int r, uint32_t lanes) {
+__device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
     const DeltaArgs& a = *c.a;
-    float* row = a.state + (((size_t)c.slot * a.n_v + c.h) * kHeadDim + r) * kHeadDim;
+    float4* row = reinterpret_cast<float4*>(a.state + (((size_t)c.slot * a.n_v + c.h) * kHeadDim + r) * kHeadDim + half * (kHeadDim / 2));
     float2* pows = reinterpret_cast<float2*>(c.base + kOffPow) + r;
-    f2 s[64];
+    float* top_v = reinterpret_cast<float*>(c.base + kOffTop) + r;           // + 256 (chunk & 1) + 128 half
+    float* top_s = top_v + 4 * kHeadDim;
+    const int q = (int)(lanes >> 21);
+    const uint32_t tm = c.tmem + lanes, tmS = tm + kTmS + 64 * half, tmD = tm + kTmD + 64 * half, tmT = tm + 32 * half;
+    float sm = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float4 x = c.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(row)[i];
-        s[2 * i] = pair(x.x, x.y);
-        s[2 * i + 1] = pair(x.z, x.w);
+    for (int b = 0; b < 2; ++b) {
+        uint32_t d[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 x = c.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : row[8 * b + j];
+            d[4 * j] = __float_as_uint(x.x), d[4 * j + 1] = __float_as_uint(x.y);
+            d[4 * j + 2] = __float_as_uint(x.z), d[4 * j + 3] = __float_as_uint(x.w);
+            sm = fmax3(sm, fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+        }
+        tc::tmem_st32(tmD + 32 * b, d);
     }
-    if (!wait(c, BAR_FULL, 0)) return;
-    uint32_t v[32];
-    float vm = read_values<TYPE>(c.base, r, v);
-    float gc = 1.f, v_up = 0.f;                      // the chunk's decay, and 1 / the unit of its new values
-    const uint32_t tm = c.tmem + lanes;
+    tc::tmem_wait_st();
+    if (!wait(c, BAR_VFULL, 0)) return;
+    uint32_t v[16];
+    float vm = read_values<TYPE>(c.base + kOffV, half, r, v);
+    // both halves' largest value of the chunk to come, and of the state before the chunk in hand
+    auto publish = [&](int i) {
+        top_v[(i & 1) * 256 + half * 128] = vm;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            tc::mbar_arrive(bar(c, BAR_VEMPTY + i % kVStages));
+            tc::mbar_arrive(bar(c, BAR_TOP + q));
+        }
+    };
+    // The powers of two of chunk i, from bounds: the state row's length before it by the largest element one chunk earlier (12)
+    // and that chunk's values; |x| <= |v| + |S|; |v'| <= |v| + |S| + the values before it, and no state row gets longer than
+    // that.  Then the chunk's values in units.
+    float d_up = 1.f, vm_before = 0.f;               // 1 / the unit of D, the largest value of the chunk before
+    float unit = 1.f, v_unit = 1.f;                  // of S and X; of V'
+    f2 x2[16];
+    auto settle = [&](int i) {
+        const int par = i & 1;
+        if (!wait(c, BAR_TOP + q, par)) return false;
+        vm = fmaxf(vm, top_v[par * 256 + (half ^ 1) * 128]);
+        sm = fmaxf(sm, top_s[(par ^ 1) * 256 + (half ^ 1) * 128]);
+        const float len = fmaf(12.f, sm, 66.f * vm_before);
+        unit = unit_of(len + vm), v_unit = 0.5f * unit_of(fmaf(66.f, vm, len));
+        vm_before = vm;
+        const f2 unit2 = pair(unit, unit);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float x, y;
+            both<TYPE>(v[j], x, y);
+            x2[j] = mul2(pair(x, y), unit2);
+        }
+        return true;
+    };
+    top_s[256 + half * 128] = sm;
+    publish(0);
+    if (!settle(0)) return;
     for (int i = 0; i < c.n_chunks; ++i) {
         const int st = i % kStages, par = i & 1;
-        const uint8_t* stage = c.base + st * kStageBytes;
-        // ---- the state after the chunk before
-        if (i > 0) {
-            const f2 g2 = pair(gc, gc), u2 = pair(v_up, v_up);
+        const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + 32 * half;
+        // ---- the state as the next operand
+        const f2 s2 = pair(unit * d_up, unit * d_up);
+        uint32_t d[64];
+        tc::tmem_ld32(tmD, *reinterpret_cast<uint32_t(*)[32]>(d));
+        tc::tmem_ld32(tmD + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
+        tc::tmem_wait_ld();
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                uint32_t d[16];
-                tc::tmem_ld16(tm + kTmS + 16 * b, d);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    s[8 * b + j] = fma2(u2, pair(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), mul2(g2, s[8 * b + j]));
-            }
-        }
-        float sm = 0.f;
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
-            float x, y;
-            unpair(s[j], x, y);
-            sm = fmax3(sm, fabsf(x), fabsf(y));
-        }
-        // ---- the powers of two of this chunk: for S; for X, |x| <= |v| + |S|; for V', |v'| <= |v| + |S| + the values before
-        const float s_unit = unit_of(sm), x_unit = unit_of(fmaf(12.f, sm, vm)), v_unit = 0.5f * unit_of(fmaf(12.f, sm, 66.f * vm));
-        const f2 s2 = pair(s_unit, s_unit);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                uint32_t hi[8], lo[8];
+                uint32_t w[16];                      // 8 columns of hi, 8 of lo
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float x, y;
-                    unpair(mul2(s2, s[16 * b + 8 * e + j]), x, y);
-                    split2(x, y, hi[j], lo[j]);
-                }
-                tmem_st8(tm + kTmS + 32 * b + 16 * e, hi);
-                tmem_st8(tm + kTmS + 32 * b + 16 * e + 8, lo);
+                for (int j = 0; j < 8; ++j)
+                    split2(mul2(s2, pair_of(d[32 * b + 16 * e + 2 * j], d[32 * b + 16 * e + 2 * j + 1])), w[j], w[8 + j]);
+                tc::tmem_st16(tmS + 32 * b + 16 * e, w);
             }
             tc::tmem_wait_st();
-            tell(c, BAR_S + b);
+            tell(c, BAR_S + 2 * half + b);
         }
-        const float* scal = reinterpret_cast<const float*>(stage + kKqBytes + kOffScal);
-        gc = scal[kScalG];
-        const float s_up = 1.f / s_unit, xs = -(x_unit * s_up), vx = v_unit / x_unit * (1.f / kTriUnit);
-        pows[(i & 1) * kHeadDim] = make_float2(s_up, 1.f / v_unit * (1.f / kTriUnit));
-        v_up = 1.f / v_unit * (1.f / kKeyUnit);
+        if (half == 0) pows[par * kHeadDim] = make_float2(1.f / unit, 1.f / (v_unit * kTriUnit));
         // ---- X = V - f (S K^T)
-        if (!wait(c, BAR_KS, par)) return;
+        if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_KS, par)) return;
         tc::fence_after_sync();
-        const f2 xs2 = pair(xs, xs), xu2 = pair(x_unit, x_unit);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t ks[16], hi[8], lo[8];
-            tc::tmem_ld16(tm + kTmKs + 16 * b, ks);
+        {
+            uint32_t ks[32];
+            tc::tmem_ld32(tmT + kTmKs, ks);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const f2 f = *reinterpret_cast<const f2*>(scal + kScalF + 16 * b + 2 * j);
-                float x, y;
-                both<TYPE>(v[8 * b + j], x, y);
-                const f2 t = fma2(mul2(f, xs2), pair(__uint_as_float(ks[2 * j]), __uint_as_float(ks[2 * j + 1])), mul2(pair(x, y), xu2));
-                unpair(t, x, y);
-                split2(x, y, hi[j], lo[j]);
+            for (int b = 0; b < 2; ++b) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scal + kScalF + 16 * b + 2 * j);
+                    const uint32_t* k = ks + 16 * b + 2 * j;
+                    split2(fma2(f.x, pair_of(k[0], k[1]), x2[8 * b + j]), hi[j], lo[j]);
+                    split2(fma2(f.y, pair_of(k[2], k[3]), x2[8 * b + j + 1]), hi[j + 1], lo[j + 1]);
+                }
+                tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
+                tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
+                tc::tmem_wait_st();
+                tell(c, BAR_X + 2 * half + b);
             }
-            tmem_st8(tm + kTmX + 8 * b, hi);
-            tmem_st8(tm + kTmX + 32 + 8 * b, lo);
-            tc::tmem_wait_st();
-            tell(c, BAR_X + b);
         }
+        // ---- while V' is formed: the decayed state for D, and its largest element
+        const float d_unit = v_unit * kKeyUnit, gd = scal[kScalG - 32 * half] * (d_unit * d_up);
+        const f2 g2 = pair(gd, gd);
+        sm = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t x = d[32 * b + 2 * j], y = d[32 * b + 2 * j + 1];
+                float gx, gy;
+                unpair(mul2(g2, pair_of(x, y)), gx, gy);
+                w[2 * j] = __float_as_uint(gx), w[2 * j + 1] = __float_as_uint(gy);
+                sm = fmax3(sm, fabsf(__uint_as_float(x)), fabsf(__uint_as_float(y)));
+            }
+            tc::tmem_st32(tmD + 32 * b, w);
+        }
+        sm *= d_up;
+        top_s[par * 256 + half * 128] = sm;
+        d_up = 1.f / d_unit;
+        const float vx = v_unit / unit * (1.f / kTriUnit);
         // ---- V', with each token's decay to the chunk's end
         if (!wait(c, BAR_V, par)) return;
         tc::fence_after_sync();
         const f2 vx2 = pair(vx, vx);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t w[16], hi[8], lo[8], one[8];
-            tc::tmem_ld16(tm + kTmV + 16 * b, w);
+        {
+            uint32_t w[32], one[16];
+            tc::tmem_ld32(tmT + kTmV, w);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const f2 d = *reinterpret_cast<const f2*>(scal + kScalD + 16 * b + 2 * j);
-                const f2 p = mul2(vx2, pair(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])));
-                float x, y;
-                unpair(p, x, y);
-                one[j] = pack_f16x2(x, y);
-                unpair(mul2(p, d), x, y);
-                split2(x, y, hi[j], lo[j]);
+            for (int b = 0; b < 2; ++b) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scal + kScalD + 16 * b + 2 * j);
+                    const uint32_t* k = w + 16 * b + 2 * j;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const f2 p = mul2(vx2, pair_of(k[2 * u], k[2 * u + 1]));
+                        float x, y;
+                        unpair(p, x, y);
+                        one[8 * b + j + u] = pack_f16x2(x, y);
+                        split2(mul2(p, u ? f.y : f.x), hi[j + u], lo[j + u]);
+                    }
+                }
+                tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
+                tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
+                tc::tmem_wait_st();
+                tell(c, BAR_D + 2 * half + b);
             }
-            tmem_st8(tm + kTmX + 8 * b, hi);
-            tmem_st8(tm + kTmX + 32 + 8 * b, lo);
-            tmem_st8(tm + kTmH + 8 * b, one);
+            tc::tmem_st16(tm + kTmH + 16 * half, one);
             tc::tmem_wait_st();
-            tell(c, BAR_D + b);
         }
         tell(c, BAR_H);
-        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));   // this chunk's values and factors have been read
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));   // this chunk's factors have been read
         // ---- the next chunk's values, while the products run
         if (i + 1 < c.n_chunks) {
-            const int nx = (i + 1) % kStages;
-            if (!wait(c, BAR_FULL + nx, ((i + 1) / kStages) & 1)) return;
-            vm = read_values<TYPE>(c.base + nx * kStageBytes, r, v);
+            const int nx = (i + 1) % kVStages;
+            if (!wait(c, BAR_VFULL + nx, ((i + 1) / kVStages) & 1)) return;
+            vm = read_values<TYPE>(c.base + kOffV + nx * kVBytes, half, r, v);
+            publish(i + 1);
+            if (!settle(i + 1)) return;
         }
         if (!wait(c, BAR_U, par)) return;
         tc::fence_after_sync();
     }
-    const f2 g2 = pair(gc, gc), u2 = pair(v_up, v_up);
+    const f2 up2 = pair(d_up, d_up);
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-        uint32_t d[16];
-        tc::tmem_ld16(tm + kTmS + 16 * b, d);
+    for (int b = 0; b < 2; ++b) {
+        uint32_t d[32];
+        tc::tmem_ld32(tmD + 32 * b, d);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             float4 o;
-            unpair(fma2(u2, pair(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1])), mul2(g2, s[8 * b + 2 * j])), o.x, o.y);
-            unpair(fma2(u2, pair(__uint_as_float(d[4 * j + 2]), __uint_as_float(d[4 * j + 3])), mul2(g2, s[8 * b + 2 * j + 1])), o.z, o.w);
-            reinterpret_cast<float4*>(row)[4 * b + j] = o;
+            unpair(mul2(up2, pair_of(d[4 * j], d[4 * j + 1])), o.x, o.y);
+            unpair(mul2(up2, pair_of(d[4 * j + 2], d[4 * j + 3])), o.z, o.w);
+            row[8 * b + j] = o;
         }
     }
 }
@@ -692,7 +782,7 @@ __device__ void output_role(const Block& c, int q, int lane) {
         if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_H, par) || !wait(c, BAR_O, par)) return;
         tc::fence_after_sync();
         const float2 unit = pows[(i & 1) * kHeadDim];
-        const float us = unit.x * a.scale, uv = unit.y * a.scale;
+        const f2 us2 = pair(unit.x * a.scale, unit.x * a.scale), uv2 = pair(unit.y * a.scale, unit.y * a.scale);
         uint32_t out[32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -703,8 +793,9 @@ __device__ void output_role(const Block& c, int q, int lane) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 o = *reinterpret_cast<const float2*>(scal + 16 * b + 2 * j);
-                out[8 * b + j] = pack2(fmaf(o.x * us, __uint_as_float(qs[2 * j]), uv * __uint_as_float(pv[2 * j])),
-                                       fmaf(o.y * us, __uint_as_float(qs[2 * j + 1]), uv * __uint_as_float(pv[2 * j + 1])), TYPE);
+                float x, y;
+                unpair(fma2(mul2(pair(o.x, o.y), us2), pair_of(qs[2 * j], qs[2 * j + 1]), mul2(uv2, pair_of(pv[2 * j], pv[2 * j + 1]))), x, y);
+                out[8 * b + j] = pack2(x, y, TYPE);
             }
         }
         tell(c, BAR_OFREE);
@@ -761,24 +852,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     if (tid == 0) {
         for (int st = 0; st < kStages; ++st) {
             tc::mbar_init(bar(c, BAR_FULL + st), 1);
-            tc::mbar_init(bar(c, BAR_EMPTY + st), 9);          // the products', the state warps' and the output warps' last use
+            tc::mbar_init(bar(c, BAR_EMPTY + st), 13);         // the products', the state warps' and the output warps' last use
+        }
+        for (int st = 0; st < kVStages; ++st) {
+            tc::mbar_init(bar(c, BAR_VFULL + st), 32);
+            tc::mbar_init(bar(c, BAR_VEMPTY + st), 8);
         }
         for (int b = 0; b < 4; ++b) {
             tc::mbar_init(bar(c, BAR_S + b), 4);
             tc::mbar_init(bar(c, BAR_X + b), 4);
             tc::mbar_init(bar(c, BAR_D + b), 4);
+            tc::mbar_init(bar(c, BAR_TOP + b), 2);
         }
         tc::mbar_init(bar(c, BAR_KS), 1);
         tc::mbar_init(bar(c, BAR_V), 1);
         tc::mbar_init(bar(c, BAR_U), 1);
-        tc::mbar_init(bar(c, BAR_H), 4);
+        tc::mbar_init(bar(c, BAR_H), 8);
         tc::mbar_init(bar(c, BAR_O), 1);
         tc::mbar_init(bar(c, BAR_OFREE), 4);
         tc::mbar_init(bar(c, BAR_DRAIN), 1);
         *c.abort_flag = 0;
         tc::fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == 12) {
         tc::tmem_alloc(smem_u32(tmem_holder), 512);
         tc::tmem_relinquish();
     }
@@ -786,24 +882,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     __syncthreads();
     tc::fence_after_sync();
     c.tmem = *tmem_holder;
-    // registers from the launch's 384 x 168: 248 + 112 + 80 for the three groups of four warps
-    if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 248;");
-        state_role<TYPE>(c, tid, (uint32_t)warp << 21);
-    } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-        output_role<TYPE>(c, warp - 4, lane);
+    // registers: the launch's 512 x 128 as 168 + 168 + 96 + 80 for the four groups of four warps
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        state_role<TYPE>(c, warp >> 2, tid & 127, (uint32_t)(warp & 3) << 21);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        output_role<TYPE>(c, warp - 8, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 8) {
-            if (lane == 0) product_role(c);
-        } else if (warp == 9) {
-            copy_role(c, lane);
-        }
+        if (warp == 12) product_role(c);
+        else if (warp == 13) copy_role(c, lane);
+        else if (warp == 14) value_role(c, lane);
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 12) {
         tc::fence_after_sync();
         tc::tmem_dealloc(c.tmem, 512);
     }
