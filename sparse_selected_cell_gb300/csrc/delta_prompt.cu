@@ -12,7 +12,7 @@
 // of each token.  The second (delta_chunk_kernel) goes through a sequence's chunks.
 //
 // Numbers.  Keys and queries enter as their FP16 selves times a power of two for each row
-// (exact but for elements 2^-33 of the row's largest); their lengths, 1 / |k|, are factors of
+// (exact but for elements below 2^-24 of the row's largest, which lose bits); their lengths, 1 / |k|, are factors of
 // columns and rows in FP32.  The state, X, V' and T are pairs of FP16, hi + lo (22 bits), in
 // products of which lo lo is left out; the state itself stays in FP32 registers.  All products
 // are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
@@ -34,8 +34,7 @@ constexpr uint32_t kTriBytes = kC * kC * 2;          // a 64 x 64 FP16 matrix, 1
 constexpr uint32_t kOffTlo = kTriBytes, kOffP = 2 * kTriBytes, kOffScal = 3 * kTriBytes;
 constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T hi, T lo, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
-constexpr float kKeyUnit = 16384.f;                  // and exp(G_C - G) / |k| of a stored key times this: 2 at most
-constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC;   // -exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
+constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1;   // -exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
 
 __device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
 
@@ -123,41 +122,76 @@ __device__ __forceinline__ f2 pair_of(uint32_t x, uint32_t y) { return pair(__ui
 __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
 // ================================================================ what does not need the state
+//
+// A block has a chunk of a key head and all its value heads, two at a time.  K K^T and Q K^T come from mma.sync over the FP16
+// rows (their diagonals give the lengths); (I + A)^-1 by halves of halves: the four 16 x 16 blocks on the diagonal by
+// substitution, a column to a thread, then [T11, 0; -T22 A21 T11, T22] for pairs of 16 and of 32, as products of FP16 pairs
+// (a column to a thread over all 64 rows took five times as long).
 constexpr int kPrepThreads = 128;
 constexpr int kAStride = 68;                         // floats to a row of A
 constexpr uint32_t kPrepA = kKqBytes, kPrepVec = kPrepA + 2 * kC * kAStride * 4;
-constexpr uint32_t kPrepBytes = kPrepVec + (2 * kC + 2 * 3 * kC) * 4 + 1024;
+constexpr int kVecs = 5;                             // of a value head: G's hi and lo in powers of two, beta, exp(G), exp(G_C - G)
+constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 1024;
 
 // Column `col` of (I + A)^-1 of an N x N block of A (strictly lower, rows kAStride apart), by substitution.
 template <int N>
 __device__ __forceinline__ void solve(const float* A, int col, float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        f2 acc[2] = {0ull, 0ull};
-        float rest = 0.f;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j + 3 < i; j += 4) {
+        for (int j = 0; j < i; j += 4) {
             const float4 w = *reinterpret_cast<const float4*>(A + i * kAStride + j);
-            acc[0] = fma2(pair(w.x, w.y), pair(x[j], x[j + 1]), acc[0]);
-            acc[1] = fma2(pair(w.z, w.w), pair(x[j + 2], x[j + 3]), acc[1]);
-        }
+            const float e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = i & ~3; j < i; ++j) rest = fmaf(A[i * kAStride + j], x[j], rest);
-        float a0, a1, b0, b1;
-        unpair(acc[0], a0, a1);
-        unpair(acc[1], b0, b1);
-        x[i] = (i == col ? 1.f : 0.f) - ((a0 + a1) + (b0 + b1) + rest);
+            for (int u = 0; u < 4; ++u)
+                if (j + u < i) acc[u] = fmaf(e[u], x[j + u], acc[u]);
+        }
+        x[i] = (i == col ? 1.f : 0.f) - ((acc[0] + acc[1]) + (acc[2] + acc[3]));
     }
 }
 
+// Operands of m16n8k16 as FP16 pairs from FP32 rows kAStride apart: A of 16 x 16 at M; B of 16 (k) x 8 (n) at M, M[k][n].
+struct Frag4 { uint32_t hi[4], lo[4]; };
+struct Frag2 { uint32_t hi[2], lo[2]; };
+__device__ __forceinline__ Frag4 frag_a(const float* M, int lane) {
+    Frag4 f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                    // rows lane / 4 and + 8, columns 2 (lane % 4) and + 8
+        const float2 x = *reinterpret_cast<const float2*>(M + ((lane >> 2) + 8 * (i & 1)) * kAStride + 2 * (lane & 3) + 8 * (i >> 1));
+        split2(pair(x.x, x.y), f.hi[i], f.lo[i]);
+    }
+    return f;
+}
+__device__ __forceinline__ Frag2 frag_b(const float* M, int lane) {
+    Frag2 f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float* x = M + (2 * (lane & 3) + 8 * i) * kAStride + (lane >> 2);
+        split2(pair(x[0], x[kAStride]), f.hi[i], f.lo[i]);
+    }
+    return f;
+}
+__device__ __forceinline__ void mma_pairs(float (&c)[4], const Frag4& a, const Frag2& b) {
+    mma16816(c, a.hi, b.hi[0], b.hi[1]);
+    mma16816(c, a.lo, b.hi[0], b.hi[1]);
+    mma16816(c, a.hi, b.lo[0], b.lo[1]);
+}
+__device__ __forceinline__ void put_tile(float* M, const float (&c)[4], float sign, int lane) {
+    float* at = M + (lane >> 2) * kAStride + 2 * (lane & 3);
+    *reinterpret_cast<float2*>(at) = make_float2(sign * c[0], sign * c[1]);
+    *reinterpret_cast<float2*>(at + 8 * kAStride) = make_float2(sign * c[2], sign * c[3]);
+}
+
 template <int TYPE>
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u - raw_u);
     float* s_A = reinterpret_cast<float*>(base + kPrepA);
     float* s_r = reinterpret_cast<float*>(base + kPrepVec);          // 1 / |k|, 1 / |q| of the FP16 rows
-    float* s_g = s_r + 2 * kC;                                       // [head of the pair][hi, lo of G in powers of two; beta][kC]
+    int* s_e = reinterpret_cast<int*>(s_r + 2 * kC);                 // the rows' powers of two
+    float* s_g = s_r + 4 * kC;                                       // [head of the pair][kVecs][kC]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int place = (int)(blockIdx.x / (unsigned)a.n_k), kh = (int)(blockIdx.x - (unsigned)place * (unsigned)a.n_k);
     wait_for_stream();
@@ -185,96 +219,114 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
     const Blobs w = blobs_of(a);
     uint8_t* kq = w.kq + ((size_t)place * a.n_k + kh) * kKqBytes;
 
-    // ---- keys and queries to FP16 rows, each times the power of two that puts its length in [2^13, 2^14)
+    // ---- keys and queries to FP16 rows, each times the power of two that puts its largest element in [2^10, 2^11)
     {
         const int l = lane & 15;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int part = 0; part < 2; ++part) {
             uint4 raw[8];
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const int r = 2 * (4 * (8 * half + p) + warp) + (lane >> 4), t = r & (kC - 1);   // rows 0..63 keys, 64.. queries
-                const uint16_t* src = r < kC ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
+                const int r = 2 * (4 * (8 * part + p) + warp) + (lane >> 4), t = r & (kC - 1);   // rows 0..63 keys, 64.. queries
+                const uint16_t* src = part == 0 ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
                 raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * l) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const int r = 2 * (4 * (8 * half + p) + warp) + (lane >> 4), t = r & (kC - 1);
-                float x[8], m = 0.f, ss = 0.f;
+                const int r = 2 * (4 * (8 * part + p) + warp) + (lane >> 4);
+                float x[8];
                 unpack8(raw[p], TYPE, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+                float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                // (a row of zeros is any power of two of itself: one that leaves 1 / |k| small)
-                const float pre = m < 0x1p-100f ? 0x1p40f : 1.f;
-                int e = m > 0.f ? 13 - f32_exponent(m * pre) : 60;
-                const float up = exp2i(e);
-                if (pre != 1.f) e += 40;
+                // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
+                const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = e > 100 ? 100 : e;
+                const f2 up = pair(exp2i(e1), exp2i(e1));
+                uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] *= pre, x[j] *= up;
-                    ss = fmaf(x[j], x[j], ss);
+                for (int j = 0; j < 4; ++j) {
+                    float u, w;
+                    f2 y = mul2(pair(x[2 * j], x[2 * j + 1]), up);
+                    if (e != e1) y = mul2(y, pair(exp2i(e - e1), exp2i(e - e1)));
+                    unpair(y, u, w);
+                    h[j] = pack_f16x2(u, w);
                 }
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const int less = ss >= 0x1p28f ? (f32_exponent(ss) >> 1) - 13 : 0;   // the largest element is in [2^13, 2^14)
-                e -= less;
-                ss *= exp2i(-2 * less);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= exp2i(-less);
-                const uint4 h = pack8(x, QSA_F16);
                 const uint32_t at = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r, l & 7);
-                *reinterpret_cast<uint4*>(base + at) = h;
-                *reinterpret_cast<uint4*>(kq + at) = h;
-                if (l == 0) s_r[r] = t < n ? __frsqrt_rn(ss + ldexpf(a.eps, 2 * e)) : 0.f;
+                *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (l == 0) s_e[r] = e;
             }
         }
     }
     __syncthreads();
-    // ---- K K^T and Q K^T: a warp has rows 16 warp .. + 15 of both, columns up to the diagonal
-    float kk[8][4], qk[8][4];
+    // ---- K K^T and Q K^T: a warp has rows 16 warp .. + 15 of both, columns up to the diagonal; of Q Q^T the diagonal's block
+    float kk[8][4], qk[8][4], qq[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = qq[i & 1][j] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t tile = base_u + (uint32_t)(k >> 2) * (kKqBytes / 2);
-        uint32_t ak[4], aq[4];
+        const int brow = (lane & 7) + ((lane >> 4) << 3), bword = 2 * (k & 3) + ((lane >> 3) & 1);
+        uint32_t ak[4], aq[4], b[4];
         ldmatrix4(tile + swz(16 * warp + (lane & 15), 2 * (k & 3) + (lane >> 4)), ak);
         ldmatrix4(tile + swz(kC + 16 * warp + (lane & 15), 2 * (k & 3) + (lane >> 4)), aq);
+        ldmatrix4(tile + swz(kC + 16 * warp + brow, bword), b);
+        mma16816(qq[0], aq, b[0], b[1]);
+        mma16816(qq[1], aq, b[2], b[3]);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             if (p > warp) continue;
-            uint32_t b[4];
-            ldmatrix4(tile + swz(16 * p + (lane & 7) + ((lane >> 4) << 3), 2 * (k & 3) + ((lane >> 3) & 1)), b);
+            ldmatrix4(tile + swz(16 * p + brow, bword), b);
             mma16816(kk[2 * p], ak, b[0], b[1]);
             mma16816(kk[2 * p + 1], ak, b[2], b[3]);
             mma16816(qk[2 * p], aq, b[0], b[1]);
             mma16816(qk[2 * p + 1], aq, b[2], b[3]);
         }
     }
-    // ---- two value heads at a time
+    // the diagonals: element (i, i) of a 16 x 16 block lies with lane 4 (i % 8) + (i % 8) / 2
+    if ((lane & 3) == (lane >> 3)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 16 * warp + (lane >> 2) + 8 * e;
+            float k2 = 0.f;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (p == warp) k2 = (lane >> 2) & 1 ? kk[2 * p + e][2 * e + 1] : kk[2 * p + e][2 * e];
+            const float q2 = (lane >> 2) & 1 ? qq[e][2 * e + 1] : qq[e][2 * e];
+            s_r[i] = i < n ? __frsqrt_rn(k2 + ldexpf(a.eps, 2 * s_e[i])) : 0.f;
+            s_r[kC + i] = i < n ? __frsqrt_rn(q2 + ldexpf(a.eps, 2 * s_e[kC + i])) : 0.f;
+        }
+    }
+    __syncthreads();
+    // the power of two that brings the largest 1 / |k| of a stored key into [1/2, 1): the chunk's key unit
+    float key_unit = fmaxf(s_r[lane], s_r[lane + 32]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) key_unit = fmaxf(key_unit, __shfl_xor_sync(0xffffffffu, key_unit, o));
+    key_unit = exp2i(min(max(-1 - f32_exponent(key_unit), 9), 16));   // (of lengths from 2^10 to 2^14.5, or of rows that eps outweighs)
+    // ---- two value heads at a time: warps 0, 1 and 2, 3
     const int rep = a.n_v / a.n_k;
     for (int h0 = 0; h0 < rep; h0 += 2) {
-        const int mine = h0 + (warp >> 1);           // the head whose gates and inverse this warp has
-        const int h = kh * rep + mine;
+        const int mine = h0 + (warp >> 1), h = kh * rep + mine;
+        const bool has = mine < rep;
         uint8_t* blob = w.head + ((size_t)place * a.n_v + h) * kHeadBytes;
-        if (mine < rep && (warp & 1) == 0) {
+        float* vec = s_g + (warp >> 1) * kVecs * kC;
+        if (has && (warp & 1) == 0) {
             // two tokens to a lane; G in powers of two, summed in FP64, clamped where a factor is long zero
             double g[2];
-            float beta[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                g[i] = 0.0, beta[i] = 0.f;
+                float beta = 0.f;
+                g[i] = 0.0;
                 if (t < n) {
                     const long long at = first + t;
                     const float x = log_decay(to_f32(a.a[at * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]);
                     g[i] = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
-                    beta[i] = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
+                    beta = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
                 }
+                vec[2 * kC + t] = beta;
             }
             double sum = g[0] + g[1];
 #pragma unroll
@@ -283,43 +335,47 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
                 if (lane >= o) sum += up;
             }
             const double G[2] = {sum - g[1], sum}, last = __shfl_sync(0xffffffffu, sum, 31);
-            float* scal = reinterpret_cast<float*>(blob + kOffScal);
-            float* vec = s_g + (warp >> 1) * 3 * kC;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                const float hi = (float)G[i], lo = (float)(G[i] - (double)hi), from = exp2f(hi) * (1.f + lo * 0.69314718f);
-                vec[t] = hi, vec[kC + t] = lo, vec[2 * kC + t] = beta[i];
-                scal[kScalF + t] = -from * s_r[t];
-                scal[kScalD + t] = exp2f((float)(last - G[i])) * s_r[t] * kKeyUnit;
-                scal[kScalO + t] = from * s_r[kC + t];
+                const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
+                vec[t] = hi, vec[kC + t] = lo;
+                vec[3 * kC + t] = exp2f(hi) * (1.f + lo * 0.69314718f);
+                vec[4 * kC + t] = exp2f((float)(last - G[i]));
             }
-            if (lane == 0) scal[kScalG] = exp2f((float)last);
+            if (lane == 0) {
+                reinterpret_cast<float*>(blob + kOffScal)[kScalG] = exp2f((float)last);
+                reinterpret_cast<float*>(blob + kOffScal)[kScalU] = key_unit;
+            }
         }
         __syncthreads();                             // also: every warp has read the keys and queries in shared memory
+        if (has) {
+            const int t = tid & (kC - 1);            // each token's factors, by a head's 64 threads
+            float* scal = reinterpret_cast<float*>(blob + kOffScal);
+            scal[kScalF + t] = -vec[3 * kC + t] * s_r[t];
+            scal[kScalD + t] = vec[4 * kC + t] * (s_r[t] * key_unit);
+            scal[kScalO + t] = vec[3 * kC + t] * s_r[kC + t];
+        }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             if (h0 + hh >= rep) continue;
-            const float* vec = s_g + hh * 3 * kC;
+            const float* ve = s_g + hh * kVecs * kC;
             float* A = s_A + hh * kC * kAStride;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 16 * warp + (lane >> 2) + 8 * e;
-                const float ghi = vec[i], glo = vec[kC + i], ka = vec[2 * kC + i] * s_r[i], qa = s_r[kC + i] * kTriUnit;
+                const float ghi = ve[i], glo = ve[kC + i], ka = ve[2 * kC + i] * s_r[i], qa = s_r[kC + i] * kTriUnit;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     if (t > 2 * warp + 1) continue;
-                    float av[2], pv[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int j = 8 * t + 2 * (lane & 3) + u;
-                        const float d = fast_exp2((ghi - vec[j]) + (glo - vec[kC + j])) * s_r[j];
-                        av[u] = j < i ? kk[t][2 * e + u] * ka * d : 0.f;
-                        pv[u] = j <= i ? qk[t][2 * e + u] * qa * d : 0.f;
-                    }
                     const int j = 8 * t + 2 * (lane & 3);
-                    *reinterpret_cast<float2*>(A + i * kAStride + j) = make_float2(av[0], av[1]);
-                    *reinterpret_cast<uint32_t*>(base + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) = pack_f16x2(pv[0], pv[1]);
+                    const float2 gj = *reinterpret_cast<const float2*>(ve + j), lj = *reinterpret_cast<const float2*>(ve + kC + j);
+                    const float2 rj = *reinterpret_cast<const float2*>(s_r + j);
+                    const float d0 = fast_exp2((ghi - gj.x) + (glo - lj.x)) * rj.x, d1 = fast_exp2((ghi - gj.y) + (glo - lj.y)) * rj.y;
+                    *reinterpret_cast<float2*>(A + i * kAStride + j) =
+                        make_float2(j < i ? kk[t][2 * e] * ka * d0 : 0.f, j + 1 < i ? kk[t][2 * e + 1] * ka * d1 : 0.f);
+                    *reinterpret_cast<uint32_t*>(base + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
+                        pack_f16x2(j <= i ? qk[t][2 * e] * qa * d0 : 0.f, j + 1 <= i ? qk[t][2 * e + 1] * qa * d1 : 0.f);
                 }
             }
         }
@@ -330,33 +386,90 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(const __grid_c
                 bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + hh * kTriBytes, kTriBytes);
             bulk_commit();
         }
-        const int col = 32 * (warp & 1) + lane;
-        const float* A = s_A + (warp >> 1) * kC * kAStride;
-        const float bc = s_g[(warp >> 1) * 3 * kC + 2 * kC + col] * kTriUnit;
-        uint8_t* T = base + (warp >> 1) * 2 * kTriBytes;
-        auto put = [&](int i, float x) {
-            const __half hi = __float2half_rn(x * bc), lo = __float2half_rn(x * bc - __half2float(hi));
-            const uint32_t at = swz(i, col >> 3) + 2 * (col & 7);
-            *reinterpret_cast<__half*>(T + at) = hi;
-            *reinterpret_cast<__half*>(T + kOffTlo + at) = lo;
-        };
-        if (warp & 1) {                              // columns from 32 on: rows from 32 on
-            float x[kC / 2];
-            if (mine < rep) solve<kC / 2>(A + (kC / 2) * kAStride + kC / 2, lane, x);
-            if (tid == 0) bulk_wait_read();
-            __syncthreads();                         // P has left
-            if (mine < rep) {
+        // ---- (I + A)^-1 of the warp pair's head, in A's place
+        float* A = s_A + (warp >> 1) * kC * kAStride;
+        const int side = warp & 1;
+        if (has) {
+            // the diagonal's blocks 2 side and 2 side + 1, a column to a thread
+            float* D = A + (32 * side + (lane & 16)) * (kAStride + 1);
+            float x[16];
+            solve<16>(D, lane & 15, x);
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kC / 2; ++i) put(kC / 2 + i, x[i]);
+            for (int i = 0; i < 16; ++i) D[i * kAStride + (lane & 15)] = x[i];
+            __syncwarp();
+            // the pair of them: T21 = -T22 (A21 T11)
+            D = A + 32 * side * (kAStride + 1);
+            float* A21 = D + 16 * kAStride;
+            const float* T22 = A21 + 16;
+            float y[2][4] = {}, z[2][4] = {};
+            const Frag4 fa = frag_a(A21, lane);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma_pairs(y[t], fa, frag_b(D + 8 * t, lane));
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) put_tile(A21 + 8 * t, y[t], 1.f, lane);
+            __syncwarp();
+            const Frag4 ft = frag_a(T22, lane);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma_pairs(z[t], ft, frag_b(A21 + 8 * t, lane));
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) put_tile(A21 + 8 * t, z[t], -1.f, lane);
+        }
+        __syncthreads();
+        {
+            // the halves: rows 32 + 16 side .. of A21 T11 (T11's block above the diagonal is zero), then of -T22 times that
+            float* A21 = A + (32 + 16 * side) * kAStride;
+            float y[4][4] = {};
+            if (has) {
+                const Frag4 f0 = frag_a(A21, lane), f1 = frag_a(A21 + 16, lane);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (t < 2) mma_pairs(y[t], f0, frag_b(A + 8 * t, lane));
+                    mma_pairs(y[t], f1, frag_b(A + 16 * kAStride + 8 * t, lane));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int t = 0; t < 4; ++t) put_tile(A21 + 8 * t, y[t], 1.f, lane);
             }
-        } else {
-            float x[kC];
-            if (mine < rep) solve<kC>(A, lane, x);
-            if (tid == 0) bulk_wait_read();
             __syncthreads();
-            if (mine < rep) {
+            float z[4][4] = {};
+            if (has) {
+                const Frag4 f0 = frag_a(A21 + 32, lane);
 #pragma unroll
-                for (int i = 0; i < kC; ++i) put(i, x[i]);
+                for (int t = 0; t < 4; ++t) mma_pairs(z[t], f0, frag_b(A + 32 * kAStride + 8 * t, lane));
+                if (side) {
+                    const Frag4 f1 = frag_a(A21 + 48, lane);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) mma_pairs(z[t], f1, frag_b(A + 48 * kAStride + 8 * t, lane));
+                }
+            }
+            if (tid == 0) bulk_wait_read();
+            __syncthreads();                         // P has left; both warps have read the product
+            if (has) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) put_tile(A21 + 8 * t, z[t], -1.f, lane);
+            }
+        }
+        __syncthreads();
+        if (has) {
+            // times beta of the column, as pairs: a thread has row tid % 64, eight columns at a time up to the diagonal's block
+            const int i = tid & (kC - 1);
+            uint8_t* T = base + (warp >> 1) * 2 * kTriBytes;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                if (t > 4 * side + 3) continue;      // rows up to 31 end in column 31 at most; what lies above the diagonal's blocks is not read
+                const float4 x = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t), y = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t + 4);
+                const float4 b0 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t), b1 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t + 4);
+                const f2 u = pair(kTriUnit, kTriUnit);
+                uint4 hi, lo;
+                split2(mul2(mul2(pair(x.x, x.y), pair(b0.x, b0.y)), u), hi.x, lo.x);
+                split2(mul2(mul2(pair(x.z, x.w), pair(b0.z, b0.w)), u), hi.y, lo.y);
+                split2(mul2(mul2(pair(y.x, y.y), pair(b1.x, b1.y)), u), hi.z, lo.z);
+                split2(mul2(mul2(pair(y.z, y.w), pair(b1.z, b1.w)), u), hi.w, lo.w);
+                *reinterpret_cast<uint4*>(T + swz(i, t)) = hi;
+                *reinterpret_cast<uint4*>(T + kOffTlo + swz(i, t)) = lo;
             }
         }
         tc::fence_proxy_async();
@@ -628,7 +741,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         vm = fmaxf(vm, top_v[par * 256 + (half ^ 1) * 128]);
         sm = fmaxf(sm, top_s[(par ^ 1) * 256 + (half ^ 1) * 128]);
         const float len = fmaf(12.f, sm, 66.f * vm_before);
-        unit = unit_of(len + vm), v_unit = 0.5f * unit_of(fmaf(66.f, vm, len));
+        unit = unit_of(len + vm), v_unit = unit_of(fmaf(66.f, vm, len));
         vm_before = vm;
         const f2 unit2 = pair(unit, unit);
 #pragma unroll
@@ -689,7 +802,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
             }
         }
         // ---- while V' is formed: the decayed state for D, and its largest element
-        const float d_unit = v_unit * kKeyUnit, gd = scal[kScalG - 32 * half] * (d_unit * d_up);
+        const float d_unit = v_unit * scal[kScalU - 32 * half], gd = scal[kScalG - 32 * half] * (d_unit * d_up);
         const f2 g2 = pair(gd, gd);
         sm = 0.f;
 #pragma unroll
