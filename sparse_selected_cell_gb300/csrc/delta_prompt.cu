@@ -129,7 +129,9 @@ __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 12
 // (a column to a thread over all 64 rows took five times as long).
 constexpr int kPrepThreads = 128;
 constexpr int kAStride = 68;                         // floats to a row of A
-constexpr uint32_t kPrepA = kKqBytes, kPrepVec = kPrepA + 2 * kC * kAStride * 4;
+// Shared memory: keys and queries, then two heads' A, then their T in A's place; P; the tokens' factors.
+constexpr uint32_t kABytes = kC * kAStride * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kTriBytes;
+static_assert(kPrepP >= kKqBytes && kABytes % 1024 == 0, "A's place");
 constexpr int kVecs = 5;                             // of a value head: G's hi and lo in powers of two, beta, exp(G), exp(G_C - G)
 constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 1024;
 
@@ -183,12 +185,13 @@ __device__ __forceinline__ void put_tile(float* M, const float (&c)[4], float si
     *reinterpret_cast<float2*>(at + 8 * kAStride) = make_float2(sign * c[2], sign * c[3]);
 }
 
-template <int TYPE>
-__global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
+// MORE: more than two value heads to a key head, so that the Gram matrices outlive the first two's inverses.
+template <int TYPE, bool MORE>
+__global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(const __grid_constant__ DeltaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u - raw_u);
-    float* s_A = reinterpret_cast<float*>(base + kPrepA);
+    float* s_A = reinterpret_cast<float*>(base);
     float* s_r = reinterpret_cast<float*>(base + kPrepVec);          // 1 / |k|, 1 / |q| of the FP16 rows
     int* s_e = reinterpret_cast<int*>(s_r + 2 * kC);                 // the rows' powers of two
     float* s_g = s_r + 4 * kC;                                       // [head of the pair][kVecs][kC]
@@ -219,43 +222,80 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __gri
     const Blobs w = blobs_of(a);
     uint8_t* kq = w.kq + ((size_t)place * a.n_k + kh) * kKqBytes;
 
+    uint4 raw[16];                                   // row 2 (4 p + warp) + lane / 16 of 64 keys, then 64 queries
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+        const int t = (2 * (4 * p + warp) + (lane >> 4)) & (kC - 1);
+        const uint16_t* src = p < 8 ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
+        raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * (lane & 15)) : make_uint4(0, 0, 0, 0);
+    }
+    // ---- the decays of two value heads, by a warp each: two tokens to a lane; G in powers of two, summed in FP64, clamped
+    // where a factor is long zero
+    const int rep = a.n_v / a.n_k;
+    auto gates = [&](int h0) {
+        const int mine = h0 + (warp >> 1), h = kh * rep + mine;
+        if (mine >= rep || (warp & 1)) return;
+        float* vec = s_g + (warp >> 1) * kVecs * kC;
+        double g[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            float beta = 0.f;
+            g[i] = 0.0;
+            if (t < n) {
+                const long long at = first + t;
+                const float x = log_decay(to_f32(a.a[at * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]);
+                g[i] = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
+                beta = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
+            }
+            vec[2 * kC + t] = beta;
+        }
+        double sum = g[0] + g[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        const double G[2] = {sum - g[1], sum}, last = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
+            vec[t] = hi, vec[kC + t] = lo;
+            vec[3 * kC + t] = exp2f(hi) * (1.f + lo * 0.69314718f);
+            vec[4 * kC + t] = exp2f((float)(last - G[i]));
+        }
+        if (lane == 0)
+            reinterpret_cast<float*>(w.head + ((size_t)place * a.n_v + h) * kHeadBytes + kOffScal)[kScalG] = exp2f((float)last);
+    };
+    gates(0);
     // ---- keys and queries to FP16 rows, each times the power of two that puts its largest element in [2^10, 2^11)
     {
         const int l = lane & 15;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            uint4 raw[8];
+        for (int p = 0; p < 16; ++p) {
+            const int r = 2 * (4 * p + warp) + (lane >> 4);
+            float x[8];
+            unpack8(raw[p], TYPE, x);
+            float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const int r = 2 * (4 * (8 * part + p) + warp) + (lane >> 4), t = r & (kC - 1);   // rows 0..63 keys, 64.. queries
-                const uint16_t* src = part == 0 ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
-                raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * l) : make_uint4(0, 0, 0, 0);
+            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
+            const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = e > 100 ? 100 : e;
+            const f2 up = pair(exp2i(e1), exp2i(e1));
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float u, w2;
+                f2 y = mul2(pair(x[2 * j], x[2 * j + 1]), up);
+                if (e != e1) y = mul2(y, pair(exp2i(e - e1), exp2i(e - e1)));
+                unpair(y, u, w2);
+                h[j] = pack_f16x2(u, w2);
             }
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const int r = 2 * (4 * (8 * part + p) + warp) + (lane >> 4);
-                float x[8];
-                unpack8(raw[p], TYPE, x);
-                float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
-                const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = e > 100 ? 100 : e;
-                const f2 up = pair(exp2i(e1), exp2i(e1));
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float u, w;
-                    f2 y = mul2(pair(x[2 * j], x[2 * j + 1]), up);
-                    if (e != e1) y = mul2(y, pair(exp2i(e - e1), exp2i(e - e1)));
-                    unpair(y, u, w);
-                    h[j] = pack_f16x2(u, w);
-                }
-                const uint32_t at = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r, l & 7);
-                *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (l == 0) s_e[r] = e;
-            }
+            const uint32_t at = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r, l & 7);
+            *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (l == 0) s_e[r] = e;
         }
     }
     __syncthreads();
@@ -306,55 +346,22 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __gri
     for (int o = 1; o < 32; o <<= 1) key_unit = fmaxf(key_unit, __shfl_xor_sync(0xffffffffu, key_unit, o));
     key_unit = exp2i(min(max(-1 - f32_exponent(key_unit), 9), 16));   // (of lengths from 2^10 to 2^14.5, or of rows that eps outweighs)
     // ---- two value heads at a time: warps 0, 1 and 2, 3
-    const int rep = a.n_v / a.n_k;
-    for (int h0 = 0; h0 < rep; h0 += 2) {
+    for (int h0 = 0; h0 < (MORE ? rep : 1); h0 += 2) {
         const int mine = h0 + (warp >> 1), h = kh * rep + mine;
         const bool has = mine < rep;
         uint8_t* blob = w.head + ((size_t)place * a.n_v + h) * kHeadBytes;
         float* vec = s_g + (warp >> 1) * kVecs * kC;
-        if (has && (warp & 1) == 0) {
-            // two tokens to a lane; G in powers of two, summed in FP64, clamped where a factor is long zero
-            double g[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                float beta = 0.f;
-                g[i] = 0.0;
-                if (t < n) {
-                    const long long at = first + t;
-                    const float x = log_decay(to_f32(a.a[at * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]);
-                    g[i] = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
-                    beta = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
-                }
-                vec[2 * kC + t] = beta;
-            }
-            double sum = g[0] + g[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double up = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += up;
-            }
-            const double G[2] = {sum - g[1], sum}, last = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
-                vec[t] = hi, vec[kC + t] = lo;
-                vec[3 * kC + t] = exp2f(hi) * (1.f + lo * 0.69314718f);
-                vec[4 * kC + t] = exp2f((float)(last - G[i]));
-            }
-            if (lane == 0) {
-                reinterpret_cast<float*>(blob + kOffScal)[kScalG] = exp2f((float)last);
-                reinterpret_cast<float*>(blob + kOffScal)[kScalU] = key_unit;
-            }
+        if (MORE && h0 > 0) {
+            gates(h0);
+            __syncthreads();
         }
-        __syncthreads();                             // also: every warp has read the keys and queries in shared memory
         if (has) {
             const int t = tid & (kC - 1);            // each token's factors, by a head's 64 threads
             float* scal = reinterpret_cast<float*>(blob + kOffScal);
             scal[kScalF + t] = -vec[3 * kC + t] * s_r[t];
             scal[kScalD + t] = vec[4 * kC + t] * (s_r[t] * key_unit);
             scal[kScalO + t] = vec[3 * kC + t] * s_r[kC + t];
+            if (t == 0) scal[kScalU] = key_unit;
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __gri
                     const float d0 = fast_exp2((ghi - gj.x) + (glo - lj.x)) * rj.x, d1 = fast_exp2((ghi - gj.y) + (glo - lj.y)) * rj.y;
                     *reinterpret_cast<float2*>(A + i * kAStride + j) =
                         make_float2(j < i ? kk[t][2 * e] * ka * d0 : 0.f, j + 1 < i ? kk[t][2 * e + 1] * ka * d1 : 0.f);
-                    *reinterpret_cast<uint32_t*>(base + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
+                    *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
                         pack_f16x2(j <= i ? qk[t][2 * e] * qa * d0 : 0.f, j + 1 <= i ? qk[t][2 * e + 1] * qa * d1 : 0.f);
                 }
             }
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __gri
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + hh * kTriBytes, kTriBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + kPrepP + hh * kTriBytes, kTriBytes);
             bulk_commit();
         }
         // ---- (I + A)^-1 of the warp pair's head, in A's place
@@ -445,42 +452,51 @@ __global__ void __launch_bounds__(kPrepThreads, 3) delta_prep_kernel(const __gri
                     for (int t = 0; t < 4; ++t) mma_pairs(z[t], f1, frag_b(A + 48 * kAStride + 8 * t, lane));
                 }
             }
-            if (tid == 0) bulk_wait_read();
-            __syncthreads();                         // P has left; both warps have read the product
+            __syncthreads();                         // both warps have read the product
             if (has) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) put_tile(A21 + 8 * t, z[t], -1.f, lane);
             }
         }
         __syncthreads();
-        if (has) {
-            // times beta of the column, as pairs: a thread has row tid % 64, eight columns at a time up to the diagonal's block
+        {
+            // times beta of the column, as pairs, in A's place: a thread has row tid % 64, eight columns at a time up to the
+            // diagonal's block (rows up to 31 end in column 31 at most; what lies above the diagonal's blocks is not read)
             const int i = tid & (kC - 1);
-            uint8_t* T = base + (warp >> 1) * 2 * kTriBytes;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (t > 4 * side + 3) continue;      // rows up to 31 end in column 31 at most; what lies above the diagonal's blocks is not read
-                const float4 x = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t), y = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t + 4);
-                const float4 b0 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t), b1 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t + 4);
+            uint4 hi[8], lo[8];
+            if (has) {
                 const f2 u = pair(kTriUnit, kTriUnit);
-                uint4 hi, lo;
-                split2(mul2(mul2(pair(x.x, x.y), pair(b0.x, b0.y)), u), hi.x, lo.x);
-                split2(mul2(mul2(pair(x.z, x.w), pair(b0.z, b0.w)), u), hi.y, lo.y);
-                split2(mul2(mul2(pair(y.x, y.y), pair(b1.x, b1.y)), u), hi.z, lo.z);
-                split2(mul2(mul2(pair(y.z, y.w), pair(b1.z, b1.w)), u), hi.w, lo.w);
-                *reinterpret_cast<uint4*>(T + swz(i, t)) = hi;
-                *reinterpret_cast<uint4*>(T + kOffTlo + swz(i, t)) = lo;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if (t > 4 * side + 3) continue;
+                    const float4 x = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t), y = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t + 4);
+                    const float4 b0 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t), b1 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t + 4);
+                    split2(mul2(mul2(pair(x.x, x.y), pair(b0.x, b0.y)), u), hi[t].x, lo[t].x);
+                    split2(mul2(mul2(pair(x.z, x.w), pair(b0.z, b0.w)), u), hi[t].y, lo[t].y);
+                    split2(mul2(mul2(pair(y.x, y.y), pair(b1.x, b1.y)), u), hi[t].z, lo[t].z);
+                    split2(mul2(mul2(pair(y.z, y.w), pair(b1.z, b1.w)), u), hi[t].w, lo[t].w);
+                }
+            }
+            __syncthreads();
+            if (has) {
+                uint8_t* T = base + (warp >> 1) * kABytes;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if (t > 4 * side + 3) continue;
+                    *reinterpret_cast<uint4*>(T + swz(i, t)) = hi[t];
+                    *reinterpret_cast<uint4*>(T + kOffTlo + swz(i, t)) = lo[t];
+                }
             }
         }
         tc::fence_proxy_async();
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * 2 * kTriBytes, 2 * kTriBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * kABytes, 2 * kTriBytes);
             bulk_commit();
             if (h0 + 2 < rep) bulk_wait_read();
         }
-        if (h0 + 2 < rep) __syncthreads();           // T has left, the gates have been read
+        if (h0 + 2 < rep) __syncthreads();           // P and T have left, the gates have been read
     }
     if (tid == 0) bulk_wait();
 }
@@ -1020,11 +1036,12 @@ template <int TYPE>
 cudaError_t launch(const DeltaArgs& a, cudaStream_t stream) {
     const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, chunks = (long long)a.n_seq * a.n_v;
     if (prep > 0x7fffffffLL || chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepBytes);
+    auto* kernel = a.n_v > 2 * a.n_k ? delta_prep_kernel<TYPE, true> : delta_prep_kernel<TYPE, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_chunk_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkBytes);
     if (e != cudaSuccess) return e;
     if (a.n_tok > 0) {
-        e = launch_overlapped(delta_prep_kernel<TYPE>, dim3((unsigned)prep), kPrepThreads, kPrepBytes, stream, a);
+        e = launch_overlapped(kernel, dim3((unsigned)prep), kPrepThreads, kPrepBytes, stream, a);
         if (e != cudaSuccess) return e;
     }
     return launch_overlapped(delta_chunk_kernel<TYPE>, dim3((unsigned)chunks), kChunkThreads, kChunkBytes, stream, a);
