@@ -133,7 +133,7 @@ constexpr int kAStride = 68;                         // floats to a row of A
 constexpr uint32_t kABytes = kC * kAStride * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kTriBytes;
 static_assert(kPrepP >= kKqBytes && kABytes % 1024 == 0, "A's place");
 constexpr int kVecs = 5;                             // of a value head: G's hi and lo in powers of two, beta, exp(G), exp(G_C - G)
-constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 1024;
+constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 4 * 8 + 1024;
 
 // Column `col` of (I + A)^-1 of an N x N block of A (strictly lower, rows kAStride apart), by substitution.
 template <int N>
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     float* s_r = reinterpret_cast<float*>(base + kPrepVec);          // 1 / |k|, 1 / |q| of the FP16 rows
     int* s_e = reinterpret_cast<int*>(s_r + 2 * kC);                 // the rows' powers of two
     float* s_g = s_r + 4 * kC;                                       // [head of the pair][kVecs][kC]
+    double* s_sum = reinterpret_cast<double*>(s_g + 2 * kVecs * kC); // of the warps' decays
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int place = (int)(blockIdx.x / (unsigned)a.n_k), kh = (int)(blockIdx.x - (unsigned)place * (unsigned)a.n_k);
     wait_for_stream();
@@ -222,6 +223,44 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     const Blobs w = blobs_of(a);
     uint8_t* kq = w.kq + ((size_t)place * a.n_k + kh) * kKqBytes;
 
+    // ---- the decays of two value heads, two warps each, a token to a thread: G in powers of two, summed in FP64, clamped
+    // where a factor is long zero; first within a warp
+    const int rep = a.n_v / a.n_k, tt = tid & (kC - 1);
+    uint16_t gate_a = 0, gate_b = 0;
+    float gate_dt = 0.f, gate_log = 0.f;
+    auto ask_gates = [&](int h0) {
+        const int h = kh * rep + h0 + (warp >> 1);
+        if (h0 + (warp >> 1) >= rep || tt >= n) return;
+        gate_a = a.a[(long long)(first + tt) * a.a_stride + h], gate_b = a.b[(long long)(first + tt) * a.b_stride + h];
+        gate_dt = a.dt_bias[h], gate_log = a.a_log[h];
+    };
+    double sum = 0.0;
+    float* vec = s_g + (warp >> 1) * kVecs * kC;
+    auto scan_gates = [&](int h0) {
+        sum = 0.0;
+        float beta = 0.f;
+        if (h0 + (warp >> 1) < rep && tt < n) {
+            const float x = log_decay(to_f32(gate_a, TYPE), gate_dt, gate_log);
+            sum = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
+            beta = sigmoid(to_f32(gate_b, TYPE));
+        }
+        vec[2 * kC + tt] = beta;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) s_sum[warp] = sum;
+    };
+    auto join_gates = [&]() {                        // behind a barrier
+        const double half = s_sum[warp & 2], last = half + s_sum[warp | 1];
+        const double G = (warp & 1) ? half + sum : sum;
+        const float hi = (float)G, lo = (float)(G - (double)hi);
+        vec[tt] = hi, vec[kC + tt] = lo;
+        vec[3 * kC + tt] = exp2f(hi) * (1.f + lo * 0.69314718f);
+        vec[4 * kC + tt] = exp2f((float)(last - G));
+    };
+    ask_gates(0);
     uint4 raw[16];                                   // row 2 (4 p + warp) + lane / 16 of 64 keys, then 64 queries
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
@@ -229,46 +268,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         const uint16_t* src = p < 8 ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
         raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * (lane & 15)) : make_uint4(0, 0, 0, 0);
     }
-    // ---- the decays of two value heads, by a warp each: two tokens to a lane; G in powers of two, summed in FP64, clamped
-    // where a factor is long zero
-    const int rep = a.n_v / a.n_k;
-    auto gates = [&](int h0) {
-        const int mine = h0 + (warp >> 1), h = kh * rep + mine;
-        if (mine >= rep || (warp & 1)) return;
-        float* vec = s_g + (warp >> 1) * kVecs * kC;
-        double g[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            float beta = 0.f;
-            g[i] = 0.0;
-            if (t < n) {
-                const long long at = first + t;
-                const float x = log_decay(to_f32(a.a[at * a.a_stride + h], TYPE), a.dt_bias[h], a.a_log[h]);
-                g[i] = x < -700.f ? -1010.0 : (double)x * 1.4426950408889634;
-                beta = sigmoid(to_f32(a.b[at * a.b_stride + h], TYPE));
-            }
-            vec[2 * kC + t] = beta;
-        }
-        double sum = g[0] + g[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += up;
-        }
-        const double G[2] = {sum - g[1], sum}, last = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
-            vec[t] = hi, vec[kC + t] = lo;
-            vec[3 * kC + t] = exp2f(hi) * (1.f + lo * 0.69314718f);
-            vec[4 * kC + t] = exp2f((float)(last - G[i]));
-        }
-        if (lane == 0)
-            reinterpret_cast<float*>(w.head + ((size_t)place * a.n_v + h) * kHeadBytes + kOffScal)[kScalG] = exp2f((float)last);
-    };
-    gates(0);
+    scan_gates(0);
     // ---- keys and queries to FP16 rows, each times the power of two that puts its largest element in [2^10, 2^11)
     {
         const int l = lane & 15;
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         }
     }
     __syncthreads();
+    join_gates();
     // ---- K K^T and Q K^T: a warp has rows 16 warp .. + 15 of both, columns up to the diagonal; of Q Q^T the diagonal's block
     float kk[8][4], qk[8][4], qq[2][4];
 #pragma unroll
@@ -350,18 +351,19 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         const int mine = h0 + (warp >> 1), h = kh * rep + mine;
         const bool has = mine < rep;
         uint8_t* blob = w.head + ((size_t)place * a.n_v + h) * kHeadBytes;
-        float* vec = s_g + (warp >> 1) * kVecs * kC;
         if (MORE && h0 > 0) {
-            gates(h0);
+            ask_gates(h0);
+            scan_gates(h0);
+            __syncthreads();
+            join_gates();
             __syncthreads();
         }
-        if (has) {
-            const int t = tid & (kC - 1);            // each token's factors, by a head's 64 threads
+        if (has) {                                   // each token's factors
             float* scal = reinterpret_cast<float*>(blob + kOffScal);
-            scal[kScalF + t] = -vec[3 * kC + t] * s_r[t];
-            scal[kScalD + t] = vec[4 * kC + t] * (s_r[t] * key_unit);
-            scal[kScalO + t] = vec[3 * kC + t] * s_r[kC + t];
-            if (t == 0) scal[kScalU] = key_unit;
+            scal[kScalF + tt] = -vec[3 * kC + tt] * s_r[tt];
+            scal[kScalD + tt] = vec[4 * kC + tt] * (s_r[tt] * key_unit);
+            scal[kScalO + tt] = vec[3 * kC + tt] * s_r[kC + tt];
+            if (tt == kC - 1) scal[kScalG] = vec[3 * kC + tt], scal[kScalU] = key_unit;
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
