@@ -25,86 +25,111 @@ __device__ __forceinline__ float sum_over(float x, float* s_part) {
     return x;
 }
 
-template <int TYPE, int LANES, int PIECES>
+// A thread has words l, l + LANES, .. (PIECES of them) of ITEMS groups, kNormThreads / LANES apart, all asked for at once.
+template <int TYPE, int LANES, int PIECES, int ITEMS>
 __global__ void __launch_bounds__(kNormThreads) group_norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int kRow = kNormThreads / LANES;       // groups side by side in a block
     __shared__ float s_part[kNormThreads / 32];
     const int l = threadIdx.x % LANES, words = a.size / 8;
-    const long long item = (long long)blockIdx.x * (kNormThreads / LANES) + threadIdx.x / LANES;
-    const bool live = item < (long long)a.n_tok * a.n_groups;
-    const long long t = live ? item / a.n_groups : 0;
-    const int g = live ? (int)(item - t * a.n_groups) : 0;
+    const unsigned groups = (unsigned)a.n_groups;
+    const long long items = (long long)a.n_tok * a.n_groups, item0 = (long long)blockIdx.x * (kRow * ITEMS);
+    // the block's first token by one wide division, its threads' from there in 32 bits
+    const unsigned t0 = (unsigned)(item0 / groups), g0 = (unsigned)(item0 - (long long)t0 * groups) + threadIdx.x / LANES;
     wait_for_stream();
-    const uint16_t* x = a.x + t * a.x_stride + (size_t)g * a.size;
-    const uint16_t* z = a.gate ? a.gate + t * a.gate_stride + (size_t)g * a.size : nullptr;
-    uint4 rx[PIECES], rz[PIECES];
+    uint4 rx[ITEMS][PIECES], rz[ITEMS][PIECES];
+    long long tok[ITEMS];
+    unsigned grp[ITEMS];
+    bool live[ITEMS];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int w = l + i * LANES;
-        rx[i] = rz[i] = make_uint4(0, 0, 0, 0);
-        if (live && w < words) {
-            rx[i] = *reinterpret_cast<const uint4*>(x + 8 * w);
-            if (z) rz[i] = *reinterpret_cast<const uint4*>(z + 8 * w);
+    for (int k = 0; k < ITEMS; ++k) {
+        const unsigned from = g0 + k * kRow, more = from / groups;
+        live[k] = item0 + threadIdx.x / LANES + k * kRow < items;
+        tok[k] = (long long)t0 + more;
+        grp[k] = from - more * groups;
+        const uint16_t* x = a.x + tok[k] * a.x_stride + (size_t)grp[k] * a.size;
+        const uint16_t* z = a.gate + tok[k] * a.gate_stride + (size_t)grp[k] * a.size;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int w = l + i * LANES;
+            rx[k][i] = rz[k][i] = make_uint4(0, 0, 0, 0);
+            if (live[k] && w < words) {
+                rx[k][i] = *reinterpret_cast<const uint4*>(x + 8 * w);
+                if (a.gate) rz[k][i] = *reinterpret_cast<const uint4*>(z + 8 * w);
+            }
         }
     }
-    float mean = 0.f;
-    if (a.centred) {
+    const float inv = 1.f / (float)a.size;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        float mean = 0.f, sq = 0.f;
+        if (a.centred) {
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                float f[8];
+                unpack8(rx[k][i], TYPE, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mean += f[j];
+            }
+            mean = sum_over<LANES>(mean, s_part) * inv;
+        }
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             float f[8];
-            unpack8(rx[i], TYPE, f);
+            unpack8(rx[k][i], TYPE, f);
+            if (l + i * LANES < words) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mean += f[j];
+                for (int j = 0; j < 8; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+            }
         }
-        mean = __fdiv_rn(sum_over<LANES>(mean, s_part), (float)a.size);
-    }
-    float sq = 0.f;
+        const float r = __frsqrt_rn(fmaf(sum_over<LANES>(sq, s_part), inv, a.eps));
+        uint16_t* out = a.out + tok[k] * a.out_stride + (size_t)grp[k] * a.size;
+        const size_t w0 = a.per_group ? (size_t)grp[k] * a.size : 0;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        float f[8];
-        unpack8(rx[i], TYPE, f);
-        if (l + i * LANES < words) {
+        for (int i = 0; i < PIECES; ++i) {
+            const int w = l + i * LANES;
+            if (!live[k] || w >= words) continue;
+            float y[8], p[8];
+            unpack8(rx[k][i], TYPE, y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+            for (int j = 0; j < 8; ++j) y[j] = (y[j] - mean) * r;
+            if (a.weight) {
+                load8(a.weight, w0 + 8 * w, a.w_type, p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= p[j];
+            }
+            if (a.bias) {
+                load8(a.bias, w0 + 8 * w, a.w_type, p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] += p[j];
+            }
+            if (a.gate) {
+                unpack8(rz[k][i], TYPE, p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= a.activation == QSA_ACT_SILU ? silu(p[j]) : p[j];
+            } else if (a.activation == QSA_ACT_SILU) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
+            }
+            *reinterpret_cast<uint4*>(out + 8 * w) = pack8(y, TYPE);
         }
-    }
-    const float r = __frsqrt_rn(__fdiv_rn(sum_over<LANES>(sq, s_part), (float)a.size) + a.eps);
-    uint16_t* out = a.out + t * a.out_stride + (size_t)g * a.size;
-    const size_t w0 = a.per_group ? (size_t)g * a.size : 0;
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int w = l + i * LANES;
-        if (!live || w >= words) continue;
-        float y[8], p[8];
-        unpack8(rx[i], TYPE, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = (y[j] - mean) * r;
-        if (a.weight) {
-            load8(a.weight, w0 + 8 * w, a.w_type, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= p[j];
-        }
-        if (a.bias) {
-            load8(a.bias, w0 + 8 * w, a.w_type, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] += p[j];
-        }
-        if (z) {
-            unpack8(rz[i], TYPE, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= a.activation == QSA_ACT_SILU ? silu(p[j]) : p[j];
-        } else if (a.activation == QSA_ACT_SILU) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
-        }
-        *reinterpret_cast<uint4*>(out + 8 * w) = pack8(y, TYPE);
     }
 }
 
+template <int TYPE, int LANES, int PIECES, int ITEMS>
+cudaError_t launch_items(const NormArgs& a, cudaStream_t stream) {
+    const long long items = (long long)a.n_tok * a.n_groups, per = (long long)kNormThreads / LANES * ITEMS, grid = (items + per - 1) / per;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_overlapped(group_norm_kernel<TYPE, LANES, PIECES, ITEMS>, dim3((unsigned)grid), kNormThreads, 0, stream, a);
+}
+
+// Two words to a thread, or four groups, once that still gives every SM a few blocks; below that one group a thread, for
+// the shortest way through.
 template <int TYPE, int LANES, int PIECES>
 cudaError_t launch_lanes(const NormArgs& a, cudaStream_t stream) {
-    const long long items = (long long)a.n_tok * a.n_groups, per = kNormThreads / LANES, grid = (items + per - 1) / per;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_overlapped(group_norm_kernel<TYPE, LANES, PIECES>, dim3((unsigned)grid), kNormThreads, 0, stream, a);
+    constexpr int kItems = PIECES >= 4 ? 1 : PIECES == 2 ? 2 : 4;
+    if (kItems > 1 && (long long)a.n_tok * a.n_groups * LANES >= 4LL * kNormThreads * kItems * 152)
+        return launch_items<TYPE, LANES, PIECES, kItems>(a, stream);
+    return launch_items<TYPE, LANES, PIECES, 1>(a, stream);
 }
 
 template <int TYPE>

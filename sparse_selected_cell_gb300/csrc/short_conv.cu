@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
     };
 
     // the first sequence that begins here or later
-    const int owned = !a.cu_tokens ? t0 : t0 == 0 ? 0 : first_from(a.cu_tokens, a.n_seq, t0);
-    if (blockIdx.x == 0 && a.cu_tokens && a.dev_status)
+    const int owned = t0 == 0 ? 0 : first_from(a.cu_tokens, a.n_seq, t0);
+    if (blockIdx.x == 0 && a.dev_status)
         for (int i = threadIdx.x; i < a.n_seq; i += kConvThreads)
             if (tokens_bad(a.cu_tokens, i, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
     if (!live) return;
@@ -96,20 +96,28 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
         skip = slot < 0 || slot >= a.n_slots;
         return slot;
     };
-    if (a.cu_tokens && s >= 0) look();
-    const int following = owned < a.n_seq ? (a.cu_tokens ? a.cu_tokens[owned] : owned) : a.n_tok;
+    if (s >= 0) look();
+    const int following = owned < a.n_seq ? a.cu_tokens[owned] : a.n_tok;
     if (RUN > 1 && t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
         if (skip) return;                            // the whole run inside one sequence
-        uint4 raw[RUN + W - 1];
+        constexpr int kBatch = 8;                    // the next batch's inputs are asked for before this one's are used
+        uint4 raw[2][kBatch];
 #pragma unroll
-        for (int i = 0; i < RUN + W - 1; ++i) raw[i] = input(t0 - (W - 1) + i);
+        for (int i = 0; i < W - 1; ++i) unpack8(input(t0 - (W - 1) + i), TYPE, win[i]);
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) unpack8(raw[i], TYPE, win[i]);
+        for (int i = 0; i < kBatch; ++i) raw[0][i] = input(t0 + i);
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            float in[8];
-            unpack8(raw[i + W - 1], TYPE, in);
-            token(t0 + i, in, true);
+        for (int n = 0; n < RUN / kBatch; ++n) {
+            if (n + 1 < RUN / kBatch) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) raw[(n + 1) & 1][i] = input(t0 + (n + 1) * kBatch + i);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float in[8];
+                unpack8(raw[n & 1][i], TYPE, in);
+                token(t0 + n * kBatch + i, in, true);
+            }
         }
         return;
     }
@@ -157,7 +165,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
         unpack8(ahead, TYPE, in);
         if (t + 1 < reach) ahead = input(t + 1);
         if (t < t1) {
-            while (s + 1 < a.n_seq && (a.cu_tokens ? a.cu_tokens[s + 1] : s + 1) <= t) {
+            while (s + 1 < a.n_seq && a.cu_tokens[s + 1] <= t) {
                 ++s;
                 enter();
             }
@@ -175,6 +183,86 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
         }
 }
 
+// One token to every sequence: a thread keeps its channels' weights and goes through every gridDim.y-th sequence, the next
+// one's state and input on their way while this one's are used.
+template <int TYPE, int W>
+__global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const __grid_constant__ ConvArgs a) {
+    const int c = (int)(blockIdx.x * kConvThreads + threadIdx.x) * 8;
+    const bool live = c < a.n_ch;
+    wait_for_stream();
+    if (!live) return;
+    float w[W][8], bias[8];
+    int slot = -1;
+    bool fresh = false;
+    uint4 held[W - 1], in = make_uint4(0, 0, 0, 0);
+    auto ask = [&](int s) {
+        slot = a.state_slots[s];
+        if (slot >= a.n_slots) {
+            if (c == 0) report(a.dev_status, QSA_DEV_BAD_STATE);
+            slot = -1;
+        }
+        fresh = a.old_lens && a.old_lens[s] <= 0;
+        if (slot < 0) return;
+        in = *reinterpret_cast<const uint4*>(a.x + (long long)s * a.x_stride + c);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+            held[i] = fresh ? make_uint4(0, 0, 0, 0)
+                            : *reinterpret_cast<const uint4*>(a.state + ((size_t)slot * (W - 1) + i) * a.n_ch + c);
+    };
+    ask((int)blockIdx.y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        float flat[8];
+        load8(a.weight, (size_t)c * W + 8 * i, a.w_type, flat);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[(8 * i + j) % W][(8 * i + j) / W] = flat[j];
+    }
+    if (a.bias) load8(a.bias, (size_t)c, a.w_type, bias);
+#pragma unroll 1
+    for (int s = (int)blockIdx.y; s < a.n_seq; s += (int)gridDim.y) {
+        const int at = slot;
+        uint4 now[W];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) now[i] = held[i];
+        now[W - 1] = in;
+        if (s + (int)gridDim.y < a.n_seq) ask(s + (int)gridDim.y);
+        if (at < 0) continue;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = bias[j];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float x[8];
+            unpack8(now[i], TYPE, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = fmaf(w[i][j], x[j], y[j]);
+            if (i > 0) *reinterpret_cast<uint4*>(a.state + ((size_t)at * (W - 1) + i - 1) * a.n_ch + c) = now[i];
+        }
+        if (a.activation == QSA_ACT_SILU) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
+        }
+        *reinterpret_cast<uint4*>(a.out + (long long)s * a.out_stride + c) = pack8(y, TYPE);
+    }
+}
+
+constexpr int kStepBlocks = 5;                       // of kConvThreads, per SM
+
+template <int TYPE, int W>
+cudaError_t launch_step(const ConvArgs& a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int cols = (a.n_ch / 8 + kConvThreads - 1) / kConvThreads;
+    int rows = sms * kStepBlocks / cols;             // as many as run at once
+    rows = rows < 1 ? 1 : rows > 65535 ? 65535 : rows;
+    if (rows > a.n_seq) rows = a.n_seq;
+    return launch_overlapped(short_conv_step_kernel<TYPE, W>, dim3((unsigned)cols, (unsigned)rows), kConvThreads, 0, stream, a);
+}
+
 template <int TYPE, int W, int RUN>
 cudaError_t launch_run(const ConvArgs& a, cudaStream_t stream) {
     const long long cols = (a.n_ch / 8 + kConvThreads - 1) / kConvThreads;
@@ -186,8 +274,9 @@ cudaError_t launch_run(const ConvArgs& a, cudaStream_t stream) {
 
 template <int TYPE, int W>
 cudaError_t launch_width(const ConvArgs& a, cudaStream_t stream) {
-    if (!a.cu_tokens || a.n_tok < 4LL * a.n_seq) return launch_run<TYPE, W, 1>(a, stream);
-    return launch_run<TYPE, W, 16>(a, stream);
+    if (!a.cu_tokens) return launch_step<TYPE, W>(a, stream);
+    if (a.n_tok < 4LL * a.n_seq) return launch_run<TYPE, W, 1>(a, stream);
+    return launch_run<TYPE, W, 32>(a, stream);
 }
 
 template <int TYPE>
