@@ -32,22 +32,24 @@ __global__ void __launch_bounds__(kNormThreads) group_norm_kernel(const __grid_c
     __shared__ float s_part[kNormThreads / 32];
     const int l = threadIdx.x % LANES, words = a.size / 8;
     const unsigned groups = (unsigned)a.n_groups;
-    const long long items = (long long)a.n_tok * a.n_groups, item0 = (long long)blockIdx.x * (kRow * ITEMS);
+    const long long item0 = (long long)blockIdx.x * (kRow * ITEMS);
     // the block's first token by one wide division, its threads' from there in 32 bits
     const unsigned t0 = (unsigned)(item0 / groups), g0 = (unsigned)(item0 - (long long)t0 * groups) + threadIdx.x / LANES;
     wait_for_stream();
     uint4 rx[ITEMS][PIECES], rz[ITEMS][PIECES];
-    long long tok[ITEMS];
-    unsigned grp[ITEMS];
+    unsigned tok[ITEMS], grp[ITEMS];
     bool live[ITEMS];
+    tok[0] = g0 / groups, grp[0] = g0 - tok[0] * groups, tok[0] += t0;
+    const unsigned more = kRow / groups, rest = kRow - more * groups;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const unsigned from = g0 + k * kRow, more = from / groups;
-        live[k] = item0 + threadIdx.x / LANES + k * kRow < items;
-        tok[k] = (long long)t0 + more;
-        grp[k] = from - more * groups;
-        const uint16_t* x = a.x + tok[k] * a.x_stride + (size_t)grp[k] * a.size;
-        const uint16_t* z = a.gate + tok[k] * a.gate_stride + (size_t)grp[k] * a.size;
+        if (k > 0) {
+            const bool over = grp[k - 1] + rest >= groups;
+            tok[k] = tok[k - 1] + more + (over ? 1u : 0u), grp[k] = grp[k - 1] + rest - (over ? groups : 0u);
+        }
+        live[k] = tok[k] < (unsigned)a.n_tok;
+        const uint16_t* x = a.x + (long long)tok[k] * a.x_stride + (size_t)grp[k] * a.size;
+        const uint16_t* z = a.gate + (long long)tok[k] * a.gate_stride + (size_t)grp[k] * a.size;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int w = l + i * LANES;
@@ -59,58 +61,84 @@ __global__ void __launch_bounds__(kNormThreads) group_norm_kernel(const __grid_c
         }
     }
     const float inv = 1.f / (float)a.size;
+    const bool silu = a.activation == QSA_ACT_SILU;
+    // weights that all groups share are read once; conditions that all threads share stay outside the elements' loops
+    constexpr bool kKeep = PIECES == 1;
+    f2 weight[4], bias[4];
+    auto shift = [&](int w, size_t w0) {
+        if (a.weight) load_pairs(a.weight, w0 + 8 * w, a.w_type, weight);
+        if (a.bias) load_pairs(a.bias, w0 + 8 * w, a.w_type, bias);
+    };
+    if (kKeep && !a.per_group && l < words) shift(l, 0);
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        float mean = 0.f, sq = 0.f;
+        float mean = 0.f;
         if (a.centred) {
+            f2 sum = 0ull;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                float f[8];
-                unpack8(rx[k][i], TYPE, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) mean += f[j];
+                f2 x[4];
+                unpack_pairs(rx[k][i], TYPE, x);
+                sum = add2(sum, add2(add2(x[0], x[1]), add2(x[2], x[3])));
             }
-            mean = sum_over<LANES>(mean, s_part) * inv;
+            float u, v;
+            unpair(sum, u, v);
+            mean = sum_over<LANES>(u + v, s_part) * inv;
         }
+        const f2 less = pair(-mean, -mean);
+        f2 sq = 0ull;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            float f[8];
-            unpack8(rx[k][i], TYPE, f);
-            if (l + i * LANES < words) {
+            if (l + i * LANES >= words) continue;
+            f2 x[4];
+            unpack_pairs(rx[k][i], TYPE, x);
+            if (a.centred) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+                for (int j = 0; j < 4; ++j) x[j] = add2(x[j], less);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sq = fma2(x[j], x[j], sq);
         }
-        const float r = __frsqrt_rn(fmaf(sum_over<LANES>(sq, s_part), inv, a.eps));
-        uint16_t* out = a.out + tok[k] * a.out_stride + (size_t)grp[k] * a.size;
-        const size_t w0 = a.per_group ? (size_t)grp[k] * a.size : 0;
+        float u, v;
+        unpair(sq, u, v);
+        const float r = rsqrtf(fmaf(sum_over<LANES>(u + v, s_part), inv, a.eps));
+        const f2 r2 = pair(r, r);
+        uint16_t* out = a.out + (long long)tok[k] * a.out_stride + (size_t)grp[k] * a.size;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             const int w = l + i * LANES;
             if (!live[k] || w >= words) continue;
-            float y[8], p[8];
-            unpack8(rx[k][i], TYPE, y);
+            f2 y[4];
+            unpack_pairs(rx[k][i], TYPE, y);
+            if (a.centred) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (y[j] - mean) * r;
+                for (int j = 0; j < 4; ++j) y[j] = add2(y[j], less);
+            }
+            if (!kKeep || a.per_group) shift(w, a.per_group ? (size_t)grp[k] * a.size : 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], r2);
             if (a.weight) {
-                load8(a.weight, w0 + 8 * w, a.w_type, p);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= p[j];
+                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], weight[j]);
             }
             if (a.bias) {
-                load8(a.bias, w0 + 8 * w, a.w_type, p);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] += p[j];
+                for (int j = 0; j < 4; ++j) y[j] = add2(y[j], bias[j]);
             }
             if (a.gate) {
-                unpack8(rz[k][i], TYPE, p);
+                f2 z[4];
+                unpack_pairs(rz[k][i], TYPE, z);
+                if (silu) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= a.activation == QSA_ACT_SILU ? silu(p[j]) : p[j];
-            } else if (a.activation == QSA_ACT_SILU) {
+                    for (int j = 0; j < 4; ++j) z[j] = silu2(z[j]);
+                }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
+                for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], z[j]);
+            } else if (silu) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = silu2(y[j]);
             }
-            *reinterpret_cast<uint4*>(out + 8 * w) = pack8(y, TYPE);
+            *reinterpret_cast<uint4*>(out + 8 * w) = pack_pairs(y, TYPE);
         }
     }
 }

@@ -91,8 +91,59 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8], int type) {
     return make_uint4(pack2(x[0], x[1], type), pack2(x[2], x[3], type), pack2(x[4], x[5], type), pack2(x[6], x[7], type));
 }
 
+// ---------------------------------------------------------------- two FP32 at a time
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Eight consecutive 16-bit elements as four pairs, and back.
+__device__ __forceinline__ void unpack_pairs(const uint4& w, int type, f2 (&x)[4]) {
+    float f[8];
+    unpack8(w, type, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+__device__ __forceinline__ uint4 pack_pairs(const f2 (&x)[4], int type) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpair(x[j], f[2 * j], f[2 * j + 1]);
+    return pack8(f, type);
+}
+__device__ __forceinline__ void load_pairs(const void* p, size_t at, int type, f2 (&x)[4]) {
+    float f[8];
+    load8(p, at, type, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+
 // x / (1 + e^-x), good to a few 2^-22 (the results are rounded to 16 bits).
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+__device__ __forceinline__ f2 silu2(f2 x) {
+    float a, b;
+    unpair(mul2(x, pair(-kLog2e, -kLog2e)), a, b);
+    unpair(add2(pair(fast_exp2(a), fast_exp2(b)), pair(1.f, 1.f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return mul2(x, pair(a, b));
+}
 
 // The decay's logarithm and the new value's weight, from the layer's two gate inputs.
 __device__ __forceinline__ float log_decay(float a, float dt_bias, float a_log) {

@@ -21,6 +21,18 @@ namespace {
 
 constexpr int kConvThreads = 128;
 
+// Weights [channel][tap] of eight channels (8 W consecutive values) as pairs of channels to a tap.
+template <int W>
+__device__ __forceinline__ void load_taps(const void* weight, size_t c, int type, f2 (&w)[W][4]) {
+    float flat[8 * W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) load8(weight, c * W + 8 * i, type, *reinterpret_cast<float(*)[8]>(flat + 8 * i));
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][j] = pair(flat[2 * j * W + i], flat[(2 * j + 1) * W + i]);
+}
+
 // The first sequence that begins at token t or later (n_seq: none), by the whole warp.
 __device__ __forceinline__ int first_from(const int32_t* cu_tokens, int n_seq, int t) {
     const int lane = threadIdx.x & 31;
@@ -37,7 +49,7 @@ __device__ __forceinline__ int first_from(const int32_t* cu_tokens, int n_seq, i
 }
 
 template <int TYPE, int W, int RUN>
-__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_constant__ ConvArgs a, const unsigned cols) {
+__global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __grid_constant__ ConvArgs a, const unsigned cols) {
     const unsigned run = blockIdx.x / cols;          // the columns of one run side by side
     const int c = (int)((blockIdx.x - run * cols) * kConvThreads + threadIdx.x) * 8;
     const int t0 = (int)run * RUN, t1 = min(t0 + RUN, a.n_tok);
@@ -46,35 +58,32 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
     const uint16_t* x = a.x + c;
     uint16_t* out = a.out + c;
     auto input = [&](int t) { return *reinterpret_cast<const uint4*>(x + (long long)t * a.x_stride); };
-    float w[W][8], bias[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
+    f2 w[W][4], bias[4] = {0ull, 0ull, 0ull, 0ull};
     if (live) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {                // [channel][tap]: 8 W consecutive values
-            float flat[8];
-            load8(a.weight, (size_t)c * W + 8 * i, a.w_type, flat);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[(8 * i + j) % W][(8 * i + j) / W] = flat[j];
-        }
-        if (a.bias) load8(a.bias, (size_t)c, a.w_type, bias);
+        load_taps<W>(a.weight, (size_t)c, a.w_type, w);
+        if (a.bias) load_pairs(a.bias, (size_t)c, a.w_type, bias);
     }
-    float win[W - 1][8];                             // inputs t - (W - 1) .. t - 1
-    auto token = [&](int t, const float (&in)[8], bool write) {
+    f2 win[W - 1][4];                                // inputs t - (W - 1) .. t - 1
+    auto token = [&](int t, const uint4& raw, bool write) {
+        f2 in[4];
+        unpack_pairs(raw, TYPE, in);
         if (write) {
-            float y[8];
+            f2 y[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 y[j] = bias[j];
 #pragma unroll
-                for (int i = 0; i < W - 1; ++i) y[j] = fmaf(w[i][j], win[i][j], y[j]);
-                y[j] = fmaf(w[W - 1][j], in[j], y[j]);
-                if (a.activation == QSA_ACT_SILU) y[j] = silu(y[j]);
+                for (int i = 0; i < W - 1; ++i) y[j] = fma2(w[i][j], win[i][j], y[j]);
+                y[j] = fma2(w[W - 1][j], in[j], y[j]);
             }
-            *reinterpret_cast<uint4*>(out + (long long)t * a.out_stride) = pack8(y, TYPE);
+            if (a.activation == QSA_ACT_SILU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = silu2(y[j]);
+            }
+            *reinterpret_cast<uint4*>(out + (long long)t * a.out_stride) = pack_pairs(y, TYPE);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
             for (int i = 0; i < W - 2; ++i) win[i][j] = win[i + 1][j];
             win[W - 2][j] = in[j];
@@ -100,23 +109,19 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
     const int following = owned < a.n_seq ? a.cu_tokens[owned] : a.n_tok;
     if (RUN > 1 && t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
         if (skip) return;                            // the whole run inside one sequence
-        constexpr int kBatch = 8;                    // the next batch's inputs are asked for before this one's are used
-        uint4 raw[2][kBatch];
+        constexpr int kAhead = 8;                    // inputs on their way
+        uint4 raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) unpack8(input(t0 - (W - 1) + i), TYPE, win[i]);
+        for (int i = 0; i < W - 1; ++i) unpack_pairs(input(t0 - (W - 1) + i), TYPE, win[i]);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) raw[0][i] = input(t0 + i);
+        for (int i = 0; i < kAhead; ++i) raw[i] = input(t0 + i);
+#pragma unroll 1
+        for (int t = t0; t < t1; t += kAhead) {
 #pragma unroll
-        for (int n = 0; n < RUN / kBatch; ++n) {
-            if (n + 1 < RUN / kBatch) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) raw[(n + 1) & 1][i] = input(t0 + (n + 1) * kBatch + i);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float in[8];
-                unpack8(raw[n & 1][i], TYPE, in);
-                token(t0 + n * kBatch + i, in, true);
+            for (int i = 0; i < kAhead; ++i) {
+                const uint4 now = raw[i];
+                if (t + kAhead < t1) raw[i] = input(t + kAhead + i);
+                token(t + i, now, true);
             }
         }
         return;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             old[i] = fresh ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(held + (size_t)i * a.n_ch);
-            unpack8(old[i], TYPE, win[i]);
+            unpack_pairs(old[i], TYPE, win[i]);
         }
         if (n == 0 && !fresh) return;
 #pragma unroll
@@ -156,13 +161,12 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {                // the inputs before the run, as far as they are the sequence's own
         const int t = t0 - (W - 1) + i;
-        unpack8(!skip && t >= begin && t < end ? input(t) : make_uint4(0, 0, 0, 0), TYPE, win[i]);
+        unpack_pairs(!skip && t >= begin && t < end ? input(t) : make_uint4(0, 0, 0, 0), TYPE, win[i]);
     }
     uint4 ahead = t0 < t1 ? input(t0) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
     for (int t = t0; t < reach; ++t) {
-        float in[8];
-        unpack8(ahead, TYPE, in);
+        const uint4 in = ahead;
         if (t + 1 < reach) ahead = input(t + 1);
         if (t < t1) {
             while (s + 1 < a.n_seq && a.cu_tokens[s + 1] <= t) {
@@ -191,17 +195,25 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const __g
     const bool live = c < a.n_ch;
     wait_for_stream();
     if (!live) return;
-    float w[W][8], bias[8];
-    int slot = -1;
-    bool fresh = false;
+    f2 w[W][4], bias[4] = {0ull, 0ull, 0ull, 0ull};
+    // slots and lengths two sequences ahead, states and inputs one
+    const int stride = (int)gridDim.y;
+    int slot = -1, slot_next = -1;
+    bool fresh = false, fresh_next = false;
     uint4 held[W - 1], in = make_uint4(0, 0, 0, 0);
+    auto ask_slot = [&](int s) {
+        slot_next = -1;
+        if (s >= a.n_seq) return;
+        slot_next = a.state_slots[s];
+        fresh_next = a.old_lens && a.old_lens[s] <= 0;
+    };
     auto ask = [&](int s) {
-        slot = a.state_slots[s];
+        slot = slot_next, fresh = fresh_next;
+        ask_slot(s + stride);
         if (slot >= a.n_slots) {
             if (c == 0) report(a.dev_status, QSA_DEV_BAD_STATE);
             slot = -1;
         }
-        fresh = a.old_lens && a.old_lens[s] <= 0;
         if (slot < 0) return;
         in = *reinterpret_cast<const uint4*>(a.x + (long long)s * a.x_stride + c);
 #pragma unroll
@@ -209,42 +221,35 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const __g
             held[i] = fresh ? make_uint4(0, 0, 0, 0)
                             : *reinterpret_cast<const uint4*>(a.state + ((size_t)slot * (W - 1) + i) * a.n_ch + c);
     };
+    ask_slot((int)blockIdx.y);
     ask((int)blockIdx.y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        float flat[8];
-        load8(a.weight, (size_t)c * W + 8 * i, a.w_type, flat);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[(8 * i + j) % W][(8 * i + j) / W] = flat[j];
-    }
-    if (a.bias) load8(a.bias, (size_t)c, a.w_type, bias);
+    load_taps<W>(a.weight, (size_t)c, a.w_type, w);
+    if (a.bias) load_pairs(a.bias, (size_t)c, a.w_type, bias);
 #pragma unroll 1
-    for (int s = (int)blockIdx.y; s < a.n_seq; s += (int)gridDim.y) {
+    for (int s = (int)blockIdx.y; s < a.n_seq; s += stride) {
         const int at = slot;
         uint4 now[W];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) now[i] = held[i];
         now[W - 1] = in;
-        if (s + (int)gridDim.y < a.n_seq) ask(s + (int)gridDim.y);
+        if (s + stride < a.n_seq) ask(s + stride);
         if (at < 0) continue;
-        float y[8];
+        f2 y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = bias[j];
+        for (int j = 0; j < 4; ++j) y[j] = bias[j];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            float x[8];
-            unpack8(now[i], TYPE, x);
+            f2 x[4];
+            unpack_pairs(now[i], TYPE, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = fmaf(w[i][j], x[j], y[j]);
+            for (int j = 0; j < 4; ++j) y[j] = fma2(w[i][j], x[j], y[j]);
             if (i > 0) *reinterpret_cast<uint4*>(a.state + ((size_t)at * (W - 1) + i - 1) * a.n_ch + c) = now[i];
         }
         if (a.activation == QSA_ACT_SILU) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = silu(y[j]);
+            for (int j = 0; j < 4; ++j) y[j] = silu2(y[j]);
         }
-        *reinterpret_cast<uint4*>(a.out + (long long)s * a.out_stride + c) = pack8(y, TYPE);
+        *reinterpret_cast<uint4*>(a.out + (long long)s * a.out_stride + c) = pack_pairs(y, TYPE);
     }
 }
 
