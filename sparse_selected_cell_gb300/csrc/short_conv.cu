@@ -49,7 +49,7 @@ __device__ __forceinline__ int first_from(const int32_t* cu_tokens, int n_seq, i
 }
 
 template <int TYPE, int W, int RUN>
-__global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __grid_constant__ ConvArgs a, const unsigned cols) {
+__global__ void __launch_bounds__(kConvThreads, 3) short_conv_kernel(const __grid_constant__ ConvArgs a, const unsigned cols) {
     const unsigned run = blockIdx.x / cols;          // the columns of one run side by side
     const int c = (int)((blockIdx.x - run * cols) * kConvThreads + threadIdx.x) * 8;
     const int t0 = (int)run * RUN, t1 = min(t0 + RUN, a.n_tok);
@@ -58,6 +58,15 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
     const uint16_t* x = a.x + c;
     uint16_t* out = a.out + c;
     auto input = [&](int t) { return *reinterpret_cast<const uint4*>(x + (long long)t * a.x_stride); };
+    // the run's first inputs and the ones before it, whoever's they are
+    constexpr int kAhead = 8;
+    uint4 raw[kAhead], before[W - 1];
+    if (RUN > 1 && live && t1 == t0 + RUN) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) before[i] = input(max(t0 - (W - 1) + i, 0));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) raw[i] = input(t0 + i);
+    }
     f2 w[W][4], bias[4] = {0ull, 0ull, 0ull, 0ull};
     if (live) {
         load_taps<W>(a.weight, (size_t)c, a.w_type, w);
@@ -109,12 +118,8 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
     const int following = owned < a.n_seq ? a.cu_tokens[owned] : a.n_tok;
     if (RUN > 1 && t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
         if (skip) return;                            // the whole run inside one sequence
-        constexpr int kAhead = 8;                    // inputs on their way
-        uint4 raw[kAhead];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) unpack_pairs(input(t0 - (W - 1) + i), TYPE, win[i]);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) raw[i] = input(t0 + i);
+        for (int i = 0; i < W - 1; ++i) unpack_pairs(before[i], TYPE, win[i]);
 #pragma unroll 1
         for (int t = t0; t < t1; t += kAhead) {
 #pragma unroll
@@ -163,22 +168,32 @@ __global__ void __launch_bounds__(kConvThreads, 4) short_conv_kernel(const __gri
         const int t = t0 - (W - 1) + i;
         unpack_pairs(!skip && t >= begin && t < end ? input(t) : make_uint4(0, 0, 0, 0), TYPE, win[i]);
     }
-    uint4 ahead = t0 < t1 ? input(t0) : make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int t = t0; t < reach; ++t) {
-        const uint4 in = ahead;
-        if (t + 1 < reach) ahead = input(t + 1);
+    // from one sequence's first token to the next one's, eight inputs at a time
+    int t = t0;
+    while (t < reach) {
+        int stop;
         if (t < t1) {
             while (s + 1 < a.n_seq && a.cu_tokens[s + 1] <= t) {
                 ++s;
                 enter();
             }
-        } else if (t >= end) {
-            break;
+            stop = min(t1, s + 1 < a.n_seq ? max(a.cu_tokens[s + 1], t + 1) : a.n_tok);
+        } else {
+            if (skip || begin < t0) break;
+            stop = min(reach, min(end, begin + W - 1));
+            if (t >= stop) break;
         }
-        const bool first = t - begin < W - 1, mine = begin >= t0;
-        if (t >= t1 && !(mine && first)) break;
-        token(t, in, !skip && t < end && (mine || !first));
+        const int from = skip ? stop : begin < t0 ? begin + W - 1 : t;   // tokens that are this run's to write
+        const int to = min(stop, end);
+        for (; t < stop; t += 8) {
+            uint4 some[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) some[i] = t + i < stop ? input(t + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (t + i < stop) token(t + i, some[i], t + i >= from && t + i < to);
+        }
+        t = stop;
     }
     if (last)
         while (s + 1 < a.n_seq) {
