@@ -49,9 +49,14 @@ struct DeltaArgs {
     long long out_stride;
     uint8_t* workspace;
     int32_t* dev_status;
+    int chunked_from;             // delta_prompt.cu: the fewest tokens of a sequence that goes by chunks
 };
 
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
+// Of a step's sequences (cu_tokens) those of up to kDeltaShort tokens, token by token: a chunk's way costs an SM to itself
+// and as much as some twenty tokens.
+constexpr int kDeltaShort = 16;
+cudaError_t launch_delta_short(const DeltaArgs& a, cudaStream_t stream);
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v);
 cudaError_t launch_delta_prompt(const DeltaArgs& a, cudaStream_t stream);
 
