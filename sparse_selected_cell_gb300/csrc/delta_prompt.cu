@@ -517,6 +517,7 @@ enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kSt
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
+constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' in FP16 lies where S K^T was, V' P^T where V' was.
@@ -599,6 +600,7 @@ __device__ void value_role(const Block& c, int lane) {
 
 // The whole warp runs this, and one elected lane issues, so that descriptors and addresses stay in uniform registers: a
 // 64-column product then takes 35 cycles; issued by a thread alone, 53, whatever its columns.
+template <int TYPE>
 __device__ void product_role(const Block& c) {
     // FP16 operands: the type fields (bits 7 to 12) zero
     constexpr uint32_t kTypes = ~((7u << 7) | (7u << 10));
@@ -648,7 +650,7 @@ __device__ void product_role(const Block& c) {
         }
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_V));
-        with_queries(stage, 8);
+        if (TYPE == QSA_F16) with_queries(stage, 8);  // (BF16 outputs would not show it)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int b = quarter(n);
@@ -945,6 +947,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     c.s = (int)(blockIdx.x / (unsigned)a.n_v);
     c.h = (int)(blockIdx.x - (unsigned)c.s * (unsigned)a.n_v);
+    if (a.n_seq > 1 && a.n_seq <= kRanked) {
+        // the longest sequences first: block b's is the one of which c.s are longer (or as long, and before it)
+        int* lens = reinterpret_cast<int*>(c.base);
+        for (int i = tid; i < a.n_seq; i += kChunkThreads) {
+            const int2 t = tokens_of(a.cu_tokens, i, a.n_tok);
+            lens[i] = t.y - t.x;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.n_seq; i += kChunkThreads) {
+            int rank = 0;
+            for (int j = 0; j < a.n_seq; ++j) rank += lens[j] > lens[i] || (lens[j] == lens[i] && j < i) ? 1 : 0;
+            if (rank == c.s) lens[kRanked] = i;
+        }
+        __syncthreads();
+        c.s = lens[kRanked];
+        __syncthreads();                             // before the place is used for anything else
+    }
     // Behind delta_prep_kernel this kernel is released when all of that one's blocks have passed their own
     // wait, so that everything before it is there already: only the copies of its results wait for it here, and every block
     // does before it ends, so that this kernel's end means that one's too.
@@ -1013,7 +1032,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         output_role<TYPE>(c, warp - 8, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 12) product_role(c);
+        if (warp == 12) product_role<TYPE>(c);
         else if (warp == 13) copy_role(c, lane);
         else if (warp == 14) value_role(c, lane);
     }
