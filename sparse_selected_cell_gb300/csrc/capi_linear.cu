@@ -105,7 +105,7 @@ int qsa_delta_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_s
                            static_cast<const uint16_t*>(v), q_stride, k_stride, v_stride, type,
                            static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), a_stride, b_stride, a_log,
                            dt_bias, state, state_slots, n_slots, old_lens, cu_tokens, n_seq, n_tok, n_k, n_v, eps, scale,
-                           static_cast<uint16_t*>(out), out_stride, static_cast<uint8_t*>(workspace), dev_status, 0};
+                           static_cast<uint16_t*>(out), out_stride, static_cast<uint8_t*>(workspace), dev_status, 0, 1};
     const int rc = check_delta(d);
     if (rc != QSA_OK || n_seq == 0) return rc;
     if (!cu_tokens || !workspace || !aligned(workspace, 256)) return QSA_ERR_ARG;
@@ -123,7 +123,7 @@ int qsa_delta_step(const void* q, int64_t q_stride, const void* k, int64_t k_str
                            static_cast<const uint16_t*>(v), q_stride, k_stride, v_stride, type,
                            static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), a_stride, b_stride, a_log,
                            dt_bias, state, state_slots, n_slots, old_lens, nullptr, n_seq, n_seq, n_k, n_v, eps, scale,
-                           static_cast<uint16_t*>(out), out_stride, nullptr, dev_status, 0};
+                           static_cast<uint16_t*>(out), out_stride, nullptr, dev_status, 0, 1};
     const int rc = check_delta(d);
     if (rc != QSA_OK || n_seq == 0) return rc;
     return cuda_status(qsa::launch_delta_step(d, static_cast<cudaStream_t>(stream)));

@@ -18,6 +18,8 @@
 // are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
 // the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
 // passes FP16's range and what counts stays in its upper bits.  P and V' in P V' are single FP16.
+#include <type_traits>
+
 #include "linear.cuh"
 #include "tc_ptx.cuh"
 
@@ -45,6 +47,37 @@ struct Blobs {
 __host__ __device__ __forceinline__ size_t places(int n_tok, int n_seq) { return (size_t)n_tok / kC + n_seq; }
 __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
     return Blobs{a.workspace, a.workspace + places(a.n_tok, a.n_seq) * a.n_k * kKqBytes};
+}
+
+// ---------------------------------------------------------------- segments
+// A state row's way through a chunk is linear in the row: S' = S R + (what the chunk's values add).  Where there are fewer
+// chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
+// each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
+// R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
+// segments' outputs, which are FP32 until then.
+constexpr int kSplitMost = 8, kSplitChunks = 8;      // segments of a sequence; chunks of a segment, at least
+constexpr int kStateFloats = kHeadDim * kHeadDim;
+__host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
+    const long long heads = (long long)n_seq * n_v;
+    const long long room = heads > 0 ? (sms / heads + 1) / 2 : 0;   // n segments take 2 n - 1 blocks
+    const int most = (int)min((long long)kSplitMost, min(room, (long long)n_tok / (kC * kSplitChunks)));
+    return most < 2 ? 1 : most;
+}
+__device__ __forceinline__ int segments_of(int chunks, int most) { return max(1, min(most, chunks / kSplitChunks)); }
+constexpr int kSplitSms = 160;                       // the SMs that the workspace's size reckons with
+
+struct Split {
+    float* plain;                                    // [0: from zeros, 1: from the identity][token][n_v][128]
+    float* ends;                                     // [sequence, head][kSplitMost]: states at segments' ends; then before the next ones
+    float* turns;                                    // [sequence, head][kSplitMost]: the segments' R
+};
+__device__ __forceinline__ Split split_of(const DeltaArgs& a) {
+    const size_t at = places(a.n_tok, a.n_seq) * ((size_t)a.n_k * kKqBytes + (size_t)a.n_v * kHeadBytes);
+    Split w;
+    w.plain = reinterpret_cast<float*>(a.workspace + at);
+    w.ends = w.plain + 2 * (size_t)a.n_tok * a.n_v * kHeadDim;
+    w.turns = w.ends + (size_t)a.n_seq * a.n_v * kSplitMost * kStateFloats;
+    return w;
 }
 
 // ---------------------------------------------------------------- PTX
@@ -530,7 +563,12 @@ struct Block {
     uint8_t* base;
     uint32_t base_u, tmem;
     volatile int* abort_flag;
-    int s, h, slot, first, n_tok, n_chunks;
+    int s, h, slot, n_tok, n_chunks;                 // of the block's part of the sequence
+    int first, chunk0;                               // its first token, and chunk of the sequence
+    int kind;                                        // 0: from the sequence's state; 1: from zeros; 2: from the identity, without values
+    float* plain;                                    // outputs in FP32 (kinds 1 and 2), or null
+    const float* state_in;                           // the pool's state (kind 0)
+    float* state_out;
     bool fresh;
 };
 __device__ __forceinline__ uint32_t bar(const Block& c, int i) { return c.base_u + kOffBar + 8u * i; }
@@ -556,7 +594,7 @@ __device__ __forceinline__ void tell(const Block& c, int i) {
 
 __device__ void copy_role(const Block& c, int lane) {
     const DeltaArgs& a = *c.a;
-    const int kh = c.h / (a.n_v / a.n_k), place0 = place_of(c.first, c.s);
+    const int kh = c.h / (a.n_v / a.n_k), place0 = place_of(c.first - c.chunk0 * kC, c.s) + c.chunk0;
     const Blobs w = blobs_of(a);
     wait_for_stream();
     int done = 0;
@@ -699,10 +737,10 @@ __device__ __forceinline__ void both(uint32_t w, float& x, float& y) {
 // 2^(14 - e) for x in [2^e, 2^(e+1)): what brings x below 2^15.
 __device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_exponent(x), -80)); }
 
-template <int TYPE>
+template <int TYPE, bool SPLIT>
 __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
     const DeltaArgs& a = *c.a;
-    float4* row = reinterpret_cast<float4*>(a.state + (((size_t)c.slot * a.n_v + c.h) * kHeadDim + r) * kHeadDim + half * (kHeadDim / 2));
+    const float4* row = reinterpret_cast<const float4*>(c.state_in + (size_t)r * kHeadDim + half * (kHeadDim / 2));
     float2* pows = reinterpret_cast<float2*>(c.base + kOffPow) + r;
     float* top_v = reinterpret_cast<float*>(c.base + kOffTop) + r;           // + 256 (chunk & 1) + 128 half
     float* top_s = top_v + 4 * kHeadDim;
@@ -714,7 +752,12 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         uint32_t d[32];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float4 x = c.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : row[8 * b + j];
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if ((!SPLIT || c.kind == 0) && !c.fresh) x = row[8 * b + j];
+            if (SPLIT && c.kind == 2) {
+                const int k = 64 * half + 32 * b + 4 * j;
+                x = make_float4(r == k ? 1.f : 0.f, r == k + 1 ? 1.f : 0.f, r == k + 2 ? 1.f : 0.f, r == k + 3 ? 1.f : 0.f);
+            }
             d[4 * j] = __float_as_uint(x.x), d[4 * j + 1] = __float_as_uint(x.y);
             d[4 * j + 2] = __float_as_uint(x.z), d[4 * j + 3] = __float_as_uint(x.w);
             sm = fmax3(sm, fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -722,9 +765,20 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         tc::tmem_st32(tmD + 32 * b, d);
     }
     tc::tmem_wait_st();
-    if (!wait(c, BAR_VFULL, 0)) return;
     uint32_t v[16];
-    float vm = read_values<TYPE>(c.base + kOffV, half, r, v);
+    float vm = 0.f;
+    auto values = [&](int i) {                       // of chunk i
+        if (SPLIT && c.kind == 2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0u;
+            vm = 0.f;
+            return true;
+        }
+        if (!wait(c, BAR_VFULL + i % kVStages, (i / kVStages) & 1)) return false;
+        vm = read_values<TYPE>(c.base + kOffV + (i % kVStages) * kVBytes, half, r, v);
+        return true;
+    };
+    if (!values(0)) return;
     // both halves' largest value of the chunk to come, and of the state before the chunk in hand
     auto publish = [&](int i) {
         top_v[(i & 1) * 256 + half * 128] = vm;
@@ -863,9 +917,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));   // this chunk's factors have been read
         // ---- the next chunk's values, while the products run
         if (i + 1 < c.n_chunks) {
-            const int nx = (i + 1) % kVStages;
-            if (!wait(c, BAR_VFULL + nx, ((i + 1) / kVStages) & 1)) return;
-            vm = read_values<TYPE>(c.base + kOffV + nx * kVBytes, half, r, v);
+            if (!values(i + 1)) return;
             publish(i + 1);
             if (!settle(i + 1)) return;
         }
@@ -873,6 +925,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         tc::fence_after_sync();
     }
     const f2 up2 = pair(d_up, d_up);
+    float4* row_out = reinterpret_cast<float4*>(c.state_out + (size_t)r * kHeadDim + half * (kHeadDim / 2));
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         uint32_t d[32];
@@ -883,12 +936,12 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
             float4 o;
             unpair(mul2(up2, pair_of(d[4 * j], d[4 * j + 1])), o.x, o.y);
             unpair(mul2(up2, pair_of(d[4 * j + 2], d[4 * j + 3])), o.z, o.w);
-            row[8 * b + j] = o;
+            row_out[8 * b + j] = o;
         }
     }
 }
 
-template <int TYPE>
+template <int TYPE, bool SPLIT>
 __device__ void output_role(const Block& c, int q, int lane) {
     const DeltaArgs& a = *c.a;
     uint16_t* mine = reinterpret_cast<uint16_t*>(c.base + kOffOut) + q * kC * 32;
@@ -900,7 +953,11 @@ __device__ void output_role(const Block& c, int q, int lane) {
         if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_H, par) || !wait(c, BAR_O, par)) return;
         tc::fence_after_sync();
         const float2 unit = pows[(i & 1) * kHeadDim];
-        const f2 us2 = pair(unit.x * a.scale, unit.x * a.scale), uv2 = pair(unit.y * a.scale, unit.y * a.scale);
+        const float scale = SPLIT && c.kind == 2 ? 1.f : a.scale;
+        const f2 us2 = pair(unit.x * scale, unit.x * scale), uv2 = pair(unit.y * scale, unit.y * scale);
+        const int n = min(kC, c.n_tok - i * kC);
+        const bool plain = SPLIT && c.plain;
+        float* whole = reinterpret_cast<float*>(mine);               // FP32 outputs pass the same place, 32 tokens at a time
         uint32_t out[32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -914,17 +971,32 @@ __device__ void output_role(const Block& c, int q, int lane) {
                 float x, y;
                 unpair(fma2(mul2(pair(o.x, o.y), us2), pair_of(qs[2 * j], qs[2 * j + 1]), mul2(uv2, pair_of(pv[2 * j], pv[2 * j + 1]))), x, y);
                 out[8 * b + j] = pack2(x, y, TYPE);
+                if (plain) {
+                    whole[(16 * (b & 1) + 2 * j) * 32 + lane] = x;
+                    whole[(16 * (b & 1) + 2 * j + 1) * 32 + lane] = y;
+                }
+            }
+            if (plain && (b & 1)) {
+                __syncwarp();
+                float* to = c.plain + ((size_t)(c.first + i * kC + 16 * (b - 1)) * a.n_v + c.h) * kHeadDim + 32 * q + 4 * (lane & 7);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = 4 * j + (lane >> 3);
+                    if (16 * (b - 1) + t < n)
+                        *reinterpret_cast<float4*>(to + (size_t)t * a.n_v * kHeadDim) = *reinterpret_cast<const float4*>(whole + t * 32 + 4 * (lane & 7));
+                }
+                __syncwarp();
             }
         }
         tell(c, BAR_OFREE);
         if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
+        if (plain) continue;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             mine[(2 * j) * 32 + lane] = (uint16_t)(out[j] & 0xFFFFu);
             mine[(2 * j + 1) * 32 + lane] = (uint16_t)(out[j] >> 16);
         }
         __syncwarp();
-        const int n = min(kC, c.n_tok - i * kC);
         uint16_t* to = a.out + (long long)(c.first + i * kC) * a.out_stride + (size_t)c.h * kHeadDim + 32 * q + 8 * (lane & 3);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -935,7 +1007,8 @@ __device__ void output_role(const Block& c, int q, int lane) {
     }
 }
 
-template <int TYPE>
+// SPLIT: sequences may be cut into segments (see above).
+template <int TYPE, bool SPLIT>
 __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __grid_constant__ DeltaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
@@ -945,8 +1018,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     c.base_u = base_u;
     c.abort_flag = reinterpret_cast<volatile int*>(c.base + kOffMisc + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    c.s = (int)(blockIdx.x / (unsigned)a.n_v);
-    c.h = (int)(blockIdx.x - (unsigned)c.s * (unsigned)a.n_v);
+    const unsigned heads = (unsigned)a.n_seq * (unsigned)a.n_v, part = SPLIT ? blockIdx.x / heads : 0u, item = blockIdx.x - part * heads;
+    c.s = (int)(item / (unsigned)a.n_v);
+    c.h = (int)(item - (unsigned)c.s * (unsigned)a.n_v);
     if (a.n_seq > 1 && a.n_seq <= kRanked) {
         // the longest sequences first: block b's is the one of which c.s are longer (or as long, and before it)
         int* lens = reinterpret_cast<int*>(c.base);
@@ -969,7 +1043,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     // does before it ends, so that this kernel's end means that one's too.
     c.slot = a.state_slots[c.s];
     const int2 span = tokens_of(a.cu_tokens, c.s, a.n_tok);
-    if (c.h == 0 && tid == 0) {
+    if (c.h == 0 && part == 0 && tid == 0) {
         if (tokens_bad(a.cu_tokens, c.s, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
         if (c.slot >= a.n_slots) report(a.dev_status, QSA_DEV_BAD_STATE);
     }
@@ -977,13 +1051,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         wait_for_stream();
         return;
     }
+    c.fresh = a.old_lens && a.old_lens[c.s] <= 0;
+    float* pool = a.state + ((size_t)c.slot * a.n_v + c.h) * kStateFloats;
+    const int chunks = (span.y - span.x + kC - 1) / kC;
+    c.kind = c.chunk0 = 0;
+    c.n_chunks = chunks;
     c.first = span.x;
     c.n_tok = span.y - span.x;
-    c.n_chunks = (c.n_tok + kC - 1) / kC;
-    c.fresh = a.old_lens && a.old_lens[c.s] <= 0;
+    c.state_in = c.state_out = pool;
+    c.plain = nullptr;
+    if (SPLIT) {
+        // parts 0 .. n_split - 1 are the segments, from zeros but the first; then all but the first from the identity
+        const int segments = segments_of(chunks, a.n_split), segment = (int)part < a.n_split ? (int)part : (int)part - a.n_split + 1;
+        if (segment >= segments) {
+            wait_for_stream();
+            return;
+        }
+        const int each = (chunks + segments - 1) / segments;
+        c.kind = (int)part >= a.n_split ? 2 : part > 0 ? 1 : 0;
+        c.chunk0 = segment * each;
+        c.n_chunks = min(each, chunks - c.chunk0);
+        c.first = span.x + c.chunk0 * kC;
+        c.n_tok = min(c.n_chunks * kC, span.y - c.first);
+        if (segments > 1) {
+            const Split w = split_of(a);
+            c.state_out = (c.kind == 2 ? w.turns : w.ends) + (((size_t)c.s * a.n_v + c.h) * kSplitMost + segment) * kStateFloats;
+            if (c.kind) c.plain = w.plain + (c.kind - 1) * (size_t)a.n_tok * a.n_v * kHeadDim;
+        }
+    }
     if (c.n_chunks == 0) {
         if (c.fresh) {
-            float4* st = reinterpret_cast<float4*>(a.state + ((size_t)c.slot * a.n_v + c.h) * kHeadDim * kHeadDim);
+            float4* st = reinterpret_cast<float4*>(pool);
             for (int i = tid; i < kHeadDim * kHeadDim / 4; i += kChunkThreads) st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         wait_for_stream();
@@ -1026,15 +1124,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     // registers: the launch's 512 x 128 as 168 + 168 + 96 + 80 for the four groups of four warps
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        state_role<TYPE>(c, warp >> 2, tid & 127, (uint32_t)(warp & 3) << 21);
+        state_role<TYPE, SPLIT>(c, warp >> 2, tid & 127, (uint32_t)(warp & 3) << 21);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        output_role<TYPE>(c, warp - 8, lane);
+        output_role<TYPE, SPLIT>(c, warp - 8, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 12) product_role<TYPE>(c);
         else if (warp == 13) copy_role(c, lane);
-        else if (warp == 14) value_role(c, lane);
+        else if (warp == 14 && !(SPLIT && c.kind == 2)) value_role(c, lane);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -1044,36 +1142,244 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     }
 }
 
+// ================================================================ segments put together
+// States from segment to segment: S before segment g + 1 = (S before g) R_g + (segment g's from zeros), a block to a sequence
+// and head.  A warp has 16 state rows, as accumulators of m16n8k16, which are the next product's A operand as they lie.
+constexpr int kJoinThreads = 256;
+constexpr int kRStride = 132;                        // floats to a row of R: the B operand's reads of two rows apart meet no bank twice
+constexpr uint32_t kJoinBytes = kHeadDim * kRStride * 4 + 64;
+
+__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ DeltaArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    float* R = reinterpret_cast<float*>(smem_raw);
+    float* s_top = R + kHeadDim * kRStride;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sq = (int)(blockIdx.x / (unsigned)a.n_v), h = (int)(blockIdx.x - (unsigned)sq * (unsigned)a.n_v);
+    wait_for_stream();
+    const int slot = a.state_slots[sq];
+    const int2 span = tokens_of(a.cu_tokens, sq, a.n_tok);
+    const int chunks = (span.y - span.x + kC - 1) / kC, segments = segments_of(chunks, a.n_split);
+    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from) return;
+    const Split w = split_of(a);
+    const size_t item = (size_t)blockIdx.x * kSplitMost;
+    const int row = 16 * warp + (lane >> 2), col = 2 * (lane & 3);
+    float s[16][4];
+    auto place = [&](float* m, int t, int e) { return reinterpret_cast<float2*>(m + (row + 8 * e) * kHeadDim + 8 * t + col); };
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 x = *place(w.ends + item * kStateFloats, t, e);
+            s[t][2 * e] = x.x, s[t][2 * e + 1] = x.y;
+        }
+    for (int g = 1; g < segments; ++g) {
+        const float* turn = w.turns + (item + g) * kStateFloats;
+        float top = 0.f;
+        __syncthreads();                             // R of the segment before has been read
+#pragma unroll 8
+        for (int i = tid; i < kStateFloats / 4; i += kJoinThreads) {
+            const float4 x = reinterpret_cast<const float4*>(turn)[i];
+            *reinterpret_cast<float4*>(R + (i / 32) * kRStride + 4 * (i & 31)) = x;
+            top = fmax3(top, fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) s_top[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, s_top[i]);
+        // powers of two: one for R, one for each state row
+        const float r_unit = unit_of(top);
+        float unit[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float m = 0.f;
+#pragma unroll
+            for (int t = 0; t < 16; ++t) m = fmax3(m, fabsf(s[t][2 * e]), fabsf(s[t][2 * e + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            unit[e] = unit_of(m);
+        }
+        float n[16][4];
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[t][j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            Frag4 f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)              // rows lane / 4 and + 8 of tiles 2 k and 2 k + 1
+                split2(mul2(pair(s[2 * k + (j >> 1)][2 * (j & 1)], s[2 * k + (j >> 1)][2 * (j & 1) + 1]), pair(unit[j & 1], unit[j & 1])), f.hi[j], f.lo[j]);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                Frag2 b;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float* x = R + (16 * k + col + 8 * i) * kRStride + 8 * t + (lane >> 2);
+                    split2(mul2(pair(x[0], x[kRStride]), pair(r_unit, r_unit)), b.hi[i], b.lo[i]);
+                }
+                mma_pairs(n[t], f, b);
+            }
+        }
+        float* add = w.ends + (item + g) * kStateFloats;
+        float* to = g + 1 < segments ? add : a.state + ((size_t)slot * a.n_v + h) * kStateFloats;
+        const float up[2] = {1.f / unit[0] / r_unit, 1.f / unit[1] / r_unit};
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 x = *place(add, t, e);
+                s[t][2 * e] = fmaf(n[t][2 * e], up[e], x.x), s[t][2 * e + 1] = fmaf(n[t][2 * e + 1], up[e], x.y);
+                *place(to, t, e) = make_float2(s[t][2 * e], s[t][2 * e + 1]);
+            }
+    }
+}
+
+// The outputs of segments behind the first: from zeros, plus scale (S before the segment) (R_t q_t).  A block takes
+// kAddChunks consecutive chunks of a sequence and head: tokens by value dims, S in shared memory as FP16 with a power of two
+// for each row, the tokens' R_t q_t likewise.
+constexpr int kAddThreads = 256, kAddChunks = 4;
+constexpr uint32_t kAddS = 0, kAddT = kHeadDim * kHeadDim * 2, kAddUnit = kAddT + kC * kHeadDim * 2;
+constexpr uint32_t kAddBytes = kAddUnit + (kHeadDim + kC) * 4 + 1024;
+
+template <int TYPE>
+__global__ void __launch_bounds__(kAddThreads) delta_add_kernel(const __grid_constant__ DeltaArgs a, const int groups) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_u - raw_u);
+    float* s_unit = reinterpret_cast<float*>(base + kAddUnit);       // 1 / the units of S's rows, then of the tokens
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const unsigned item = blockIdx.x / (unsigned)groups;
+    const int group = (int)(blockIdx.x - item * (unsigned)groups);
+    const int sq = (int)(item / (unsigned)a.n_v), h = (int)(item - (unsigned)sq * (unsigned)a.n_v);
+    wait_for_stream();
+    const int slot = a.state_slots[sq];
+    const int2 span = tokens_of(a.cu_tokens, sq, a.n_tok);
+    const int chunks = (span.y - span.x + kC - 1) / kC, segments = segments_of(chunks, a.n_split);
+    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from) return;
+    const int each = (chunks + segments - 1) / segments;
+    const Split w = split_of(a);
+    // COUNT of a warp's rows (every eighth, from r on), a lane's four elements of each: the largest, the unit, FP16 into a tile
+    // of two 64-dim halves; rows from `there` on are zeros
+    auto put_rows = [&](auto count, const float* src, size_t apart, int there, uint32_t tile, uint32_t half_bytes, int r, float* up) {
+        constexpr int kCount = decltype(count)::value;
+        float4 x[kCount];
+#pragma unroll
+        for (int i = 0; i < kCount; ++i)
+            x[i] = r + 8 * i < there ? reinterpret_cast<const float4*>(src + (r + 8 * i) * apart)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float unit = unit_of(m);
+            *reinterpret_cast<uint2*>(base + tile + (lane >> 4) * half_bytes + swz(r + 8 * i, (lane & 15) >> 1) + 8 * (lane & 1)) =
+                make_uint2(pack_f16x2(x[i].x * unit, x[i].y * unit), pack_f16x2(x[i].z * unit, x[i].w * unit));
+            if (lane == 0) up[r + 8 * i] = 1.f / unit;
+        }
+    };
+    int held = -1;
+    for (int c = group * kAddChunks; c < min(chunks, (group + 1) * kAddChunks); ++c) {
+        const int g = c / each;
+        if (g == 0) continue;
+        const int first = span.x + c * kC, n = min(kC, span.y - first);
+        __syncthreads();                             // the tiles of the chunk before have been read
+        if (g != held) {
+            held = g;
+            const float* S = w.ends + ((size_t)item * kSplitMost + g - 1) * kStateFloats;
+            put_rows(std::integral_constant<int, 8>{}, S, kHeadDim, kHeadDim, kAddS, kHeadDim * 128, warp, s_unit);
+            put_rows(std::integral_constant<int, 8>{}, S, kHeadDim, kHeadDim, kAddS, kHeadDim * 128, warp + 64, s_unit);
+        }
+        const float* turned = w.plain + (size_t)a.n_tok * a.n_v * kHeadDim + ((size_t)first * a.n_v + h) * kHeadDim;
+        put_rows(std::integral_constant<int, 8>{}, turned, (size_t)a.n_v * kHeadDim, n, kAddT, kC * 128, warp, s_unit + kHeadDim);
+        // the outputs so far, on their way meanwhile
+        const float* from = w.plain + ((size_t)first * a.n_v + h) * kHeadDim;
+        float2 so_far[2][8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = 16 * (warp & 3) + (lane >> 2) + 8 * e;
+                so_far[e][j] = t < n ? *reinterpret_cast<const float2*>(from + (size_t)t * a.n_v * kHeadDim + 64 * (warp >> 2) + 8 * j + 2 * (lane & 3))
+                                     : make_float2(0.f, 0.f);
+            }
+        __syncthreads();
+        const int m0 = 16 * (warp & 3), n0 = 64 * (warp >> 2);       // tokens m0 .. + 15, value dims n0 .. + 63
+        float acc[8][4];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t f[4], b[4];
+            ldmatrix4(base_u + kAddT + (k >> 2) * (kC * 128) + swz(m0 + (lane & 15), 2 * (k & 3) + (lane >> 4)), f);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                ldmatrix4(base_u + kAddS + (k >> 2) * (kHeadDim * 128) + swz(n0 + 16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * (k & 3) + ((lane >> 3) & 1)), b);
+                mma16816(acc[2 * t], f, b[0], b[1]);
+                mma16816(acc[2 * t + 1], f, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = m0 + (lane >> 2) + 8 * e;
+            if (t >= n) continue;
+            const float up = s_unit[kHeadDim + t] * a.scale;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = n0 + 8 * j + 2 * (lane & 3);
+                const float2 x = so_far[e][j];
+                *reinterpret_cast<uint32_t*>(a.out + (long long)(first + t) * a.out_stride + (size_t)h * kHeadDim + d) =
+                    pack2(fmaf(acc[j][2 * e], up * s_unit[d], x.x), fmaf(acc[j][2 * e + 1], up * s_unit[d + 1], x.y), TYPE);
+            }
+        }
+    }
+}
+
 template <int TYPE>
 cudaError_t launch(DeltaArgs a, cudaStream_t stream) {
-    const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, chunks = (long long)a.n_seq * a.n_v;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    a.n_split = most_segments(a.n_tok, a.n_seq, a.n_v, sms < kSplitSms ? sms : kSplitSms);
+    const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, heads = (long long)a.n_seq * a.n_v, chunks = heads * (2 * a.n_split - 1);
     if (prep > 0x7fffffffLL || chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // Lengths are device data.  Few tokens in all: every sequence is short.  Several sequences: some may be.
     if (a.n_tok <= kDeltaShort || a.n_seq > 1) {
-        const cudaError_t e = launch_delta_short(a, stream);
+        e = launch_delta_short(a, stream);
         if (e != cudaSuccess || a.n_tok <= kDeltaShort) return e;
         a.chunked_from = kDeltaShort + 1;
     }
     auto* kernel = a.n_v > 2 * a.n_k ? delta_prep_kernel<TYPE, true> : delta_prep_kernel<TYPE, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_chunk_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkBytes);
-    if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepBytes);
+    auto* chunk_kernel = a.n_split > 1 ? delta_chunk_kernel<TYPE, true> : delta_chunk_kernel<TYPE, false>;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkBytes);
     if (e != cudaSuccess) return e;
     // The chunks' blocks beside the first kernel's only where that one's all run at once and leave SMs free: one sequence of 61
     // tokens takes 20.0 us instead of 22.9, one of 8,192, whose chunks' blocks then take the SMs as they come free, 467 instead of 412.
     const int early = prep + chunks <= sms;
     e = launch_overlapped(kernel, dim3((unsigned)prep), kPrepThreads, kPrepBytes, stream, a, early);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(delta_chunk_kernel<TYPE>, dim3((unsigned)chunks), kChunkThreads, kChunkBytes, stream, a);
+    e = launch_overlapped(chunk_kernel, dim3((unsigned)chunks), kChunkThreads, kChunkBytes, stream, a);
+    if (e != cudaSuccess || a.n_split < 2) return e;
+    e = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_add_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAddBytes);
+    if (e == cudaSuccess) e = launch_overlapped(delta_join_kernel, dim3((unsigned)heads), kJoinThreads, kJoinBytes, stream, a);
+    if (e != cudaSuccess) return e;
+    const int groups = (a.n_tok / kC + 1 + kAddChunks - 1) / kAddChunks;
+    return launch_overlapped(delta_add_kernel<TYPE>, dim3((unsigned)(heads * groups)), kAddThreads, kAddBytes, stream, a, groups);
 }
 
 }  // namespace
 
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v) {
-    return places(n_tok, n_seq) * ((size_t)n_k * kKqBytes + (size_t)n_v * kHeadBytes) + 256;
+    size_t bytes = places(n_tok, n_seq) * ((size_t)n_k * kKqBytes + (size_t)n_v * kHeadBytes) + 256;
+    if (most_segments(n_tok, n_seq, n_v, kSplitSms) > 1)
+        bytes += ((size_t)n_tok * kHeadDim + (size_t)n_seq * kSplitMost * kStateFloats) * 2 * n_v * 4;
+    return bytes;
 }
 
 cudaError_t launch_delta_prompt(const DeltaArgs& a, cudaStream_t stream) {

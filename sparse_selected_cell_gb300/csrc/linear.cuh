@@ -50,6 +50,7 @@ struct DeltaArgs {
     uint8_t* workspace;
     int32_t* dev_status;
     int chunked_from;             // delta_prompt.cu: the fewest tokens of a sequence that goes by chunks
+    int n_split;                  // delta_prompt.cu: the most segments a sequence's chunks are cut into
 };
 
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
