@@ -109,15 +109,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 
 // D (+)= A B^T, A in Tensor Memory, issued by the lane that has `leader` set (one of a converged warp).
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add, uint32_t leader) {
-    if (add)
-        asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-                     " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
-                     ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader) : "memory");
-    else
-        asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 t, 0, 0;\n"
-                     " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
-                     ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader) : "memory");
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add, uint32_t leader) {
+    asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader), "r"(add) : "memory");
 }
 
 // x and y as FP16 pairs: hi the nearest, lo the nearest of what is left (x - hi is exact).
@@ -556,7 +551,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' in FP16 lies where S K^T was, V' P^T where V' was.
 constexpr uint32_t kTmS = 0, kTmKs = 128, kTmH = 128, kTmQs = 192, kTmX = 256, kTmV = 320, kTmPv = 320, kTmD = 384;
 // The quarters of an operand in the order in which they are there: each half's first, each half's second.
-__device__ __forceinline__ constexpr int quarter(int i) { return i == 1 ? 2 : i == 2 ? 1 : i; }
+__device__ __forceinline__ constexpr int quarter(int i) { return ((i & 1) << 1) | (i >> 1); }
 
 struct Block {
     const DeltaArgs* a;
@@ -573,17 +568,19 @@ struct Block {
 };
 __device__ __forceinline__ uint32_t bar(const Block& c, int i) { return c.base_u + kOffBar + 8u * i; }
 __device__ __forceinline__ bool wait(const Block& c, int i, int parity) {
-    // inline, without a call: the groups of warps have registers of their own number
-    if (tc::mbar_try_wait(bar(c, i), (uint32_t)parity)) return true;
-    const uint64_t t0 = tc::globaltimer_ns();
+    // inline, without a call (the groups of warps have registers of their own number), and short: the loops of all roles
+    // together have to stay in the instruction caches, which neighbouring SMs share
+    uint64_t since = 0;
 #pragma unroll 1
-    for (uint32_t n = 1;; ++n) {
-        if (tc::mbar_try_wait(bar(c, i), (uint32_t)parity)) return true;
-        if ((n & 15u) == 0 && (*c.abort_flag || tc::globaltimer_ns() - t0 > kWaitNs)) break;
+    while (!tc::mbar_try_wait(bar(c, i), (uint32_t)parity)) {
+        const uint64_t now = tc::globaltimer_ns();
+        if (since == 0) since = now;
+        if (*c.abort_flag || now - since > kWaitNs) {
+            *c.abort_flag = 1;                       // reported at the block's end
+            return false;
+        }
     }
-    *c.abort_flag = 1;
-    report(c.a->dev_status, QSA_DEV_WAIT_TIMEOUT);
-    return false;
+    return true;
 }
 // The warp's stores to Tensor Memory, and its loads from it, are done: tell whoever waits on `i`.
 __device__ __forceinline__ void tell(const Block& c, int i) {
@@ -623,7 +620,7 @@ __device__ void value_role(const Block& c, int lane) {
         const int vs = i % kVStages;
         if (i >= kVStages && !wait(c, BAR_VEMPTY + vs, (i / kVStages - 1) & 1)) break;
         const uint32_t to = c.base_u + kOffV + vs * kVBytes + lane * 16;
-#pragma unroll 8
+#pragma unroll 4
         for (int p = 0; p < kC / 2; ++p) {
             // tokens that the last chunk does not have are filled with zeros (their factors are zero, but what lies there might be no number)
             const int t = i * kC + 2 * p + (lane >> 4);
@@ -649,24 +646,27 @@ __device__ void product_role(const Block& c) {
     uint32_t leader;
     asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(leader));
     auto with_queries = [&](uint64_t stage, int lo) {       // S Q^T, of the hi or the lo
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            product(c.tmem + kTmQs, c.tmem + kTmS + 16 * k + lo,
-                             dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + kC * 128 + (k & 3) * 32) >> 4), id64, k > 0 || lo, leader);
+            for (int k = 0; k < 4; ++k)
+                product(c.tmem + kTmQs, c.tmem + kTmS + 64 * half + 16 * k + lo,
+                        dkq0 + stage + ((half * (kKqBytes / 2) + kC * 128 + k * 32) >> 4), id64, half | k | lo, leader);
     };
     for (int i = 0; i < c.n_chunks && ok; ++i) {
         const int st = i % kStages, par = i & 1;
         const uint64_t stage = (uint64_t)(st * kStageBytes) >> 4, tri = stage + (kKqBytes >> 4);
         if (!(ok = wait(c, BAR_FULL + st, (i / kStages) & 1))) break;
-#pragma unroll
+#pragma unroll 1
         for (int n = 0; n < 4; ++n) {
-            if (!(ok = wait(c, BAR_S + quarter(n), par))) break;
+            const int q = quarter(n);
+            if (!(ok = wait(c, BAR_S + q, par))) break;
             tc::fence_after_sync();
 #pragma unroll
-            for (int k = 2 * quarter(n); k < 2 * quarter(n) + 2; ++k) {
-                const uint64_t d = dkq0 + stage + (((k >> 2) * (kKqBytes / 2) + (k & 3) * 32) >> 4);
-                product(c.tmem + kTmKs, c.tmem + kTmS + 16 * k, d, id64, k > 0, leader);
-                product(c.tmem + kTmKs, c.tmem + kTmS + 16 * k + 8, d, id64, true, leader);
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t d = dkq0 + stage + (((q >> 1) * (kKqBytes / 2) + (q & 1) * 64 + k * 32) >> 4);
+                product(c.tmem + kTmKs, c.tmem + kTmS + 32 * q + 16 * k, d, id64, q | k, leader);
+                product(c.tmem + kTmKs, c.tmem + kTmS + 32 * q + 16 * k + 8, d, id64, 1, leader);
             }
         }
         if (!ok) break;
@@ -674,39 +674,38 @@ __device__ void product_role(const Block& c) {
         if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
         tc::fence_after_sync();
         with_queries(stage, 0);
-#pragma unroll
+#pragma unroll 1
         for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
             const int b = quarter(n);
             if (!(ok = wait(c, BAR_X + b, par))) break;
             tc::fence_after_sync();
-            const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
+            const uint32_t id = id64 - (uint32_t)b * (2u << 17);     // 64 - 16 b columns
             const uint64_t d = dkq0 + tri + ((b * 2048 + b * 32) >> 4);
             const uint32_t at = c.tmem + kTmX + 8 * b, to = c.tmem + kTmV + 16 * b;
-            product(to, at, d, id, b > 0, leader);
-            product(to, at + 32, d, id, true, leader);
-            product(to, at, d + (kOffTlo >> 4), id, true, leader);
+            product(to, at, d, id, b, leader);
+            product(to, at + 32, d, id, 1, leader);
+            product(to, at, d + (kOffTlo >> 4), id, 1, leader);
         }
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_V));
         if (TYPE == QSA_F16) with_queries(stage, 8);  // (BF16 outputs would not show it)
-#pragma unroll
+#pragma unroll 1
         for (int n = 0; n < 4; ++n) {
             const int b = quarter(n);
             if (!(ok = wait(c, BAR_D + b, par))) break;
             tc::fence_after_sync();
             const uint64_t d = dkt0 + stage + ((b * 2048) >> 4);
-            product(c.tmem + kTmD, c.tmem + kTmX + 8 * b, d, idD, true, leader);
-            product(c.tmem + kTmD, c.tmem + kTmX + 32 + 8 * b, d, idD, true, leader);
+            product(c.tmem + kTmD, c.tmem + kTmX + 8 * b, d, idD, 1, leader);
+            product(c.tmem + kTmD, c.tmem + kTmX + 32 + 8 * b, d, idD, 1, leader);
         }
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_U));
         if (!(ok = wait(c, BAR_H, par))) break;
         tc::fence_after_sync();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const uint32_t id = tc::idesc_bf16(128, 64 - 16 * b, false, false) & kTypes;
-            product(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4), id, b > 0, leader);
-        }
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b)
+            product(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4),
+                    id64 - (uint32_t)b * (2u << 17), b, leader);
         tc::commit_elect(bar(c, BAR_O));
         tc::commit_elect(bar(c, BAR_EMPTY + st));
     }
@@ -819,18 +818,16 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + 32 * half;
         // ---- the state as the next operand
         const f2 s2 = pair(unit * d_up, unit * d_up);
-        uint32_t d[64];
-        tc::tmem_ld32(tmD, *reinterpret_cast<uint32_t(*)[32]>(d));
-        tc::tmem_ld32(tmD + 32, *reinterpret_cast<uint32_t(*)[32]>(d + 32));
-        tc::tmem_wait_ld();
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 2; ++b) {
+            uint32_t d[32];
+            tc::tmem_ld32(tmD + 32 * b, d);
+            tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t w[16];                      // 8 columns of hi, 8 of lo
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    split2(mul2(s2, pair_of(d[32 * b + 16 * e + 2 * j], d[32 * b + 16 * e + 2 * j + 1])), w[j], w[8 + j]);
+                for (int j = 0; j < 8; ++j) split2(mul2(s2, pair_of(d[16 * e + 2 * j], d[16 * e + 2 * j + 1])), w[j], w[8 + j]);
                 tc::tmem_st16(tmS + 32 * b + 16 * e, w);
             }
             tc::tmem_wait_st();
@@ -864,18 +861,19 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         const float d_unit = v_unit * scal[kScalU - 32 * half], gd = scal[kScalG - 32 * half] * (d_unit * d_up);
         const f2 g2 = pair(gd, gd);
         sm = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 2; ++b) {
-            uint32_t w[32];
+            uint32_t d[32];
+            tc::tmem_ld32(tmD + 32 * b, d);
+            tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const uint32_t x = d[32 * b + 2 * j], y = d[32 * b + 2 * j + 1];
+                sm = fmax3(sm, fabsf(__uint_as_float(d[2 * j])), fabsf(__uint_as_float(d[2 * j + 1])));
                 float gx, gy;
-                unpair(mul2(g2, pair_of(x, y)), gx, gy);
-                w[2 * j] = __float_as_uint(gx), w[2 * j + 1] = __float_as_uint(gy);
-                sm = fmax3(sm, fabsf(__uint_as_float(x)), fabsf(__uint_as_float(y)));
+                unpair(mul2(g2, pair_of(d[2 * j], d[2 * j + 1])), gx, gy);
+                d[2 * j] = __float_as_uint(gx), d[2 * j + 1] = __float_as_uint(gy);
             }
-            tc::tmem_st32(tmD + 32 * b, w);
+            tc::tmem_st32(tmD + 32 * b, d);
         }
         sm *= d_up;
         top_s[par * 256 + half * 128] = sm;
@@ -958,51 +956,44 @@ __device__ void output_role(const Block& c, int q, int lane) {
         const int n = min(kC, c.n_tok - i * kC);
         const bool plain = SPLIT && c.plain;
         float* whole = reinterpret_cast<float*>(mine);               // FP32 outputs pass the same place, 32 tokens at a time
-        uint32_t out[32];
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             uint32_t qs[16], pv[16];
             tc::tmem_ld16(tm + kTmQs + 16 * b, qs);
             tc::tmem_ld16(tm + kTmPv + 16 * b, pv);
             tc::tmem_wait_ld();
+            if (b == 3) tell(c, BAR_OFREE);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 o = *reinterpret_cast<const float2*>(scal + 16 * b + 2 * j);
+                const f2 o = *reinterpret_cast<const f2*>(scal + 16 * b + 2 * j);
                 float x, y;
-                unpair(fma2(mul2(pair(o.x, o.y), us2), pair_of(qs[2 * j], qs[2 * j + 1]), mul2(uv2, pair_of(pv[2 * j], pv[2 * j + 1]))), x, y);
-                out[8 * b + j] = pack2(x, y, TYPE);
+                unpair(fma2(mul2(o, us2), pair_of(qs[2 * j], qs[2 * j + 1]), mul2(uv2, pair_of(pv[2 * j], pv[2 * j + 1]))), x, y);
                 if (plain) {
                     whole[(16 * (b & 1) + 2 * j) * 32 + lane] = x;
                     whole[(16 * (b & 1) + 2 * j + 1) * 32 + lane] = y;
+                } else {
+                    const uint32_t two = pack2(x, y, TYPE);
+                    mine[(16 * b + 2 * j) * 32 + lane] = (uint16_t)(two & 0xFFFFu);
+                    mine[(16 * b + 2 * j + 1) * 32 + lane] = (uint16_t)(two >> 16);
                 }
             }
             if (plain && (b & 1)) {
                 __syncwarp();
                 float* to = c.plain + ((size_t)(c.first + i * kC + 16 * (b - 1)) * a.n_v + c.h) * kHeadDim + 32 * q + 4 * (lane & 7);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = 4 * j + (lane >> 3);
+#pragma unroll 1
+                for (int t = lane >> 3; t < 32; t += 4)
                     if (16 * (b - 1) + t < n)
                         *reinterpret_cast<float4*>(to + (size_t)t * a.n_v * kHeadDim) = *reinterpret_cast<const float4*>(whole + t * 32 + 4 * (lane & 7));
-                }
                 __syncwarp();
             }
         }
-        tell(c, BAR_OFREE);
         if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
         if (plain) continue;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            mine[(2 * j) * 32 + lane] = (uint16_t)(out[j] & 0xFFFFu);
-            mine[(2 * j + 1) * 32 + lane] = (uint16_t)(out[j] >> 16);
-        }
         __syncwarp();
         uint16_t* to = a.out + (long long)(c.first + i * kC) * a.out_stride + (size_t)c.h * kHeadDim + 32 * q + 8 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int t = 8 * j + (lane >> 2);
-            if (t < n) *reinterpret_cast<uint4*>(to + (long long)t * a.out_stride) = *reinterpret_cast<const uint4*>(mine + t * 32 + 8 * (lane & 3));
-        }
+#pragma unroll 2
+        for (int t = lane >> 2; t < n; t += 8)
+            *reinterpret_cast<uint4*>(to + (long long)t * a.out_stride) = *reinterpret_cast<const uint4*>(mine + t * 32 + 8 * (lane & 3));
         __syncwarp();
     }
 }
@@ -1136,6 +1127,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     }
     tc::fence_before_sync();
     __syncthreads();
+    if (tid == 0 && *c.abort_flag) report(a.dev_status, QSA_DEV_WAIT_TIMEOUT);
     if (warp == 12) {
         tc::fence_after_sync();
         tc::tmem_dealloc(c.tmem, 512);
