@@ -273,42 +273,41 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         vec[4 * kC + tt] = exp2f((float)(last - G));
     };
     ask_gates(0);
-    uint4 raw[16];                                   // row 2 (4 p + warp) + lane / 16 of 64 keys, then 64 queries
-#pragma unroll
+    // rows into their places as they are: a thread's own 16-byte words, rows 2 (4 p + warp) + lane / 16 of 64 keys, then 64 queries
+    const int l = lane & 15;
+    const uint32_t own = (uint32_t)(l >> 3) * (kKqBytes / 2);
+#pragma unroll 4
     for (int p = 0; p < 16; ++p) {
-        const int t = (2 * (4 * p + warp) + (lane >> 4)) & (kC - 1);
-        const uint16_t* src = p < 8 ? a.k + (long long)(first + t) * a.k_stride : a.q + (long long)(first + t) * a.q_stride;
-        raw[p] = t < n ? *reinterpret_cast<const uint4*>(src + (size_t)kh * kHeadDim + 8 * (lane & 15)) : make_uint4(0, 0, 0, 0);
+        const int r = 2 * (4 * p + warp) + (lane >> 4), t = r & (kC - 1);
+        const uint16_t* src = p < 8 ? a.k + (long long)(first + min(t, n - 1)) * a.k_stride : a.q + (long long)(first + min(t, n - 1)) * a.q_stride;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(base_u + own + swz(r, l & 7)), "l"(src + (size_t)kh * kHeadDim + 8 * l), "r"(t < n ? 16 : 0) : "memory");
     }
     scan_gates(0);
     // ---- keys and queries to FP16 rows, each times the power of two that puts its largest element in [2^10, 2^11)
-    {
-        const int l = lane & 15;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+    for (int p = 0; p < 16; ++p) {
+        const int r = 2 * (4 * p + warp) + (lane >> 4);
+        const uint32_t at = own + swz(r, l & 7);
+        float x[8];
+        unpack8(*reinterpret_cast<const uint4*>(base + at), TYPE, x);
+        float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
 #pragma unroll
-        for (int p = 0; p < 16; ++p) {
-            const int r = 2 * (4 * p + warp) + (lane >> 4);
-            float x[8];
-            unpack8(raw[p], TYPE, x);
-            float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
+        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
+        const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = min(e, 100);
+        const f2 up = pair(exp2i(e1), exp2i(e1)), more = pair(exp2i(e - e1), exp2i(e - e1));
+        uint32_t h[4];
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
-            const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = e > 100 ? 100 : e;
-            const f2 up = pair(exp2i(e1), exp2i(e1));
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float u, w2;
-                f2 y = mul2(pair(x[2 * j], x[2 * j + 1]), up);
-                if (e != e1) y = mul2(y, pair(exp2i(e - e1), exp2i(e - e1)));
-                unpair(y, u, w2);
-                h[j] = pack_f16x2(u, w2);
-            }
-            const uint32_t at = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r, l & 7);
-            *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (l == 0) s_e[r] = e;
+        for (int j = 0; j < 4; ++j) {
+            float u, w2;
+            unpair(mul2(mul2(pair(x[2 * j], x[2 * j + 1]), up), more), u, w2);
+            h[j] = pack_f16x2(u, w2);
         }
+        *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (l == 0) s_e[r] = e;
     }
     __syncthreads();
     join_gates();
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = qq[i & 1][j] = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 8; ++k) {
         const uint32_t tile = base_u + (uint32_t)(k >> 2) * (kKqBytes / 2);
         const int brow = (lane & 7) + ((lane >> 4) << 3), bword = 2 * (k & 3) + ((lane >> 3) & 1);
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             scal[kScalO + tt] = vec[3 * kC + tt] * s_r[kC + tt];
             if (tt == kC - 1) scal[kScalG] = vec[3 * kC + tt], scal[kScalU] = key_unit;
         }
-#pragma unroll
+#pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
             if (h0 + hh >= rep) continue;
             const float* ve = s_g + hh * kVecs * kC;
