@@ -17,7 +17,8 @@
 // products of which lo lo is left out; the state itself stays in FP32 registers.  All products
 // are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
 // the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
-// passes FP16's range and what counts stays in its upper bits.  P and V' in P V' are single FP16.
+// passes FP16's range and what counts stays in its upper bits.  In P V' P is single
+// FP16, and so is V' for BF16 outputs, which would not show more.
 #include <type_traits>
 
 #include "linear.cuh"
@@ -547,7 +548,8 @@ static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memo
 constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
-// products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' in FP16 lies where S K^T was, V' P^T where V' was.
+// products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T
+// where V' was.
 constexpr uint32_t kTmS = 0, kTmKs = 128, kTmH = 128, kTmQs = 192, kTmX = 256, kTmV = 320, kTmPv = 320, kTmD = 384;
 // The quarters of an operand in the order in which they are there: each half's first, each half's second.
 __device__ __forceinline__ constexpr int quarter(int i) { return ((i & 1) << 1) | (i >> 1); }
@@ -702,9 +704,12 @@ __device__ void product_role(const Block& c) {
         if (!(ok = wait(c, BAR_H, par))) break;
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b)
-            product(c.tmem + kTmPv + 16 * b, c.tmem + kTmH + 8 * b, dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4),
-                    id64 - (uint32_t)b * (2u << 17), b, leader);
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t to = c.tmem + kTmPv + 16 * b, at = c.tmem + kTmH + 8 * b, id = id64 - (uint32_t)b * (2u << 17);
+            const uint64_t d = dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4);
+            product(to, at, d, id, b, leader);
+            if (TYPE == QSA_F16) product(to, at + 32, d, id, 1, leader);
+        }
         tc::commit_elect(bar(c, BAR_O));
         tc::commit_elect(bar(c, BAR_EMPTY + st));
     }
@@ -883,7 +888,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         tc::fence_after_sync();
         const f2 vx2 = pair(vx, vx);
         {
-            uint32_t w[32], one[16];
+            uint32_t w[32], one[16], rest[16];
             tc::tmem_ld32(tmT + kTmV, w);
             tc::tmem_wait_ld();
 #pragma unroll
@@ -896,9 +901,13 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const f2 p = mul2(vx2, pair_of(k[2 * u], k[2 * u + 1]));
-                        float x, y;
-                        unpair(p, x, y);
-                        one[8 * b + j + u] = pack_f16x2(x, y);
+                        if (TYPE == QSA_F16) {
+                            split2(p, one[8 * b + j + u], rest[8 * b + j + u]);
+                        } else {
+                            float x, y;
+                            unpair(p, x, y);
+                            one[8 * b + j + u] = pack_f16x2(x, y);
+                        }
                         split2(mul2(p, u ? f.y : f.x), hi[j + u], lo[j + u]);
                     }
                 }
@@ -908,6 +917,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 tell(c, BAR_D + 2 * half + b);
             }
             tc::tmem_st16(tm + kTmH + 16 * half, one);
+            if (TYPE == QSA_F16) tc::tmem_st16(tm + kTmH + 32 + 16 * half, rest);
             tc::tmem_wait_st();
         }
         tell(c, BAR_H);
@@ -1013,7 +1023,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     c.h = (int)(item - (unsigned)c.s * (unsigned)a.n_v);
     if (a.n_seq > 1 && a.n_seq <= kRanked) {
         // the longest sequences first: block b's is the one of which c.s are longer (or as long, and before it)
-        int* lens = reinterpret_cast<int*>(c.base);
+        int* lens = reinterpret_cast<int*>(c.base + kOffOut);         // (no bulk copy ever writes there)
         for (int i = tid; i < a.n_seq; i += kChunkThreads) {
             const int2 t = tokens_of(a.cu_tokens, i, a.n_tok);
             lens[i] = t.y - t.x;
@@ -1026,7 +1036,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         }
         __syncthreads();
         c.s = lens[kRanked];
-        __syncthreads();                             // before the place is used for anything else
+        __syncthreads();
     }
     // Behind delta_prep_kernel this kernel is released when all of that one's blocks have passed their own
     // wait, so that everything before it is there already: only the copies of its results wait for it here, and every block
