@@ -25,6 +25,12 @@ bool rows_ok(const void* p, int64_t stride, int64_t width) {
 constexpr int32_t kMaxHeads = 1 << 16;
 constexpr int32_t kMaxTokens = 1 << 30;
 
+// Blocks of a launch: two to a sequence and value head, one to a chunk (at most n_tok / 64 + n_seq) and key head.
+bool sizes_fit(int32_t n_tok, int32_t n_seq, int32_t n_k, int32_t n_v) {
+    return n_v <= kMaxHeads && n_tok <= kMaxTokens && (long long)n_seq * n_v <= kMaxTokens / 2 &&
+           (n_tok / 64 + (long long)n_seq) * n_k <= kMaxTokens;
+}
+
 // Whether two arrays of n tokens, `width` 16-bit elements of each in use, share a byte (strides in elements).  Rows
 // interleave where both are slices of one wider array: equal strides, and offsets that keep them apart.
 bool overlap(const void* p, int64_t ps, int64_t pw, const void* q, int64_t qs, int64_t qw, int64_t n) {
@@ -41,7 +47,7 @@ int check_delta(const qsa::DeltaArgs& a) {
     if (a.n_seq < 0 || a.n_tok < 0 || a.n_slots < 0 || a.n_k <= 0 || a.n_v <= 0 || a.n_v % a.n_k != 0 || !type16(a.type))
         return QSA_ERR_ARG;
     if (!(a.eps >= 0.f) || !std::isfinite(a.eps) || !std::isfinite(a.scale)) return QSA_ERR_ARG;
-    if (a.n_v > kMaxHeads || a.n_tok > kMaxTokens || (long long)a.n_seq * a.n_v > kMaxTokens) return QSA_ERR_UNSUPPORTED;
+    if (!sizes_fit(a.n_tok, a.n_seq, a.n_k, a.n_v)) return QSA_ERR_UNSUPPORTED;
     if (a.n_seq == 0) return QSA_OK;
     if (!a.state_slots || !a.a_log || !a.dt_bias || !aligned(a.state, 16) || (a.n_slots > 0 && !a.state)) return QSA_ERR_ARG;
     if (a.n_tok == 0) return QSA_OK;
@@ -88,9 +94,7 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
 }
 
 size_t qsa_delta_prompt_workspace_bytes(int32_t n_tok, int32_t n_seq, int32_t n_k, int32_t n_v) {
-    if (n_tok < 0 || n_seq < 0 || n_k <= 0 || n_v <= 0 || n_v % n_k != 0 || n_v > kMaxHeads || n_tok > kMaxTokens ||
-        (long long)n_seq * n_v > kMaxTokens)
-        return 0;
+    if (n_tok < 0 || n_seq < 0 || n_k <= 0 || n_v <= 0 || n_v % n_k != 0 || !sizes_fit(n_tok, n_seq, n_k, n_v)) return 0;
     return qsa::delta_prompt_workspace(n_tok, n_seq, n_k, n_v);
 }
 

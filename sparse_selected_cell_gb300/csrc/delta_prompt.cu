@@ -803,7 +803,9 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         vm = fmaxf(vm, top_v[par * 256 + (half ^ 1) * 128]);
         sm = fmaxf(sm, top_s[(par ^ 1) * 256 + (half ^ 1) * 128]);
         const float len = fmaf(12.f, sm, 66.f * vm_before);
-        unit = unit_of(len + vm), v_unit = unit_of(fmaf(66.f, vm, len));
+        // (no more than 2^60 finer than the chunk before's: its results are brought to them by a factor that stays finite)
+        const float finest = 0x1p60f / d_up;
+        unit = fminf(unit_of(len + vm), finest), v_unit = fminf(unit_of(fmaf(66.f, vm, len)), finest);
         vm_before = vm;
         const f2 unit2 = pair(unit, unit);
 #pragma unroll

@@ -97,3 +97,16 @@ def test_a_step_of_everything(qsa):  # noqa: F811
         cu = i32([0] + list(itertools.accumulate(order)))
         check_prompt(qsa, inputs, state, slots, old if turn == 0 else None, cu)
     assert cu_of(lens).shape == cu.shape
+
+
+@pytest.mark.parametrize("size", [2.0 ** 50, 2.0 ** -50])
+def test_nothing_left_after_large_values(qsa, size):  # noqa: F811
+    """Chunks of values far out, then decays that leave nothing of them and values of zero or of ordinary size: what was large
+    neither lingers in the units nor turns zeros into something else."""
+    inputs, state, slots, old, cu = batch([64 * 9], 1, 2, torch.bfloat16, seed=3)
+    q, k, v, a, b, a_log, dt = (x.clone() for x in inputs)
+    v[:128] *= size
+    v[128:320] = 0
+    a[128:192] = 80.0
+    a_log.fill_(3.0)
+    check_prompt(qsa, (q, k, v, a, b, a_log, dt), state * size, slots, old, cu)
