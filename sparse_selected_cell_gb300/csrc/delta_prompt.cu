@@ -86,6 +86,10 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -674,7 +678,6 @@ __device__ void product_role(const Block& c) {
         tc::commit_elect(bar(c, BAR_KS));
         if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
         tc::fence_after_sync();
-        with_queries(stage, 0);
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
             const int b = quarter(n);
@@ -689,6 +692,7 @@ __device__ void product_role(const Block& c) {
         }
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_V));
+        with_queries(stage, 0);
         if (TYPE == QSA_F16) with_queries(stage, 8);  // (BF16 outputs would not show it)
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
@@ -991,10 +995,12 @@ __device__ void output_role(const Block& c, int q, int lane) {
             if (plain && (b & 1)) {
                 __syncwarp();
                 float* to = c.plain + ((size_t)(c.first + i * kC + 16 * (b - 1)) * a.n_v + c.h) * kHeadDim + 32 * q + 4 * (lane & 7);
-#pragma unroll 1
-                for (int t = lane >> 3; t < 32; t += 4)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = (lane >> 3) + 4 * j;
                     if (16 * (b - 1) + t < n)
                         *reinterpret_cast<float4*>(to + (size_t)t * a.n_v * kHeadDim) = *reinterpret_cast<const float4*>(whole + t * 32 + 4 * (lane & 7));
+                }
                 __syncwarp();
             }
         }
@@ -1149,13 +1155,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 // States from segment to segment: S before segment g + 1 = (S before g) R_g + (segment g's from zeros), a block to a sequence
 // and head.  A warp has 16 state rows, as accumulators of m16n8k16, which are the next product's A operand as they lie.
 constexpr int kJoinThreads = 256;
-constexpr int kRStride = 132;                        // floats to a row of R: the B operand's reads of two rows apart meet no bank twice
-constexpr uint32_t kJoinBytes = kHeadDim * kRStride * 4 + 64;
+constexpr uint32_t kRBytes = kHeadDim * kHeadDim * 2, kJoinBytes = 2 * kRBytes + 64 + 1024;
 
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ DeltaArgs a) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    float* R = reinterpret_cast<float*>(smem_raw);
-    float* s_top = R + kHeadDim * kRStride;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_u - raw_u);         // R as FP16 pairs: hi, then lo, two halves of 64 columns each
+    float* s_top = reinterpret_cast<float*>(base + 2 * kRBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sq = (int)(blockIdx.x / (unsigned)a.n_v), h = (int)(blockIdx.x - (unsigned)sq * (unsigned)a.n_v);
     wait_for_stream();
@@ -1176,19 +1182,18 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
             s[t][2 * e] = x.x, s[t][2 * e + 1] = x.y;
         }
     for (int g = 1; g < segments; ++g) {
-        const float* turn = w.turns + (item + g) * kStateFloats;
+        const float4* turn = reinterpret_cast<const float4*>(w.turns + (item + g) * kStateFloats);
+        constexpr int kEach = kStateFloats / 4 / kJoinThreads;
+        float4 rows[kEach];                          // four columns of R's rows warp, warp + 8, ..
         float top = 0.f;
-        __syncthreads();                             // R of the segment before has been read
-#pragma unroll 8
-        for (int i = tid; i < kStateFloats / 4; i += kJoinThreads) {
-            const float4 x = reinterpret_cast<const float4*>(turn)[i];
-            *reinterpret_cast<float4*>(R + (i / 32) * kRStride + 4 * (i & 31)) = x;
-            top = fmax3(top, fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) rows[i] = turn[tid + i * kJoinThreads];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) top = fmax3(top, fmaxf(fabsf(rows[i].x), fabsf(rows[i].y)), fmaxf(fabsf(rows[i].z), fabsf(rows[i].w)));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0) s_top[warp] = top;
-        __syncthreads();
+        __syncthreads();                             // (the products of the segment before are done, too)
 #pragma unroll
         for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, s_top[i]);
         // powers of two: one for R, one for each state row
@@ -1203,6 +1208,28 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             unit[e] = unit_of(m);
         }
+        // S before segment g for delta_add_kernel, in its place: FP16 in units as that one's tile, then 1 / the units
+        uint8_t* image = reinterpret_cast<uint8_t*>(w.ends + (item + g - 1) * kStateFloats);
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<uint32_t*>(image + (t >> 3) * (kHeadDim * 128) + swz(row + 8 * e, t & 7) + 4 * (lane & 3)) =
+                    pack_f16x2(s[t][2 * e] * unit[e], s[t][2 * e + 1] * unit[e]);
+        if ((lane & 3) == 0) {
+            reinterpret_cast<float*>(image + kHeadDim * kHeadDim * 2)[row] = 1.f / unit[0];
+            reinterpret_cast<float*>(image + kHeadDim * kHeadDim * 2)[row + 8] = 1.f / unit[1];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            uint2 hi, lo;
+            split2(mul2(pair(rows[i].x, rows[i].y), pair(r_unit, r_unit)), hi.x, lo.x);
+            split2(mul2(pair(rows[i].z, rows[i].w), pair(r_unit, r_unit)), hi.y, lo.y);
+            uint8_t* at = base + (lane >> 4) * (kHeadDim * 128) + swz(warp + 8 * i, (lane & 15) >> 1) + 8 * (lane & 1);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + kRBytes) = lo;
+        }
+        __syncthreads();
         float n[16][4];
 #pragma unroll
         for (int t = 0; t < 16; ++t)
@@ -1215,18 +1242,21 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
             for (int j = 0; j < 4; ++j)              // rows lane / 4 and + 8 of tiles 2 k and 2 k + 1
                 split2(mul2(pair(s[2 * k + (j >> 1)][2 * (j & 1)], s[2 * k + (j >> 1)][2 * (j & 1) + 1]), pair(unit[j & 1], unit[j & 1])), f.hi[j], f.lo[j]);
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                Frag2 b;
+            for (int t = 0; t < 8; ++t) {            // columns 16 t .. + 15: R's rows 16 k .. + 15 as they lie, transposed
+                uint32_t hi[4], lo[4];
+                const uint32_t at = base_u + (t >> 2) * (kHeadDim * 128) + swz(16 * k + (lane & 15), 2 * (t & 3) + (lane >> 4));
+                ldmatrix4t(at, hi);
+                ldmatrix4t(at + kRBytes, lo);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float* x = R + (16 * k + col + 8 * i) * kRStride + 8 * t + (lane >> 2);
-                    split2(mul2(pair(x[0], x[kRStride]), pair(r_unit, r_unit)), b.hi[i], b.lo[i]);
+                for (int u = 0; u < 2; ++u) {
+                    mma16816(n[2 * t + u], f.hi, hi[2 * u], hi[2 * u + 1]);
+                    mma16816(n[2 * t + u], f.lo, hi[2 * u], hi[2 * u + 1]);
+                    mma16816(n[2 * t + u], f.hi, lo[2 * u], lo[2 * u + 1]);
                 }
-                mma_pairs(n[t], f, b);
             }
         }
         float* add = w.ends + (item + g) * kStateFloats;
-        float* to = g + 1 < segments ? add : a.state + ((size_t)slot * a.n_v + h) * kStateFloats;
+        float* pool = a.state + ((size_t)slot * a.n_v + h) * kStateFloats;
         const float up[2] = {1.f / unit[0] / r_unit, 1.f / unit[1] / r_unit};
 #pragma unroll
         for (int t = 0; t < 16; ++t)
@@ -1234,20 +1264,20 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
             for (int e = 0; e < 2; ++e) {
                 const float2 x = *place(add, t, e);
                 s[t][2 * e] = fmaf(n[t][2 * e], up[e], x.x), s[t][2 * e + 1] = fmaf(n[t][2 * e + 1], up[e], x.y);
-                *place(to, t, e) = make_float2(s[t][2 * e], s[t][2 * e + 1]);
+                if (g + 1 == segments) *place(pool, t, e) = make_float2(s[t][2 * e], s[t][2 * e + 1]);
             }
     }
 }
 
 // The outputs of segments behind the first: from zeros, plus scale (S before the segment) (R_t q_t).  A block takes
 // kAddChunks consecutive chunks of a sequence and head: tokens by value dims, S in shared memory as FP16 with a power of two
-// for each row, the tokens' R_t q_t likewise.
-constexpr int kAddThreads = 256, kAddChunks = 4;
+// for each row (as delta_join_kernel left it), the tokens' R_t q_t likewise.
+constexpr int kAddThreads = 256, kAddChunks = 2;
 constexpr uint32_t kAddS = 0, kAddT = kHeadDim * kHeadDim * 2, kAddUnit = kAddT + kC * kHeadDim * 2;
 constexpr uint32_t kAddBytes = kAddUnit + (kHeadDim + kC) * 4 + 1024;
 
 template <int TYPE>
-__global__ void __launch_bounds__(kAddThreads) delta_add_kernel(const __grid_constant__ DeltaArgs a, const int groups) {
+__global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_constant__ DeltaArgs a, const int groups) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u - raw_u);
@@ -1263,39 +1293,41 @@ __global__ void __launch_bounds__(kAddThreads) delta_add_kernel(const __grid_con
     if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from) return;
     const int each = (chunks + segments - 1) / segments;
     const Split w = split_of(a);
-    // COUNT of a warp's rows (every eighth, from r on), a lane's four elements of each: the largest, the unit, FP16 into a tile
-    // of two 64-dim halves; rows from `there` on are zeros
-    auto put_rows = [&](auto count, const float* src, size_t apart, int there, uint32_t tile, uint32_t half_bytes, int r, float* up) {
-        constexpr int kCount = decltype(count)::value;
-        float4 x[kCount];
-#pragma unroll
-        for (int i = 0; i < kCount; ++i)
-            x[i] = r + 8 * i < there ? reinterpret_cast<const float4*>(src + (r + 8 * i) * apart)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float unit = unit_of(m);
-            *reinterpret_cast<uint2*>(base + tile + (lane >> 4) * half_bytes + swz(r + 8 * i, (lane & 15) >> 1) + 8 * (lane & 1)) =
-                make_uint2(pack_f16x2(x[i].x * unit, x[i].y * unit), pack_f16x2(x[i].z * unit, x[i].w * unit));
-            if (lane == 0) up[r + 8 * i] = 1.f / unit;
-        }
-    };
-    int held = -1;
-    for (int c = group * kAddChunks; c < min(chunks, (group + 1) * kAddChunks); ++c) {
+    const size_t apart = (size_t)a.n_v * kHeadDim;
+    int held = 0;
+    for (int c = max(group * kAddChunks, each); c < min(chunks, (group + 1) * kAddChunks); ++c) {
         const int g = c / each;
-        if (g == 0) continue;
         const int first = span.x + c * kC, n = min(kC, span.y - first);
         __syncthreads();                             // the tiles of the chunk before have been read
         if (g != held) {
             held = g;
-            const float* S = w.ends + ((size_t)item * kSplitMost + g - 1) * kStateFloats;
-            put_rows(std::integral_constant<int, 8>{}, S, kHeadDim, kHeadDim, kAddS, kHeadDim * 128, warp, s_unit);
-            put_rows(std::integral_constant<int, 8>{}, S, kHeadDim, kHeadDim, kAddS, kHeadDim * 128, warp + 64, s_unit);
+            const uint8_t* S = reinterpret_cast<const uint8_t*>(w.ends + ((size_t)item * kSplitMost + g - 1) * kStateFloats);
+#pragma unroll
+            for (int i = 0; i < (int)(kAddT / 16) / kAddThreads; ++i) {
+                const uint32_t at = 16 * (tid + i * kAddThreads);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base_u + kAddS + at), "l"(S + at) : "memory");
+            }
+            if (tid < kHeadDim) s_unit[tid] = reinterpret_cast<const float*>(S + kAddT)[tid];
         }
-        const float* turned = w.plain + (size_t)a.n_tok * a.n_v * kHeadDim + ((size_t)first * a.n_v + h) * kHeadDim;
-        put_rows(std::integral_constant<int, 8>{}, turned, (size_t)a.n_v * kHeadDim, n, kAddT, kC * 128, warp, s_unit + kHeadDim);
+        // R_t q_t of eight tokens of a warp (every eighth), a lane's four elements of each: the largest, the unit, FP16; zeros
+        // from the sequence's end on
+        const float* turned = w.plain + (size_t)a.n_tok * apart + (size_t)first * apart + h * kHeadDim;
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = warp + 8 * i < n ? reinterpret_cast<const float4*>(turned + (warp + 8 * i) * apart)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = warp + 8 * i;
+            float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float unit = unit_of(m);
+            *reinterpret_cast<uint2*>(base + kAddT + (lane >> 4) * (kC * 128) + swz(r, (lane & 15) >> 1) + 8 * (lane & 1)) =
+                make_uint2(pack_f16x2(x[i].x * unit, x[i].y * unit), pack_f16x2(x[i].z * unit, x[i].w * unit));
+            if (lane == 0) s_unit[kHeadDim + r] = 1.f / unit;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         // the outputs so far, on their way meanwhile
         const float* from = w.plain + ((size_t)first * a.n_v + h) * kHeadDim;
         float2 so_far[2][8];
@@ -1304,7 +1336,7 @@ __global__ void __launch_bounds__(kAddThreads) delta_add_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int t = 16 * (warp & 3) + (lane >> 2) + 8 * e;
-                so_far[e][j] = t < n ? *reinterpret_cast<const float2*>(from + (size_t)t * a.n_v * kHeadDim + 64 * (warp >> 2) + 8 * j + 2 * (lane & 3))
+                so_far[e][j] = t < n ? *reinterpret_cast<const float2*>(from + t * apart + 64 * (warp >> 2) + 8 * j + 2 * (lane & 3))
                                      : make_float2(0.f, 0.f);
             }
         __syncthreads();
