@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kConvThreads, 3) short_conv_kernel(const __gri
     // the run's first inputs and the ones before it, whoever's they are
     constexpr int kAhead = 8;
     uint4 raw[kAhead], before[W - 1];
-    if (RUN > 1 && live && t1 == t0 + RUN) {
+    if (live && t1 == t0 + RUN) {
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) before[i] = input(max(t0 - (W - 1) + i, 0));
 #pragma unroll
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kConvThreads, 3) short_conv_kernel(const __gri
     };
     if (s >= 0) look();
     const int following = owned < a.n_seq ? a.cu_tokens[owned] : a.n_tok;
-    if (RUN > 1 && t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
+    if (t0 - begin >= W - 1 && end >= t1 && following >= t1 && t1 == t0 + RUN && !last) {
         if (skip) return;                            // the whole run inside one sequence
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) unpack_pairs(before[i], TYPE, win[i]);
@@ -292,10 +292,21 @@ cudaError_t launch_run(const ConvArgs& a, cudaStream_t stream) {
                              (unsigned)cols);
 }
 
+// Runs of 32 tokens where they are many; runs of 8 as long as there are no more than kShortRuns blocks of these to an SM: then
+// what counts is how soon a run is through, the more so the more sequences begin in it.  Of 8,192 channels, runs of 8 and of 32:
+// 64 sequences x 2 tokens 7.4 and 23.9 us, 512 x 4 36.6 and 43.2, 1 x 256 4.4 and 8.6, 1 x 2,048 13.8 and 15.4; 9 x 1-2,000
+// (8,600 tokens) 51.5 and 45.9.  Runs of 1 take 58.2 us instead of 26.6 for 512 x 2, and win nowhere by more than half a us.
+constexpr int kShortRuns = 32;
+
 template <int TYPE, int W>
 cudaError_t launch_width(const ConvArgs& a, cudaStream_t stream) {
     if (!a.cu_tokens) return launch_step<TYPE, W>(a, stream);
-    if (a.n_tok < 4LL * a.n_seq) return launch_run<TYPE, W, 1>(a, stream);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long cols = (a.n_ch / 8 + kConvThreads - 1) / kConvThreads;
+    if (a.n_tok / 8 * cols <= (long long)kShortRuns * sms) return launch_run<TYPE, W, 8>(a, stream);
     return launch_run<TYPE, W, 32>(a, stream);
 }
 

@@ -138,3 +138,15 @@ def test_refusals(qsa):
         with pytest.raises((TypeError, ValueError, RuntimeError)):
             call(**bad)
     call()
+
+
+@pytest.mark.parametrize("width,dtype", [(4, torch.bfloat16), (2, torch.float16)])
+def test_many_tokens(qsa, width, dtype):
+    """Steps of so many tokens and channels that runs of 32 tokens are taken: sequences of every length around them, and one alone."""
+    ragged = [n for lens in LENS for n in lens]
+    for lens in (ragged + [1900, 31, 32, 33, 0], [2600]):
+        x, w, bias, state, slots, old, cu = make(lens, 16392, width, dtype, seed=len(lens))
+        want, new_state, size = ref.short_conv(x, w, state, slots, old, cu, bias, True)
+        got = qsa.short_conv(x, w, state, slots, old, cu, bias=bias)
+        ref.check_conv(got, want, size, dtype, width, 16392)
+        assert torch.equal(state, new_state)
