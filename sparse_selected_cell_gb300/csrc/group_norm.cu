@@ -154,7 +154,7 @@ cudaError_t launch_items(const NormArgs& a, cudaStream_t stream) {
 // the shortest way through.
 template <int TYPE, int LANES, int PIECES>
 cudaError_t launch_lanes(const NormArgs& a, cudaStream_t stream) {
-    constexpr int kItems = PIECES >= 4 ? 1 : PIECES == 2 ? 2 : 4;
+    constexpr int kItems = PIECES == 1 ? 4 : 1;
     if (kItems > 1 && (long long)a.n_tok * a.n_groups * LANES >= 4LL * kNormThreads * kItems * 152)
         return launch_items<TYPE, LANES, PIECES, kItems>(a, stream);
     return launch_items<TYPE, LANES, PIECES, 1>(a, stream);
