@@ -56,7 +56,7 @@ struct DeltaArgs {
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
 // Of a step's sequences (cu_tokens) those of up to kDeltaShort tokens, token by token: a chunk's way costs an SM to itself
 // and as much as some twenty tokens.
-constexpr int kDeltaShort = 16;
+constexpr int kDeltaShort = 32;
 cudaError_t launch_delta_short(const DeltaArgs& a, cudaStream_t stream);
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v);
 cudaError_t launch_delta_prompt(const DeltaArgs& a, cudaStream_t stream);

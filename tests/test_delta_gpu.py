@@ -54,6 +54,11 @@ def test_prompt(qsa, lens, n_k, n_v, dtype):
     check_prompt(qsa, *batch(lens, n_k, n_v, dtype, seed=len(lens) + n_v, apart=(n_v % 2) * 8))
 
 
+@pytest.mark.parametrize("lens", [[31], [32], [33], [32, 0, 1, 33, 31, 7, 34], [8] * 9 + [200]], ids=lambda n: "-".join(map(str, n)))
+def test_where_chunks_begin(qsa, lens):
+    check_prompt(qsa, *batch(lens, 2, 6, torch.bfloat16, seed=len(lens)))
+
+
 def test_long_prompt(qsa):
     check_prompt(qsa, *batch([1500, 700], 1, 2, torch.bfloat16, seed=5))
 
