@@ -56,7 +56,7 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
 // segments' outputs, which are FP32 until then.
-constexpr int kSplitMost = 8, kSplitChunks = 8;      // segments of a sequence; chunks of a segment, at least
+constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
     const long long heads = (long long)n_seq * n_v;
