@@ -13,7 +13,9 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("lens,n_k,n_v,dtype", [([1024], 1, 1, torch.bfloat16), ([1031], 2, 6, torch.float16),
                                                 ([4200], 1, 2, torch.bfloat16), ([2049, 100, 0, 1500], 1, 1, torch.float16),
-                                                ([1100, 17], 4, 8, torch.bfloat16), ([3000], 8, 16, torch.bfloat16)])
+                                                ([1100, 17], 4, 8, torch.bfloat16), ([3000], 8, 16, torch.bfloat16),
+                                                ([2047], 1, 1, torch.float16), ([2048], 1, 1, torch.bfloat16), ([3100], 2, 6, torch.float16),
+                                                ([2200, 3400], 4, 8, torch.bfloat16), ([9000], 1, 2, torch.bfloat16)])
 def test_segments(qsa, lens, n_k, n_v, dtype):  # noqa: F811
     check_prompt(qsa, *batch(lens, n_k, n_v, dtype, seed=len(lens) + n_v))
 
@@ -21,13 +23,13 @@ def test_segments(qsa, lens, n_k, n_v, dtype):  # noqa: F811
 @pytest.mark.parametrize("name", ["no decay", "strong decay", "no write", "full write", "one key no decay", "opposite keys",
                                   "zero keys", "uneven values", "values that jump"])
 def test_values_in_segments(qsa, name):  # noqa: F811
-    inputs, state, slots, old, cu = batch([1090, 520], 1, 2, torch.bfloat16, seed=4)
+    inputs, state, slots, old, cu = batch([2180, 1040], 1, 2, torch.bfloat16, seed=4)
     check_prompt(qsa, gated(inputs, **CASES[name]), state, slots, None, cu, eps=1e-3 if name == "zero keys" else 1e-6)
 
 
 def test_segments_left_out_and_behind(qsa):  # noqa: F811
     """A long sequence without a slot, tokens behind the last sequence: rows and states stay as they are."""
-    lens = [1200, 1300, 600]
+    lens = [2200, 2300, 600]
     inputs, state, slots, old, cu = batch(lens, 1, 2, torch.bfloat16, seed=9)
     tail = [torch.cat((x, torch.full((90, *x.shape[1:]), float("nan"), dtype=x.dtype, device="cuda"))) for x in inputs[:5]]
     slots[1] = -1
@@ -36,7 +38,7 @@ def test_segments_left_out_and_behind(qsa):  # noqa: F811
     out, given = torch.full((n + 90, 2, 128), 9.0, dtype=torch.bfloat16, device="cuda"), state.clone()
     qsa.delta_prompt(*tail, *inputs[5:], state, slots, old, cu, out=out)
     ref.check_delta(out[:n], state, want, SCALE, torch.bfloat16, True, slots)
-    assert bool((out[1200:2500] == 9.0).all()) and bool((out[n:] == 9.0).all())
+    assert bool((out[2200:4500] == 9.0).all()) and bool((out[n:] == 9.0).all())
     rest = sorted(set(range(5)) - {int(slots[0]), int(slots[2])})
     assert torch.equal(state[rest], given[rest])
 
@@ -60,7 +62,7 @@ def test_short_sequences(qsa, lens):  # noqa: F811
     check_prompt(qsa, *batch(lens, 2, 4, torch.float16, seed=len(lens)))
 
 
-@pytest.mark.parametrize("lens", [[61], [1100], [90, 1200]])
+@pytest.mark.parametrize("lens", [[61], [1100], [2100], [90, 2200]])
 def test_repeated_captured_and_side_by_side(qsa, lens):  # noqa: F811
     """The same bits again; from a captured call; and from two calls at once, on two streams, with a workspace and states each."""
     inputs, state, slots, _, cu = batch(lens, 1, 2, torch.bfloat16, seed=11)
@@ -90,7 +92,7 @@ def test_repeated_captured_and_side_by_side(qsa, lens):  # noqa: F811
 
 def test_a_step_of_everything(qsa):  # noqa: F811
     """Long, ordinary, short and empty sequences, fresh ones and ones that go on, over three steps."""
-    lens = [1500, 1, 0, 300, 16, 64, 17, 2]
+    lens = [2500, 1, 0, 300, 16, 64, 17, 2]
     inputs, state, slots, old, _ = batch(lens, 1, 2, torch.bfloat16, seed=21)
     for turn in range(3):
         order = lens[turn:] + lens[:turn]
@@ -99,11 +101,12 @@ def test_a_step_of_everything(qsa):  # noqa: F811
     assert cu_of(lens).shape == cu.shape
 
 
+@pytest.mark.parametrize("chunks", [9, 33])
 @pytest.mark.parametrize("size", [2.0 ** 50, 2.0 ** -50])
-def test_nothing_left_after_large_values(qsa, size):  # noqa: F811
+def test_nothing_left_after_large_values(qsa, size, chunks):  # noqa: F811
     """Chunks of values far out, then decays that leave nothing of them and values of zero or of ordinary size: what was large
     neither lingers in the units nor turns zeros into something else."""
-    inputs, state, slots, old, cu = batch([64 * 9], 1, 2, torch.bfloat16, seed=3)
+    inputs, state, slots, old, cu = batch([64 * chunks], 1, 2, torch.bfloat16, seed=3)
     q, k, v, a, b, a_log, dt = (x.clone() for x in inputs)
     v[:128] *= size
     v[128:320] = 0

@@ -121,7 +121,7 @@ def test_a_step_on_another_stream(qsa):  # noqa: F811
 
 # ---------------------------------------------------------------- inputs written late
 
-@pytest.mark.parametrize("lens", [[61], [1, 1, 1], [9, 3], [400, 70, 1], [1100]])
+@pytest.mark.parametrize("lens", [[61], [1, 1, 1], [9, 3], [400, 70, 1], [1100], [2300]])
 def test_late_prompts(qsa, late, lens):  # noqa: F811
     def step(seed):
         inputs, state, slots, old, cu = batch(lens, 1, 2, torch.bfloat16, seed=seed)
