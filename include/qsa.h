@@ -406,7 +406,7 @@ enum { QSA_ACT_NONE = 0, QSA_ACT_SILU = 1 };
  *   - weight [n_ch][width], bias [n_ch] or NULL, of w_type: `type` or QSA_F32,
  *     16-byte aligned.
  *   - state: [n_slots][width - 1][n_ch] of `type`, the last inputs, oldest first;
- *     16-byte aligned.
+ *     16-byte aligned; must not overlap any other argument.
  *   - cu_tokens NULL: one token to every sequence (n_seq == n_tok). */
 int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* weight, const void* bias,
                    int32_t w_type, int32_t width, int32_t activation, void* state, const int32_t* state_slots,
@@ -427,14 +427,29 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
  *     a_log, dt_bias: FP32 [n_v].  a_log = -infinity: no decay; b = infinity: beta = 1.
  *   - eps >= 0; scale is finite.
  *   - state: FP32 [n_slots][n_v][128][128], the key dim innermost, 16-byte aligned.
- *   - Chunks of 64 tokens on the tensor cores; the state and all sums in FP32, the
- *     state's and the new values' operands as pairs of FP16 (22 bits, with a power
- *     of two per value dim).  The products that end in `out` alone are of FP16 factors
- *     (relative 2^-11 each).  The same call gives the same bits; how a sequence is
- *     split into steps changes its last bits.
+ *   - Sequences of more than 32 tokens go by chunks of 64 on the tensor cores; the
+ *     state and all sums in FP32, the state's and the new values' operands as pairs of
+ *     FP16 (22 bits, with a power of two per value dim).  The products that end in
+ *     `out` alone are of FP16 factors (2^-12 each, relative); for FP16 outputs the
+ *     state and the new values are pairs there, too.  Shorter ones go token by token,
+ *     in FP32 throughout (in a step of one sequence, if n_tok <= 32).  Where the step
+ *     has few heads (n_seq n_v below half the SMs) and many tokens, long sequences are
+ *     cut into segments that run at once and are put together afterwards.
+ *   - The same call gives the same bits, and no sequence's results depend on the
+ *     contents of others; how a sequence is split into steps, and the step's n_seq,
+ *     n_tok and n_v where they decide on segments, change the last bits.
+ *   - Range: any finite values and states of magnitudes from 2^-90 to 2^120 or zero.
+ *     By chunks, keys and queries likewise (their rows are scaled by powers of two;
+ *     elements below 2^-24 of their row's largest lose bits; rows 2^54 and more below
+ *     sqrt(eps) count as zeros, and what short ones add to the state is lost below
+ *     2^-28 of their chunk's values).  Token by token their squares are summed in FP32 as
+ *     they are (lengths from 2^-60 to 2^60).  A row of zeros needs eps > 0.  NaN and
+ *     infinities stay in their sequence.
+ *   - state and workspace must not overlap any other argument.
  *   - workspace: device memory of at least qsa_delta_prompt_workspace_bytes(n_tok,
- *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept.  Two
- *     calls that can overlap on the device need one each.
+ *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept: about
+ *     512 n_k + 400 n_v bytes a token, and 1024 n_v more where segments may be cut.
+ *     Two calls that can overlap on the device need one each, captured ones too.
  *   - n_seq == 0 returns QSA_OK with no launch. */
 int qsa_delta_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, int32_t type, const void* a, int64_t a_stride, const void* b,
@@ -448,7 +463,8 @@ int qsa_delta_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_s
 size_t qsa_delta_prompt_workspace_bytes(int32_t n_tok, int32_t n_seq, int32_t n_k, int32_t n_v);
 
 /* The same for one token of every sequence (token s is sequence s's), FP32
- * throughout: the decode step, one launch, no workspace. */
+ * throughout: the decode step, one launch, no workspace.  Keys and queries as token by
+ * token above. */
 int qsa_delta_step(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                    int64_t v_stride, int32_t type, const void* a, int64_t a_stride, const void* b,
                    int64_t b_stride, const float* a_log, const float* dt_bias, float* state,

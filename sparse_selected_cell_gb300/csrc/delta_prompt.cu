@@ -18,7 +18,15 @@
 // are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
 // the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
 // passes FP16's range and what counts stays in its upper bits.  In P V' P is single
-// FP16, and so is V' for BF16 outputs, which would not show more.
+// FP16, and so is V' for BF16 outputs, which would not show more; S Q^T takes the state's lo for
+// FP16 outputs only.
+//
+// Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
+// 4,096 tokens 351 + 579 us, 1 x 61 14 + 15 (the second begins beside the first: 20 in all);
+// 1 x 8,192, cut into segments, 67 + 217, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
+// 24 x 1-2,000: 104 + 183.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
+// the first is bound by shared memory (59 % of its cycles) and by waiting on it, the second by a
+// chain of dependent steps, see there.
 #include <type_traits>
 
 #include "linear.cuh"
@@ -37,7 +45,8 @@ constexpr uint32_t kTriBytes = kC * kC * 2;          // a 64 x 64 FP16 matrix, 1
 constexpr uint32_t kOffTlo = kTriBytes, kOffP = 2 * kTriBytes, kOffScal = 3 * kTriBytes;
 constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T hi, T lo, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
-constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1;   // -exp(G) / |k|, exp(G_C - G) / |k|, exp(G) / |q|, exp(G_C)
+// -exp(G) / |k|, exp(G_C - G) / |k| times the chunk's key unit, exp(G) / |q|, of 64 tokens each; then exp(G_C) and the key unit
+constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1;
 
 __device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
 
@@ -55,7 +64,8 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 4,096 tokens 196 and 231 us with 32 value heads, 118
+// and 122 for 1 x 2,048; 1 x 8,192 193 and 397 with 8.  Segments of 8 chunks lose: 1 x 1,024 80 and 69 us.
 constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
@@ -140,7 +150,8 @@ __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 12
 // A block has a chunk of a key head and all its value heads, two at a time.  K K^T and Q K^T come from mma.sync over the FP16
 // rows (their diagonals give the lengths); (I + A)^-1 by halves of halves: the four 16 x 16 blocks on the diagonal by
 // substitution, a column to a thread, then [T11, 0; -T22 A21 T11, T22] for pairs of 16 and of 32, as products of FP16 pairs
-// (a column to a thread over all 64 rows took five times as long).
+// (a column to a thread over all 64 rows took five times as long).  Four blocks to an SM hide one another's waits; 256 threads
+// to a block, with the products and rows halved, had a single chunk through 7 % sooner and took 45 % longer for many.
 constexpr int kPrepThreads = 128;
 constexpr int kAStride = 68;                         // floats to a row of A
 // Shared memory: keys and queries, then two heads' A, then their T in A's place; P; the tokens' factors.
@@ -534,7 +545,11 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 //                         D = V'^T K (hi, lo), V'^T P^T
 //   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
-// the first quarter of its operand is there, and S Q^T is issued in the pauses.
+// the first quarter of its operand is there, and S Q^T is issued behind V', while its pairs are
+// formed.  A chunk takes some 4,900 cycles with few blocks, 5,400 with all SMs at work (they
+// fetch instructions through caches that neighbours share); the products are 1,850 of them (the
+// tensor pipe is 24 % active), the pairs' conversions as much again, the rest are the waits from
+// one to the other.
 constexpr int kChunkThreads = 512;
 constexpr int kStages = 3, kVStages = 2;
 constexpr uint32_t kStageBytes = kKqBytes + kHeadBytes, kVBytes = kC * kHeadDim * 2;
@@ -549,7 +564,7 @@ enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kSt
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
-constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length
+constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 283 us instead of 318)
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T
@@ -746,7 +761,6 @@ __device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_ex
 
 template <int TYPE, bool SPLIT>
 __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
-    const DeltaArgs& a = *c.a;
     const float4* row = reinterpret_cast<const float4*>(c.state_in + (size_t)r * kHeadDim + half * (kHeadDim / 2));
     float2* pows = reinterpret_cast<float2*>(c.base + kOffPow) + r;
     float* top_v = reinterpret_cast<float*>(c.base + kOffTop) + r;           // + 256 (chunk & 1) + 128 half
@@ -807,8 +821,9 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         vm = fmaxf(vm, top_v[par * 256 + (half ^ 1) * 128]);
         sm = fmaxf(sm, top_s[(par ^ 1) * 256 + (half ^ 1) * 128]);
         const float len = fmaf(12.f, sm, 66.f * vm_before);
-        // (no more than 2^60 finer than the chunk before's: its results are brought to them by a factor that stays finite)
-        const float finest = 0x1p60f / d_up;
+        // (no more than 2^100 finer than the chunk before's: its results are brought to them by a factor that stays finite, 2^116 at
+        // most with the key unit; from 1, where the first chunk's state is, nothing is cut)
+        const float finest = 0x1p100f / d_up;
         unit = fminf(unit_of(len + vm), finest), v_unit = fminf(unit_of(fmaf(66.f, vm, len)), finest);
         vm_before = vm;
         const f2 unit2 = pair(unit, unit);

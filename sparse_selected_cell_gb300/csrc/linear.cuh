@@ -42,7 +42,7 @@ struct DeltaArgs {
     const int32_t* state_slots;
     int n_slots;
     const int32_t* old_lens;      // or null
-    const int32_t* cu_tokens;     // or null: one token to every sequence
+    const int32_t* cu_tokens;     // null for launch_delta_step: one token to every sequence
     int n_seq, n_tok, n_k, n_v;
     float eps, scale;
     uint16_t* out;
@@ -54,8 +54,9 @@ struct DeltaArgs {
 };
 
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
-// Of a step's sequences (cu_tokens) those of up to kDeltaShort tokens, token by token: a chunk's way costs an SM to itself
-// and as much as some twenty tokens.
+// Of a step's sequences (cu_tokens) those of up to kDeltaShort tokens, token by token: a chunk of any length takes its SM for as
+// long as a full one.  With 32 value heads, in a graph, token by token and by chunks: 1 sequence x 16 tokens 6.9 and 19.5 us,
+// 1 x 32 11.6 and 19.5, 8 x 32 37.3 and 38.6, 64 x 32 229.6 and 230.1; 8 x 40 45.3 and 38.9.
 constexpr int kDeltaShort = 32;
 cudaError_t launch_delta_short(const DeltaArgs& a, cudaStream_t stream);
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v);

