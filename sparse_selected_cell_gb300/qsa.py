@@ -306,7 +306,7 @@ def decode_attn(q, k_pool, v_pool, k_scale, v_scale, page_tables, sel, sel_count
 # fails are they gone through one by one, for the message.
 
 _TYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
-_I8, _I32, _F64, _BF = torch.int8, torch.int32, torch.float64, torch.bfloat16
+_I8, _I32, _F32, _F64, _BF = torch.int8, torch.int32, torch.float32, torch.float64, torch.bfloat16
 _T16 = (torch.bfloat16, torch.float16)
 _OUT = (torch.bfloat16, torch.float16, torch.float32)
 _SCALE = (torch.float16, torch.int16, torch.uint16)
@@ -841,14 +841,21 @@ def delta_prompt_workspace_bytes(n_tok: int, n_seq: int, n_k: int, n_v: int) -> 
     return int(lib().qsa_delta_prompt_workspace_bytes(int(n_tok), int(n_seq), int(n_k), int(n_v)))
 
 
-def _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, n_tok, n_k, n_v):
-    return (dev >= 0 and dev == _current() and dtype in _T16 and _rows_ok(q, dtype, dev, n_tok, n_k, q.stride())
-            and _rows_ok(k, dtype, dev, n_tok, n_k, k.stride()) and _rows_ok(v, dtype, dev, n_tok, n_v, v.stride())
-            and n_k > 0 and n_v > 0 and n_v % n_k == 0 and _flat_ok(a, dtype, dev, n_tok, n_v, a.stride())
-            and _flat_ok(b, dtype, dev, n_tok, n_v, b.stride()) and _ok(a_log, torch.float32, dev, (n_v,))
-            and _ok(dt_bias, torch.float32, dev, (n_v,)) and _ok(state, torch.float32, dev, (state.shape[0], n_v, 128, 128))
-            and _seqs_ok(state_slots, old_lens, cu_tokens, dev)
-            and (out is None or _rows_ok(out, dtype, dev, n_tok, n_v, out.stride())))
+def _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, strides) -> bool:
+    """Whether the arguments fit together (written out, since a decode step's call is as long as its checks)."""
+    qs, ks, vs, as_, bs, os_ = strides
+    keys, values, gates, per = q.shape, v.shape, a.shape, a_log.shape
+    n_tok, n_k, d = keys
+    n_v = values[1]
+    return (dev >= 0 and dev == _current() and dtype in _T16 and d == 128 and n_k > 0 and n_v > 0 and n_v % n_k == 0
+            and k.dtype is dtype and v.dtype is dtype and a.dtype is dtype and b.dtype is dtype
+            and k.shape == keys and values == (n_tok, n_v, 128) and gates == (n_tok, n_v) and b.shape == gates
+            and k.get_device() == dev and v.get_device() == dev and a.get_device() == dev and b.get_device() == dev
+            and qs[2] == 1 and ks[2] == 1 and vs[2] == 1 and (n_k == 1 or (qs[1] == 128 and ks[1] == 128))
+            and (n_v == 1 or (vs[1] == 128 and as_[1] == 1 and bs[1] == 1))
+            and per == (n_v,) and _ok(a_log, _F32, dev, per) and _ok(dt_bias, _F32, dev, per)
+            and _ok(state, _F32, dev, (state.shape[0], n_v, 128, 128)) and _seqs_ok(state_slots, old_lens, cu_tokens, dev)
+            and (out is None or _rows_ok(out, dtype, dev, n_tok, n_v, os_)))
 
 
 def _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out):
@@ -882,12 +889,13 @@ def delta_prompt(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu
     (None: all go on), cu_tokens as in short_conv -> out [n_tok, n_v, 128].  A workspace that is not given is allocated."""
     try:
         dev, dtype = q.get_device(), q.dtype
+        strides = qs, ks, vs, as_, bs, os_ = (q.stride(), k.stride(), v.stride(), a.stride(), b.stride(),
+                                              None if out is None else out.stride())
         n_tok, n_k, n_v, n_seq = q.shape[0], q.shape[1], v.shape[1], state_slots.shape[0]
         good = (cu_tokens is not None
-                and _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, n_tok,
-                              n_k, n_v)
+                and _delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out, dev, dtype, strides)
                 and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
-    except (AttributeError, IndexError):
+    except (AttributeError, IndexError, ValueError):
         good = False
     if not good:
         _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu_tokens, out)
@@ -895,15 +903,14 @@ def delta_prompt(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, cu
             _want(workspace, "workspace", (getattr(workspace, "dtype", None),), q.get_device())
         raise ValueError("delta_prompt: arguments do not fit together")
     if out is None:
-        out = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream)
+        out, os_ = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream), (n_v * gen.HEAD_DIM,)
     if workspace is None:
         workspace = _empty(delta_prompt_workspace_bytes(n_tok, n_seq, n_k, n_v), torch.uint8, q.device, stream)
     rc = (_lib or lib()).qsa_delta_prompt_packed(_PROMPT_ARGS(
-        q.data_ptr(), _apart(q.stride(), n_tok, n_k), k.data_ptr(), _apart(k.stride(), n_tok, n_k), v.data_ptr(),
-        _apart(v.stride(), n_tok, n_v), _TYPE[dtype], a.data_ptr(), a.stride(0) if n_tok > 1 else n_v, b.data_ptr(),
-        b.stride(0) if n_tok > 1 else n_v, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(),
-        state.shape[0], _at(old_lens), cu_tokens.data_ptr(), n_seq, n_tok, n_k, n_v, eps,
-        gen.HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), _apart(out.stride(), n_tok, n_v),
+        q.data_ptr(), _apart(qs, n_tok, n_k), k.data_ptr(), _apart(ks, n_tok, n_k), v.data_ptr(), _apart(vs, n_tok, n_v),
+        _TYPE[dtype], a.data_ptr(), as_[0] if n_tok > 1 else n_v, b.data_ptr(), bs[0] if n_tok > 1 else n_v, a_log.data_ptr(),
+        dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(), state.shape[0], _at(old_lens), cu_tokens.data_ptr(), n_seq,
+        n_tok, n_k, n_v, eps, gen.HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), _apart(os_, n_tok, n_v),
         workspace.data_ptr(), workspace.nbytes, _status_of(dev_status, dev), _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_delta_prompt", rc)
@@ -917,22 +924,23 @@ def delta_step(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens: Opti
     -> out [n_seq, n_v, 128]."""
     try:
         dev, dtype = q.get_device(), q.dtype
+        strides = qs, ks, vs, as_, bs, os_ = (q.stride(), k.stride(), v.stride(), a.stride(), b.stride(),
+                                              None if out is None else out.stride())
         n_tok, n_k, n_v = q.shape[0], q.shape[1], v.shape[1]
-        good = (_delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, None, out, dev, dtype, n_tok, n_k, n_v)
+        good = (_delta_ok(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, None, out, dev, dtype, strides)
                 and state_slots.shape[0] == n_tok)
-    except (AttributeError, IndexError):
+    except (AttributeError, IndexError, ValueError):
         good = False
     if not good:
         _refuse_delta(q, k, v, a, b, a_log, dt_bias, state, state_slots, old_lens, None, out)
         raise ValueError("delta_step: arguments do not fit together (one token to a sequence)")
     if out is None:
-        out = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream)
+        out, os_ = _empty((n_tok, n_v, gen.HEAD_DIM), dtype, q.device, stream), (n_v * gen.HEAD_DIM,)
     rc = (_lib or lib()).qsa_delta_step_packed(_STEP_ARGS(
-        q.data_ptr(), _apart(q.stride(), n_tok, n_k), k.data_ptr(), _apart(k.stride(), n_tok, n_k), v.data_ptr(),
-        _apart(v.stride(), n_tok, n_v), _TYPE[dtype], a.data_ptr(), a.stride(0) if n_tok > 1 else n_v, b.data_ptr(),
-        b.stride(0) if n_tok > 1 else n_v, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(),
-        state.shape[0], _at(old_lens), n_tok, n_k, n_v, eps, gen.HEAD_DIM ** -0.5 if scale is None else scale,
-        out.data_ptr(), _apart(out.stride(), n_tok, n_v), _status_of(dev_status, dev), _stream_of(stream, dev)))
+        q.data_ptr(), _apart(qs, n_tok, n_k), k.data_ptr(), _apart(ks, n_tok, n_k), v.data_ptr(), _apart(vs, n_tok, n_v),
+        _TYPE[dtype], a.data_ptr(), as_[0] if n_tok > 1 else n_v, b.data_ptr(), bs[0] if n_tok > 1 else n_v, a_log.data_ptr(),
+        dt_bias.data_ptr(), state.data_ptr(), state_slots.data_ptr(), state.shape[0], _at(old_lens), n_tok, n_k, n_v, eps,
+        gen.HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), _apart(os_, n_tok, n_v), _status_of(dev_status, dev), _stream_of(stream, dev)))
     if rc != QSA_OK:
         raise QsaError("qsa_delta_step", rc)
     return out
