@@ -677,7 +677,7 @@ __device__ void product_role(const Block& c) {
         const int st = i % kStages, par = i & 1;
         const uint64_t stage = (uint64_t)(st * kStageBytes) >> 4, tri = stage + (kKqBytes >> 4);
         if (!(ok = wait(c, BAR_FULL + st, (i / kStages) & 1))) break;
-#pragma unroll 1
+#pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int q = quarter(n);
             if (!(ok = wait(c, BAR_S + q, par))) break;
@@ -693,7 +693,7 @@ __device__ void product_role(const Block& c) {
         tc::commit_elect(bar(c, BAR_KS));
         if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
         tc::fence_after_sync();
-#pragma unroll 1
+#pragma unroll
         for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
             const int b = quarter(n);
             if (!(ok = wait(c, BAR_X + b, par))) break;
@@ -709,7 +709,7 @@ __device__ void product_role(const Block& c) {
         tc::commit_elect(bar(c, BAR_V));
         with_queries(stage, 0);
         if (TYPE == QSA_F16) with_queries(stage, 8);  // (BF16 outputs would not show it)
-#pragma unroll 1
+#pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int b = quarter(n);
             if (!(ok = wait(c, BAR_D + b, par))) break;
@@ -722,7 +722,7 @@ __device__ void product_role(const Block& c) {
         tc::commit_elect(bar(c, BAR_U));
         if (!(ok = wait(c, BAR_H, par))) break;
         tc::fence_after_sync();
-#pragma unroll 1
+#pragma unroll
         for (int b = 0; b < 4; ++b) {
             const uint32_t to = c.tmem + kTmPv + 16 * b, at = c.tmem + kTmH + 8 * b, id = id64 - (uint32_t)b * (2u << 17);
             const uint64_t d = dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4);
@@ -969,6 +969,12 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
     }
 }
 
+// Registers that a load from Tensor Memory has filled: nothing that uses them moves before this.
+__device__ __forceinline__ void arrived(uint32_t (&x)[16], uint32_t (&y)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(x[j]), "+r"(y[j]));
+}
+
 template <int TYPE, bool SPLIT>
 __device__ void output_role(const Block& c, int q, int lane) {
     const DeltaArgs& a = *c.a;
@@ -986,13 +992,13 @@ __device__ void output_role(const Block& c, int q, int lane) {
         const int n = min(kC, c.n_tok - i * kC);
         const bool plain = SPLIT && c.plain;
         float* whole = reinterpret_cast<float*>(mine);               // FP32 outputs pass the same place, 32 tokens at a time
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            uint32_t qs[16], pv[16];
-            tc::tmem_ld16(tm + kTmQs + 16 * b, qs);
-            tc::tmem_ld16(tm + kTmPv + 16 * b, pv);
-            tc::tmem_wait_ld();
-            if (b == 3) tell(c, BAR_OFREE);
+        // a quarter's accumulators are on their way while the one before is written
+        uint32_t qs[2][16], pv[2][16];
+        auto ask = [&](int b, int to) {
+            tc::tmem_ld16(tm + kTmQs + 16 * b, qs[to]);
+            tc::tmem_ld16(tm + kTmPv + 16 * b, pv[to]);
+        };
+        auto put = [&](int b, const uint32_t (&qs)[16], const uint32_t (&pv)[16]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const f2 o = *reinterpret_cast<const f2*>(scal + 16 * b + 2 * j);
@@ -1018,6 +1024,19 @@ __device__ void output_role(const Block& c, int q, int lane) {
                 }
                 __syncwarp();
             }
+        };
+        ask(0, 0);
+#pragma unroll 1
+        for (int b = 0; b < 4; b += 2) {
+            tc::tmem_wait_ld();
+            arrived(qs[0], pv[0]);
+            ask(b + 1, 1);
+            put(b, qs[0], pv[0]);
+            tc::tmem_wait_ld();
+            arrived(qs[1], pv[1]);
+            if (b == 0) ask(2, 0);
+            else tell(c, BAR_OFREE);
+            put(b + 1, qs[1], pv[1]);
         }
         if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
         if (plain) continue;
