@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = qq[i & 1][j] = 0.f;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t tile = base_u + (uint32_t)(k >> 2) * (kKqBytes / 2);
         const int brow = (lane & 7) + ((lane >> 4) << 3), bword = 2 * (k & 3) + ((lane >> 3) & 1);
@@ -545,11 +545,14 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 //                         D = V'^T K (hi, lo), V'^T P^T
 //   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
-// the first quarter of its operand is there, and S Q^T is issued behind V', while its pairs are
-// formed.  A chunk takes some 4,900 cycles with few blocks, 5,400 with all SMs at work (they
-// fetch instructions through caches that neighbours share); the products are 1,850 of them (the
-// tensor pipe is 24 % active), the pairs' conversions as much again, the rest are the waits from
-// one to the other.
+// the first half of its operand is there, and S Q^T is issued behind V', while its pairs are
+// formed.  A chunk takes some 4,300 cycles with few blocks, 4,700 with all SMs at work (they
+// fetch instructions through caches that neighbours share): 1,000 until the last warp has S as
+// pairs, 500 until K S^T is there, 950 for X, 400 for V', 950 for its pairs, then 700 for D, beside
+// which the next values are brought to their units.  The tensor pipe is busy for 1,850 of them,
+// and a warp's issue slots for a third; conversions to pairs and the outputs' share them.
+// (The next values read while K S^T is formed, and brought to their units before V': 5 % slower,
+// the outputs of the chunk before are written then.)
 constexpr int kChunkThreads = 512;
 constexpr int kStages = 3, kVStages = 2;
 constexpr uint32_t kStageBytes = kKqBytes + kHeadBytes, kVBytes = kC * kHeadDim * 2;
@@ -559,7 +562,7 @@ constexpr uint32_t kOffPow = kOffOut + 4 * kC * 64;                  // [chunk &
 constexpr uint32_t kOffTop = kOffPow + 2 * kHeadDim * 8;             // [chunk & 1][half][value dim]: largest value; then largest of S
 constexpr uint32_t kOffBar = kOffTop + 2 * 2 * 2 * kHeadDim * 4;
 enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kStages, BAR_VEMPTY = BAR_VFULL + kVStages,
-       BAR_S = BAR_VEMPTY + kVStages, BAR_X = BAR_S + 4, BAR_D = BAR_X + 4, BAR_TOP = BAR_D + 4, BAR_KS = BAR_TOP + 4,
+       BAR_S = BAR_VEMPTY + kVStages, BAR_X = BAR_S + 2, BAR_D = BAR_X + 2, BAR_TOP = BAR_D + 2, BAR_KS = BAR_TOP + 4,
        BAR_V, BAR_U, BAR_H, BAR_O, BAR_OFREE, BAR_DRAIN, NUM_BARS };
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
@@ -570,7 +573,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T
 // where V' was.
 constexpr uint32_t kTmS = 0, kTmKs = 128, kTmH = 128, kTmQs = 192, kTmX = 256, kTmV = 320, kTmPv = 320, kTmD = 384;
-// The quarters of an operand in the order in which they are there: each half's first, each half's second.
+// The quarters of an operand in the order in which they are there: each half's first, each half's second.  Two of them have a
+// barrier (one each took 1 to 3 % longer: what counts is the issuing warp's time).
 __device__ __forceinline__ constexpr int quarter(int i) { return ((i & 1) << 1) | (i >> 1); }
 
 struct Block {
@@ -680,8 +684,10 @@ __device__ void product_role(const Block& c) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int q = quarter(n);
-            if (!(ok = wait(c, BAR_S + q, par))) break;
-            tc::fence_after_sync();
+            if (!(n & 1)) {
+                if (!(ok = wait(c, BAR_S + n / 2, par))) break;
+                tc::fence_after_sync();
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint64_t d = dkq0 + stage + (((q >> 1) * (kKqBytes / 2) + (q & 1) * 64 + k * 32) >> 4);
@@ -696,8 +702,10 @@ __device__ void product_role(const Block& c) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
             const int b = quarter(n);
-            if (!(ok = wait(c, BAR_X + b, par))) break;
-            tc::fence_after_sync();
+            if (!(n & 1)) {
+                if (!(ok = wait(c, BAR_X + n / 2, par))) break;
+                tc::fence_after_sync();
+            }
             const uint32_t id = id64 - (uint32_t)b * (2u << 17);     // 64 - 16 b columns
             const uint64_t d = dkq0 + tri + ((b * 2048 + b * 32) >> 4);
             const uint32_t at = c.tmem + kTmX + 8 * b, to = c.tmem + kTmV + 16 * b;
@@ -712,8 +720,10 @@ __device__ void product_role(const Block& c) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int b = quarter(n);
-            if (!(ok = wait(c, BAR_D + b, par))) break;
-            tc::fence_after_sync();
+            if (!(n & 1)) {
+                if (!(ok = wait(c, BAR_D + n / 2, par))) break;
+                tc::fence_after_sync();
+            }
             const uint64_t d = dkt0 + stage + ((b * 2048) >> 4);
             product(c.tmem + kTmD, c.tmem + kTmX + 8 * b, d, idD, 1, leader);
             product(c.tmem + kTmD, c.tmem + kTmX + 32 + 8 * b, d, idD, 1, leader);
@@ -856,7 +866,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 tc::tmem_st16(tmS + 32 * b + 16 * e, w);
             }
             tc::tmem_wait_st();
-            tell(c, BAR_S + 2 * half + b);
+            tell(c, BAR_S + b);
         }
         if (half == 0) pows[par * kHeadDim] = make_float2(1.f / unit, 1.f / (v_unit * kTriUnit));
         // ---- X = V - f (S K^T)
@@ -879,7 +889,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
                 tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
                 tc::tmem_wait_st();
-                tell(c, BAR_X + 2 * half + b);
+                tell(c, BAR_X + b);
             }
         }
         // ---- while V' is formed: the decayed state for D, and its largest element
@@ -935,7 +945,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
                 tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
                 tc::tmem_wait_st();
-                tell(c, BAR_D + 2 * half + b);
+                tell(c, BAR_D + b);
             }
             tc::tmem_st16(tm + kTmH + 16 * half, one);
             if (TYPE == QSA_F16) tc::tmem_st16(tm + kTmH + 32 + 16 * half, rest);
@@ -1140,9 +1150,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
             tc::mbar_init(bar(c, BAR_VEMPTY + st), 8);
         }
         for (int b = 0; b < 4; ++b) {
-            tc::mbar_init(bar(c, BAR_S + b), 4);
-            tc::mbar_init(bar(c, BAR_X + b), 4);
-            tc::mbar_init(bar(c, BAR_D + b), 4);
+            if (b < 2) {
+                tc::mbar_init(bar(c, BAR_S + b), 8);
+                tc::mbar_init(bar(c, BAR_X + b), 8);
+                tc::mbar_init(bar(c, BAR_D + b), 8);
+            }
             tc::mbar_init(bar(c, BAR_TOP + b), 2);
         }
         tc::mbar_init(bar(c, BAR_KS), 1);
