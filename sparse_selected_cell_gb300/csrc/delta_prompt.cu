@@ -984,77 +984,108 @@ __device__ __forceinline__ void arrived(uint32_t (&x)[16], uint32_t (&y)[16]) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(x[j]), "+r"(y[j]));
 }
+// 16 lanes x 32 columns as m16n8 accumulators lie: r[4 k + 2 e + u] is lane lane / 4 + 8 e, column 8 k + 2 (lane % 4) + u.
+__device__ __forceinline__ void tmem_ld_tiles(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr) : "memory");
+}
+// Four 8 x 8 tiles of pairs along a column, transposed into rows of 16 bytes, whose addresses the lanes give, eight to a tile.
+__device__ __forceinline__ void stmatrix4t(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 
-template <int TYPE, bool SPLIT>
+// Value dims by tokens become tokens by value dims: accumulators as matrix tiles, so that a transposing store takes 16 tokens x
+// 16 dims at once (a token's 16 bits at a time, a lane to a dim, it is twice the instructions, which the state warps pay for).
+// PLAIN: segments' FP32 outputs.
+template <int TYPE, bool PLAIN>
 __device__ void output_role(const Block& c, int q, int lane) {
     const DeltaArgs& a = *c.a;
-    uint16_t* mine = reinterpret_cast<uint16_t*>(c.base + kOffOut) + q * kC * 32;
-    const float2* pows = reinterpret_cast<const float2*>(c.base + kOffPow) + 32 * q + lane;
+    const uint32_t mine_u = c.base_u + kOffOut + q * kC * 64;        // a token's 32 dims: four 16-byte words, word w at w ^ (token / 2) % 4
+    uint8_t* mine = c.base + kOffOut + q * kC * 64;
+    float* whole = reinterpret_cast<float*>(mine);                   // FP32 outputs, 32 tokens at a time: dim d at d ^ 8 ((token / 2) % 4)
+    const float2* pows = reinterpret_cast<const float2*>(c.base + kOffPow) + 32 * q + (lane >> 2);
     const uint32_t tm = c.tmem + ((uint32_t)q << 21);
+    const int col = 2 * (lane & 3);
+    // where this lane's row of the tiles goes: token (lane % 8) + 8 (lane / 16) of 16, word (lane / 8) % 2 of two
+    const int row = (lane & 7) + 8 * (lane >> 4), word = (lane >> 3) & 1;
     for (int i = 0; i < c.n_chunks; ++i) {
         const int st = i % kStages, par = i & 1;
         const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + kScalO;
         if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_H, par) || !wait(c, BAR_O, par)) return;
         tc::fence_after_sync();
-        const float2 unit = pows[(i & 1) * kHeadDim];
-        const float scale = SPLIT && c.kind == 2 ? 1.f : a.scale;
-        const f2 us2 = pair(unit.x * scale, unit.x * scale), uv2 = pair(unit.y * scale, unit.y * scale);
+        const float scale = PLAIN && c.kind == 2 ? 1.f : a.scale;
         const int n = min(kC, c.n_tok - i * kC);
-        const bool plain = SPLIT && c.plain;
-        float* whole = reinterpret_cast<float*>(mine);               // FP32 outputs pass the same place, 32 tokens at a time
-        // a quarter's accumulators are on their way while the one before is written
+        // the next 16 dims' or 32 tokens' accumulators are on their way while the ones before are written
         uint32_t qs[2][16], pv[2][16];
-        auto ask = [&](int b, int to) {
-            tc::tmem_ld16(tm + kTmQs + 16 * b, qs[to]);
-            tc::tmem_ld16(tm + kTmPv + 16 * b, pv[to]);
+        auto ask = [&](int half, int h) {            // 32 tokens of 16 dims
+            tmem_ld_tiles(tm + ((uint32_t)h << 20) + kTmQs + 32 * half, qs[h]);
+            tmem_ld_tiles(tm + ((uint32_t)h << 20) + kTmPv + 32 * half, pv[h]);
         };
-        auto put = [&](int b, const uint32_t (&qs)[16], const uint32_t (&pv)[16]) {
+        auto put = [&](int half, int h) {
+            uint32_t w[4];
+            f2 us[2], uv[2];                         // of dims 16 h + 8 e + lane / 4
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const f2 o = *reinterpret_cast<const f2*>(scal + 16 * b + 2 * j);
-                float x, y;
-                unpair(fma2(mul2(o, us2), pair_of(qs[2 * j], qs[2 * j + 1]), mul2(uv2, pair_of(pv[2 * j], pv[2 * j + 1]))), x, y);
-                if (plain) {
-                    whole[(16 * (b & 1) + 2 * j) * 32 + lane] = x;
-                    whole[(16 * (b & 1) + 2 * j + 1) * 32 + lane] = y;
-                } else {
-                    const uint32_t two = pack2(x, y, TYPE);
-                    mine[(16 * b + 2 * j) * 32 + lane] = (uint16_t)(two & 0xFFFFu);
-                    mine[(16 * b + 2 * j + 1) * 32 + lane] = (uint16_t)(two >> 16);
-                }
+            for (int e = 0; e < 2; ++e) {
+                const float2 unit = pows[(i & 1) * kHeadDim + 16 * h + 8 * e];
+                us[e] = pair(unit.x * scale, unit.x * scale), uv[e] = pair(unit.y * scale, unit.y * scale);
             }
-            if (plain && (b & 1)) {
-                __syncwarp();
-                float* to = c.plain + ((size_t)(c.first + i * kC + 16 * (b - 1)) * a.n_v + c.h) * kHeadDim + 32 * q + 4 * (lane & 7);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = (lane >> 3) + 4 * j;
-                    if (16 * (b - 1) + t < n)
-                        *reinterpret_cast<float4*>(to + (size_t)t * a.n_v * kHeadDim) = *reinterpret_cast<const float4*>(whole + t * 32 + 4 * (lane & 7));
+            for (int k = 0; k < 4; ++k) {
+                const f2 o = *reinterpret_cast<const f2*>(scal + 32 * half + 8 * k + col);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 4 * k + 2 * e;
+                    float x, y;
+                    unpair(fma2(mul2(o, us[e]), pair_of(qs[h][r], qs[h][r + 1]), mul2(uv[e], pair_of(pv[h][r], pv[h][r + 1]))), x, y);
+                    if (PLAIN) {
+                        float* to = whole + (8 * k + col) * 32 + ((16 * h + 8 * e + (lane >> 2)) ^ (4 * col));
+                        to[0] = x, to[32] = y;
+                    } else {
+                        w[2 * (k & 1) + e] = pack2(x, y, TYPE);
+                    }
                 }
-                __syncwarp();
+                if (!PLAIN && (k & 1)) {
+                    const int t = 32 * half + 8 * (k - 1) + row;
+                    stmatrix4t(mine_u + t * 64 + (((2 * h + word) ^ ((t >> 1) & 3)) << 4), w);
+                }
             }
         };
         ask(0, 0);
 #pragma unroll 1
-        for (int b = 0; b < 4; b += 2) {
+        for (int half = 0; half < 2; ++half) {
             tc::tmem_wait_ld();
             arrived(qs[0], pv[0]);
-            ask(b + 1, 1);
-            put(b, qs[0], pv[0]);
+            ask(half, 1);
+            put(half, 0);
             tc::tmem_wait_ld();
             arrived(qs[1], pv[1]);
-            if (b == 0) ask(2, 0);
+            if (half == 0) ask(1, 0);
             else tell(c, BAR_OFREE);
-            put(b + 1, qs[1], pv[1]);
+            put(half, 1);
+            if (PLAIN) {
+                __syncwarp();
+                float* to = c.plain + ((size_t)(c.first + i * kC + 32 * half) * a.n_v + c.h) * kHeadDim + 32 * q + 4 * (lane & 7);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = (lane >> 3) + 4 * j;
+                    if (32 * half + t < n)
+                        *reinterpret_cast<float4*>(to + (size_t)t * a.n_v * kHeadDim) =
+                            *reinterpret_cast<const float4*>(whole + t * 32 + ((4 * (lane & 7)) ^ (8 * ((t >> 1) & 3))));
+                }
+                __syncwarp();
+            }
         }
         if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
-        if (plain) continue;
+        if (PLAIN) continue;
         __syncwarp();
         uint16_t* to = a.out + (long long)(c.first + i * kC) * a.out_stride + (size_t)c.h * kHeadDim + 32 * q + 8 * (lane & 3);
 #pragma unroll 2
         for (int t = lane >> 2; t < n; t += 8)
-            *reinterpret_cast<uint4*>(to + (long long)t * a.out_stride) = *reinterpret_cast<const uint4*>(mine + t * 32 + 8 * (lane & 3));
+            *reinterpret_cast<uint4*>(to + (long long)t * a.out_stride) =
+                *reinterpret_cast<const uint4*>(mine + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
         __syncwarp();
     }
 }
@@ -1181,7 +1212,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         state_role<TYPE, SPLIT>(c, warp >> 2, tid & 127, (uint32_t)(warp & 3) << 21);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        output_role<TYPE, SPLIT>(c, warp - 8, lane);
+        if (SPLIT && c.plain) output_role<TYPE, true>(c, warp - 8, lane);
+        else output_role<TYPE, false>(c, warp - 8, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 12) product_role<TYPE>(c);
