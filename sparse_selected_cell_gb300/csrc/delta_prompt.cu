@@ -22,9 +22,9 @@
 // FP16 outputs only.
 //
 // Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
-// 4,096 tokens 351 + 579 us, 1 x 61 14 + 15 (the second begins beside the first: 20 in all);
-// 1 x 8,192, cut into segments, 67 + 217, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
-// 24 x 1-2,000: 104 + 183.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
+// 4,096 tokens 347 + 467 us, 1 x 61 14 + 14 (the second begins beside the first: 19 in all);
+// 1 x 8,192, cut into segments, 66 + 167, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
+// 24 x 1-2,000: 103 + 153.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
 // the first is bound by shared memory (59 % of its cycles) and by waiting on it, the second by a
 // chain of dependent steps, see there.
 #include <type_traits>
@@ -64,8 +64,9 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 4,096 tokens 196 and 231 us with 32 value heads, 118
-// and 122 for 1 x 2,048; 1 x 8,192 193 and 397 with 8.  Segments of 8 chunks lose: 1 x 1,024 80 and 69 us.
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 297 and 365 us with 32 value heads, 180
+// and 318 with 8; 1 x 4,096 170 and 192 with 32; 1 x 2,048 105 and 102 with 32, 83 and 89 with 8.  Segments of 8 chunks lose:
+// 1 x 1,024 73 and 59 us.
 constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
@@ -548,8 +549,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 //   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
 // the first half of its operand is there, and S Q^T is issued behind V', while its pairs are
-// formed.  A chunk takes some 4,300 cycles with few blocks, 4,700 with all SMs at work (they
-// fetch instructions through caches that neighbours share): 1,000 until the last warp has S as
+// formed.  A chunk takes some 4,500 cycles, 4,650 with all SMs at work: 1,000 until the last warp has S as
 // pairs, 500 until K S^T is there, 950 for X, 400 for V', 950 for its pairs, then 700 for D, beside
 // which the next values are brought to their units.  The tensor pipe is busy for 1,850 of them,
 // and a warp's issue slots for a third; conversions to pairs and the outputs' share them.
@@ -569,7 +569,7 @@ enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kSt
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
-constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 283 us instead of 318)
+constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 251 us instead of 279)
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T
