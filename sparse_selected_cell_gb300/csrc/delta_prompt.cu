@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     // done, and it waits for this one before it reads what this one writes (1 x 61 tokens 19.5 us instead of 23).
     release_next();
     // the last sequence whose places begin here or before (every warp for itself)
-    int s;
-    {
+    int s = 0;
+    if (a.n_seq > 1) {
         int lo = 0, len = a.n_seq;                   // the first sequence whose places begin behind this one: in [lo, lo + len]
         while (len > 0) {
             const int step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
@@ -292,43 +292,53 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         vec[4 * kC + tt] = exp2f((float)(last - G));
     };
     ask_gates(0);
-    // rows into their places as they are: a thread's own 16-byte words, rows 2 (4 p + warp) + lane / 16 of 64 keys, then 64 queries
-    const int l = lane & 15;
-    const uint32_t own = (uint32_t)(l >> 3) * (kKqBytes / 2);
-#pragma unroll 4
-    for (int p = 0; p < 16; ++p) {
-        const int r = 2 * (4 * p + warp) + (lane >> 4), t = r & (kC - 1);
-        const uint16_t* src = p < 8 ? a.k + (long long)(first + min(t, n - 1)) * a.k_stride : a.q + (long long)(first + min(t, n - 1)) * a.q_stride;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     ::"r"(base_u + own + swz(r, l & 7)), "l"(src + (size_t)kh * kHeadDim + 8 * l), "r"(t < n ? 16 : 0) : "memory");
-    }
+    // rows into their places as they are: a thread's own 16-byte words, rows 8 p + r0 of 64 keys, then of 64 queries
+    const int l = lane & 15, r0 = 2 * warp + (lane >> 4);
+    const uint32_t own = (uint32_t)(l >> 3) * (kKqBytes / 2) + swz(r0, l & 7);
+    auto ask_rows = [&](const uint16_t* from, long long stride, uint32_t to) {
+        const uint16_t* src = from + (long long)(first + r0) * stride + (size_t)kh * kHeadDim + 8 * l;
+        const uint16_t* some = from + (long long)first * stride;     // (any address that may be read, where there is no token)
+#pragma unroll
+        for (int p = 0; p < kC / 8; ++p) {
+            const bool there = 8 * p + r0 < n;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(to + 1024 * p), "l"(there ? src : some), "r"(there ? 16 : 0) : "memory");
+            src += 8 * stride;
+        }
+    };
+    ask_rows(a.k, a.k_stride, base_u + own);
+    ask_rows(a.q, a.q_stride, base_u + own + kC * 128);
     scan_gates(0);
     // ---- keys and queries to FP16 rows, each times the power of two that puts its largest element in [2^10, 2^11)
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 4
     for (int p = 0; p < 16; ++p) {
-        const int r = 2 * (4 * p + warp) + (lane >> 4);
-        const uint32_t at = own + swz(r, l & 7);
+        const int r = 8 * p + r0;
+        const uint32_t at = own + 1024 * p;
         float x[8];
         unpack8(*reinterpret_cast<const uint4*>(base + at), TYPE, x);
         float m = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // in two steps, since 2^e may be beyond FP32; a row of zeros is any power of two of itself: one that leaves 1 / |k| small
-        const int e = m >= 0x1p-126f ? 10 - f32_exponent(m) : m > 0.f ? 136 : 90, e1 = min(e, 100);
-        const f2 up = pair(exp2i(e1), exp2i(e1)), more = pair(exp2i(e - e1), exp2i(e - e1));
+        // a row of zeros is any power of two of itself: one that leaves 1 / |k| small
+        const int e = m > 0.f ? min(10 - f32_exponent(m), 126) : 90;
+        const f2 up = pair(exp2i(e), exp2i(e));
         uint32_t h[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float u, w2;
-            unpair(mul2(mul2(pair(x[2 * j], x[2 * j + 1]), up), more), u, w2);
+            unpair(mul2(pair(x[2 * j], x[2 * j + 1]), up), u, w2);
             h[j] = pack_f16x2(u, w2);
         }
         *reinterpret_cast<uint4*>(base + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(kq + at) = make_uint4(h[0], h[1], h[2], h[3]);
         if (l == 0) s_e[r] = e;
     }
+    tc::fence_proxy_async();
     __syncthreads();
+    if (tid == 0) {
+        bulk_store(kq, base_u, kKqBytes);
+        bulk_commit();
+    }
     join_gates();
     // ---- K K^T and Q K^T: a warp has rows 16 warp .. + 15 of both, columns up to the diagonal; of Q Q^T the diagonal's block
     float kk[8][4], qk[8][4], qq[2][4];
@@ -370,6 +380,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             s_r[kC + i] = i < n ? __frsqrt_rn(q2 + ldexpf(a.eps, 2 * s_e[kC + i])) : 0.f;
         }
     }
+    if (tid == 0) bulk_wait_read();                  // the rows have left, A may come in their place
     __syncthreads();
     // the power of two that brings the largest 1 / |k| of a stored key into [1/2, 1): the chunk's key unit
     float key_unit = fmaxf(s_r[lane], s_r[lane + 32]);
