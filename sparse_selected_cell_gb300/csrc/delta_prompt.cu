@@ -411,21 +411,33 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             if (h0 + hh >= rep) continue;
             const float* ve = s_g + hh * kVecs * kC;
             float* A = s_A + hh * kC * kAStride;
+            f2 ghi[2], glo[2], ka[2], qa[2];
+            const f2 less = pair(-1.f, -1.f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 16 * warp + (lane >> 2) + 8 * e;
-                const float ghi = ve[i], glo = ve[kC + i], ka = ve[2 * kC + i] * s_r[i], qa = s_r[kC + i] * kTriUnit;
+                const float k1 = ve[2 * kC + i] * s_r[i], q1 = s_r[kC + i] * kTriUnit;
+                ghi[e] = pair(ve[i], ve[i]), glo[e] = pair(ve[kC + i], ve[kC + i]), ka[e] = pair(k1, k1), qa[e] = pair(q1, q1);
+            }
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    if (t > 2 * warp + 1) continue;
+            for (int p = 0; p < 4; ++p) {
+                if (p > warp) continue;
+#pragma unroll
+                for (int t = 2 * p; t < 2 * p + 2; ++t) {
                     const int j = 8 * t + 2 * (lane & 3);
-                    const float2 gj = *reinterpret_cast<const float2*>(ve + j), lj = *reinterpret_cast<const float2*>(ve + kC + j);
-                    const float2 rj = *reinterpret_cast<const float2*>(s_r + j);
-                    const float d0 = fast_exp2((ghi - gj.x) + (glo - lj.x)) * rj.x, d1 = fast_exp2((ghi - gj.y) + (glo - lj.y)) * rj.y;
-                    *reinterpret_cast<float2*>(A + i * kAStride + j) =
-                        make_float2(j < i ? kk[t][2 * e] * ka * d0 : 0.f, j + 1 < i ? kk[t][2 * e + 1] * ka * d1 : 0.f);
-                    *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
-                        pack_f16x2(j <= i ? qk[t][2 * e] * qa * d0 : 0.f, j + 1 <= i ? qk[t][2 * e + 1] * qa * d1 : 0.f);
+                    const f2 gj = *reinterpret_cast<const f2*>(ve + j), lj = *reinterpret_cast<const f2*>(ve + kC + j), rj = *reinterpret_cast<const f2*>(s_r + j);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 16 * warp + (lane >> 2) + 8 * e;
+                        float x, y;
+                        unpair(add2(fma2(less, gj, ghi[e]), fma2(less, lj, glo[e])), x, y);
+                        const f2 d = mul2(pair(fast_exp2(x), fast_exp2(y)), rj);
+                        unpair(mul2(mul2(pair(kk[t][2 * e], kk[t][2 * e + 1]), ka[e]), d), x, y);
+                        *reinterpret_cast<float2*>(A + i * kAStride + j) = make_float2(j < i ? x : 0.f, j + 1 < i ? y : 0.f);
+                        unpair(mul2(mul2(pair(qk[t][2 * e], qk[t][2 * e + 1]), qa[e]), d), x, y);
+                        *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
+                            pack_f16x2(j <= i ? x : 0.f, j + 1 <= i ? y : 0.f);
+                    }
                 }
             }
         }
