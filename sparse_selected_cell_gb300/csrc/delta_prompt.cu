@@ -22,9 +22,9 @@
 // FP16 outputs only.
 //
 // Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
-// 4,096 tokens 347 + 467 us, 1 x 61 14 + 14 (the second begins beside the first: 19 in all);
-// 1 x 8,192, cut into segments, 66 + 167, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
-// 24 x 1-2,000: 103 + 153.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
+// 4,096 tokens 318 + 462 us, 1 x 61 13 + 14 (the second begins beside the first: 18 in all);
+// 1 x 8,192, cut into segments, 60 + 166, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
+// 24 x 1-2,000: 95 + 152.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
 // the first is bound by shared memory (59 % of its cycles) and by waiting on it, the second by a
 // chain of dependent steps, see there.
 #include <type_traits>
@@ -64,9 +64,9 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 297 and 365 us with 32 value heads, 180
-// and 318 with 8; 1 x 4,096 170 and 192 with 32; 1 x 2,048 105 and 102 with 32, 83 and 89 with 8.  Segments of 8 chunks lose:
-// 1 x 1,024 73 and 59 us.
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 291 and 357 us with 32 value heads, 177
+// and 317 with 8; 1 x 4,096 166 and 187 with 32; 1 x 2,048 101 and 98 with 32, 80 and 88 with 8.  Segments of 8 chunks lose:
+// 1 x 1,024 70 and 56 us.
 constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
@@ -154,7 +154,8 @@ __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 12
 // rows (their diagonals give the lengths); (I + A)^-1 by halves of halves: the four 16 x 16 blocks on the diagonal by
 // substitution, a column to a thread, then [T11, 0; -T22 A21 T11, T22] for pairs of 16 and of 32, as products of FP16 pairs
 // (a column to a thread over all 64 rows took five times as long).  Four blocks to an SM hide one another's waits; 256 threads
-// to a block, with the products and rows halved, had a single chunk through 7 % sooner and took 45 % longer for many.
+// to a block, with the products and rows halved, had a single chunk through 7 % sooner and took 45 % longer for many;
+// five blocks in 96 registers took 2 % longer, three 17 %; rows of Q K^T from the other end, so that all warps have ten blocks, 7 %.
 constexpr int kPrepThreads = 128;
 constexpr int kAStride = 68;                         // floats to a row of A
 // Shared memory: keys and queries, then two heads' A, then their T in A's place; P; the tokens' factors.
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     const int place = (int)(blockIdx.x / (unsigned)a.n_k), kh = (int)(blockIdx.x - (unsigned)place * (unsigned)a.n_k);
     wait_for_stream();
     // From here on, once all blocks run, the chunks' kernel may set itself up beside this one: whatever was before this one is
-    // done, and it waits for this one before it reads what this one writes (1 x 61 tokens 19.5 us instead of 23).
+    // done, and it waits for this one before it reads what this one writes (1 x 61 tokens 19 us instead of 23).
     release_next();
     // the last sequence whose places begin here or before (every warp for itself)
     int s = 0;
@@ -592,7 +593,7 @@ enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kSt
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
-constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 251 us instead of 279)
+constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 240 us instead of 269)
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T

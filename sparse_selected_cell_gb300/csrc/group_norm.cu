@@ -6,7 +6,7 @@
 // taken first and the squares of what is left after it, in FP32, without a second read.
 //
 // 8,192 tokens x 32 groups x 128 with a gate (201 MB) take 34.1 us, 5.9 TB/s, 0.87 of what a
-// plain copy reaches: half the issue slots are taken (unpacking, SiLU's two special functions an
+// plain copy reaches: 70 % of the issue slots are taken (unpacking, SiLU's two special functions an
 // element, packing), so the loads do not queue up as a copy's do.
 #include "linear.cuh"
 
@@ -154,7 +154,7 @@ cudaError_t launch_items(const NormArgs& a, cudaStream_t stream) {
     return launch_overlapped(group_norm_kernel<TYPE, LANES, PIECES, ITEMS>, dim3((unsigned)grid), kNormThreads, 0, stream, a);
 }
 
-// Two groups to a thread, six blocks to an SM, once that still gives every SM a few blocks: 8,192 tokens x 32 x 128 with a gate
+// Two groups to a thread, six blocks to an SM (40 registers, some of them spilled), once that still gives every SM a few blocks: 8,192 tokens x 32 x 128 with a gate
 // 33.8 us instead of 38.0 (four groups in as many registers as they take: 37.8; in 40 registers: 42.4).  Below that one group a
 // thread, for the shortest way through: 512 x 32 x 128 3.5 us instead of 3.9.
 template <int TYPE, int LANES, int PIECES>
