@@ -1042,7 +1042,16 @@ __device__ void output_role(const Block& c, int q, int lane) {
         const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + kScalO;
         if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_H, par) || !wait(c, BAR_O, par)) return;
         tc::fence_after_sync();
+        // 1 / the units of dims 16 h + 8 e + lane / 4, read before BAR_OFREE: two chunks on they are overwritten
         const float scale = PLAIN && c.kind == 2 ? 1.f : a.scale;
+        float2 unit[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                unit[h][e] = pows[(i & 1) * kHeadDim + 16 * h + 8 * e];
+                unit[h][e].x *= scale, unit[h][e].y *= scale;
+            }
         const int n = min(kC, c.n_tok - i * kC);
         // the next 16 dims' or 32 tokens' accumulators are on their way while the ones before are written
         uint32_t qs[2][16], pv[2][16];
@@ -1052,12 +1061,10 @@ __device__ void output_role(const Block& c, int q, int lane) {
         };
         auto put = [&](int half, int h) {
             uint32_t w[4];
-            f2 us[2], uv[2];                         // of dims 16 h + 8 e + lane / 4
+            f2 us[2], uv[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float2 unit = pows[(i & 1) * kHeadDim + 16 * h + 8 * e];
-                us[e] = pair(unit.x * scale, unit.x * scale), uv[e] = pair(unit.y * scale, unit.y * scale);
-            }
+            for (int e = 0; e < 2; ++e)
+                us[e] = pair(unit[h][e].x, unit[h][e].x), uv[e] = pair(unit[h][e].y, unit[h][e].y);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const f2 o = *reinterpret_cast<const f2*>(scal + 32 * half + 8 * k + col);
@@ -1104,9 +1111,9 @@ __device__ void output_role(const Block& c, int q, int lane) {
                 __syncwarp();
             }
         }
+        __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(c, BAR_EMPTY + st));
         if (PLAIN) continue;
-        __syncwarp();
         uint16_t* to = a.out + (long long)(c.first + i * kC) * a.out_stride + (size_t)c.h * kHeadDim + 32 * q + 8 * (lane & 3);
 #pragma unroll 2
         for (int t = lane >> 2; t < n; t += 8)
@@ -1236,6 +1243,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         state_role<TYPE, SPLIT>(c, warp >> 2, tid & 127, (uint32_t)(warp & 3) << 21);
+        tc::tmem_wait_st();                          // (of a chunk that a wait running out has ended)
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (SPLIT && c.plain) output_role<TYPE, true>(c, warp - 8, lane);
