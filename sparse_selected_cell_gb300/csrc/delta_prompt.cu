@@ -23,7 +23,7 @@
 //
 // Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
 // 4,096 tokens 318 + 462 us, 1 x 61 13 + 14 (the second begins beside the first: 18 in all);
-// 1 x 8,192, cut into segments, 60 + 166, and 19 + 53 to put them together.  FP16, 8 and 16 heads,
+// 1 x 8,192, cut into segments, 60 + 166, and 19 + 49 to put them together.  FP16, 8 and 16 heads,
 // 24 x 1-2,000: 95 + 152.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
 // the first is bound by shared memory (59 % of its cycles) and by waiting on it, the second by a
 // chain of dependent steps, see there.
@@ -64,8 +64,8 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 291 and 357 us with 32 value heads, 177
-// and 317 with 8; 1 x 4,096 166 and 187 with 32; 1 x 2,048 101 and 98 with 32, 80 and 88 with 8.  Segments of 8 chunks lose:
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 286 and 357 us with 32 value heads, 173
+// and 317 with 8; 1 x 4,096 163 and 187 with 32; 1 x 2,048 99 and 98 with 32, 79 and 88 with 8.  Segments of 8 chunks lose:
 // 1 x 1,024 70 and 56 us.
 constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
@@ -1023,6 +1023,11 @@ __device__ __forceinline__ void stmatrix4t(uint32_t addr, const uint32_t (&r)[4]
                  ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
 // Value dims by tokens become tokens by value dims: accumulators as matrix tiles, so that a transposing store takes 16 tokens x
 // 16 dims at once (a token's 16 bits at a time, a lane to a dim, it is twice the instructions, which the state warps pay for).
 // PLAIN: segments' FP32 outputs.
@@ -1469,18 +1474,28 @@ __global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_
                 mma16816(acc[2 * t + 1], f, b[2], b[3]);
             }
         }
+        __syncthreads();                             // R_t q_t has been read: the outputs in its place, then out by rows
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = m0 + (lane >> 2) + 8 * e;
-            if (t >= n) continue;
-            const float up = s_unit[kHeadDim + t] * a.scale;
+        for (int j = 0; j < 8; j += 2) {             // tiles: tokens 0-7 and 8-15 of dims 8 j, then of dims 8 (j + 1)
+            uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int d = n0 + 8 * j + 2 * (lane & 3);
-                const float2 x = so_far[e][j];
-                *reinterpret_cast<uint32_t*>(a.out + (long long)(first + t) * a.out_stride + (size_t)h * kHeadDim + d) =
-                    pack2(fmaf(acc[j][2 * e], up * s_unit[d], x.x), fmaf(acc[j][2 * e + 1], up * s_unit[d + 1], x.y), TYPE);
+            for (int e = 0; e < 2; ++e) {
+                const float up = s_unit[kHeadDim + m0 + (lane >> 2) + 8 * e] * a.scale;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float2 unit = *reinterpret_cast<const float2*>(s_unit + n0 + 8 * (j + u) + 2 * (lane & 3)), x = so_far[e][j + u];
+                    w[2 * u + e] = pack2(fmaf(acc[j + u][2 * e], up * unit.x, x.x), fmaf(acc[j + u][2 * e + 1], up * unit.y, x.y), TYPE);
+                }
             }
+            stmatrix4(base_u + kAddT + (warp >> 2) * (kC * 128) + swz(m0 + (lane & 15), j + (lane >> 4)), w);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = tid + i * kAddThreads, t = at >> 4, word = at & 15;
+            if (t < n)
+                *reinterpret_cast<uint4*>(a.out + (long long)(first + t) * a.out_stride + (size_t)h * kHeadDim + 8 * word) =
+                    *reinterpret_cast<const uint4*>(base + kAddT + (word >> 3) * (kC * 128) + swz(t, word & 7));
         }
     }
 }
