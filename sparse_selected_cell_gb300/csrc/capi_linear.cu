@@ -78,7 +78,8 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
         (w_type != type && w_type != QSA_F32) || !act_ok(activation))
         return QSA_ERR_ARG;
     if (!cu_tokens && n_seq != n_tok) return QSA_ERR_ARG;
-    if (n_tok > kMaxTokens || n_seq > kMaxTokens || n_ch > kMaxHeads * qsa::kHeadDim) return QSA_ERR_UNSUPPORTED;
+    if (n_tok > kMaxTokens || n_seq > kMaxTokens || n_ch > kMaxHeads * qsa::kHeadDim || !qsa::short_conv_fits(n_tok, n_ch))
+        return QSA_ERR_UNSUPPORTED;
     if (n_seq == 0) return QSA_OK;
     if (!weight || !state_slots || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(state, 16) ||
         (n_slots > 0 && !state))
@@ -140,7 +141,8 @@ int qsa_group_norm(const void* x, int64_t x_stride, const void* gate, int64_t ga
     if (n_tok < 0 || n_groups <= 0 || size <= 0 || size % 8 != 0 || !type16(type) ||
         (w_type != type && w_type != QSA_F32) || !act_ok(activation) || !(eps >= 0.f) || !std::isfinite(eps))
         return QSA_ERR_ARG;
-    if (size > 8192 || n_groups > kMaxHeads || n_tok > kMaxTokens) return QSA_ERR_UNSUPPORTED;
+    if (size > 8192 || n_groups > kMaxHeads || n_tok > kMaxTokens || !qsa::group_norm_fits(n_tok, n_groups, size))
+        return QSA_ERR_UNSUPPORTED;
     if (n_tok == 0) return QSA_OK;
     const int64_t row = (int64_t)n_groups * size;
     if (!rows_ok(x, x_stride, row) || !rows_ok(out, out_stride, row) || (gate && !rows_ok(gate, gate_stride, row)))

@@ -150,7 +150,6 @@ __global__ void __launch_bounds__(kNormThreads, ITEMS == 2 ? 6 : 1) group_norm_k
 template <int TYPE, int LANES, int PIECES, int ITEMS>
 cudaError_t launch_items(const NormArgs& a, cudaStream_t stream) {
     const long long items = (long long)a.n_tok * a.n_groups, per = (long long)kNormThreads / LANES * ITEMS, grid = (items + per - 1) / per;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_overlapped(group_norm_kernel<TYPE, LANES, PIECES, ITEMS>, dim3((unsigned)grid), kNormThreads, 0, stream, a);
 }
 
@@ -181,6 +180,15 @@ cudaError_t launch_type(const NormArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// A block has one group of more than 128 words, eight of more than 32; of shorter ones, being many, two to every thread group.
+bool group_norm_fits(long long n_tok, long long n_groups, int size) {
+    const int words = size / 8;
+    int lanes = 1;
+    while (lanes < words && lanes < 32) lanes *= 2;
+    const long long each = words > 128 ? 1 : words > 32 ? kNormThreads / 32 : kNormThreads / lanes * 2;
+    return (n_tok * n_groups + each - 1) / each <= 0x7fffffffLL;
+}
 
 cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t stream) {
     return a.type == QSA_F16 ? launch_type<QSA_F16>(a, stream) : launch_type<QSA_BF16>(a, stream);

@@ -25,6 +25,7 @@ struct ConvArgs {
     int32_t* dev_status;
 };
 
+bool short_conv_fits(long long n_tok, long long n_ch);   // into one launch
 cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t stream);
 
 struct DeltaArgs {
@@ -77,6 +78,7 @@ struct NormArgs {
     long long out_stride;
 };
 
+bool group_norm_fits(long long n_tok, long long n_groups, int size);   // into one launch
 cudaError_t launch_group_norm(const NormArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- device helpers

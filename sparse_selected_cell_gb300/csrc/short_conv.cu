@@ -291,7 +291,6 @@ template <int TYPE, int W, int RUN>
 cudaError_t launch_run(const ConvArgs& a, cudaStream_t stream) {
     const long long cols = (a.n_ch / 8 + kConvThreads - 1) / kConvThreads;
     const long long runs = a.n_tok > 0 ? (a.n_tok + RUN - 1LL) / RUN : 1;
-    if (cols * runs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_overlapped(short_conv_kernel<TYPE, W, RUN>, dim3((unsigned)(cols * runs)), kConvThreads, 0, stream, a,
                              (unsigned)cols);
 }
@@ -321,6 +320,11 @@ cudaError_t launch_type(const ConvArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// Blocks of the runs of 32 tokens, which many tokens are cut into.
+bool short_conv_fits(long long n_tok, long long n_ch) {
+    return (n_tok + 31) / 32 * ((n_ch / 8 + kConvThreads - 1) / kConvThreads) <= 0x7fffffffLL;
+}
 
 cudaError_t launch_short_conv(const ConvArgs& a, cudaStream_t stream) {
     return a.type == QSA_F16 ? launch_type<QSA_F16>(a, stream) : launch_type<QSA_BF16>(a, stream);
