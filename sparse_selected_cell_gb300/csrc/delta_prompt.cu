@@ -707,6 +707,8 @@ __device__ void product_role(const Block& c) {
         const int st = i % kStages, par = i & 1;
         const uint64_t stage = (uint64_t)(st * kStageBytes) >> 4, tri = stage + (kKqBytes >> 4);
         if (!(ok = wait(c, BAR_FULL + st, (i / kStages) & 1))) break;
+        // V' P^T of the chunk before reads columns that S K^T writes, and products of different accumulators may pass one another
+        if (i > 0 && !(ok = wait(c, BAR_O, par ^ 1))) break;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int q = quarter(n);
