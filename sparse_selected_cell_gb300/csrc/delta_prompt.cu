@@ -41,9 +41,12 @@ constexpr int kC = 64;                               // tokens of a chunk
 // Chunk c of sequence s has place first / 64 + s + c, first being the sequence's first token:
 // places never meet, and none passes n_tok / 64 + n_seq.
 constexpr uint32_t kKqBytes = 2 * kC * kHeadDim * 2; // keys, then queries: two 64-dim halves of 128 rows, 128-byte swizzle
-constexpr uint32_t kTriBytes = kC * kC * 2;          // a 64 x 64 FP16 matrix, 128-byte swizzle
-constexpr uint32_t kOffTlo = kTriBytes, kOffP = 2 * kTriBytes, kOffScal = 3 * kTriBytes;
-constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T hi, T lo, P, the factors of each token
+// T and P are lower triangular, FP16, as tiles of 32 rows of 128 bytes, 128-byte swizzle: rows 32 to 63 a tile each for hi and
+// lo, rows 0 to 31, whose second half is zero, one tile for both, hi and lo side by side (of P there is no lo).
+constexpr uint32_t kTileBytes = kC / 2 * 128;
+constexpr uint32_t kTBytes = 3 * kTileBytes, kPBytes = 2 * kTileBytes;
+constexpr uint32_t kOffP = kTBytes, kOffScal = kOffP + kPBytes;
+constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
 // -exp(G) / |k|, exp(G_C - G) / |k| times the chunk's key unit, exp(G) / |q|, of 64 tokens each; then exp(G_C) and the key unit
 constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1;
@@ -159,8 +162,8 @@ __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 12
 constexpr int kPrepThreads = 128;
 constexpr int kAStride = 68;                         // floats to a row of A
 // Shared memory: keys and queries, then two heads' A, then their T in A's place; P; the tokens' factors.
-constexpr uint32_t kABytes = kC * kAStride * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kTriBytes;
-static_assert(kPrepP >= kKqBytes && kABytes % 1024 == 0, "A's place");
+constexpr uint32_t kABytes = kC * kAStride * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kPBytes;
+static_assert(kPrepP >= kKqBytes && kABytes % 1024 == 0 && kTBytes <= kABytes, "A's place");
 constexpr int kVecs = 5;                             // of a value head: G's hi and lo in powers of two, beta, exp(G), exp(G_C - G)
 constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 4 * 8 + 1024;
 
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                if (p > warp) continue;
+                if (p > (warp | 1)) continue;        // (zeros above the diagonal's blocks, too, up to the tile's end)
 #pragma unroll
                 for (int t = 2 * p; t < 2 * p + 2; ++t) {
                     const int j = 8 * t + 2 * (lane & 3);
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
                         unpair(mul2(mul2(pair(kk[t][2 * e], kk[t][2 * e + 1]), ka[e]), d), x, y);
                         *reinterpret_cast<float2*>(A + i * kAStride + j) = make_float2(j < i ? x : 0.f, j + 1 < i ? y : 0.f);
                         unpair(mul2(mul2(pair(qk[t][2 * e], qk[t][2 * e + 1]), qa[e]), d), x, y);
-                        *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kTriBytes + swz(i, t) + 4 * (lane & 3)) =
+                        *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kPBytes + swz(i, t) + 4 * (lane & 3)) =
                             pack_f16x2(j <= i ? x : 0.f, j + 1 <= i ? y : 0.f);
                     }
                 }
@@ -446,7 +449,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + kPrepP + hh * kTriBytes, kTriBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + kPrepP + hh * kPBytes, kPBytes);
             bulk_commit();
         }
         // ---- (I + A)^-1 of the warp pair's head, in A's place
@@ -516,8 +519,8 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         }
         __syncthreads();
         {
-            // times beta of the column, as pairs, in A's place: a thread has row tid % 64, eight columns at a time up to the
-            // diagonal's block (rows up to 31 end in column 31 at most; what lies above the diagonal's blocks is not read)
+            // times beta of the column, as pairs, in A's place: a thread has row tid % 64, eight columns at a time up to its
+            // tile's end (zeros above the diagonal, as A has them there)
             const int i = tid & (kC - 1);
             uint4 hi[8], lo[8];
             if (has) {
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
                 for (int t = 0; t < 8; ++t) {
                     if (t > 4 * side + 3) continue;
                     *reinterpret_cast<uint4*>(T + swz(i, t)) = hi[t];
-                    *reinterpret_cast<uint4*>(T + kOffTlo + swz(i, t)) = lo[t];
+                    *reinterpret_cast<uint4*>(T + (side ? kTileBytes + swz(i, t) : swz(i, t + 4))) = lo[t];
                 }
             }
         }
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * kABytes, 2 * kTriBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * kABytes, kTBytes);
             bulk_commit();
             if (h0 + 2 < rep) bulk_wait_read();
         }
@@ -690,6 +693,7 @@ __device__ void product_role(const Block& c) {
     // FP16 operands: the type fields (bits 7 to 12) zero
     constexpr uint32_t kTypes = ~((7u << 7) | (7u << 10));
     constexpr uint32_t id64 = tc::idesc_bf16(128, 64, false, false) & kTypes;
+    constexpr uint32_t id32 = tc::idesc_bf16(128, kC / 2, false, false) & kTypes;
     constexpr uint32_t idD = tc::idesc_bf16(128, kHeadDim, false, true) & kTypes;       // B = keys, key dims along the row
     const uint64_t dkq0 = tc::smem_desc(c.base_u, 16, 1024, 2), dkt0 = tc::smem_desc(c.base_u, kKqBytes / 2, 1024, 2);
     bool ok = true;
@@ -728,18 +732,22 @@ __device__ void product_role(const Block& c) {
         if (i > 0 && !(ok = wait(c, BAR_OFREE, par ^ 1))) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens from 16 b on take tokens 16 b .. 16 b + 15
+        for (int n = 0; n < 4; ++n) {                // T is lower triangular: tokens 0 to 31 take tokens 0 to 31 only
             const int b = quarter(n);
             if (!(n & 1)) {
                 if (!(ok = wait(c, BAR_X + n / 2, par))) break;
                 tc::fence_after_sync();
             }
-            const uint32_t id = id64 - (uint32_t)b * (2u << 17);     // 64 - 16 b columns
-            const uint64_t d = dkq0 + tri + ((b * 2048 + b * 32) >> 4);
-            const uint32_t at = c.tmem + kTmX + 8 * b, to = c.tmem + kTmV + 16 * b;
-            product(to, at, d, id, b, leader);
-            product(to, at + 32, d, id, 1, leader);
-            product(to, at, d + (kOffTlo >> 4), id, 1, leader);
+            const uint32_t at = c.tmem + kTmX + 8 * b;
+            const uint64_t d = dkq0 + tri + ((b * 32) >> 4);
+            if (b < 2) {
+                product(c.tmem + kTmV, at, d, id32, b, leader);
+                product(c.tmem + kTmV, at + 32, d, id32, 1, leader);
+                product(c.tmem + kTmV, at, d + (64 >> 4), id32, 1, leader);
+            }
+            product(c.tmem + kTmV + 32, at, d + (kTileBytes >> 4), id32, b, leader);
+            product(c.tmem + kTmV + 32, at + 32, d + (kTileBytes >> 4), id32, 1, leader);
+            product(c.tmem + kTmV + 32, at, d + (2 * kTileBytes >> 4), id32, 1, leader);
         }
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_V));
@@ -762,10 +770,14 @@ __device__ void product_role(const Block& c) {
         tc::fence_after_sync();
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const uint32_t to = c.tmem + kTmPv + 16 * b, at = c.tmem + kTmH + 8 * b, id = id64 - (uint32_t)b * (2u << 17);
-            const uint64_t d = dkq0 + tri + ((kOffP + b * 2048 + b * 32) >> 4);
-            product(to, at, d, id, b, leader);
-            if (TYPE == QSA_F16) product(to, at + 32, d, id, 1, leader);
+            const uint32_t at = c.tmem + kTmH + 8 * b;
+            const uint64_t d = dkq0 + tri + ((kOffP + b * 32) >> 4);
+            if (b < 2) {
+                product(c.tmem + kTmPv, at, d, id32, b, leader);
+                if (TYPE == QSA_F16) product(c.tmem + kTmPv, at + 32, d, id32, 1, leader);
+            }
+            product(c.tmem + kTmPv + 32, at, d + (kTileBytes >> 4), id32, b, leader);
+            if (TYPE == QSA_F16) product(c.tmem + kTmPv + 32, at + 32, d + (kTileBytes >> 4), id32, 1, leader);
         }
         tc::commit_elect(bar(c, BAR_O));
         tc::commit_elect(bar(c, BAR_EMPTY + st));
