@@ -429,9 +429,8 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
  *   - state: FP32 [n_slots][n_v][128][128], the key dim innermost, 16-byte aligned.
  *   - Sequences of more than 32 tokens go by chunks of 64 on the tensor cores; the
  *     state and all sums in FP32, the state's and the new values' operands as pairs of
- *     FP16 (22 bits, with a power of two per value dim).  The products that end in
- *     `out` alone are of FP16 factors (2^-12 each, relative); for FP16 outputs the
- *     state and the new values are pairs there, too.  Shorter ones go token by token,
+ *     FP16 (22 bits, with a power of two per value dim), and so are the other factors
+ *     of the products that end in `out`.  Shorter ones go token by token,
  *     in FP32 throughout (in a step of one sequence, if n_tok <= 32).  Where the step
  *     has few heads (n_seq n_v below half the SMs) and many tokens, long sequences are
  *     cut into segments that run at once and are put together afterwards.

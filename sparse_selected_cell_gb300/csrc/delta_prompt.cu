@@ -13,13 +13,13 @@
 //
 // Numbers.  Keys and queries enter as their FP16 selves times a power of two for each row
 // (exact but for elements below 2^-24 of the row's largest, which lose bits); their lengths, 1 / |k|, are factors of
-// columns and rows in FP32.  The state, X, V' and T are pairs of FP16, hi + lo (22 bits), in
-// products of which lo lo is left out; the state itself stays in FP32 registers.  All products
+// columns and rows in FP32.  The state, X, V', T and P are pairs of FP16, hi + lo (22 bits), in
+// products of which lo lo is left out; the state itself stays in FP32.  All products
 // are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
 // the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
-// passes FP16's range and what counts stays in its upper bits.  In P V' P is single
-// FP16, and so is V' for BF16 outputs, which would not show more; S Q^T takes the state's lo for
-// FP16 outputs only.
+// passes FP16's range and what counts stays in its upper bits.  (Products that end in outputs of
+// single FP16, S Q^T without the state's lo, cost outputs 2^-12 of their row's length: 12 x 4,096
+// 782 us instead of 825, 1 x 8,192 292 instead of 327.)
 //
 // Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
 // 4,096 tokens 318 + 462 us, 1 x 61 13 + 14 (the second begins beside the first: 18 in all);
@@ -41,11 +41,10 @@ constexpr int kC = 64;                               // tokens of a chunk
 // Chunk c of sequence s has place first / 64 + s + c, first being the sequence's first token:
 // places never meet, and none passes n_tok / 64 + n_seq.
 constexpr uint32_t kKqBytes = 2 * kC * kHeadDim * 2; // keys, then queries: two 64-dim halves of 128 rows, 128-byte swizzle
-// T and P are lower triangular, FP16, as tiles of 32 rows of 128 bytes, 128-byte swizzle: rows 32 to 63 a tile each for hi and
-// lo, rows 0 to 31, whose second half is zero, one tile for both, hi and lo side by side (of P there is no lo).
-constexpr uint32_t kTileBytes = kC / 2 * 128;
-constexpr uint32_t kTBytes = 3 * kTileBytes, kPBytes = 2 * kTileBytes;
-constexpr uint32_t kOffP = kTBytes, kOffScal = kOffP + kPBytes;
+// T and P are lower triangular, pairs of FP16, as tiles of 32 rows of 128 bytes, 128-byte swizzle: rows 0 to 31, whose second
+// half is zero, one tile for both, hi and lo side by side; rows 32 to 63 a tile for hi and one for lo.
+constexpr uint32_t kTileBytes = kC / 2 * 128, kTriBytes = 3 * kTileBytes;
+constexpr uint32_t kOffP = kTriBytes, kOffScal = 2 * kTriBytes;
 constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
 // -exp(G) / |k|, exp(G_C - G) / |k| times the chunk's key unit, exp(G) / |q|, of 64 tokens each; then exp(G_C) and the key unit
@@ -160,10 +159,11 @@ __device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 12
 // to a block, with the products and rows halved, had a single chunk through 7 % sooner and took 45 % longer for many;
 // five blocks in 96 registers took 2 % longer, three 17 %; rows of Q K^T from the other end, so that all warps have ten blocks, 7 %.
 constexpr int kPrepThreads = 128;
-constexpr int kAStride = 68;                         // floats to a row of A
-// Shared memory: keys and queries, then two heads' A, then their T in A's place; P; the tokens' factors.
-constexpr uint32_t kABytes = kC * kAStride * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kPBytes;
-static_assert(kPrepP >= kKqBytes && kABytes % 1024 == 0 && kTBytes <= kABytes, "A's place");
+// A's blocks of 32 x 32: rows and columns 0 to 31, rows 32 to 63 of the same columns, rows and columns 32 to 63.
+constexpr int kAStride = 36, kABlock = kC / 2 * kAStride;   // floats to a row of a block, to a block
+// Shared memory: keys and queries; in their place two heads' A, then their T in A's place, and P; the tokens' factors.
+constexpr uint32_t kABytes = 3 * kABlock * 4, kPrepP = 2 * kABytes, kPrepVec = kPrepP + 2 * kTriBytes;
+static_assert(kPrepVec >= kKqBytes && kPrepP % 1024 == 0 && kTriBytes <= kABytes, "A's place");
 constexpr int kVecs = 5;                             // of a value head: G's hi and lo in powers of two, beta, exp(G), exp(G_C - G)
 constexpr uint32_t kPrepBytes = kPrepVec + (4 * kC + 2 * kVecs * kC) * 4 + 4 * 8 + 1024;
 
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         for (int hh = 0; hh < 2; ++hh) {
             if (h0 + hh >= rep) continue;
             const float* ve = s_g + hh * kVecs * kC;
-            float* A = s_A + hh * kC * kAStride;
+            float* A = s_A + hh * 3 * kABlock;
             f2 ghi[2], glo[2], ka[2], qa[2];
             const f2 less = pair(-1.f, -1.f);
 #pragma unroll
@@ -437,10 +437,14 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
                         unpair(add2(fma2(less, gj, ghi[e]), fma2(less, lj, glo[e])), x, y);
                         const f2 d = mul2(pair(fast_exp2(x), fast_exp2(y)), rj);
                         unpair(mul2(mul2(pair(kk[t][2 * e], kk[t][2 * e + 1]), ka[e]), d), x, y);
-                        *reinterpret_cast<float2*>(A + i * kAStride + j) = make_float2(j < i ? x : 0.f, j + 1 < i ? y : 0.f);
+                        *reinterpret_cast<float2*>(A + (warp < 2 ? 0 : 1 + (p >> 1)) * kABlock + (i & 31) * kAStride + (j & 31)) =
+                            make_float2(j < i ? x : 0.f, j + 1 < i ? y : 0.f);
                         unpair(mul2(mul2(pair(qk[t][2 * e], qk[t][2 * e + 1]), qa[e]), d), x, y);
-                        *reinterpret_cast<uint32_t*>(base + kPrepP + hh * kPBytes + swz(i, t) + 4 * (lane & 3)) =
-                            pack_f16x2(j <= i ? x : 0.f, j + 1 <= i ? y : 0.f);
+                        uint32_t hi, lo;
+                        split2(pair(j <= i ? x : 0.f, j + 1 <= i ? y : 0.f), hi, lo);
+                        uint8_t* P = base + kPrepP + hh * kTriBytes + 4 * (lane & 3);
+                        *reinterpret_cast<uint32_t*>(P + swz(i, t)) = hi;
+                        *reinterpret_cast<uint32_t*>(P + (warp < 2 ? swz(i, t + 4) : kTileBytes + swz(i, t))) = lo;
                     }
                 }
             }
@@ -449,15 +453,15 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + kPrepP + hh * kPBytes, kPBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes + kOffP, base_u + kPrepP + hh * kTriBytes, kTriBytes);
             bulk_commit();
         }
         // ---- (I + A)^-1 of the warp pair's head, in A's place
-        float* A = s_A + (warp >> 1) * kC * kAStride;
+        float* A = s_A + (warp >> 1) * 3 * kABlock;
         const int side = warp & 1;
         if (has) {
             // the diagonal's blocks 2 side and 2 side + 1, a column to a thread
-            float* D = A + (32 * side + (lane & 16)) * (kAStride + 1);
+            float* D = A + 2 * side * kABlock + (lane & 16) * (kAStride + 1);
             float x[16];
             solve<16>(D, lane & 15, x);
             __syncwarp();
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             for (int i = 0; i < 16; ++i) D[i * kAStride + (lane & 15)] = x[i];
             __syncwarp();
             // the pair of them: T21 = -T22 (A21 T11)
-            D = A + 32 * side * (kAStride + 1);
+            D = A + 2 * side * kABlock;
             float* A21 = D + 16 * kAStride;
             const float* T22 = A21 + 16;
             float y[2][4] = {}, z[2][4] = {};
@@ -486,7 +490,8 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         __syncthreads();
         {
             // the halves: rows 32 + 16 side .. of A21 T11 (T11's block above the diagonal is zero), then of -T22 times that
-            float* A21 = A + (32 + 16 * side) * kAStride;
+            float* A21 = A + kABlock + 16 * side * kAStride;
+            const float* T22 = A21 + kABlock;
             float y[4][4] = {};
             if (has) {
                 const Frag4 f0 = frag_a(A21, lane), f1 = frag_a(A21 + 16, lane);
@@ -502,13 +507,13 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             __syncthreads();
             float z[4][4] = {};
             if (has) {
-                const Frag4 f0 = frag_a(A21 + 32, lane);
+                const Frag4 f0 = frag_a(T22, lane);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) mma_pairs(z[t], f0, frag_b(A + 32 * kAStride + 8 * t, lane));
+                for (int t = 0; t < 4; ++t) mma_pairs(z[t], f0, frag_b(A + kABlock + 8 * t, lane));
                 if (side) {
-                    const Frag4 f1 = frag_a(A21 + 48, lane);
+                    const Frag4 f1 = frag_a(T22 + 16, lane);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) mma_pairs(z[t], f1, frag_b(A + 48 * kAStride + 8 * t, lane));
+                    for (int t = 0; t < 4; ++t) mma_pairs(z[t], f1, frag_b(A + kABlock + 16 * kAStride + 8 * t, lane));
                 }
             }
             __syncthreads();                         // both warps have read the product
@@ -528,7 +533,8 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     if (t > 4 * side + 3) continue;
-                    const float4 x = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t), y = *reinterpret_cast<const float4*>(A + i * kAStride + 8 * t + 4);
+                    const float* row = A + (side + (t >> 2)) * kABlock + (i & 31) * kAStride + 8 * (t & 3);
+                    const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + 4);
                     const float4 b0 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t), b1 = *reinterpret_cast<const float4*>(vec + 2 * kC + 8 * t + 4);
                     split2(mul2(mul2(pair(x.x, x.y), pair(b0.x, b0.y)), u), hi[t].x, lo[t].x);
                     split2(mul2(mul2(pair(x.z, x.w), pair(b0.z, b0.w)), u), hi[t].y, lo[t].y);
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             }
             __syncthreads();
             if (has) {
-                uint8_t* T = base + (warp >> 1) * kABytes;
+                uint8_t* T = base + (warp >> 1) * kTriBytes;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     if (t > 4 * side + 3) continue;
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         __syncthreads();
         if (tid == 0) {
             for (int hh = 0; hh < 2 && h0 + hh < rep; ++hh)
-                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * kABytes, kTBytes);
+                bulk_store(w.head + ((size_t)place * a.n_v + kh * rep + h0 + hh) * kHeadBytes, base_u + hh * kTriBytes, kTriBytes);
             bulk_commit();
             if (h0 + 2 < rep) bulk_wait_read();
         }
@@ -569,10 +575,10 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 // accumulator and written back as the next one's A operand, with no exchange at all.
 //   state warps (0-7)     two warps to 32 value dims, each with half the key dims and half the tokens:
 //                         S (FP32 registers) -> pair;  X^T = V^T - (S K^T) f -> pair;
-//                         V'^T -> pair with each token's decay, and once in FP16;  S = g S + D
+//                         V'^T -> pair with each token's decay, and pair without;  S = g S + D
 //   output warps (8-11)   O^T = (S Q^T) o + V'^T P^T, to the type, to rows of tokens
 //   warp 12               issues all products:  S K^T (hi, lo), S Q^T (hi, lo), V'^T = X^T T^T (hi hi, lo hi, hi lo),
-//                         D = V'^T K (hi, lo), V'^T P^T
+//                         D = V'^T K (hi, lo), V'^T P^T (hi hi, lo hi, hi lo)
 //   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
 // the first half of its operand is there, and S Q^T is issued behind V', while its pairs are
@@ -599,7 +605,7 @@ static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memo
 constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 240 us instead of 269)
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
-// products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without (FP16; for FP16 outputs hi, lo) lies where S K^T was, V' P^T
+// products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without lies where S K^T was, V' P^T
 // where V' was.
 constexpr uint32_t kTmS = 0, kTmKs = 128, kTmH = 128, kTmQs = 192, kTmX = 256, kTmV = 320, kTmPv = 320, kTmD = 384;
 // The quarters of an operand in the order in which they are there: each half's first, each half's second.  Two of them have a
@@ -688,7 +694,6 @@ __device__ void value_role(const Block& c, int lane) {
 
 // The whole warp runs this, and one elected lane issues, so that descriptors and addresses stay in uniform registers: a
 // 64-column product then takes 35 cycles; issued by a thread alone, 53, whatever its columns.
-template <int TYPE>
 __device__ void product_role(const Block& c) {
     // FP16 operands: the type fields (bits 7 to 12) zero
     constexpr uint32_t kTypes = ~((7u << 7) | (7u << 10));
@@ -752,7 +757,7 @@ __device__ void product_role(const Block& c) {
         if (!ok) break;
         tc::commit_elect(bar(c, BAR_V));
         with_queries(stage, 0);
-        if (TYPE == QSA_F16) with_queries(stage, 8);  // (BF16 outputs would not show it)
+        with_queries(stage, 8);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int b = quarter(n);
@@ -774,10 +779,12 @@ __device__ void product_role(const Block& c) {
             const uint64_t d = dkq0 + tri + ((kOffP + b * 32) >> 4);
             if (b < 2) {
                 product(c.tmem + kTmPv, at, d, id32, b, leader);
-                if (TYPE == QSA_F16) product(c.tmem + kTmPv, at + 32, d, id32, 1, leader);
+                product(c.tmem + kTmPv, at + 32, d, id32, 1, leader);
+                product(c.tmem + kTmPv, at, d + (64 >> 4), id32, 1, leader);
             }
             product(c.tmem + kTmPv + 32, at, d + (kTileBytes >> 4), id32, b, leader);
-            if (TYPE == QSA_F16) product(c.tmem + kTmPv + 32, at + 32, d + (kTileBytes >> 4), id32, 1, leader);
+            product(c.tmem + kTmPv + 32, at + 32, d + (kTileBytes >> 4), id32, 1, leader);
+            product(c.tmem + kTmPv + 32, at, d + (2 * kTileBytes >> 4), id32, 1, leader);
         }
         tc::commit_elect(bar(c, BAR_O));
         tc::commit_elect(bar(c, BAR_EMPTY + st));
@@ -959,9 +966,10 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         tc::fence_after_sync();
         const f2 vx2 = pair(vx, vx);
         {
-            uint32_t w[32], one[16], rest[16];
+            uint32_t w[32];
             tc::tmem_ld32(tmT + kTmV, w);
             tc::tmem_wait_ld();
+            // with decays first: the chain waits for them
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 uint32_t hi[8], lo[8];
@@ -969,26 +977,19 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 for (int j = 0; j < 8; j += 2) {
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scal + kScalD + 16 * b + 2 * j);
                     const uint32_t* k = w + 16 * b + 2 * j;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const f2 p = mul2(vx2, pair_of(k[2 * u], k[2 * u + 1]));
-                        if (TYPE == QSA_F16) {
-                            split2(p, one[8 * b + j + u], rest[8 * b + j + u]);
-                        } else {
-                            float x, y;
-                            unpair(p, x, y);
-                            one[8 * b + j + u] = pack_f16x2(x, y);
-                        }
-                        split2(mul2(p, u ? f.y : f.x), hi[j + u], lo[j + u]);
-                    }
+                    split2(mul2(mul2(vx2, pair_of(k[0], k[1])), f.x), hi[j], lo[j]);
+                    split2(mul2(mul2(vx2, pair_of(k[2], k[3])), f.y), hi[j + 1], lo[j + 1]);
                 }
                 tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
                 tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
                 tc::tmem_wait_st();
                 tell(c, BAR_D + b);
             }
+            uint32_t one[16], rest[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) split2(mul2(vx2, pair_of(w[2 * j], w[2 * j + 1])), one[j], rest[j]);
             tc::tmem_st16(tm + kTmH + 16 * half, one);
-            if (TYPE == QSA_F16) tc::tmem_st16(tm + kTmH + 32 + 16 * half, rest);
+            tc::tmem_st16(tm + kTmH + 32 + 16 * half, rest);
             tc::tmem_wait_st();
         }
         tell(c, BAR_H);
@@ -1269,7 +1270,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         else output_role<TYPE, false>(c, warp - 8, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 12) product_role<TYPE>(c);
+        if (warp == 12) product_role(c);
         else if (warp == 13) copy_role(c, lane);
         else if (warp == 14 && !(SPLIT && c.kind == 2)) value_role(c, lane);
     }
@@ -1287,6 +1288,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
 // and head.  A warp has 16 state rows, as accumulators of m16n8k16, which are the next product's A operand as they lie.
 constexpr int kJoinThreads = 256;
 constexpr uint32_t kRBytes = kHeadDim * kHeadDim * 2, kJoinBytes = 2 * kRBytes + 64 + 1024;
+static_assert(2 * kRBytes == kStateFloats * 4, "a state as pairs in its own place");
+// 1 / the units of the rows of S before segment g, of a sequence and head: where the first segment's R would be, which has none.
+__device__ __forceinline__ float* units_of(const Split& w, size_t item, int g) { return w.turns + item * kSplitMost * kStateFloats + g * kHeadDim; }
+static_assert(kSplitMost * kHeadDim <= kStateFloats, "the units' place");
 
 __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ DeltaArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -1339,17 +1344,21 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             unit[e] = unit_of(m);
         }
-        // S before segment g for delta_add_kernel, in its place: FP16 in units as that one's tile, then 1 / the units
+        // S before segment g for delta_add_kernel, in its place: pairs of FP16 in units as that one's tiles, hi, then lo
         uint8_t* image = reinterpret_cast<uint8_t*>(w.ends + (item + g - 1) * kStateFloats);
 #pragma unroll
         for (int t = 0; t < 16; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint32_t*>(image + (t >> 3) * (kHeadDim * 128) + swz(row + 8 * e, t & 7) + 4 * (lane & 3)) =
-                    pack_f16x2(s[t][2 * e] * unit[e], s[t][2 * e + 1] * unit[e]);
+            {
+                uint32_t hi, lo;
+                split2(mul2(pair(s[t][2 * e], s[t][2 * e + 1]), pair(unit[e], unit[e])), hi, lo);
+                uint32_t* at = reinterpret_cast<uint32_t*>(image + (t >> 3) * (kHeadDim * 128) + swz(row + 8 * e, t & 7) + 4 * (lane & 3));
+                at[0] = hi, at[kRBytes / 4] = lo;
+            }
         if ((lane & 3) == 0) {
-            reinterpret_cast<float*>(image + kHeadDim * kHeadDim * 2)[row] = 1.f / unit[0];
-            reinterpret_cast<float*>(image + kHeadDim * kHeadDim * 2)[row + 8] = 1.f / unit[1];
+            float* units = units_of(w, blockIdx.x, g);
+            units[row] = 1.f / unit[0], units[row + 8] = 1.f / unit[1];
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
@@ -1401,14 +1410,14 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
 }
 
 // The outputs of segments behind the first: from zeros, plus scale (S before the segment) (R_t q_t).  A block takes
-// kAddChunks consecutive chunks of a sequence and head: tokens by value dims, S in shared memory as FP16 with a power of two
-// for each row (as delta_join_kernel left it), the tokens' R_t q_t likewise.
-constexpr int kAddThreads = 256, kAddChunks = 2;
-constexpr uint32_t kAddS = 0, kAddT = kHeadDim * kHeadDim * 2, kAddUnit = kAddT + kC * kHeadDim * 2;
+// kAddChunks consecutive chunks of a sequence and head: tokens by value dims, S in shared memory as pairs of FP16 with a power
+// of two for each row (as delta_join_kernel left it), the tokens' R_t q_t likewise.
+constexpr int kAddThreads = 256, kAddChunks = 4;
+constexpr uint32_t kAddS = 0, kAddT = 2 * kRBytes, kAddTlo = kC * kHeadDim * 2, kAddUnit = kAddT + 2 * kAddTlo;
 constexpr uint32_t kAddBytes = kAddUnit + (kHeadDim + kC) * 4 + 1024;
 
 template <int TYPE>
-__global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_constant__ DeltaArgs a, const int groups) {
+__global__ void __launch_bounds__(kAddThreads, 2) delta_add_kernel(const __grid_constant__ DeltaArgs a, const int groups) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u = smem_u32(smem_raw), base_u = (raw_u + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_u - raw_u);
@@ -1438,7 +1447,7 @@ __global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_
                 const uint32_t at = 16 * (tid + i * kAddThreads);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base_u + kAddS + at), "l"(S + at) : "memory");
             }
-            if (tid < kHeadDim) s_unit[tid] = reinterpret_cast<const float*>(S + kAddT)[tid];
+            if (tid < kHeadDim) s_unit[tid] = units_of(w, item, g)[tid];
         }
         // R_t q_t of eight tokens of a warp (every eighth), a lane's four elements of each: the largest, the unit, FP16; zeros
         // from the sequence's end on
@@ -1454,8 +1463,12 @@ __global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float unit = unit_of(m);
-            *reinterpret_cast<uint2*>(base + kAddT + (lane >> 4) * (kC * 128) + swz(r, (lane & 15) >> 1) + 8 * (lane & 1)) =
-                make_uint2(pack_f16x2(x[i].x * unit, x[i].y * unit), pack_f16x2(x[i].z * unit, x[i].w * unit));
+            uint2 hi, lo;
+            split2(mul2(pair(x[i].x, x[i].y), pair(unit, unit)), hi.x, lo.x);
+            split2(mul2(pair(x[i].z, x[i].w), pair(unit, unit)), hi.y, lo.y);
+            uint8_t* at = base + kAddT + (lane >> 4) * (kC * 128) + swz(r, (lane & 15) >> 1) + 8 * (lane & 1);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + kAddTlo) = lo;
             if (lane == 0) s_unit[kHeadDim + r] = 1.f / unit;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1479,13 +1492,21 @@ __global__ void __launch_bounds__(kAddThreads, 3) delta_add_kernel(const __grid_
             for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            uint32_t f[4], b[4];
-            ldmatrix4(base_u + kAddT + (k >> 2) * (kC * 128) + swz(m0 + (lane & 15), 2 * (k & 3) + (lane >> 4)), f);
+            uint32_t f[4], fl[4], b[4], bl[4];
+            const uint32_t at = base_u + kAddT + (k >> 2) * (kC * 128) + swz(m0 + (lane & 15), 2 * (k & 3) + (lane >> 4));
+            ldmatrix4(at, f);
+            ldmatrix4(at + kAddTlo, fl);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                ldmatrix4(base_u + kAddS + (k >> 2) * (kHeadDim * 128) + swz(n0 + 16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * (k & 3) + ((lane >> 3) & 1)), b);
-                mma16816(acc[2 * t], f, b[0], b[1]);
-                mma16816(acc[2 * t + 1], f, b[2], b[3]);
+                const uint32_t rows = base_u + kAddS + (k >> 2) * (kHeadDim * 128) + swz(n0 + 16 * t + (lane & 7) + ((lane >> 4) << 3), 2 * (k & 3) + ((lane >> 3) & 1));
+                ldmatrix4(rows, b);
+                ldmatrix4(rows + kRBytes, bl);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    mma16816(acc[2 * t + u], f, b[2 * u], b[2 * u + 1]);
+                    mma16816(acc[2 * t + u], fl, b[2 * u], b[2 * u + 1]);
+                    mma16816(acc[2 * t + u], f, bl[2 * u], bl[2 * u + 1]);
+                }
             }
         }
         __syncthreads();                             // R_t q_t has been read: the outputs in its place, then out by rows
