@@ -383,7 +383,10 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
  *     nowhere falling; qsa_extend_tables writes it).  n_tok is what the token arrays
  *     hold; tokens from cu_tokens[n_seq] on belong to nobody: nothing of theirs is
  *     used, and their rows of the outputs stay as they are.  Bounds that fall or lie
- *     outside [0, n_tok] are clamped and reported (QSA_DEV_BAD_SEQ_LEN).
+ *     outside [0, n_tok] are clamped and reported (QSA_DEV_BAD_SEQ_LEN).  Where they
+ *     fall, sequences may come to share tokens: which one's rows these end as is not
+ *     specified, and qsa_delta_prompt leaves out those of more than 32 tokens whose
+ *     bounds are out of order with another's.
  *   - state_slots: int32 [n_seq], the sequence's place in the state pool, or < 0: the
  *     sequence is left out, nothing of it is read and its rows of the outputs stay
  *     as they are (padding of a batch).  A slot past the pool is treated alike and

@@ -61,6 +61,19 @@ __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
     return Blobs{a.workspace, a.workspace + places(a.n_tok, a.n_seq) * a.n_k * kKqBytes};
 }
 
+// Whether sequence s, of tokens [span.x, span.y), lies behind all earlier sequences' bounds and before all later ones' (by the
+// whole block).  Where bounds fall, sequences can share tokens and places; those that pass here share none, and are the ones
+// that delta_prep_kernel finds for their places.  The others are left out.
+__device__ __forceinline__ bool in_order(const DeltaArgs& a, int s, int2 span) {
+    if (a.n_seq == 1) return true;
+    bool off = false;
+    for (int i = threadIdx.x; i <= a.n_seq; i += blockDim.x) {
+        const int b = min(max(a.cu_tokens[i], 0), a.n_tok);
+        off = off || (i < s ? b > span.x : i > s + 1 && b < span.y);
+    }
+    return !__syncthreads_or(off);
+}
+
 // ---------------------------------------------------------------- segments
 // A state row's way through a chunk is linear in the row: S' = S R + (what the chunk's values add).  Where there are fewer
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
@@ -1187,6 +1200,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         wait_for_stream();
         return;
     }
+    if (!in_order(a, c.s, span)) {
+        wait_for_stream();
+        return;
+    }
     c.fresh = a.old_lens && a.old_lens[c.s] <= 0;
     float* pool = a.state + ((size_t)c.slot * a.n_v + c.h) * kStateFloats;
     const int chunks = (span.y - span.x + kC - 1) / kC;
@@ -1304,7 +1321,7 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
     const int slot = a.state_slots[sq];
     const int2 span = tokens_of(a.cu_tokens, sq, a.n_tok);
     const int chunks = (span.y - span.x + kC - 1) / kC, segments = segments_of(chunks, a.n_split);
-    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from) return;
+    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from || !in_order(a, sq, span)) return;
     const Split w = split_of(a);
     const size_t item = (size_t)blockIdx.x * kSplitMost;
     const int row = 16 * warp + (lane >> 2), col = 2 * (lane & 3);
@@ -1430,7 +1447,7 @@ __global__ void __launch_bounds__(kAddThreads, 2) delta_add_kernel(const __grid_
     const int slot = a.state_slots[sq];
     const int2 span = tokens_of(a.cu_tokens, sq, a.n_tok);
     const int chunks = (span.y - span.x + kC - 1) / kC, segments = segments_of(chunks, a.n_split);
-    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from) return;
+    if (slot < 0 || slot >= a.n_slots || segments < 2 || span.y - span.x < a.chunked_from || !in_order(a, sq, span)) return;
     const int each = (chunks + segments - 1) / segments;
     const Split w = split_of(a);
     const size_t apart = (size_t)a.n_v * kHeadDim;
