@@ -616,6 +616,7 @@ constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
 constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 240 us instead of 269)
+static_assert(kSplitSms <= kRanked, "where sequences are cut, their order is looked at with their lengths");
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
 // products are added.  X and, after V' is formed, V' with decays: hi, lo.  V' without lies where S K^T was, V' P^T
@@ -1170,21 +1171,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     const unsigned heads = (unsigned)a.n_seq * (unsigned)a.n_v, part = SPLIT ? blockIdx.x / heads : 0u, item = blockIdx.x - part * heads;
     c.s = (int)(item / (unsigned)a.n_v);
     c.h = (int)(item - (unsigned)c.s * (unsigned)a.n_v);
+    bool ordered = true;
     if (a.n_seq > 1 && a.n_seq <= kRanked) {
-        // the longest sequences first: block b's is the one of which c.s are longer (or as long, and before it)
-        int* lens = reinterpret_cast<int*>(c.base + kOffOut);         // (no bulk copy ever writes there)
-        for (int i = tid; i < a.n_seq; i += kChunkThreads) {
-            const int2 t = tokens_of(a.cu_tokens, i, a.n_tok);
-            lens[i] = t.y - t.x;
-        }
+        // the longest sequences first: block b's is the one of which c.s are longer (or as long, and before it); and whether it is
+        // in order with all others, as in_order has it
+        int* bounds = reinterpret_cast<int*>(c.base + kOffOut);       // (no bulk copy ever writes there)
+        for (int i = tid; i <= a.n_seq; i += kChunkThreads) bounds[i] = min(max(a.cu_tokens[i], 0), a.n_tok);
         __syncthreads();
         for (int i = tid; i < a.n_seq; i += kChunkThreads) {
-            int rank = 0;
-            for (int j = 0; j < a.n_seq; ++j) rank += lens[j] > lens[i] || (lens[j] == lens[i] && j < i) ? 1 : 0;
-            if (rank == c.s) lens[kRanked] = i;
+            const int first = bounds[i], end = max(bounds[i + 1], first);
+            int rank = 0, off = 0;
+            for (int j = 0, at = bounds[0]; j < a.n_seq; ++j) {
+                const int next = bounds[j + 1], len = max(next - at, 0);
+                rank += len > end - first || (len == end - first && j < i) ? 1 : 0;
+                off += j < i ? at > first : j > i && next < end;
+                at = next;
+            }
+            if (rank == c.s) bounds[kRanked + 1] = off ? -1 - i : i;
         }
         __syncthreads();
-        c.s = lens[kRanked];
+        c.s = bounds[kRanked + 1];
+        ordered = c.s >= 0;
+        c.s = ordered ? c.s : -1 - c.s;
         __syncthreads();
     }
     // Behind delta_prep_kernel this kernel is released when all of that one's blocks have passed their own
@@ -1196,11 +1204,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
         if (tokens_bad(a.cu_tokens, c.s, a.n_tok)) report(a.dev_status, QSA_DEV_BAD_SEQ_LEN);
         if (c.slot >= a.n_slots) report(a.dev_status, QSA_DEV_BAD_STATE);
     }
-    if (c.slot < 0 || c.slot >= a.n_slots || span.y - span.x < a.chunked_from) {
-        wait_for_stream();
-        return;
-    }
-    if (!in_order(a, c.s, span)) {
+    if (c.slot < 0 || c.slot >= a.n_slots || span.y - span.x < a.chunked_from || !ordered ||
+        (!SPLIT && a.n_seq > kRanked && !in_order(a, c.s, span))) {      // (segments: fewer sequences than SMs)
         wait_for_stream();
         return;
     }
