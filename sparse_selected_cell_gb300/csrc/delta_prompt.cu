@@ -15,8 +15,9 @@
 // (exact but for elements below 2^-24 of the row's largest, which lose bits); their lengths, 1 / |k|, are factors of
 // columns and rows in FP32.  The state, X, V', T and P are pairs of FP16, hi + lo (22 bits), in
 // products of which lo lo is left out; the state itself stays in FP32.  All products
-// are summed in FP32.  The pairs of a value dim share a power of two, chosen from bounds that
-// the rule gives (a chunk lengthens a state row by its values' sum at most), so that nothing
+// are summed in FP32.  The pairs of a value dim and chunk share a power of two (S, X, V' and V' as it is
+// left at the chunk's end each their own), chosen from bounds that the rule gives (a chunk lengthens a state row by its values'
+// sum at most) with the decays of the gates, so that nothing
 // passes FP16's range and what counts stays in its upper bits.  (Products that end in outputs of
 // single FP16, S Q^T without the state's lo, cost outputs 2^-12 of their row's length: 12 x 4,096
 // 782 us instead of 825, 1 x 8,192 292 instead of 327.)
@@ -47,8 +48,10 @@ constexpr uint32_t kTileBytes = kC / 2 * 128, kTriBytes = 3 * kTileBytes;
 constexpr uint32_t kOffP = kTriBytes, kOffScal = 2 * kTriBytes;
 constexpr uint32_t kHeadBytes = kOffScal + 1024;     // T, P, the factors of each token
 constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 at most, are stored times this
-// -exp(G) / |k|, exp(G_C - G) / |k| times the chunk's key unit, exp(G) / |q|, of 64 tokens each; then exp(G_C) and the key unit
-constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1;
+// -exp(G) / |k|, exp(G_C - G) / |k| times the chunk's key unit, exp(G) / |q|, of 64 tokens each; then exp(G_C), the key unit and
+// exp(G) of the first token; then exp(G_C - G) of 64 tokens in the call's type, rounded up
+constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1, kScalFirst = kScalG + 2, kScalE = kScalG + 4;
+static_assert((kScalE + kC / 2) * 4 <= 1024, "the factors' place");
 
 __device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
 
@@ -146,6 +149,28 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint
     asm volatile("{\n .reg .pred e, t;\n setp.ne.b32 e, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, t;\n}"
                  ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(leader), "r"(add) : "memory");
+}
+
+// A factor of at most 1 in the call's type, nowhere below what it was (FP16's smallest for what is below that).
+template <int TYPE>
+__device__ __forceinline__ uint16_t rounded_up(float x) {
+    if (TYPE == QSA_F16) return max(__half_as_ushort(__float2half_ru(x)), (unsigned short)1);
+    return __bfloat16_as_ushort(__float2bfloat16_ru(x));
+}
+// Two values of the call's type at once: the one of larger magnitude (the sign is of no use), and products.
+template <int TYPE>
+__device__ __forceinline__ uint32_t larger2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    if (TYPE == QSA_F16) asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    else asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t times2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    if (TYPE == QSA_F16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
 }
 
 // x and y as FP16 pairs: hi the nearest, lo the nearest of what is left (x - hi is exact).
@@ -421,7 +446,8 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
             scal[kScalF + tt] = -vec[3 * kC + tt] * s_r[tt];
             scal[kScalD + tt] = vec[4 * kC + tt] * (s_r[tt] * key_unit);
             scal[kScalO + tt] = vec[3 * kC + tt] * s_r[kC + tt];
-            if (tt == kC - 1) scal[kScalG] = vec[3 * kC + tt], scal[kScalU] = key_unit;
+            if (tt == kC - 1) scal[kScalG] = vec[3 * kC + tt], scal[kScalU] = key_unit, scal[kScalFirst] = vec[3 * kC];
+            reinterpret_cast<uint16_t*>(scal + kScalE)[tt] = rounded_up<TYPE>(vec[4 * kC + tt]);
         }
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
@@ -608,10 +634,11 @@ constexpr uint32_t kOffV = kStages * kStageBytes;
 constexpr uint32_t kOffOut = kOffV + kVStages * kVBytes;             // [output warp][token][32 dims]
 constexpr uint32_t kOffPow = kOffOut + 4 * kC * 64;                  // [chunk & 1][value dim]: 1 / the units of S Q^T and of V' P^T
 constexpr uint32_t kOffTop = kOffPow + 2 * kHeadDim * 8;             // [chunk & 1][half][value dim]: largest value; then largest of S
-constexpr uint32_t kOffBar = kOffTop + 2 * 2 * 2 * kHeadDim * 4;
+constexpr uint32_t kOffDec = kOffTop + 2 * 2 * 2 * kHeadDim * 4;     // [half][value dim], the call's type: largest value with its decay
+constexpr uint32_t kOffBar = kOffDec + 2 * kHeadDim * 2;
 enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kStages, BAR_VEMPTY = BAR_VFULL + kVStages,
        BAR_S = BAR_VEMPTY + kVStages, BAR_X = BAR_S + 2, BAR_D = BAR_X + 2, BAR_TOP = BAR_D + 2, BAR_KS = BAR_TOP + 4,
-       BAR_V, BAR_U, BAR_H, BAR_O, BAR_OFREE, BAR_DRAIN, NUM_BARS };
+       BAR_V, BAR_U, BAR_H, BAR_O, BAR_OFREE, BAR_DRAIN, BAR_DEC, NUM_BARS = BAR_DEC + 4 };
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
@@ -808,27 +835,35 @@ __device__ void product_role(const Block& c) {
     if (!tc::mbar_wait_drain(bar(c, BAR_DRAIN), 0, kWaitNs)) report(c.a->dev_status, QSA_DEV_WAIT_TIMEOUT);
 }
 
-// This thread's value dim of half a chunk's values, two tokens to a word, and the largest of them.
-template <int TYPE>
-__device__ __forceinline__ float read_values(const uint8_t* values, int half, int r, uint32_t (&v)[16]) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(values) + half * (kC / 2) * kHeadDim + r;
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const uint32_t x = p[(2 * j) * kHeadDim], y = p[(2 * j + 1) * kHeadDim];
-        v[j] = x | (y << 16);
-        m = fmax3(m, fabsf(to_f32((uint16_t)x, TYPE)), fabsf(to_f32((uint16_t)y, TYPE)));
-    }
-    return m;
-}
 template <int TYPE>
 __device__ __forceinline__ void both(uint32_t w, float& x, float& y) {
     x = to_f32((uint16_t)(w & 0xFFFFu), TYPE);
     y = to_f32((uint16_t)(w >> 16), TYPE);
 }
+template <int TYPE>
+__device__ __forceinline__ float larger_of(uint32_t w) {
+    float x, y;
+    both<TYPE>(w, x, y);
+    return fmaxf(fabsf(x), fabsf(y));
+}
+// This thread's value dim of half a chunk's values, two tokens to a word, and the largest of them.
+template <int TYPE>
+__device__ __forceinline__ float read_values(const uint8_t* values, int half, int r, uint32_t (&v)[16]) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(values) + half * (kC / 2) * kHeadDim + r;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t x = p[(2 * j) * kHeadDim], y = p[(2 * j + 1) * kHeadDim];
+        v[j] = x | (y << 16);
+        m = larger2<TYPE>(m, v[j]);
+    }
+    return larger_of<TYPE>(m);
+}
 
 // 2^(14 - e) for x in [2^e, 2^(e+1)): what brings x below 2^15.
 __device__ __forceinline__ float unit_of(float x) { return exp2i(14 - max(f32_exponent(x), -80)); }
+// 1 / x for a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse(float x) { return __uint_as_float(0x7F000000u - __float_as_uint(x)); }
 
 template <int TYPE, bool SPLIT>
 __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
@@ -880,32 +915,28 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
             tc::mbar_arrive(bar(c, BAR_TOP + q));
         }
     };
-    // The powers of two of chunk i, from bounds: the state row's length before it by the largest element one chunk earlier (12)
-    // and that chunk's values; |x| <= |v| + |S|; |v'| <= |v| + |S| + the values before it, and no state row gets longer than
-    // that.  Then the chunk's values in units.
-    float d_up = 1.f, vm_before = 0.f;               // 1 / the unit of D, the largest value of the chunk before
-    float unit = 1.f, v_unit = 1.f;                  // of S and X; of V'
-    f2 x2[16];
+    // The powers of two of chunk i, one each for S, X, V' and D, from bounds, all with the decays that the gates give: the state
+    // row's length before the chunk by its largest element one chunk earlier (12) and that chunk's values, both as far as they
+    // are left at that chunk's end; |x| <= |v| + |S|, the state from its first token on; |v'| <= that + the values before it; with
+    // its decay to the chunk's end, |S| and values as they are left there.  (What the gates have forgotten has no say from the next
+    // chunk on; within the chunk that forgets it X and V' hold what is below 2^-14 of it with fewer bits, below 2^-38 with none.
+    // With one unit for S and X, from bounds without decays, 12 x 4,096 tokens took 810 us instead of 854, and what was forgotten
+    // cost the chunk behind it its bits.)
+    float d_up = 1.f;                                // 1 / the unit of D
+    float len = 0.f, s_unit = 1.f;                   // of the state row before the chunk
+    float g_tot = 1.f, v_dec = 0.f;                  // of the chunk before: the decay of all of it, the largest value with its decay
+    // (units no more than 2^100 finer than what they come from: factors from one to the next stay finite, 2^116 at
+    // most with the key unit; from 1, where the first chunk's state is, nothing is cut)
     auto settle = [&](int i) {
         const int par = i & 1;
         if (!wait(c, BAR_TOP + q, par)) return false;
         vm = fmaxf(vm, top_v[par * 256 + (half ^ 1) * 128]);
         sm = fmaxf(sm, top_s[(par ^ 1) * 256 + (half ^ 1) * 128]);
-        const float len = fmaf(12.f, sm, 66.f * vm_before);
-        // (no more than 2^100 finer than the chunk before's: its results are brought to them by a factor that stays finite, 2^116 at
-        // most with the key unit; from 1, where the first chunk's state is, nothing is cut)
-        const float finest = 0x1p100f / d_up;
-        unit = fminf(unit_of(len + vm), finest), v_unit = fminf(unit_of(fmaf(66.f, vm, len)), finest);
-        vm_before = vm;
-        const f2 unit2 = pair(unit, unit);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            float x, y;
-            both<TYPE>(v[j], x, y);
-            x2[j] = mul2(pair(x, y), unit2);
-        }
+        len = fmaf(12.f * g_tot, sm, 66.f * v_dec);
+        s_unit = fminf(unit_of(len), 0x1p100f * inverse(d_up));
         return true;
     };
+    uint16_t* dec = reinterpret_cast<uint16_t*>(c.base + kOffDec) + r;       // + 128 half
     top_s[256 + half * 128] = sm;
     publish(0);
     if (!settle(0)) return;
@@ -913,7 +944,7 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         const int st = i % kStages, par = i & 1;
         const float* scal = reinterpret_cast<const float*>(c.base + st * kStageBytes + kKqBytes + kOffScal) + 32 * half;
         // ---- the state as the next operand
-        const f2 s2 = pair(unit * d_up, unit * d_up);
+        const f2 s2 = pair(s_unit * d_up, s_unit * d_up);
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
             uint32_t d[32];
@@ -929,9 +960,38 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
             tc::tmem_wait_st();
             tell(c, BAR_S + b);
         }
-        if (half == 0) pows[par * kHeadDim] = make_float2(1.f / unit, 1.f / (v_unit * kTriUnit));
+        // ---- while S K^T is formed: the units of X and V', the values in X's, and the largest of them with its decay
+        if (!wait(c, BAR_FULL + st, (i / kStages) & 1)) return;
+        g_tot = scal[kScalG - 32 * half];
+        const float seen = scal[kScalFirst - 32 * half] * len;
+        const float unit = fminf(unit_of(vm + seen), 0x1p100f * s_unit), v_unit = fminf(unit_of(fmaf(66.f, vm, seen)), unit);
+        if (half == 0) pows[par * kHeadDim] = make_float2(inverse(s_unit), inverse(v_unit * kTriUnit));
+        f2 x2[16];
+        uint32_t md = 0u;
+        {
+            const uint4* decays = reinterpret_cast<const uint4*>(scal + kScalE - 16 * half);
+            const f2 unit2 = pair(unit, unit);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint4 w = decays[b];
+                const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float x, y;
+                    both<TYPE>(v[4 * b + j], x, y);
+                    x2[4 * b + j] = mul2(pair(x, y), unit2);
+                    md = larger2<TYPE>(md, times2<TYPE>(v[4 * b + j], e[j]));
+                }
+            }
+        }
+        md = larger2<TYPE>(md, md >> 16);
+        dec[half * kHeadDim] = (uint16_t)(md & 0x7FFFu);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar(c, BAR_DEC + q));
         // ---- X = V - f (S K^T)
-        if (!wait(c, BAR_FULL + st, (i / kStages) & 1) || !wait(c, BAR_KS, par)) return;
+        const float up = unit * inverse(s_unit);
+        const f2 up2 = pair(up, up);
+        if (!wait(c, BAR_KS, par)) return;
         tc::fence_after_sync();
         {
             uint32_t ks[32];
@@ -944,8 +1004,8 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 for (int j = 0; j < 8; j += 2) {
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scal + kScalF + 16 * b + 2 * j);
                     const uint32_t* k = ks + 16 * b + 2 * j;
-                    split2(fma2(f.x, pair_of(k[0], k[1]), x2[8 * b + j]), hi[j], lo[j]);
-                    split2(fma2(f.y, pair_of(k[2], k[3]), x2[8 * b + j + 1]), hi[j + 1], lo[j + 1]);
+                    split2(fma2(mul2(f.x, up2), pair_of(k[0], k[1]), x2[8 * b + j]), hi[j], lo[j]);
+                    split2(fma2(mul2(f.y, up2), pair_of(k[2], k[3]), x2[8 * b + j + 1]), hi[j + 1], lo[j + 1]);
                 }
                 tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
                 tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
@@ -954,7 +1014,11 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
             }
         }
         // ---- while V' is formed: the decayed state for D, and its largest element
-        const float d_unit = v_unit * scal[kScalU - 32 * half], gd = scal[kScalG - 32 * half] * (d_unit * d_up);
+        if (!wait(c, BAR_DEC + q, par)) return;
+        // (FP16 products round to 2^-25 at the nearest)
+        v_dec = larger_of<TYPE>(md & 0x7FFFu | (uint32_t)dec[(half ^ 1) * kHeadDim] << 16) + (TYPE == QSA_F16 ? 0x1p-24f : 0.f);
+        const float dv_unit = fminf(unit_of(fmaf(g_tot, len, 66.f * v_dec)), 0x1p100f * fminf(unit, inverse(d_up)));
+        const float d_unit = dv_unit * scal[kScalU - 32 * half], gd = g_tot * (d_unit * d_up);
         const f2 g2 = pair(gd, gd);
         sm = 0.f;
 #pragma unroll 1
@@ -973,12 +1037,12 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
         }
         sm *= d_up;
         top_s[par * 256 + half * 128] = sm;
-        d_up = 1.f / d_unit;
-        const float vx = v_unit / unit * (1.f / kTriUnit);
+        d_up = inverse(d_unit);
+        const float down = inverse(unit) * (1.f / kTriUnit), vx = v_unit * down, dx = dv_unit * down;
         // ---- V', with each token's decay to the chunk's end
         if (!wait(c, BAR_V, par)) return;
         tc::fence_after_sync();
-        const f2 vx2 = pair(vx, vx);
+        const f2 vx2 = pair(vx, vx), dx2 = pair(dx, dx);
         {
             uint32_t w[32];
             tc::tmem_ld32(tmT + kTmV, w);
@@ -991,8 +1055,8 @@ __device__ void state_role(const Block& c, int half, int r, uint32_t lanes) {
                 for (int j = 0; j < 8; j += 2) {
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scal + kScalD + 16 * b + 2 * j);
                     const uint32_t* k = w + 16 * b + 2 * j;
-                    split2(mul2(mul2(vx2, pair_of(k[0], k[1])), f.x), hi[j], lo[j]);
-                    split2(mul2(mul2(vx2, pair_of(k[2], k[3])), f.y), hi[j + 1], lo[j + 1]);
+                    split2(mul2(mul2(dx2, pair_of(k[0], k[1])), f.x), hi[j], lo[j]);
+                    split2(mul2(mul2(dx2, pair_of(k[2], k[3])), f.y), hi[j + 1], lo[j + 1]);
                 }
                 tmem_st8(tm + kTmX + 16 * half + 8 * b, hi);
                 tmem_st8(tm + kTmX + 32 + 16 * half + 8 * b, lo);
@@ -1262,6 +1326,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
                 tc::mbar_init(bar(c, BAR_D + b), 8);
             }
             tc::mbar_init(bar(c, BAR_TOP + b), 2);
+            tc::mbar_init(bar(c, BAR_DEC + b), 2);
         }
         tc::mbar_init(bar(c, BAR_KS), 1);
         tc::mbar_init(bar(c, BAR_V), 1);
