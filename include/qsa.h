@@ -490,7 +490,8 @@ int qsa_delta_step(const void* q, int64_t q_stride, const void* k, int64_t k_str
  *     equal strides; otherwise it must not overlap them.
  *   - weight, bias: [size], or [n_groups][size] when per_group, or NULL (ones,
  *     zeros), of w_type: `type` or QSA_F32, 16-byte aligned.
- *   - eps >= 0. */
+ *   - eps >= 0.  Squares are summed in FP32 as they are: x - m of magnitudes up to 2^57;
+ *     without an eps that outweighs them, their root mean square no less than 2^-60. */
 int qsa_group_norm(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, int32_t type,
                    const void* weight, const void* bias, int32_t w_type, int32_t per_group, int32_t n_tok,
                    int32_t n_groups, int32_t size, float eps, int32_t centred, int32_t activation, void* out,
