@@ -388,9 +388,10 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
  *     specified, and qsa_delta_prompt leaves out those of more than 32 tokens whose
  *     bounds are out of order with another's.
  *   - state_slots: int32 [n_seq], the sequence's place in the state pool, or < 0: the
- *     sequence is left out, nothing of it is read and its rows of the outputs stay
- *     as they are (padding of a batch).  A slot past the pool is treated alike and
- *     reported (QSA_DEV_BAD_STATE).  Slots >= 0 must be distinct.
+ *     sequence is left out, nothing of it is used and its rows of the outputs stay
+ *     as they are (padding of a batch; its tokens' rows exist all the same and may be
+ *     read).  A slot past the pool is treated alike and reported (QSA_DEV_BAD_STATE).
+ *     Slots >= 0 must be distinct.
  *   - old_lens: int32 [n_seq], how many tokens the sequence had before this step
  *     (qsa_extend_tables' seq_lens).  Where it is <= 0 the state starts from zeros
  *     and the pool's contents are not read.  NULL: every sequence goes on.
