@@ -447,7 +447,8 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
  *     sqrt(eps) count as zeros, and what short ones add to the state is lost below
  *     2^-28 of their chunk's values).  Token by token their squares are summed in FP32 as
  *     they are (lengths from 2^-60 to 2^60).  A row of zeros needs eps > 0.  NaN and
- *     infinities stay in their sequence.
+ *     infinities stay in their sequence; by chunks they spoil all of their chunk of 64
+ *     tokens, earlier ones too (a value's own value dim alone).
  *   - By chunks, a value dim's new values of a chunk of 64 tokens share a power of two
  *     with the largest value in the chunk and with the state row that its first token
  *     leaves.  What the gates forget within a chunk leaves errors of 2^-30 of it in
