@@ -457,8 +457,11 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
  *     chunk's end or by its first token leaves none.
  *   - state and workspace must not overlap any other argument.
  *   - workspace: device memory of at least qsa_delta_prompt_workspace_bytes(n_tok,
- *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept: about
- *     512 n_k + 400 n_v bytes a token, and 1024 n_v more where segments may be cut.
+ *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept:
+ *     32,768 n_k + 25,600 n_v bytes for each of n_tok / 64 + n_seq chunks, or for each of
+ *     n_tok / 32 in a step of several sequences if those are fewer; where segments may
+ *     be cut 1,024 n_v bytes a token and 1 MB n_seq n_v more; 256 bytes for up to 32
+ *     tokens.
  *     Two calls that can overlap on the device need one each, captured ones too.
  *   - n_seq == 0 returns QSA_OK with no launch. */
 int qsa_delta_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -40,7 +40,9 @@ constexpr int kC = 64;                               // tokens of a chunk
 
 // ---------------------------------------------------------------- workspace
 // Chunk c of sequence s has place first / 64 + s + c, first being the sequence's first token:
-// places never meet, and none passes n_tok / 64 + n_seq.
+// places never meet, and none passes n_tok / 64 + n_seq.  In a step of several sequences only
+// those of more than 32 tokens have chunks; there first / 32 + c will do as well, which ends at
+// n_tok / 32: the smaller of the two is taken.
 constexpr uint32_t kKqBytes = 2 * kC * kHeadDim * 2; // keys, then queries: two 64-dim halves of 128 rows, 128-byte swizzle
 // T and P are lower triangular, pairs of FP16, as tiles of 32 rows of 128 bytes, 128-byte swizzle: rows 0 to 31, whose second
 // half is zero, one tile for both, hi and lo side by side; rows 32 to 63 a tile for hi and one for lo.
@@ -53,13 +55,19 @@ constexpr float kTriUnit = 16384.f;                  // T's and P's elements, 1 
 constexpr int kScalF = 0, kScalD = kC, kScalO = 2 * kC, kScalG = 3 * kC, kScalU = kScalG + 1, kScalFirst = kScalG + 2, kScalE = kScalG + 4;
 static_assert((kScalE + kC / 2) * 4 <= 1024, "the factors' place");
 
-__device__ __forceinline__ int place_of(int first, int s) { return first / kC + s; }
+static_assert(kDeltaShort >= kC / 2, "places that do not meet");
+__host__ __device__ __forceinline__ bool by_tokens(int n_tok, int n_seq) { return n_seq > 1 && n_tok / (kC / 2) < n_tok / kC + n_seq; }
+__device__ __forceinline__ int place_of(const DeltaArgs& a, int first, int s) {
+    return by_tokens(a.n_tok, a.n_seq) ? first / (kC / 2) : first / kC + s;
+}
 
 struct Blobs {
     uint8_t* kq;                                     // [place][n_k][kKqBytes]
     uint8_t* head;                                   // [place][n_v][kHeadBytes]
 };
-__host__ __device__ __forceinline__ size_t places(int n_tok, int n_seq) { return (size_t)n_tok / kC + n_seq; }
+__host__ __device__ __forceinline__ size_t places(int n_tok, int n_seq) {
+    return by_tokens(n_tok, n_seq) ? (size_t)n_tok / (kC / 2) : (size_t)n_tok / kC + n_seq;
+}
 __device__ __forceinline__ Blobs blobs_of(const DeltaArgs& a) {
     return Blobs{a.workspace, a.workspace + places(a.n_tok, a.n_seq) * a.n_k * kKqBytes};
 }
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
         int lo = 0, len = a.n_seq;                   // the first sequence whose places begin behind this one: in [lo, lo + len]
         while (len > 0) {
             const int step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
-            const bool behind = at >= lo + len || place_of(min(max(a.cu_tokens[at], 0), a.n_tok), at) > place;
+            const bool behind = at >= lo + len || place_of(a, min(max(a.cu_tokens[at], 0), a.n_tok), at) > place;
             const unsigned there = __ballot_sync(0xffffffffu, behind);
             const int f = there ? __ffs(there) - 1 : 32;
             const int from = min(lo + f * step, lo + len);
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     const int slot = a.state_slots[s];
     if (slot < 0 || slot >= a.n_slots) return;
     const int2 span = tokens_of(a.cu_tokens, s, a.n_tok);
-    const int first = span.x + (place - place_of(span.x, s)) * kC, n = min(kC, span.y - first);
+    const int first = span.x + (place - place_of(a, span.x, s)) * kC, n = min(kC, span.y - first);
     if (first < span.x || n <= 0 || span.y - span.x < a.chunked_from) return;
     const Blobs w = blobs_of(a);
     uint8_t* kq = w.kq + ((size_t)place * a.n_k + kh) * kKqBytes;
@@ -691,7 +699,7 @@ __device__ __forceinline__ void tell(const Block& c, int i) {
 
 __device__ void copy_role(const Block& c, int lane) {
     const DeltaArgs& a = *c.a;
-    const int kh = c.h / (a.n_v / a.n_k), place0 = place_of(c.first - c.chunk0 * kC, c.s) + c.chunk0;
+    const int kh = c.h / (a.n_v / a.n_k), place0 = place_of(a, c.first - c.chunk0 * kC, c.s) + c.chunk0;
     const Blobs w = blobs_of(a);
     wait_for_stream();
     int done = 0;
@@ -1657,6 +1665,7 @@ cudaError_t launch(DeltaArgs a, cudaStream_t stream) {
 }  // namespace
 
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v) {
+    if (n_tok <= kDeltaShort) return 256;            // (token by token, without)
     size_t bytes = places(n_tok, n_seq) * ((size_t)n_k * kKqBytes + (size_t)n_v * kHeadBytes) + 256;
     if (most_segments(n_tok, n_seq, n_v, kSplitSms) > 1)
         bytes += ((size_t)n_tok * kHeadDim + (size_t)n_seq * kSplitMost * kStateFloats) * 2 * n_v * 4;
