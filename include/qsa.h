@@ -384,8 +384,8 @@ int qsa_extend_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t 
  *     hold; tokens from cu_tokens[n_seq] on belong to nobody: nothing of theirs is
  *     used, and their rows of the outputs stay as they are.  Bounds that fall or lie
  *     outside [0, n_tok] are clamped and reported (QSA_DEV_BAD_SEQ_LEN).  Where they
- *     fall, sequences may come to share tokens: which one's rows these end as is not
- *     specified, and qsa_delta_prompt leaves out those of more than 32 tokens whose
+ *     fall, sequences may come to share tokens: what their rows and states end as is
+ *     not specified, and qsa_delta_prompt leaves out those of more than 32 tokens whose
  *     bounds are out of order with another's.
  *   - state_slots: int32 [n_seq], the sequence's place in the state pool, or < 0: the
  *     sequence is left out, nothing of it is used and its rows of the outputs stay
@@ -451,10 +451,11 @@ int qsa_short_conv(const void* x, int64_t x_stride, int32_t type, const void* we
  *     tokens, earlier ones too (a value's own value dim alone).
  *   - By chunks, a value dim's new values of a chunk of 64 tokens share a power of two
  *     with the largest value in the chunk and with the state row that its first token
- *     leaves.  What the gates forget within a chunk leaves errors of 2^-30 of it in
- *     the chunk's outputs and of 2^-34 in the state (beside FP32's: visible where what
- *     is forgotten is some 2^16 times what follows).  What they have forgotten at the
- *     chunk's end or by its first token leaves none.
+ *     leaves.  That largest leaves errors of 2^-30 of it in the outputs of all of the
+ *     chunk's tokens and of 2^-34 in the state, beside FP32's: they show where it is
+ *     some 2^16 times what others of them are made of, those before it or behind a
+ *     gate that has forgotten it.  What the gates have forgotten at the chunk's end or
+ *     by its first token leaves none.
  *   - state and workspace must not overlap any other argument.
  *   - workspace: device memory of at least qsa_delta_prompt_workspace_bytes(n_tok,
  *     n_seq, n_k, n_v) bytes, 256-byte aligned, contents neither set nor kept:

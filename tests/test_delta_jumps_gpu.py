@@ -89,3 +89,18 @@ def test_what_forgotten_values_leave(qsa, size):  # noqa: F811
         assert bool((row <= FINE * end[s].square().sum(-1).sqrt() + 2.0 ** -34 * top).all())
         off = (got[lo + 30:lo + 50].double() - want[lo + 30:lo + 50]).abs()
         assert bool((off <= want[lo + 30:lo + 50].abs() * 2.0 ** -8 + 2.0 ** -30 * top).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 24])
+def test_what_comes_later(qsa, size):  # noqa: F811
+    """Large values at a chunk's end: the outputs before them, within the same errors; the chunk before is as it was."""
+    inputs, state, slots, _, cu = batch([128], 1, 2, torch.bfloat16, seed=6)
+    v = inputs[2].clone()
+    v[120:] *= size
+    inputs = (*inputs[:2], v, *inputs[3:])
+    want, size_of = norms.delta(*inputs, state, slots, None, cu, 1e-6, SCALE)
+    got = qsa.delta_prompt(*inputs, state, slots, None, cu)
+    norms.check(got[:64], want[:64], size_of[:64], torch.bfloat16)
+    top = v[64:].double().abs().amax(0)
+    off = (got[64:120].double() - want[64:120]).abs()
+    assert bool((off <= want[64:120].abs() * 2.0 ** -8 * 1.01 + 2.0 ** -17 * size_of[64:120] + 2.0 ** -30 * top).all())
