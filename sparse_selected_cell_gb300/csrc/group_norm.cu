@@ -159,8 +159,14 @@ cudaError_t launch_items(const NormArgs& a, cudaStream_t stream) {
 template <int TYPE, int LANES, int PIECES>
 cudaError_t launch_lanes(const NormArgs& a, cudaStream_t stream) {
     constexpr int kItems = PIECES == 1 ? 2 : 1;
-    if (kItems > 1 && (long long)a.n_tok * a.n_groups * LANES >= 4LL * kNormThreads * kItems * 152)
-        return launch_items<TYPE, LANES, PIECES, kItems>(a, stream);
+    if (kItems > 1) {
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if ((long long)a.n_tok * a.n_groups * LANES >= 4LL * kNormThreads * kItems * sms)
+            return launch_items<TYPE, LANES, PIECES, kItems>(a, stream);
+    }
     return launch_items<TYPE, LANES, PIECES, 1>(a, stream);
 }
 
