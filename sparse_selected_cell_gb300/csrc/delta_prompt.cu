@@ -651,6 +651,11 @@ constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
 constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 240 us instead of 269)
+// Sequences that the chunks' kernel has blocks for: by length, no more than can have more than kDeltaShort tokens (64 sequences x
+// 16 tokens x 32 heads 126 us instead of 138; the first kernel for short ones has looked at the others' bounds and slots).
+__host__ __device__ __forceinline__ int ranks(int n_tok, int n_seq) {
+    return n_seq > 1 && n_seq <= kRanked ? min(n_seq, n_tok / (kDeltaShort + 1)) : n_seq;
+}
 static_assert(kSplitSms <= kRanked, "where sequences are cut, their order is looked at with their lengths");
 constexpr uint64_t kWaitNs = 1000000000ull;
 // Tensor Memory columns.  S: for each 16 key dims 8 columns of hi and 8 of lo.  D: FP32, the decayed state, to which the chunk's
@@ -1240,7 +1245,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) delta_chunk_kernel(const __g
     c.base_u = base_u;
     c.abort_flag = reinterpret_cast<volatile int*>(c.base + kOffMisc + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const unsigned heads = (unsigned)a.n_seq * (unsigned)a.n_v, part = SPLIT ? blockIdx.x / heads : 0u, item = blockIdx.x - part * heads;
+    const unsigned heads = (unsigned)ranks(a.n_tok, a.n_seq) * (unsigned)a.n_v, part = SPLIT ? blockIdx.x / heads : 0u, item = blockIdx.x - part * heads;
     c.s = (int)(item / (unsigned)a.n_v);
     c.h = (int)(item - (unsigned)c.s * (unsigned)a.n_v);
     bool ordered = true;
@@ -1637,7 +1642,8 @@ cudaError_t launch(DeltaArgs a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     a.n_split = most_segments(a.n_tok, a.n_seq, a.n_v, sms < kSplitSms ? sms : kSplitSms);
-    const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, heads = (long long)a.n_seq * a.n_v, chunks = heads * (2 * a.n_split - 1);
+    const long long prep = (long long)places(a.n_tok, a.n_seq) * a.n_k, heads = (long long)a.n_seq * a.n_v,
+                    chunks = (long long)ranks(a.n_tok, a.n_seq) * a.n_v * (2 * a.n_split - 1);
     if (prep > 0x7fffffffLL || chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // Lengths are device data.  Few tokens in all: every sequence is short.  Several sequences: some may be.
     if (a.n_tok <= kDeltaShort || a.n_seq > 1) {
