@@ -90,12 +90,14 @@ __device__ __forceinline__ bool in_order(const DeltaArgs& a, int s, int2 span) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 286 and 357 us with 32 value heads, 173
-// and 317 with 8; 1 x 4,096 163 and 187 with 32; 1 x 2,048 99 and 98 with 32, 79 and 88 with 8.  Segments of 8 chunks lose:
-// 1 x 1,024 70 and 56 us.
-constexpr int kSplitMost = 8, kSplitChunks = 16;      // segments of a sequence; chunks of a segment, at least
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 338 and 407 us with 32 value heads, 206
+// and 362 with 8; 1 x 4,096 184 and 211 with 32, 131 and 184 with 8; 1 x 2,560 143 and 138 with 32, 134 and 133 with 16, 111 and
+// 122 with 8; 1 x 2,048 125 and 110, 105 and 106, 98 and 98: so from 40 chunks in a step on.  Segments of 8 chunks took 1 x 1,024
+// 88 us instead of 61.
+constexpr int kSplitMost = 8, kSplitChunks = 16, kSplitFrom = 40;   // segments of a sequence; chunks of a segment, of a step at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
+    if (n_tok < kC * kSplitFrom) return 1;
     const long long heads = (long long)n_seq * n_v;
     const long long room = heads > 0 ? (sms / heads + 1) / 2 : 0;   // n segments take 2 n - 1 blocks
     const int most = (int)min((long long)kSplitMost, min(room, (long long)n_tok / (kC * kSplitChunks)));
