@@ -15,18 +15,18 @@
 // (exact but for elements below 2^-24 of the row's largest, which lose bits); their lengths, 1 / |k|, are factors of
 // columns and rows in FP32.  The state, X, V', T and P are pairs of FP16, hi + lo (22 bits), in
 // products of which lo lo is left out; the state itself stays in FP32.  All products
-// are summed in FP32.  The pairs of a value dim and chunk share a power of two (S, X, V' and V' as it is
-// left at the chunk's end each their own), chosen from bounds that the rule gives (a chunk lengthens a state row by its values'
-// sum at most) with the decays of the gates, so that nothing
-// passes FP16's range and what counts stays in its upper bits.  (Products that end in outputs of
+// are summed in FP32.  The pairs of a value dim and chunk share a power of two (S, X, V' and V'
+// as it is left at the chunk's end each their own), chosen from bounds that the rule gives (a
+// chunk lengthens a state row by its values' sum at most) with the decays of the gates, so that
+// nothing passes FP16's range and what counts stays in its upper bits.  (Products that end in outputs of
 // single FP16, S Q^T without the state's lo, cost outputs 2^-12 of their row's length: 12 x 4,096
 // 782 us instead of 825, 1 x 8,192 292 instead of 327.)
 //
 // Times (BF16, 16 key and 32 value heads; the first kernel's and the second's): 12 sequences x
-// 4,096 tokens 318 + 462 us, 1 x 61 13 + 14 (the second begins beside the first: 18 in all);
-// 1 x 8,192, cut into segments, 60 + 166, and 19 + 49 to put them together.  FP16, 8 and 16 heads,
-// 24 x 1-2,000: 95 + 152.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
-// the first is bound by shared memory (59 % of its cycles) and by waiting on it, the second by a
+// 4,096 tokens 329 + 504 us, 1 x 61 12 + 14 (the second begins beside the first: 18 in all);
+// 1 x 8,192, cut into segments, 62 + 186, and 21 + 71 to put them together.  FP16, 8 and 16 heads,
+// 24 x 1-2,000: 98 + 159.  Neither bytes nor products bound them (12 x 4,096: 183 us of bytes):
+// the first is bound by shared memory (60 % of its cycles) and by waiting on it, the second by a
 // chain of dependent steps, see there.
 #include <type_traits>
 
@@ -90,10 +90,10 @@ __device__ __forceinline__ bool in_order(const DeltaArgs& a, int s, int2 span) {
 // chains (sequences times value heads) than SMs, a long sequence is cut into segments that run at once: the first as it is;
 // each other one from a state of zeros, and once more without values from the identity, which gives its R and, as outputs,
 // R_t q_t.  delta_join_kernel then takes the states from segment to segment, and delta_add_kernel adds S R_t q_t to the
-// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 338 and 407 us with 32 value heads, 206
-// and 362 with 8; 1 x 4,096 184 and 211 with 32, 131 and 184 with 8; 1 x 2,560 143 and 138 with 32, 134 and 133 with 16, 111 and
-// 122 with 8; 1 x 2,048 125 and 110, 105 and 106, 98 and 98: so from 40 chunks in a step on.  Segments of 8 chunks took 1 x 1,024
-// 88 us instead of 61.
+// segments' outputs, which are FP32 until then.  Cut and in one piece: 1 x 8,192 tokens 328 and 385 us with 32 value heads, 202
+// and 340 with 8; 1 x 4,096 180 and 200 with 32, 128 and 175 with 8; 1 x 2,560 140 and 132 with 32, 132 and 126 with 16, 109 and
+// 116 with 8; 1 x 2,048 122 and 105, 103 and 100, 96 and 93.  The border lies at 46 chunks with 32 heads, 44 with 16 and 36 with 8:
+// 40 chunks in a step is what the rule asks for.  Segments of 8 chunks took 1 x 1,024 86 us instead of 59.
 constexpr int kSplitMost = 8, kSplitChunks = 16, kSplitFrom = 40;   // segments of a sequence; chunks of a segment, of a step at least
 constexpr int kStateFloats = kHeadDim * kHeadDim;
 __host__ __device__ __forceinline__ int most_segments(int n_tok, int n_seq, int n_v, int sms) {
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
     const int place = (int)(blockIdx.x / (unsigned)a.n_k), kh = (int)(blockIdx.x - (unsigned)place * (unsigned)a.n_k);
     wait_for_stream();
     // From here on, once all blocks run, the chunks' kernel may set itself up beside this one: whatever was before this one is
-    // done, and it waits for this one before it reads what this one writes (1 x 61 tokens 19 us instead of 23).
+    // done, and it waits for this one before it reads what this one writes (1 x 61 tokens 18 us instead of 22).
     release_next();
     // the last sequence whose places begin here or before (every warp for itself)
     int s = 0;
@@ -619,11 +619,11 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 //
 // A block has one sequence and value head.  Everything is transposed: the 128 value dims are
 // the tensor core's rows (Tensor Memory's lanes), tokens or key dims its columns, so that a
-// thread of the state warps owns a value dim: its state row stays in the thread's registers,
+// thread of the state warps owns a value dim: its state row stays in its lane, in FP32,
 // and whatever passes from one product to the next is a thread's own row, read from the
 // accumulator and written back as the next one's A operand, with no exchange at all.
 //   state warps (0-7)     two warps to 32 value dims, each with half the key dims and half the tokens:
-//                         S (FP32 registers) -> pair;  X^T = V^T - (S K^T) f -> pair;
+//                         S -> pair;  X^T = V^T - (S K^T) f -> pair;
 //                         V'^T -> pair with each token's decay, and pair without;  S = g S + D
 //   output warps (8-11)   O^T = (S Q^T) o + V'^T P^T, to the type, to rows of tokens
 //   warp 12               issues all products:  S K^T (hi, lo), S Q^T (hi, lo), V'^T = X^T T^T (hi hi, lo hi, hi lo),
@@ -631,12 +631,13 @@ __global__ void __launch_bounds__(kPrepThreads, MORE ? 3 : 4) delta_prep_kernel(
 //   warps 13, 14          copy a chunk's operands and values ahead
 // The chain of one chunk is S K^T -> X -> V' -> D -> S; each of its products begins as soon as
 // the first half of its operand is there, and S Q^T is issued behind V', while its pairs are
-// formed.  A chunk takes some 4,500 cycles, 4,650 with all SMs at work: 1,000 until the last warp has S as
-// pairs, 500 until K S^T is there, 950 for X, 400 for V', 950 for its pairs, then 700 for D, beside
-// which the next values are brought to their units.  The tensor pipe is busy for 1,850 of them,
-// and a warp's issue slots for a third; conversions to pairs and the outputs' share them.
-// (The next values read while K S^T is formed, and brought to their units before V': 5 % slower,
-// the outputs of the chunk before are written then.)
+// formed.  A chunk takes some 5,100 cycles: 750 until a warp has S as pairs, 850 until K S^T is there (the units are
+// chosen and the values brought to theirs meanwhile), 600 for X, 1,050 for V' (the state is scaled meanwhile), 750 for its
+// pairs with and without decays, then 1,250 for D, beside which the next values are read.  The tensor pipe is busy for 1,850
+// of them, and the issue slots for two fifths; conversions to pairs and the outputs' share them.
+// (The next values read while K S^T is formed took 5 % longer, the outputs of the chunk before are written then; V' without
+// decays as pairs by the output warps 6 %; S Q^T's hi before V', and the largest values with their decays found by a warp of
+// its own or by the output warps, the same.)
 constexpr int kChunkThreads = 512;
 constexpr int kStages = 3, kVStages = 2;
 constexpr uint32_t kStageBytes = kKqBytes + kHeadBytes, kVBytes = kC * kHeadDim * 2;
@@ -652,9 +653,9 @@ enum { BAR_FULL = 0, BAR_EMPTY = BAR_FULL + kStages, BAR_VFULL = BAR_EMPTY + kSt
 constexpr uint32_t kOffMisc = kOffBar + NUM_BARS * 8;
 constexpr uint32_t kChunkBytes = kOffMisc + 16 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kChunkBytes <= 227 * 1024, "shared memory");
-constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 240 us instead of 269)
+constexpr int kRanked = 256;                         // sequences, at most, whose blocks go by length (24 x 1-2,000: 249 us instead of 279)
 // Sequences that the chunks' kernel has blocks for: by length, no more than can have more than kDeltaShort tokens (64 sequences x
-// 16 tokens x 32 heads 126 us instead of 138; the first kernel for short ones has looked at the others' bounds and slots).
+// 16 tokens x 32 heads 126 us instead of 138); delta_short_kernel has looked at the others' bounds and slots.
 __host__ __device__ __forceinline__ int ranks(int n_tok, int n_seq) {
     return n_seq > 1 && n_seq <= kRanked ? min(n_seq, n_tok / (kDeltaShort + 1)) : n_seq;
 }

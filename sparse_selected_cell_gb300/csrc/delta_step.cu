@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) delta_step_kernel(const __gri
 // query with their factors, the gates) is formed for all tokens at once, eight threads to a token, and kept in shared memory;
 // the chain from token to token is then S k, S q and the update, on pairs of FP32: 0.3 us a token (0.8 when each token's
 // factors were formed in the chain).  Many sequences are bound by FP32 operations, four to a state element and token:
-// 64 x 16 tokens x 32 heads take 134 us, of which the states' bytes would need 40.
+// 64 x 16 tokens x 32 heads take 112 us (126 with the chunks' kernels, which end at once), of which the states' bytes would need 40.
 template <int TYPE>
 __global__ void __launch_bounds__(32 * kStepWarps) delta_short_kernel(const __grid_constant__ DeltaArgs a) {
     constexpr int kParts = kHeadDim / kStepRows;

@@ -56,9 +56,9 @@ struct DeltaArgs {
 
 cudaError_t launch_delta_step(const DeltaArgs& a, cudaStream_t stream);
 // Of a step's sequences (cu_tokens) those of up to kDeltaShort tokens, token by token: a chunk of any length takes its SM for as
-// long as a full one.  With 32 value heads, in a graph, token by token and by chunks: 1 sequence x 16 tokens 6.8 and 17.2 us,
-// 1 x 32 11.6 and 17.3, 8 x 24 30.4 and 33.7, 64 x 24 184 and 211, 8 x 32 37.4 and 34.0, 64 x 32 230 and 214; 1 x 40 14.3 and
-// 17.5, 8 x 40 45.2 and 34.0.
+// long as a full one.  With 32 value heads, in a graph, token by token and by chunks: 1 sequence x 16 tokens 6.9 and 17.4 us,
+// 1 x 32 11.6 and 17.5, 8 x 24 30.0 and 34.2, 64 x 24 182 and 218, 8 x 32 37.6 and 34.4, 64 x 32 235 and 220; 1 x 40 14.4 and
+// 17.5, 8 x 40 45.5 and 34.5.  The border lies at some 45 tokens for one sequence and near 28 for many; this is one number for both.
 constexpr int kDeltaShort = 32;
 cudaError_t launch_delta_short(const DeltaArgs& a, cudaStream_t stream);
 size_t delta_prompt_workspace(int n_tok, int n_seq, int n_k, int n_v);
