@@ -104,3 +104,20 @@ def test_what_comes_later(qsa, size):  # noqa: F811
     top = v[64:].double().abs().amax(0)
     off = (got[64:120].double() - want[64:120]).abs()
     assert bool((off <= want[64:120].abs() * 2.0 ** -8 * 1.01 + 2.0 ** -17 * size_of[64:120] + 2.0 ** -30 * top).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 30, 2.0 ** 50, 2.0 ** 100])
+@pytest.mark.parametrize("lens", [[250], [64 * 42]], ids=["chunks", "segments"])
+def test_forgotten_within_a_chunk_then_everything(qsa, lens, size):  # noqa: F811
+    """What is far below a chunk's largest is rounded, to zero at worst, never to more than twice itself: all stays finite and of its
+    size, and from where the gates forget that, too, all is right again."""
+    inputs, state, slots, cu = jump(lens, torch.bfloat16, size, (0, 30), 30)
+    inputs[3][128] = 80.0
+    want, size_of = norms.delta(*inputs, state, slots, None, cu, 1e-6, SCALE)
+    end = ref.delta(*inputs, state, slots, None, cu, 1e-6, SCALE, ref.CHUNK)[1]
+    got = qsa.delta_prompt(*inputs, state, slots, None, cu)
+    assert bool(torch.isfinite(got).all()) and bool(torch.isfinite(state).all())
+    assert bool((got[30:128].double().abs().amax(0) <= 4 * want[30:128].abs().amax(0) + SCALE * 2.0 ** -7).all())
+    norms.check(got[128:], want[128:], size_of[128:], torch.bfloat16)
+    s = slots.long()
+    assert float((state[s] - end[s]).square().sum().sqrt()) <= FINE * float(end[s].square().sum().sqrt())
